@@ -91,8 +91,12 @@ enum {
   DSA_DEV_BAD_GRID_W = 8,   /* grid width < 1 (attention mass)             */
   DSA_DEV_BAD_ORDER = 9,    /* request_order entry outside 0..batch-1      */
   DSA_DEV_FREE_LIST_FULL = 10, /* dsa_evict_pages: more pages than capacity  */
-  DSA_DEV_BAD_QLEN = 11     /* dsa_prefill_sparse: q_len < 0 or above
-                               min(seq_len, max_q)                          */
+  DSA_DEV_BAD_QLEN = 11,    /* dsa_prefill_sparse: q_len < 0 or above
+                               min(seq_len, max_q); dsa_quant_write: new_len
+                               likewise; dsa_quant_read: rows outside the
+                               request or more than max_rows                */
+  DSA_DEV_BAD_SCALE = 12    /* 8-bit cache: a scale that is not a power of two
+                               in 2^-40 .. 2^40                             */
 };
 
 /* Problem sizes, shared by all calls on one KV cache. */
@@ -498,6 +502,167 @@ dsa_status dsa_prefill_plan(const dsa_dims* dims, int32_t max_q, int32_t* warps,
  */
 dsa_status dsa_set_prefill_split(int32_t parts);
 int32_t dsa_get_prefill_split(void);
+
+/*
+ * dsa_rope -- rotary position embedding with 1 to 4 position axes (time, height
+ * and width of an image or video token; text tokens have the same position on
+ * every axis).  The head_dim / 2 pairs of a head turn by
+ *   angle_i = positions[token][pair_axis[i]] * inv_freq[i]   (radians).
+ * Held by value on the host; the calls copy it.
+ *   axes       1..4
+ *   pairing    DSA_ROPE_HALVES: pair i is elements (i, i + head_dim/2);
+ *              DSA_ROPE_NEIGHBOURS: elements (2i, 2i+1)
+ *   inv_freq   radians per position of pair i, finite, |inv_freq| <= 2 pi (0
+ *              leaves the pair as it is: partial rotary embeddings)
+ *   pair_axis  axis of pair i, 0..axes-1
+ * Entries past head_dim / 2 are ignored.
+ */
+typedef enum { DSA_ROPE_HALVES = 0, DSA_ROPE_NEIGHBOURS = 1 } dsa_rope_pairing;
+typedef struct {
+  int32_t axes;
+  int32_t pairing;
+  double inv_freq[64];
+  uint8_t pair_axis[64];
+} dsa_rope;
+
+/*
+ * dsa_rope_axes -- rotate the query and key heads of `tokens` tokens:
+ *   (x, y) -> (x cos a - y sin a, y cos a + x sin a)   for every pair of a head,
+ * with a = angle_i above, kept as a 64-bit fixed-point fraction of a turn (far
+ * positions lose nothing), the rotation in fp32, rounded once to the output.
+ * The model side of the method's decode step: the pages it serves are image
+ * models whose tokens sit on a grid, so a token's rows, columns and frame are
+ * positions of their own.
+ *   dims          hq, hkv, head_dim, q_dtype (q, q_out) and kv_dtype (k, k_out)
+ *   tokens        >= 0 (0 is a no-op)
+ *   positions     [tokens][rope->axes] int32 (device), any value
+ *   q, q_out      [tokens][hq][head_dim], token t at element t * q_stride (and
+ *                 t * q_out_stride): slices of a fused projection are fine
+ *   k, k_out      [tokens][hkv][head_dim], likewise with k_stride, k_out_stride
+ * q and q_out, or k and k_out, may both be NULL (nothing done for them); an
+ * output may be its own input (same pointer and stride), else they must not
+ * overlap.  Pointers are 16-byte aligned and strides multiples of 16 bytes, at
+ * least hq (or hkv) * head_dim elements; else DSA_ERR_INVALID_ARG.
+ */
+dsa_status dsa_rope_axes(const dsa_dims* dims, const dsa_rope* rope, int32_t tokens,
+                         const int32_t* positions, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                         int64_t k_out_stride, void* stream);
+
+/*
+ * dsa_quant_cache -- a paged K/V cache held in 8 bits: half the bytes of the
+ * bf16 pages, so twice the rows in memory and half the bytes per decode step.
+ *   k_codes, v_codes  [num_pages][hkv][16][head_dim] e4m3 (4 exponent bits, 3
+ *                     mantissa bits, largest 448, NaN but no infinity): the 16
+ *                     rows of one (page, kv head) are contiguous
+ *   k_scale, v_scale  [num_pages][hkv] float32, powers of two in 2^-40 .. 2^40:
+ *                     the value of an element is code * scale
+ * A power of two costs an 8-bit float format nothing (its step is relative) and
+ * keeps everything exact that can be: reading back to bf16, and re-scaling the
+ * rows a page already holds when a larger row arrives (unless they fall below
+ * the format's smallest normal).  All pointers are device pointers owned by the
+ * caller, codes 16-byte aligned; num_pages * hkv * 16 < 2^32.  dims describes it
+ * as for the other calls, except that dims->kv_dtype is the type of K/V rows
+ * outside the cache (dsa_quant_write, dsa_quant_read; ignored by attention).
+ */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  float* k_scale;
+  float* v_scale;
+} dsa_quant_cache;
+
+/*
+ * dsa_quant_write -- append rows to the 8-bit cache, quantising them on the way.
+ * The last new_len[b] rows of request b, positions L_b - new_len[b] .. L_b - 1, come
+ * from k_new / v_new.  For each (page, kv head) that receives rows, and for K and V
+ * each by itself:
+ *   a     = largest finite magnitude of the new rows in that page
+ *   scale = the smallest 2^e with a <= 448 * 2^e, e limited to -40 .. 40; if the
+ *           page already holds rows before the new ones, at least its old scale
+ *   code  = round-to-nearest-even e4m3 of x / scale, saturated at +-448; NaN and
+ *           infinite elements become NaN
+ * and where the scale grew, the page's earlier rows are re-scaled to it (rounded
+ * to nearest even again).  Slots of the page after the last row keep their bytes.
+ *   max_new      row slots per request in k_new / v_new (>= 0; 0 is a no-op)
+ *   k_new, v_new [batch][max_new][hkv][head_dim] (kv_dtype, device, 16-byte
+ *                aligned): slot t of request b is row L_b - new_len[b] + t, at
+ *                element (b * max_new + t) * new_stride
+ *   new_stride   elements between two slots, >= hkv * head_dim, a multiple of
+ *                16 bytes (a slice of a fused projection is fine)
+ *   page_table, seq_len  as in dsa_decode_dense, L_b counting the new rows
+ *   new_len      [batch] int32 (device), 0 <= new_len[b] <= min(L_b, max_new), or
+ *                NULL: max_new for every request
+ * No page may receive rows twice in one call.  Invalid sizes set
+ * DSA_DEV_BAD_SEQ_LEN / _QLEN, a page id outside the pool DSA_DEV_BAD_PAGE, an
+ * old scale that is none DSA_DEV_BAD_SCALE; the rows concerned are not written.
+ */
+dsa_status dsa_quant_write(const dsa_dims* dims, const dsa_quant_cache* cache, int32_t max_new,
+                           const void* k_new, const void* v_new, int64_t new_stride,
+                           const int32_t* page_table, const int32_t* seq_len,
+                           const int32_t* new_len, void* ws, void* stream);
+
+/*
+ * dsa_quant_read -- rows of the 8-bit cache back as bf16 or fp32 (kv_dtype): rows
+ * row_start[b] .. row_start[b] + row_count[b] - 1 of request b as code * scale
+ * (exact: an e4m3 value times a power of two is a bf16 value).
+ *   max_rows     row slots per request in k_out / v_out (>= 0; 0 is a no-op)
+ *   row_start, row_count  [batch] int32 (device), row_start >= 0,
+ *                0 <= row_count <= max_rows, row_start + row_count <= L_b
+ *   k_out, v_out [batch][max_rows][hkv][head_dim] (kv_dtype, device, 16-byte
+ *                aligned; either may be NULL); slots t >= row_count[b] are not
+ *                written
+ * Invalid rows set DSA_DEV_BAD_QLEN (or _BAD_SEQ_LEN, _BAD_PAGE, _BAD_SCALE) and
+ * are not written.
+ */
+dsa_status dsa_quant_read(const dsa_dims* dims, const dsa_quant_cache* cache, int32_t max_rows,
+                          const int32_t* page_table, const int32_t* seq_len,
+                          const int32_t* row_start, const int32_t* row_count, void* k_out,
+                          void* v_out, void* ws, void* stream);
+
+/*
+ * dsa_decode_dense_quant, dsa_decode_sparse_quant, dsa_decode_sparse_masked_quant --
+ * dsa_decode_dense, dsa_decode_sparse and dsa_decode_sparse_masked over the 8-bit
+ * cache: the same row sets, softmax and errors, K and V dequantised in registers
+ * (k = code * scale).  Arguments as there, with the cache in the place of
+ * k_pages / v_pages and without the append (dsa_quant_write stores the step's row
+ * first).  out has q's type (q_dtype: what the model's next product reads), lse is
+ * float32.  bf16 q: the products are exact in fp32 and the softmax weights are
+ * rounded to 11 bits for the product with V, below out's own rounding; fp32 q:
+ * q and the weights enter as two 11-bit halves, about 2^-22.
+ * dsa_decode_sparse_quant takes the kept lists of dsa_build_index and schedules
+ * requests by its order like dsa_decode_sparse.
+ * The calls use the partials and the arrival counters of `ws` (the counters are
+ * back at zero after every call).
+ */
+dsa_status dsa_decode_dense_quant(const dsa_dims* dims, const void* q,
+                                  const dsa_quant_cache* cache, const int32_t* page_table,
+                                  const int32_t* seq_len, float scale, void* out, float* lse,
+                                  void* ws, void* stream);
+dsa_status dsa_decode_sparse_quant(const dsa_dims* dims, const void* q,
+                                   const dsa_quant_cache* cache, const int32_t* page_table,
+                                   const int32_t* seq_len, const int32_t* kept_idx,
+                                   const int32_t* kept_cnt, float scale, void* out, float* lse,
+                                   void* ws, void* stream);
+dsa_status dsa_decode_sparse_masked_quant(const dsa_dims* dims, const void* q,
+                                          const dsa_quant_cache* cache, const int32_t* page_table,
+                                          const int32_t* seq_len, const int32_t* prompt_len,
+                                          const int32_t* window, const uint32_t* keep_mask,
+                                          const int32_t* request_order, float scale, void* out,
+                                          float* lse, void* ws, void* stream);
+
+/*
+ * dsa_prefill_sparse_quant -- dsa_prefill_sparse over the 8-bit cache: several
+ * query tokens per request, each over its own causal kept set (their rows
+ * already written with dsa_quant_write).  Arguments and errors as there; q and out
+ * are bf16 (q_dtype), else DSA_ERR_UNSUPPORTED.
+ */
+dsa_status dsa_prefill_sparse_quant(const dsa_dims* dims, int32_t max_q, const void* q,
+                                    const dsa_quant_cache* cache, const int32_t* page_table,
+                                    const int32_t* seq_len, const int32_t* q_len,
+                                    const int32_t* prompt_len, const int32_t* window,
+                                    const uint32_t* keep_mask, const int32_t* request_order,
+                                    float scale, void* out, float* lse, void* ws, void* stream);
 
 /*
  * Waits for `stream`, then reads the workspace error word into *code_out (one of

@@ -43,6 +43,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "mma.cuh"
+#include "rows.cuh"
 #include "warp_attn.cuh"
 
 namespace dsa {
@@ -146,21 +147,6 @@ struct DecodeTiling {
 constexpr int kRowsDense = kModeDense;  // rows 0..L-1
 constexpr int kRowsList = kModeList;    // the kept list written by dsa_build_index
 constexpr int kRowsMask = kModeMask;    // the kept set built in the kernel from the mask
-
-// Position (0..31) of the set bit of rank r (0-based, ascending) in w; any
-// value in 0..31 when w has no such bit.
-__device__ __forceinline__ int select_bit(unsigned w, int r) {
-  int pos = 0, c = __popc(w & 0xffffu);
-  if (r >= c) { r -= c; w >>= 16; pos += 16; }
-  c = __popc(w & 0xffu);
-  if (r >= c) { r -= c; w >>= 8; pos += 8; }
-  c = __popc(w & 0xfu);
-  if (r >= c) { r -= c; w >>= 4; pos += 4; }
-  c = __popc(w & 0x3u);
-  if (r >= c) { r -= c; w >>= 2; pos += 2; }
-  if (r >= static_cast<int>(w & 1u)) pos += 1;
-  return pos;
-}
 
 template <int MODE>
 __device__ __forceinline__ int request_rows(const DecodeLaunch& a, int b, int hk, int L) {

@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "dsa.h"
+#include "host.h"
 #include "internal.h"
 
 // Build-time tuning knobs: waves of resident CTAs the chunking aims for.  Kept
@@ -40,67 +41,10 @@
 namespace dsa {
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 // Process-wide: CTAs per cluster of sparse decode (dsa_set_sparse_cluster).
 std::atomic<int> g_sparse_cluster{DSA_SPARSE_CLUSTER};
 // Process-wide: parts of dsa_prefill_sparse's units (dsa_set_prefill_split).
 std::atomic<int> g_prefill_split{0};
-
-bool dims_valid(const dsa_dims* d) {
-  if (d == nullptr) return false;
-  if (d->batch < 0 || d->hq < 1 || d->hkv < 1 || d->head_dim < 1) return false;
-  if (d->hq % d->hkv != 0) return false;
-  if (d->num_pages < 1 || d->max_pages_per_req < 1 || d->max_window < 0) return false;
-  if (d->mask_words < 1 || static_cast<int64_t>(d->mask_words) * 32 < d->max_window) return false;
-  if (d->max_kept < 1) return false;
-  if (d->q_dtype != DSA_F32 && d->q_dtype != DSA_BF16) return false;
-  if (d->kv_dtype != DSA_F32 && d->kv_dtype != DSA_BF16) return false;
-  // page_table entries index rows as page * 16 * hkv * head_dim elements in 64-bit math;
-  // logical positions are int32.
-  if (static_cast<int64_t>(d->max_pages_per_req) * kPage > INT32_MAX / 2) return false;
-  return true;
-}
-
-bool dims_supported(const dsa_dims* d) {
-  const int g = d->hq / d->hkv;
-  return d->page_size == kPage && (d->head_dim == 64 || d->head_dim == 128) &&
-         (g == 1 || g == 2 || g == 4 || g == 8);
-}
-
-dsa_status check_dims(const dsa_dims* d) {
-  if (!dims_valid(d)) return DSA_ERR_INVALID_ARG;
-  if (!dims_supported(d)) return DSA_ERR_UNSUPPORTED;
-  return DSA_OK;
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Upper bound of chunks per (request, kv head) for a row count n_max.
-int chunk_bound(int64_t n_max) {
-  const int64_t c = ceil_div(n_max, kChunkQuantum);
-  return static_cast<int>(c < kMaxChunks ? (c < 1 ? 1 : c) : kMaxChunks);
-}
-
-int64_t dense_rows(const dsa_dims* d) { return static_cast<int64_t>(d->max_pages_per_req) * kPage; }
-
-size_t partial_bytes(const dsa_dims* d, int per_head_floats) {
-  const int64_t n_max = dense_rows(d) > d->max_kept ? dense_rows(d) : d->max_kept;
-  return static_cast<size_t>(d->batch) * d->hq * chunk_bound(n_max) * per_head_floats *
-         sizeof(float);
-}
-
-int sm_count() {
-  static int cache[kMaxDevices] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  if (dev >= 0 && dev < kMaxDevices && cache[dev] > 0) return cache[dev];
-  int n = 1;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    n = 1;
-  if (dev >= 0 && dev < kMaxDevices) cache[dev] = n;
-  return n;
-}
 
 // Rows per CTA: enough CTAs for `waves` waves of resident CTAs, at most
 // kMaxChunks chunks per (request, kv head), a multiple of the CTA's rows per pass.
@@ -127,61 +71,6 @@ void choose_chunks(int64_t n_max, int64_t units, int resident, int quantum, int 
   *chunk = static_cast<int>(c);
   *num_chunks = static_cast<int>(ceil_div(n_max, c));
 }
-
-dsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
-
-int32_t* err_word(void* ws) { return reinterpret_cast<int32_t*>(ws); }
-
-float* partials(void* ws) {
-  return reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(ws) + kWsHeader);
-}
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-// Partials region of the workspace, the same for every entry point.
-size_t partials_region(const dsa_dims* d) {
-  const size_t dec = partial_bytes(d, d->head_dim + 2);
-  const size_t mass = partial_bytes(d, 6);
-  // dsa_prefill_sparse's split parts: at most one wave of resident CTAs, at
-  // most kMultiPartWarpsPerSm warps of 16 (query, head) rows each per SM
-  const size_t multi = static_cast<size_t>(sm_count()) * kMultiPartWarpsPerSm * 16 *
-                       (d->head_dim + 2) * sizeof(float);
-  size_t r = dec > mass ? dec : mass;
-  if (multi > r) r = multi;
-  return round_up(r, 256);
-}
-
-// [batch][hkv] kept counts of dsa_decode_sparse_masked, after the partials.
-int32_t* unit_rows(const dsa_dims* d, void* ws) {
-  return reinterpret_cast<int32_t*>(reinterpret_cast<unsigned char*>(ws) + kWsHeader +
-                                    partials_region(d));
-}
-
-size_t unit_ints_region(const dsa_dims* d) {
-  return round_up(static_cast<size_t>(d->batch) * d->hkv * sizeof(int32_t), 256);
-}
-
-// [batch] request schedule dsa_build_index leaves for dsa_decode_sparse, after
-// the kept counts of the fused call.
-int32_t* sched_region(const dsa_dims* d, void* ws) {
-  return reinterpret_cast<int32_t*>(reinterpret_cast<unsigned char*>(ws) + kWsHeader +
-                                    partials_region(d) + unit_ints_region(d));
-}
-
-size_t sched_bytes(const dsa_dims* d) {
-  return round_up(static_cast<size_t>(d->batch) * sizeof(int32_t), 256);
-}
-
-// Arrival counters of dsa_prefill_sparse's split units, after the schedule.
-int32_t* multi_count_region(const dsa_dims* d, void* ws) {
-  return reinterpret_cast<int32_t*>(reinterpret_cast<unsigned char*>(ws) + kWsHeader +
-                                    partials_region(d) + unit_ints_region(d) + sched_bytes(d));
-}
-
-constexpr size_t kMultiCountBytes = kMultiCounters * sizeof(int32_t);
-
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct Plan {
   int chunk, num_chunks, quantum, per_sm, cluster, warps, tile_rows, build;

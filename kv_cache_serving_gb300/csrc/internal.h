@@ -197,4 +197,113 @@ struct DecodeShape {
 DecodeShape decode_shape_bf16(int head_dim, int group, int mode, int build);
 DecodeShape decode_shape_f32(int head_dim, int group, int mode, int build);
 
+// ---- 8-bit K/V cache (quant_*.cu) and rotary positions (rope.cu) ----
+
+struct QuantDecodeLaunch {
+  const void* q;
+  int q_bf16;                // else fp32; out has the same type
+  const uint8_t* k;          // [num_pages][hkv][16][head_dim] e4m3
+  const uint8_t* v;
+  const float* k_scale;      // [num_pages][hkv]
+  const float* v_scale;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const int32_t* kept_idx;    // kModeList only
+  const int32_t* kept_cnt;    // kModeList only
+  const int32_t* prompt_len;  // kModeMask only
+  const int32_t* window;      // kModeMask only
+  const uint32_t* keep_mask;  // kModeMask only
+  const int32_t* order;       // kModeMask only: request at each position, or null
+  const int32_t* sched;       // kModeList only: as in DecodeLaunch
+  const int32_t* sched_tag;
+  int32_t sched_expect;
+  int32_t batch, hq, hkv, group, head_dim, max_pages, num_pages, max_kept;
+  int32_t max_window, mask_words;
+  float scale_log2;
+  void* out;
+  float* lse;
+  float* part;       // partial states, quant_part_floats() each
+  int32_t* count;    // arrival counters, 0 between launches
+  int32_t* err;
+  int32_t parts;     // sparse rows: CTAs per unit at most (set by the launch)
+  int32_t min_tiles; // dense rows: least tiles per CTA (set by the launch)
+  int64_t part_cap;  // floats the workspace holds at `part`
+  int32_t sms;
+};
+
+// Floats of one partial state of `group` heads, whole 16-byte pieces.
+constexpr __host__ __device__ int quant_part_floats(int group, int head_dim) {
+  return (group * (head_dim + 2) + 3) / 4 * 4;
+}
+// Most CTAs that share one unit of sparse rows, and the least tiles (16 rows) a
+// CTA of the dense call takes: four for each of its warps.
+constexpr int kQuantMaxParts = 8;
+constexpr int kQuantMinTiles = 16;
+
+// Several query tokens per request over the 8-bit cache: q and out bf16.
+struct QuantChunkLaunch {
+  const uint16_t* q;  // [batch][max_q][hq][head_dim] bf16
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const int32_t* q_len;
+  const int32_t* prompt_len;
+  const int32_t* window;
+  const uint32_t* keep_mask;
+  const int32_t* order;
+  int32_t batch, hq, hkv, group_log2, head_dim, max_pages, num_pages;
+  int32_t max_window, mask_words, max_q;
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  float* part;
+  int32_t* count;
+  int32_t* err;
+  int64_t part_cap;
+  int32_t q_tiles, parts;  // set by the launch
+  int32_t sms;
+};
+
+struct QuantRowsLaunch {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int rows_bf16;             // type of the rows outside the cache, else fp32
+  const void* k_rows;        // write: new rows
+  const void* v_rows;
+  void* k_out;               // read: where the rows go, or null
+  void* v_out;
+  int64_t stride;            // write: elements between two row slots
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const int32_t* start;      // read: first row of each request
+  const int32_t* count;      // rows of each request, or null (max_rows each)
+  int32_t batch, hkv, head_dim, max_pages, num_pages;
+  int32_t max_rows, slots;   // row slots per request; pages they can touch
+  int32_t* err;
+};
+
+struct RopeLaunch {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
+  const int32_t* positions;  // [tokens][axes]
+  int32_t tokens, hq, hkv, head_dim, axes, neighbours;
+  int q_bf16, k_bf16;
+  uint64_t turn[64];         // pair i: 2^64 turns per position, modulo 2^64
+  uint8_t pair_axis[64];
+};
+
+cudaError_t launch_quant_decode(const QuantDecodeLaunch& a, int mode, cudaStream_t s);
+cudaError_t launch_quant_chunk(const QuantChunkLaunch& a, cudaStream_t s);
+cudaError_t launch_quant_write(const QuantRowsLaunch& a, cudaStream_t s);
+cudaError_t launch_quant_read(const QuantRowsLaunch& a, cudaStream_t s);
+cudaError_t launch_rope(const RopeLaunch& a, int sms, cudaStream_t s);
+
 }  // namespace dsa

@@ -1,0 +1,137 @@
+// rope.cu -- rotary positions with several axes on the query and key heads of a batch
+// of tokens, q and k in one launch.
+//
+// Pair i of every head of a token turns by positions[axis(i)] * inv_freq[i].  The angle
+// is a fixed-point fraction of a turn: the host gives pair i's turns per position as a
+// 64-bit fraction, the kernel multiplies by the position modulo 2^64 -- which is the
+// reduction to one turn, exact for any position -- and takes the sine and cosine of the
+// top 32 bits (error 2^-32 turns) with sincospi.
+//
+// Bound by HBM: each element is read and written once.  A CTA computes the table of
+// its tokens' sines and cosines in shared memory once for all heads, then streams the
+// heads; a thread handles 8 pairs (two 16-byte loads and stores with bf16).
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mma.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* p, size_t at, float (&x)[8]) {
+  if constexpr (BF16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16_lo(w[i]);
+      x[2 * i + 1] = bf16_hi(w[i]);
+    }
+  } else {
+    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
+    const float4 u = f[0], v = f[1];
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void* p, size_t at, const float (&x)[8]) {
+  if constexpr (BF16) {
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + at) =
+        make_uint4(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]), bf16x2_rn(x[4], x[5]),
+                   bf16x2_rn(x[6], x[7]));
+  } else {
+    float4* f = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + at);
+    f[0] = make_float4(x[0], x[1], x[2], x[3]);
+    f[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// 8 pairs p0 .. p0 + 7 of the head at element `at`.
+template <int D, bool BF16, bool NEAR>
+__device__ __forceinline__ void rotate8(const void* in, size_t at_in, void* out, size_t at_out,
+                                        int p0, const float2* cs) {
+  const int lo = NEAR ? 2 * p0 : p0, hi = NEAR ? 2 * p0 + 8 : p0 + D / 2;
+  float u[8], v[8];
+  load8<BF16>(in, at_in + lo, u);
+  load8<BF16>(in, at_in + hi, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 t = cs[p0 + i];
+    float& x = NEAR ? (i < 4 ? u[2 * i] : v[2 * i - 8]) : u[i];
+    float& y = NEAR ? (i < 4 ? u[2 * i + 1] : v[2 * i - 7]) : v[i];
+    const float rx = x * t.x - y * t.y, ry = y * t.x + x * t.y;
+    x = rx;
+    y = ry;
+  }
+  store8<BF16>(out, at_out + lo, u);
+  store8<BF16>(out, at_out + hi, v);
+}
+
+template <int D, bool QBF, bool KBF, bool NEAR, int TT>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeLaunch a) {
+  constexpr int kPairs = D / 2, kGroups = kPairs / 8;
+  __shared__ float2 cs[TT][kPairs];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t0 = blockIdx.x * TT, nt = min(TT, a.tokens - t0);
+  for (int x = threadIdx.x; x < nt * kPairs; x += kRopeThreads) {
+    const int t = x / kPairs, i = x % kPairs;
+    const int64_t pos = a.positions[static_cast<size_t>(t0 + t) * a.axes + a.pair_axis[i]];
+    const uint64_t turn = static_cast<uint64_t>(pos) * a.turn[i];
+    // signed half turns in [-1, 1)
+    const float half = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+    float s, c;
+    sincospif(half, &s, &c);
+    cs[t][i] = make_float2(c, s);
+  }
+  __syncthreads();
+  const int nq = a.q != nullptr ? a.hq : 0, nk = a.k != nullptr ? a.hkv : 0;
+  const int per = (nq + nk) * kGroups;
+  for (int x = threadIdx.x; x < nt * per; x += kRopeThreads) {
+    const int t = x / per, y = x % per;
+    const int h = y / kGroups, p0 = 8 * (y % kGroups);
+    const size_t tok = static_cast<size_t>(t0 + t);
+    if (h < nq)
+      rotate8<D, QBF, NEAR>(a.q, tok * a.q_stride + static_cast<size_t>(h) * D, a.q_out,
+                            tok * a.q_out_stride + static_cast<size_t>(h) * D, p0, cs[t]);
+    else
+      rotate8<D, KBF, NEAR>(a.k, tok * a.k_stride + static_cast<size_t>(h - nq) * D, a.k_out,
+                            tok * a.k_out_stride + static_cast<size_t>(h - nq) * D, p0, cs[t]);
+  }
+}
+
+template <int D, bool QBF, bool KBF, bool NEAR>
+cudaError_t launch_tokens(const RopeLaunch& a, int sms, cudaStream_t s) {
+  // four tokens per CTA once that still fills the GPU (the table then costs each
+  // thread one sine), else one
+  if (a.tokens >= 16 * sms)
+    return launch_pdl(rope_kernel<D, QBF, KBF, NEAR, 4>, dim3((a.tokens + 3) / 4),
+                      dim3(kRopeThreads), 0, s, a);
+  return launch_pdl(rope_kernel<D, QBF, KBF, NEAR, 1>, dim3(a.tokens), dim3(kRopeThreads), 0, s, a);
+}
+template <int D, bool QBF, bool KBF>
+cudaError_t launch_pairing(const RopeLaunch& a, int sms, cudaStream_t s) {
+  return a.neighbours ? launch_tokens<D, QBF, KBF, true>(a, sms, s)
+                      : launch_tokens<D, QBF, KBF, false>(a, sms, s);
+}
+template <int D>
+cudaError_t launch_types(const RopeLaunch& a, int sms, cudaStream_t s) {
+  if (a.q_bf16)
+    return a.k_bf16 ? launch_pairing<D, true, true>(a, sms, s)
+                    : launch_pairing<D, true, false>(a, sms, s);
+  return a.k_bf16 ? launch_pairing<D, false, true>(a, sms, s)
+                  : launch_pairing<D, false, false>(a, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeLaunch& a, int sms, cudaStream_t s) {
+  return a.head_dim == 128 ? launch_types<128>(a, sms, s) : launch_types<64>(a, sms, s);
+}
+
+}  // namespace dsa

@@ -19,7 +19,7 @@ NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 DSA_F32, DSA_BF16 = 0, 1
 DEV_ERRORS = {0: "OK", 1: "BAD_SEQ_LEN", 2: "BAD_PROMPT", 3: "BAD_WINDOW", 4: "BAD_PAGE",
               5: "BAD_INDEX", 6: "BAD_COUNT", 7: "TIMEOUT", 8: "BAD_GRID_W", 9: "BAD_ORDER",
-              10: "FREE_LIST_FULL", 11: "BAD_QLEN"}
+              10: "FREE_LIST_FULL", 11: "BAD_QLEN", 12: "BAD_SCALE"}
 PAGE = 16
 
 
@@ -45,6 +45,19 @@ class dsa_host_io(ctypes.Structure):
                 ("host_out", ctypes.c_void_p), ("out_bytes", ctypes.c_size_t)]
 
 
+ROPE_HALVES, ROPE_NEIGHBOURS = 0, 1
+
+
+class dsa_rope(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("pairing", ctypes.c_int32),
+                ("inv_freq", ctypes.c_double * 64), ("pair_axis", ctypes.c_uint8 * 64)]
+
+
+class dsa_quant_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
 _lib = None
 _lib_path = None
 
@@ -65,7 +78,9 @@ def _load():
         path = _build.build()
     lib = ctypes.CDLL(path)
     P, I32, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+    I64 = ctypes.c_int64
     D = ctypes.POINTER(dsa_dims)
+    C = ctypes.POINTER(dsa_quant_cache)
     sig = {
         "dsa_version": ([], I32),
         "dsa_status_string": ([I32], ctypes.c_char_p),
@@ -92,6 +107,14 @@ def _load():
         "dsa_prefill_plan": ([D, I32] + [ctypes.POINTER(I32)] * 6, I32),
         "dsa_set_prefill_split": ([I32], I32),
         "dsa_get_prefill_split": ([], I32),
+        "dsa_rope_axes": ([D, ctypes.POINTER(dsa_rope), I32, P, P, I64, P, I64, P, I64, P, I64,
+                           P], I32),
+        "dsa_quant_write": ([D, C, I32, P, P, I64, P, P, P, P, P], I32),
+        "dsa_quant_read": ([D, C, I32, P, P, P, P, P, P, P, P], I32),
+        "dsa_decode_dense_quant": ([D, P, C, P, P, F32, P, P, P, P], I32),
+        "dsa_decode_sparse_quant": ([D, P, C, P, P, P, P, F32, P, P, P, P], I32),
+        "dsa_decode_sparse_masked_quant": ([D, P, C, P, P, P, P, P, P, F32, P, P, P, P], I32),
+        "dsa_prefill_sparse_quant": ([D, I32, P, C, P, P, P, P, P, P, P, F32, P, P, P, P], I32),
         "dsa_get_device_error": ([P, P, ctypes.POINTER(I32)], I32),
         "dsa_clear_device_error": ([P, P], I32),
     }
@@ -382,6 +405,238 @@ def dsa_attention_mass(dims, q, k_pages, page_table, seq_len, prompt_len, window
         _ptr(grid_w, _I32, "grid_w"), int(r_local), int(r_diag), float(scale),
         _ptr(mass, torch.float32, "mass"), _ptr(offset_mass, torch.float32, "offset_mass"),
         _ptr(ws), _stream(stream)), "dsa_attention_mass")
+
+
+def make_rope(inv_freq, pair_axis, pairing="halves", axes=None) -> dsa_rope:
+    """A dsa_rope: inv_freq[i] radians per position and pair_axis[i] the position axis
+    of pair i, head_dim / 2 of each; pairing "halves" (elements i and i + head_dim/2)
+    or "neighbours" (2i and 2i + 1); axes: columns of positions (default: as many as
+    pair_axis names)."""
+    inv_freq, pair_axis = [float(x) for x in inv_freq], [int(x) for x in pair_axis]
+    if len(inv_freq) != len(pair_axis) or not 1 <= len(inv_freq) <= 64:
+        raise ValueError("make_rope: one inv_freq and one pair_axis for each pair, at most 64")
+    if pairing not in ("halves", "neighbours"):
+        raise ValueError(f"make_rope: pairing {pairing!r}")
+    if min(pair_axis) < 0 or max(pair_axis) > 3:
+        raise ValueError("make_rope: pair_axis outside 0..3")
+    r = dsa_rope(axes=max(pair_axis) + 1 if axes is None else int(axes),
+                 pairing=ROPE_HALVES if pairing == "halves" else ROPE_NEIGHBOURS)
+    r.pairs = len(inv_freq)
+    for i, (f, a) in enumerate(zip(inv_freq, pair_axis)):
+        r.inv_freq[i], r.pair_axis[i] = f, a
+    return r
+
+
+def rope_sections(sections, interleaved=False) -> list:
+    """pair_axis for make_rope: sections[a] pairs turn with axis a, as whole blocks, or
+    dealt out in turn (axis 0, 1, 2, 0, 1, 2, ...) until an axis has its share."""
+    left = [int(n) for n in sections]
+    if not interleaved:
+        return [a for a, n in enumerate(left) for _ in range(n)]
+    out = []
+    while any(n > 0 for n in left):
+        for a, n in enumerate(left):
+            if n > 0:
+                left[a] -= 1
+                out.append(a)
+    return out
+
+
+def _here(*tensors):
+    """The calls launch on the current device: refuse tensors of another one."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, current device cuda:{dev}")
+
+
+def _rows_view(t, heads, head_dim, dtype, what):
+    """Pointer and row stride of [..., heads, head_dim] whose rows are evenly spaced (the
+    last two dimensions contiguous: slices of a fused projection are fine)."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() < 3 or tuple(t.shape[-2:]) != (heads, head_dim):
+        raise ValueError(f"{what} must be [..., {heads}, {head_dim}]")
+    if (t.stride(-1) != 1 and head_dim > 1) or (t.stride(-2) != head_dim and heads > 1):
+        raise ValueError(f"{what}: the heads of a row must be contiguous")
+    row = None  # elements between rows, from the innermost row dimension that has several
+    for i in range(t.dim() - 3, -1, -1):
+        if t.shape[i] == 1:
+            continue
+        if row is None:
+            row, span = t.stride(i), t.stride(i) * t.shape[i]
+        elif t.stride(i) != span:
+            raise ValueError(f"{what}: rows must be evenly spaced")
+        else:
+            span = t.stride(i) * t.shape[i]
+    return ctypes.c_void_p(t.data_ptr()), heads * head_dim if row is None else row
+
+
+def _types(dims):
+    return tuple(torch.bfloat16 if c == DSA_BF16 else torch.float32
+                 for c in (dims.q_dtype, dims.kv_dtype))
+
+
+def _shape(t, want, what):
+    if t is not None and tuple(t.shape) != tuple(want):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(want)}")
+
+
+def dsa_rope_axes(dims, rope, positions, q, k, q_out, k_out, stream=None):
+    """Rotate q [tokens, hq, head_dim] into q_out and k [tokens, hkv, head_dim] into k_out
+    (either pair may be None; an output may be its own input) by the tokens'
+    positions [tokens, axes] int32.  Rows may be strided (slices of a fused projection)."""
+    if positions.dim() != 2 or positions.shape[1] != rope.axes:
+        raise ValueError(f"positions must be [tokens, {rope.axes}]")
+    if getattr(rope, "pairs", dims.head_dim // 2) != dims.head_dim // 2:
+        raise ValueError(f"rope has {rope.pairs} pairs, head_dim {dims.head_dim}")
+    n = positions.shape[0]
+    qd, kd = _types(dims)
+    args = []
+    for t, heads, dt, what in ((q, dims.hq, qd, "q"), (k, dims.hkv, kd, "k"),
+                               (q_out, dims.hq, qd, "q_out"), (k_out, dims.hkv, kd, "k_out")):
+        _shape(t, (n, heads, dims.head_dim), what)
+        args += _rows_view(t, heads, dims.head_dim, dt, what)
+    _here(positions, q, k, q_out, k_out)
+    _check(_load().dsa_rope_axes(ctypes.byref(dims), ctypes.byref(rope), n,
+                                 _ptr(positions, _I32, "positions"), *args, _stream(stream)),
+           "dsa_rope_axes")
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def quant_cache(k_codes, v_codes, k_scale, v_scale) -> dsa_quant_cache:
+    """dsa_quant_cache over codes [num_pages, hkv, 16, head_dim] (float8_e4m3fn or their
+    bytes) and scales [num_pages, hkv] float32; keeps the tensors alive."""
+    for t, what in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+        _ptr(t, _CODES, what)
+        if t.dim() != 4 or t.shape[2] != PAGE:
+            raise ValueError(f"{what} must be [num_pages, hkv, {PAGE}, head_dim]")
+    _shape(v_codes, k_codes.shape, "v_codes")
+    for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _ptr(t, torch.float32, what)
+        _shape(t, k_codes.shape[:2], what)
+    c = dsa_quant_cache(*(t.data_ptr() for t in (k_codes, v_codes, k_scale, v_scale)))
+    c.tensors = (k_codes, v_codes, k_scale, v_scale)
+    return c
+
+
+def _cache(dims, cache):
+    """The cache as a C argument, its shape checked against dims."""
+    if not isinstance(cache, dsa_quant_cache):
+        raise TypeError("cache must be a dsa_quant_cache (see quant_cache)")
+    if hasattr(cache, "tensors"):
+        _shape(cache.tensors[0], (dims.num_pages, dims.hkv, PAGE, dims.head_dim), "cache codes")
+        _here(*cache.tensors)
+    return ctypes.byref(cache)
+
+
+def dsa_quant_write(dims, cache, k_new, v_new, page_table, seq_len, new_len, ws, stream=None):
+    """Quantise k_new / v_new [batch, max_new, hkv, head_dim] into the cache as the last
+    new_len[b] rows of each request (new_len None: all max_new slots)."""
+    kd = _types(dims)[1]
+    if k_new.dim() != 4 or k_new.shape[0] != dims.batch:
+        raise ValueError("k_new must be [batch, max_new, hkv, head_dim]")
+    _shape(v_new, k_new.shape, "v_new")
+    k, ks = _rows_view(k_new, dims.hkv, dims.head_dim, kd, "k_new")
+    v, vs = _rows_view(v_new, dims.hkv, dims.head_dim, kd, "v_new")
+    if ks != vs:
+        raise ValueError("k_new and v_new must have the same row stride")
+    _here(k_new, v_new, page_table, seq_len, new_len, ws)
+    _check(_load().dsa_quant_write(
+        ctypes.byref(dims), _cache(dims, cache), int(k_new.shape[1]), k, v, ks,
+        _ptr(page_table, _I32, "page_table"), _ptr(seq_len, _I32, "seq_len"),
+        _ptr(new_len, _I32, "new_len"), _ptr(ws), _stream(stream)), "dsa_quant_write")
+
+
+def dsa_quant_read(dims, cache, page_table, seq_len, row_start, row_count, k_out, v_out, ws,
+                   stream=None):
+    """Rows row_start[b] .. + row_count[b] - 1 of each request out of the cache into
+    k_out / v_out [batch, max_rows, hkv, head_dim] (either may be None)."""
+    out = k_out if k_out is not None else v_out
+    if out is None:
+        raise ValueError("k_out or v_out must be given")
+    kd = _types(dims)[1]
+    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+        _shape(t, (dims.batch, out.shape[1], dims.hkv, dims.head_dim), what)
+    _here(k_out, v_out, page_table, seq_len, row_start, row_count, ws)
+    _check(_load().dsa_quant_read(
+        ctypes.byref(dims), _cache(dims, cache), int(out.shape[1]),
+        _ptr(page_table, _I32, "page_table"), _ptr(seq_len, _I32, "seq_len"),
+        _ptr(row_start, _I32, "row_start"), _ptr(row_count, _I32, "row_count"),
+        _ptr(k_out, kd, "k_out"), _ptr(v_out, kd, "v_out"), _ptr(ws), _stream(stream)),
+        "dsa_quant_read")
+
+
+def _attn_out(dims, q, out, lse, rows):
+    """Pointers of q, out (q's type) and lse, their shapes checked."""
+    qd = _types(dims)[0]
+    shape = tuple(rows) + (dims.hq, dims.head_dim)
+    _shape(q, shape, "q")
+    _shape(out, shape, "out")
+    _shape(lse, shape[:-1], "lse")
+    _here(q, out, lse)
+    return _ptr(q, qd, "q"), _ptr(out, qd, "out"), _ptr(lse, torch.float32, "lse")
+
+
+def dsa_decode_dense_quant(dims, q, cache, page_table, seq_len, scale, out, lse, ws, stream=None):
+    """dsa_decode_dense over the 8-bit cache; out has q's type."""
+    qp, op, lp = _attn_out(dims, q, out, lse, (dims.batch,))
+    _here(page_table, seq_len, ws)
+    _check(_load().dsa_decode_dense_quant(
+        ctypes.byref(dims), qp, _cache(dims, cache), _ptr(page_table, _I32, "page_table"),
+        _ptr(seq_len, _I32, "seq_len"), float(scale), op, lp, _ptr(ws), _stream(stream)),
+        "dsa_decode_dense_quant")
+
+
+def dsa_decode_sparse_quant(dims, q, cache, page_table, seq_len, kept_idx, kept_cnt, scale, out,
+                            lse, ws, stream=None):
+    """dsa_decode_sparse over the 8-bit cache (kept lists from dsa_build_index); out has
+    q's type."""
+    qp, op, lp = _attn_out(dims, q, out, lse, (dims.batch,))
+    _here(page_table, seq_len, kept_idx, kept_cnt, ws)
+    _check(_load().dsa_decode_sparse_quant(
+        ctypes.byref(dims), qp, _cache(dims, cache), _ptr(page_table, _I32, "page_table"),
+        _ptr(seq_len, _I32, "seq_len"), _ptr(kept_idx, _I32, "kept_idx"),
+        _ptr(kept_cnt, _I32, "kept_cnt"), float(scale), op, lp, _ptr(ws), _stream(stream)),
+        "dsa_decode_sparse_quant")
+
+
+def dsa_decode_sparse_masked_quant(dims, q, cache, page_table, seq_len, prompt_len, window,
+                                   keep_mask, scale, out, lse, ws, stream=None,
+                                   request_order=None):
+    """dsa_decode_sparse_masked over the 8-bit cache, without the append; out has q's
+    type."""
+    qp, op, lp = _attn_out(dims, q, out, lse, (dims.batch,))
+    _here(page_table, seq_len, prompt_len, window, keep_mask, request_order, ws)
+    _check(_load().dsa_decode_sparse_masked_quant(
+        ctypes.byref(dims), qp, _cache(dims, cache), _ptr(page_table, _I32, "page_table"),
+        _ptr(seq_len, _I32, "seq_len"), _ptr(prompt_len, _I32, "prompt_len"),
+        _ptr(window, _I32, "window"), _ptr(keep_mask, _MASK, "keep_mask"),
+        _ptr(request_order, _I32, "request_order"), float(scale), op, lp, _ptr(ws),
+        _stream(stream)), "dsa_decode_sparse_masked_quant")
+
+
+def dsa_prefill_sparse_quant(dims, q, cache, page_table, seq_len, q_len, prompt_len, window,
+                             keep_mask, scale, out, lse, ws, stream=None, request_order=None):
+    """dsa_prefill_sparse over the 8-bit cache: q and out [batch, max_q, hq, head_dim]
+    bf16, lse [batch, max_q, hq] f32 or None."""
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, max_q, hq, head_dim]")
+    qp, op, lp = _attn_out(dims, q, out, lse, (dims.batch, q.shape[1]))
+    _here(page_table, seq_len, q_len, prompt_len, window, keep_mask, request_order, ws)
+    _check(_load().dsa_prefill_sparse_quant(
+        ctypes.byref(dims), int(q.shape[1]), qp, _cache(dims, cache),
+        _ptr(page_table, _I32, "page_table"), _ptr(seq_len, _I32, "seq_len"),
+        _ptr(q_len, _I32, "q_len"), _ptr(prompt_len, _I32, "prompt_len"),
+        _ptr(window, _I32, "window"), _ptr(keep_mask, _MASK, "keep_mask"),
+        _ptr(request_order, _I32, "request_order"), float(scale), op, lp, _ptr(ws),
+        _stream(stream)), "dsa_prefill_sparse_quant")
 
 
 PLAN_DENSE, PLAN_SPARSE, PLAN_MASKED = 0, 1, 2

@@ -252,3 +252,82 @@ class DecodeBatch:
 
     def check(self, what="libdsa"):
         dsa.check_device_error(self.ws, what)
+
+
+class QuantBatch:
+    """A DecodeBatch whose K/V cache is held in 8 bits: e4m3 codes [num_pages, hkv, 16, d]
+    and power-of-two scales [num_pages, hkv] (dsa_quant_cache).  Lengths, masks, page
+    table and workspace are the batch's own; out has q's type."""
+
+    def __init__(self, batch: DecodeBatch):
+        self.batch = batch
+        d, dev = batch.dims, batch.device
+        shape = (d.num_pages, d.hkv, dsa.PAGE, d.head_dim)
+        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=dev)
+                          .view(torch.float8_e4m3fn) for _ in range(2))
+        self.k_scale, self.v_scale = (torch.ones(shape[:2], dtype=torch.float32, device=dev)
+                                      for _ in range(2))
+        self.cache = dsa.quant_cache(self.k, self.v, self.k_scale, self.v_scale)
+        self.out = torch.empty_like(batch.q)
+        self.lse = torch.empty_like(batch.lse)
+
+    @classmethod
+    def from_batch(cls, batch: DecodeBatch) -> "QuantBatch":
+        """The batch's own pages quantised: every page is written like a request of its
+        own, with as many rows as its request has there."""
+        self = cls(batch)
+        d = batch.dims
+        table = batch.page_table.cpu().numpy()
+        rows = np.zeros(d.num_pages, np.int32)
+        for b, L in enumerate(batch._host_lengths[0]):
+            for p in range((int(L) + dsa.PAGE - 1) // dsa.PAGE):
+                if table[b, p] >= 0:
+                    rows[table[b, p]] = min(dsa.PAGE, int(L) - p * dsa.PAGE)
+        used = np.flatnonzero(rows)
+        dims = dsa.make_dims(len(used), d.hkv, d.hkv, d.head_dim, d.num_pages, 1, 0, 1, 1,
+                             d.kv_dtype, d.kv_dtype)
+        at = torch.as_tensor(used, device=batch.device)
+        n = _i32(rows[used], batch.device)
+        ws = dsa.alloc_workspace(dims, batch.device)
+        dsa.dsa_quant_write(dims, self.cache, batch.k_pages[at], batch.v_pages[at],
+                            at.to(torch.int32)[:, None].contiguous(), n, n, ws)
+        dsa.check_device_error(ws, "QuantBatch.from_batch")
+        return self
+
+    def write(self, k_new, v_new, new_len=None, stream=None):
+        """Append k_new / v_new [batch, max_new, hkv, d] as the last rows of the requests."""
+        b = self.batch
+        dsa.dsa_quant_write(b.dims, self.cache, k_new, v_new, b.page_table, b.seq_len, new_len,
+                            b.ws, stream)
+
+    def read(self, row_start, row_count, k_out, v_out, stream=None):
+        b = self.batch
+        dsa.dsa_quant_read(b.dims, self.cache, b.page_table, b.seq_len, row_start, row_count, k_out,
+                           v_out, b.ws, stream)
+
+    def decode_dense(self, out=None, lse=None, stream=None):
+        b, out, lse = self.batch, self.out if out is None else out, self.lse if lse is None else lse
+        dsa.dsa_decode_dense_quant(b.dims, b.q, self.cache, b.page_table, b.seq_len, b.scale, out,
+                                   lse, b.ws, stream)
+        return out, lse
+
+    def decode_sparse(self, out=None, lse=None, stream=None):
+        """Over the batch's kept lists (DecodeBatch.build_index)."""
+        b, out, lse = self.batch, self.out if out is None else out, self.lse if lse is None else lse
+        dsa.dsa_decode_sparse_quant(b.dims, b.q, self.cache, b.page_table, b.seq_len, b.kept_idx,
+                                    b.kept_cnt, b.scale, out, lse, b.ws, stream)
+        return out, lse
+
+    def decode_sparse_masked(self, out=None, lse=None, stream=None, request_order=None):
+        b, out, lse = self.batch, self.out if out is None else out, self.lse if lse is None else lse
+        dsa.dsa_decode_sparse_masked_quant(b.dims, b.q, self.cache, b.page_table, b.seq_len,
+                                           b.prompt_len, b.window, b.keep_mask, b.scale, out, lse,
+                                           b.ws, stream, request_order)
+        return out, lse
+
+    def prefill_sparse(self, q, q_len, out, lse, stream=None, request_order=None):
+        b = self.batch
+        dsa.dsa_prefill_sparse_quant(b.dims, q, self.cache, b.page_table, b.seq_len, q_len,
+                                     b.prompt_len, b.window, b.keep_mask, b.scale, out, lse, b.ws,
+                                     stream, request_order)
+        return out, lse
