@@ -2,6 +2,7 @@
 // and pointers, the device's SM count, and the regions of the workspace.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -14,6 +15,44 @@
 namespace dsa {
 
 constexpr int kMaxDevices = 64;
+
+// Resident CTAs per SM of one kernel at one shared-memory size, and the permission to
+// launch with it, asked of the runtime once per device (each call of it costs a
+// microsecond of a decode step's launch).  One object per kernel; any thread.
+class KernelSlots {
+ public:
+  cudaError_t get(const void* kern, int threads, int smem, int* per_sm) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kMaxDevices;
+    const uint64_t want = (static_cast<uint64_t>(static_cast<uint32_t>(smem)) << 32) | 0x80000000u;
+    if (known) {
+      const uint64_t v = cache_[dev].load(std::memory_order_acquire);
+      if ((v & ~0x7fffffffull) == want) {
+        *per_sm = static_cast<int>(v & 0x7fffffffu);
+        return cudaSuccess;
+      }
+    }
+    // the permission never shrinks: a launch of another size on another thread keeps it
+    int most = 0;
+    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             most - static_cast<int>(fa.sharedSizeBytes));
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kern, threads, smem);
+    if (e != cudaSuccess) return e;
+    if (known) cache_[dev].store(want | static_cast<uint32_t>(*per_sm), std::memory_order_release);
+    return *per_sm < 1 ? cudaErrorLaunchOutOfResources : cudaSuccess;
+  }
+
+ private:
+  std::atomic<uint64_t> cache_[kMaxDevices] = {};
+};
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

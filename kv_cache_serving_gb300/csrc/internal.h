@@ -265,6 +265,7 @@ struct QuantChunkLaunch {
   int64_t part_cap;
   int32_t q_tiles, parts;  // set by the launch
   int32_t sms;
+  int32_t split_setting;   // dsa_set_prefill_split
 };
 
 struct QuantRowsLaunch {
@@ -302,6 +303,9 @@ struct RopeLaunch {
 
 cudaError_t launch_quant_decode(const QuantDecodeLaunch& a, int mode, cudaStream_t s);
 cudaError_t launch_quant_chunk(const QuantChunkLaunch& a, cudaStream_t s);
+// The tcgen05 kernel of the call (head_dim 128), and whether it takes a call.
+bool quant_chunk_tc_fits(const QuantChunkLaunch& a);
+cudaError_t launch_quant_chunk_tc(const QuantChunkLaunch& a, cudaStream_t s);
 cudaError_t launch_quant_write(const QuantRowsLaunch& a, cudaStream_t s);
 cudaError_t launch_quant_read(const QuantRowsLaunch& a, cudaStream_t s);
 cudaError_t launch_rope(const RopeLaunch& a, int sms, cudaStream_t s);

@@ -315,6 +315,7 @@ dsa_status dsa_prefill_sparse_quant(const dsa_dims* dims, int32_t max_q, const v
   a.count = multi_count_region(dims, ws);
   a.err = err_word(ws);
   a.sms = sm_count();
+  a.split_setting = dsa_get_prefill_split();
   return from_cuda(launch_quant_chunk(a, static_cast<cudaStream_t>(stream)));
 }
 

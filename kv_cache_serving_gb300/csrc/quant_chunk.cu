@@ -26,6 +26,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "internal.h"
 #include "mma.cuh"
 #include "quant.cuh"
@@ -471,26 +472,26 @@ cudaError_t launch_one(QuantChunkLaunch a, cudaStream_t s) {
   using Sh = ChunkShape<D, KG>;
   auto kern = quant_chunk_kernel<D, KG>;
   const int smem = Sh::smem(a.max_window / 32 + 1);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  static KernelSlots cache;
   int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kCW * 32, smem);
+  const cudaError_t e = cache.get(reinterpret_cast<const void*>(kern), kCW * 32, smem, &per_sm);
   if (e != cudaSuccess) return e;
-  if (per_sm < 1) return cudaErrorLaunchOutOfResources;
   const int per_cta = (kCols * Sh::KC) >> a.group_log2;
   a.q_tiles = (a.max_q + per_cta - 1) / per_cta;
   const int64_t units = static_cast<int64_t>(a.q_tiles) * a.hkv * a.batch;
   const int64_t slots = static_cast<int64_t>(per_sm) * a.sms;
-  // parts of a unit: only when the units leave half of the slots empty; a part
-  // keeps two stages of pages
+  // parts of a unit: by the setting, else only when the units leave half of the slots
+  // empty (a part keeps two stages of pages); as many as the workspace holds
   int64_t parts = 1;
-  if (units * 2 <= slots && units <= kMultiCounters) {
+  if (a.split_setting >= 2) {
+    parts = a.split_setting;
+  } else if (a.split_setting == 0 && units * 2 <= slots) {
     parts = slots / units;
     const int64_t most = (a.max_pages + 2 * kCW - 1) / (2 * kCW);
     if (parts > most) parts = most;
     if (parts > kQuantMaxParts) parts = kQuantMaxParts;
-    if (units * parts * Sh::KC * Sh::kStateWords * 32 > a.part_cap) parts = 1;
   }
+  if (units > kMultiCounters || units * parts * Sh::KC * Sh::kStateWords * 32 > a.part_cap) parts = 1;
   a.parts = parts < 1 ? 1 : static_cast<int32_t>(parts);
   if (units * a.parts > INT32_MAX) return cudaErrorInvalidValue;
   return launch_pdl(kern, dim3(static_cast<unsigned>(units * a.parts)), dim3(kCW * 32),
@@ -508,6 +509,7 @@ cudaError_t launch_cols(const QuantChunkLaunch& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_quant_chunk(const QuantChunkLaunch& a, cudaStream_t s) {
+  if (a.head_dim == 128 && quant_chunk_tc_fits(a)) return launch_quant_chunk_tc(a, s);
   return a.head_dim == 128 ? launch_cols<128>(a, s) : launch_cols<64>(a, s);
 }
 

@@ -29,6 +29,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "host.h"
 #include "internal.h"
 #include "mma.cuh"
 #include "quant.cuh"
@@ -655,12 +656,10 @@ template <int D, int MODE, bool XQ>
 cudaError_t launch_one(QuantDecodeLaunch a, cudaStream_t s) {
   auto kern = quant_decode_kernel<D, MODE, XQ>;
   constexpr int smem = QuantRing<D>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  static KernelSlots cache;
   int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kQW * 32, smem);
+  const cudaError_t e = cache.get(reinterpret_cast<const void*>(kern), kQW * 32, smem, &per_sm);
   if (e != cudaSuccess) return e;
-  if (per_sm < 1) return cudaErrorLaunchOutOfResources;
   const int64_t slots = static_cast<int64_t>(per_sm) * a.sms;
   const int64_t units = static_cast<int64_t>(a.batch) * a.hkv;
   int64_t grid;

@@ -442,47 +442,64 @@ def rope_sections(sections, interleaved=False) -> list:
     return out
 
 
-def _here(*tensors):
-    """The calls launch on the current device: refuse tensors of another one."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, current device cuda:{dev}")
+def _arg(t, dtype, dev, what):
+    """Device address of a contiguous CUDA tensor of `dtype` (or one of several) on device
+    `dev`, or None.  The calls launch on the current device, so a tensor of another one
+    is refused."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise TypeError(f"{what} must be a CUDA tensor on the current device cuda:{dev}, not on "
+                        f"{t.device}")
+    if t.dtype is not dtype and not (dtype.__class__ is tuple and t.dtype in dtype):
+        raise TypeError(f"{what} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
 
 
-def _rows_view(t, heads, head_dim, dtype, what):
-    """Pointer and row stride of [..., heads, head_dim] whose rows are evenly spaced (the
+def _rows_arg(t, heads, head_dim, dtype, dev, what):
+    """Address and row stride of [..., heads, head_dim] whose rows are evenly spaced (the
     last two dimensions contiguous: slices of a fused projection are fine)."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise TypeError(f"{what} must be a CUDA tensor on the current device cuda:{dev}, not on "
+                        f"{t.device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{what} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() < 3 or tuple(t.shape[-2:]) != (heads, head_dim):
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 3 or shape[-2] != heads or shape[-1] != head_dim:
         raise ValueError(f"{what} must be [..., {heads}, {head_dim}]")
-    if (t.stride(-1) != 1 and head_dim > 1) or (t.stride(-2) != head_dim and heads > 1):
+    if stride[-1] != 1 or (stride[-2] != head_dim and heads > 1):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
     row = None  # elements between rows, from the innermost row dimension that has several
-    for i in range(t.dim() - 3, -1, -1):
-        if t.shape[i] == 1:
+    for i in range(len(shape) - 3, -1, -1):
+        if shape[i] == 1:
             continue
         if row is None:
-            row, span = t.stride(i), t.stride(i) * t.shape[i]
-        elif t.stride(i) != span:
+            row = stride[i]
+        elif stride[i] != span:
             raise ValueError(f"{what}: rows must be evenly spaced")
-        else:
-            span = t.stride(i) * t.shape[i]
-    return ctypes.c_void_p(t.data_ptr()), heads * head_dim if row is None else row
+        span = stride[i] * shape[i]
+    return t.data_ptr(), heads * head_dim if row is None else row
 
 
-def _types(dims):
-    return tuple(torch.bfloat16 if c == DSA_BF16 else torch.float32
-                 for c in (dims.q_dtype, dims.kv_dtype))
+def _launch_on(stream):
+    """Current device and the cudaStream_t to launch on."""
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)  # current_stream() costs a microsecond
+    if stream.device_index != dev:
+        raise ValueError(f"stream on cuda:{stream.device_index}, current device cuda:{dev}")
+    return dev, stream.cuda_stream
+
+
+_TYPE = {DSA_F32: torch.float32, DSA_BF16: torch.bfloat16}
 
 
 def _shape(t, want, what):
-    if t is not None and tuple(t.shape) != tuple(want):
+    if t is not None and t.shape != want:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(want)}")
 
 
@@ -492,19 +509,19 @@ def dsa_rope_axes(dims, rope, positions, q, k, q_out, k_out, stream=None):
     positions [tokens, axes] int32.  Rows may be strided (slices of a fused projection)."""
     if positions.dim() != 2 or positions.shape[1] != rope.axes:
         raise ValueError(f"positions must be [tokens, {rope.axes}]")
-    if getattr(rope, "pairs", dims.head_dim // 2) != dims.head_dim // 2:
-        raise ValueError(f"rope has {rope.pairs} pairs, head_dim {dims.head_dim}")
-    n = positions.shape[0]
-    qd, kd = _types(dims)
-    args = []
-    for t, heads, dt, what in ((q, dims.hq, qd, "q"), (k, dims.hkv, kd, "k"),
-                               (q_out, dims.hq, qd, "q_out"), (k_out, dims.hkv, kd, "k_out")):
-        _shape(t, (n, heads, dims.head_dim), what)
-        args += _rows_view(t, heads, dims.head_dim, dt, what)
-    _here(positions, q, k, q_out, k_out)
-    _check(_load().dsa_rope_axes(ctypes.byref(dims), ctypes.byref(rope), n,
-                                 _ptr(positions, _I32, "positions"), *args, _stream(stream)),
-           "dsa_rope_axes")
+    hd = dims.head_dim
+    if getattr(rope, "pairs", hd // 2) != hd // 2:
+        raise ValueError(f"rope has {rope.pairs} pairs, head_dim {hd}")
+    dev, st = _launch_on(stream)
+    n, hq, hkv = positions.shape[0], dims.hq, dims.hkv
+    qt, kt = _TYPE.get(dims.q_dtype), _TYPE.get(dims.kv_dtype)
+    for t, heads, what in ((q, hq, "q"), (k, hkv, "k"), (q_out, hq, "q_out"), (k_out, hkv, "k_out")):
+        _shape(t, (n, heads, hd), what)
+    _check(_load().dsa_rope_axes(
+        dims, rope, n, _arg(positions, _I32, dev, "positions"),
+        *_rows_arg(q, hq, hd, qt, dev, "q"), *_rows_arg(k, hkv, hd, kt, dev, "k"),
+        *_rows_arg(q_out, hq, hd, qt, dev, "q_out"), *_rows_arg(k_out, hkv, hd, kt, dev, "k_out"),
+        st), "dsa_rope_axes")
 
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -513,45 +530,49 @@ _CODES = (torch.float8_e4m3fn, torch.uint8)
 def quant_cache(k_codes, v_codes, k_scale, v_scale) -> dsa_quant_cache:
     """dsa_quant_cache over codes [num_pages, hkv, 16, head_dim] (float8_e4m3fn or their
     bytes) and scales [num_pages, hkv] float32; keeps the tensors alive."""
-    for t, what in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-        _ptr(t, _CODES, what)
-        if t.dim() != 4 or t.shape[2] != PAGE:
-            raise ValueError(f"{what} must be [num_pages, hkv, {PAGE}, head_dim]")
+    dev = k_codes.get_device()
+    if dev < 0:
+        raise TypeError("k_codes must be a CUDA tensor")
+    if k_codes.dim() != 4 or k_codes.shape[2] != PAGE:
+        raise ValueError(f"k_codes must be [num_pages, hkv, {PAGE}, head_dim]")
     _shape(v_codes, k_codes.shape, "v_codes")
     for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _ptr(t, torch.float32, what)
         _shape(t, k_codes.shape[:2], what)
-    c = dsa_quant_cache(*(t.data_ptr() for t in (k_codes, v_codes, k_scale, v_scale)))
+    c = dsa_quant_cache(_arg(k_codes, _CODES, dev, "k_codes"), _arg(v_codes, _CODES, dev, "v_codes"),
+                        _arg(k_scale, torch.float32, dev, "k_scale"),
+                        _arg(v_scale, torch.float32, dev, "v_scale"))
     c.tensors = (k_codes, v_codes, k_scale, v_scale)
     return c
 
 
-def _cache(dims, cache):
-    """The cache as a C argument, its shape checked against dims."""
-    if not isinstance(cache, dsa_quant_cache):
+def _cache(dims, cache, dev):
+    """The cache, checked against dims."""
+    if cache.__class__ is not dsa_quant_cache:
         raise TypeError("cache must be a dsa_quant_cache (see quant_cache)")
-    if hasattr(cache, "tensors"):
-        _shape(cache.tensors[0], (dims.num_pages, dims.hkv, PAGE, dims.head_dim), "cache codes")
-        _here(*cache.tensors)
-    return ctypes.byref(cache)
+    codes = cache.tensors[0] if hasattr(cache, "tensors") else None
+    if codes is not None:
+        _shape(codes, (dims.num_pages, dims.hkv, PAGE, dims.head_dim), "cache codes")
+        if codes.get_device() != dev:
+            raise TypeError(f"cache on {codes.device}, current device cuda:{dev}")
+    return cache
 
 
 def dsa_quant_write(dims, cache, k_new, v_new, page_table, seq_len, new_len, ws, stream=None):
     """Quantise k_new / v_new [batch, max_new, hkv, head_dim] into the cache as the last
     new_len[b] rows of each request (new_len None: all max_new slots)."""
-    kd = _types(dims)[1]
     if k_new.dim() != 4 or k_new.shape[0] != dims.batch:
         raise ValueError("k_new must be [batch, max_new, hkv, head_dim]")
     _shape(v_new, k_new.shape, "v_new")
-    k, ks = _rows_view(k_new, dims.hkv, dims.head_dim, kd, "k_new")
-    v, vs = _rows_view(v_new, dims.hkv, dims.head_dim, kd, "v_new")
+    dev, st = _launch_on(stream)
+    kt = _TYPE.get(dims.kv_dtype)
+    k, ks = _rows_arg(k_new, dims.hkv, dims.head_dim, kt, dev, "k_new")
+    v, vs = _rows_arg(v_new, dims.hkv, dims.head_dim, kt, dev, "v_new")
     if ks != vs:
         raise ValueError("k_new and v_new must have the same row stride")
-    _here(k_new, v_new, page_table, seq_len, new_len, ws)
     _check(_load().dsa_quant_write(
-        ctypes.byref(dims), _cache(dims, cache), int(k_new.shape[1]), k, v, ks,
-        _ptr(page_table, _I32, "page_table"), _ptr(seq_len, _I32, "seq_len"),
-        _ptr(new_len, _I32, "new_len"), _ptr(ws), _stream(stream)), "dsa_quant_write")
+        dims, _cache(dims, cache, dev), k_new.shape[1], k, v, ks,
+        _arg(page_table, _I32, dev, "page_table"), _arg(seq_len, _I32, dev, "seq_len"),
+        _arg(new_len, _I32, dev, "new_len"), _arg(ws, torch.uint8, dev, "ws"), st), "dsa_quant_write")
 
 
 def dsa_quant_read(dims, cache, page_table, seq_len, row_start, row_count, k_out, v_out, ws,
@@ -561,36 +582,34 @@ def dsa_quant_read(dims, cache, page_table, seq_len, row_start, row_count, k_out
     out = k_out if k_out is not None else v_out
     if out is None:
         raise ValueError("k_out or v_out must be given")
-    kd = _types(dims)[1]
-    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-        _shape(t, (dims.batch, out.shape[1], dims.hkv, dims.head_dim), what)
-    _here(k_out, v_out, page_table, seq_len, row_start, row_count, ws)
+    want = (dims.batch, out.shape[1], dims.hkv, dims.head_dim)
+    _shape(k_out, want, "k_out")
+    _shape(v_out, want, "v_out")
+    dev, st = _launch_on(stream)
+    kt = _TYPE.get(dims.kv_dtype)
     _check(_load().dsa_quant_read(
-        ctypes.byref(dims), _cache(dims, cache), int(out.shape[1]),
-        _ptr(page_table, _I32, "page_table"), _ptr(seq_len, _I32, "seq_len"),
-        _ptr(row_start, _I32, "row_start"), _ptr(row_count, _I32, "row_count"),
-        _ptr(k_out, kd, "k_out"), _ptr(v_out, kd, "v_out"), _ptr(ws), _stream(stream)),
-        "dsa_quant_read")
+        dims, _cache(dims, cache, dev), want[1], _arg(page_table, _I32, dev, "page_table"),
+        _arg(seq_len, _I32, dev, "seq_len"), _arg(row_start, _I32, dev, "row_start"),
+        _arg(row_count, _I32, dev, "row_count"), _arg(k_out, kt, dev, "k_out"),
+        _arg(v_out, kt, dev, "v_out"), _arg(ws, torch.uint8, dev, "ws"), st), "dsa_quant_read")
 
 
-def _attn_out(dims, q, out, lse, rows):
-    """Pointers of q, out (q's type) and lse, their shapes checked."""
-    qd = _types(dims)[0]
-    shape = tuple(rows) + (dims.hq, dims.head_dim)
-    _shape(q, shape, "q")
-    _shape(out, shape, "out")
-    _shape(lse, shape[:-1], "lse")
-    _here(q, out, lse)
-    return _ptr(q, qd, "q"), _ptr(out, qd, "out"), _ptr(lse, torch.float32, "lse")
+def _q_out(dims, q, out, lse, dev, rows):
+    """Addresses of q, out (q's type) and lse, their shapes checked."""
+    _shape(q, rows + (dims.hq, dims.head_dim), "q")
+    _shape(out, q.shape, "out")
+    _shape(lse, rows + (dims.hq,), "lse")
+    qt = _TYPE.get(dims.q_dtype)
+    return _arg(q, qt, dev, "q"), _arg(out, qt, dev, "out"), _arg(lse, torch.float32, dev, "lse")
 
 
 def dsa_decode_dense_quant(dims, q, cache, page_table, seq_len, scale, out, lse, ws, stream=None):
     """dsa_decode_dense over the 8-bit cache; out has q's type."""
-    qp, op, lp = _attn_out(dims, q, out, lse, (dims.batch,))
-    _here(page_table, seq_len, ws)
+    dev, st = _launch_on(stream)
+    qp, op, lp = _q_out(dims, q, out, lse, dev, (dims.batch,))
     _check(_load().dsa_decode_dense_quant(
-        ctypes.byref(dims), qp, _cache(dims, cache), _ptr(page_table, _I32, "page_table"),
-        _ptr(seq_len, _I32, "seq_len"), float(scale), op, lp, _ptr(ws), _stream(stream)),
+        dims, qp, _cache(dims, cache, dev), _arg(page_table, _I32, dev, "page_table"),
+        _arg(seq_len, _I32, dev, "seq_len"), scale, op, lp, _arg(ws, torch.uint8, dev, "ws"), st),
         "dsa_decode_dense_quant")
 
 
@@ -598,12 +617,12 @@ def dsa_decode_sparse_quant(dims, q, cache, page_table, seq_len, kept_idx, kept_
                             lse, ws, stream=None):
     """dsa_decode_sparse over the 8-bit cache (kept lists from dsa_build_index); out has
     q's type."""
-    qp, op, lp = _attn_out(dims, q, out, lse, (dims.batch,))
-    _here(page_table, seq_len, kept_idx, kept_cnt, ws)
+    dev, st = _launch_on(stream)
+    qp, op, lp = _q_out(dims, q, out, lse, dev, (dims.batch,))
     _check(_load().dsa_decode_sparse_quant(
-        ctypes.byref(dims), qp, _cache(dims, cache), _ptr(page_table, _I32, "page_table"),
-        _ptr(seq_len, _I32, "seq_len"), _ptr(kept_idx, _I32, "kept_idx"),
-        _ptr(kept_cnt, _I32, "kept_cnt"), float(scale), op, lp, _ptr(ws), _stream(stream)),
+        dims, qp, _cache(dims, cache, dev), _arg(page_table, _I32, dev, "page_table"),
+        _arg(seq_len, _I32, dev, "seq_len"), _arg(kept_idx, _I32, dev, "kept_idx"),
+        _arg(kept_cnt, _I32, dev, "kept_cnt"), scale, op, lp, _arg(ws, torch.uint8, dev, "ws"), st),
         "dsa_decode_sparse_quant")
 
 
@@ -612,14 +631,14 @@ def dsa_decode_sparse_masked_quant(dims, q, cache, page_table, seq_len, prompt_l
                                    request_order=None):
     """dsa_decode_sparse_masked over the 8-bit cache, without the append; out has q's
     type."""
-    qp, op, lp = _attn_out(dims, q, out, lse, (dims.batch,))
-    _here(page_table, seq_len, prompt_len, window, keep_mask, request_order, ws)
+    dev, st = _launch_on(stream)
+    qp, op, lp = _q_out(dims, q, out, lse, dev, (dims.batch,))
     _check(_load().dsa_decode_sparse_masked_quant(
-        ctypes.byref(dims), qp, _cache(dims, cache), _ptr(page_table, _I32, "page_table"),
-        _ptr(seq_len, _I32, "seq_len"), _ptr(prompt_len, _I32, "prompt_len"),
-        _ptr(window, _I32, "window"), _ptr(keep_mask, _MASK, "keep_mask"),
-        _ptr(request_order, _I32, "request_order"), float(scale), op, lp, _ptr(ws),
-        _stream(stream)), "dsa_decode_sparse_masked_quant")
+        dims, qp, _cache(dims, cache, dev), _arg(page_table, _I32, dev, "page_table"),
+        _arg(seq_len, _I32, dev, "seq_len"), _arg(prompt_len, _I32, dev, "prompt_len"),
+        _arg(window, _I32, dev, "window"), _arg(keep_mask, _MASK, dev, "keep_mask"),
+        _arg(request_order, _I32, dev, "request_order"), scale, op, lp,
+        _arg(ws, torch.uint8, dev, "ws"), st), "dsa_decode_sparse_masked_quant")
 
 
 def dsa_prefill_sparse_quant(dims, q, cache, page_table, seq_len, q_len, prompt_len, window,
@@ -628,15 +647,15 @@ def dsa_prefill_sparse_quant(dims, q, cache, page_table, seq_len, q_len, prompt_
     bf16, lse [batch, max_q, hq] f32 or None."""
     if q.dim() != 4:
         raise ValueError("q must be [batch, max_q, hq, head_dim]")
-    qp, op, lp = _attn_out(dims, q, out, lse, (dims.batch, q.shape[1]))
-    _here(page_table, seq_len, q_len, prompt_len, window, keep_mask, request_order, ws)
+    dev, st = _launch_on(stream)
+    max_q = q.shape[1]
+    qp, op, lp = _q_out(dims, q, out, lse, dev, (dims.batch, max_q))
     _check(_load().dsa_prefill_sparse_quant(
-        ctypes.byref(dims), int(q.shape[1]), qp, _cache(dims, cache),
-        _ptr(page_table, _I32, "page_table"), _ptr(seq_len, _I32, "seq_len"),
-        _ptr(q_len, _I32, "q_len"), _ptr(prompt_len, _I32, "prompt_len"),
-        _ptr(window, _I32, "window"), _ptr(keep_mask, _MASK, "keep_mask"),
-        _ptr(request_order, _I32, "request_order"), float(scale), op, lp, _ptr(ws),
-        _stream(stream)), "dsa_prefill_sparse_quant")
+        dims, max_q, qp, _cache(dims, cache, dev), _arg(page_table, _I32, dev, "page_table"),
+        _arg(seq_len, _I32, dev, "seq_len"), _arg(q_len, _I32, dev, "q_len"),
+        _arg(prompt_len, _I32, dev, "prompt_len"), _arg(window, _I32, dev, "window"),
+        _arg(keep_mask, _MASK, dev, "keep_mask"), _arg(request_order, _I32, dev, "request_order"),
+        scale, op, lp, _arg(ws, torch.uint8, dev, "ws"), st), "dsa_prefill_sparse_quant")
 
 
 PLAN_DENSE, PLAN_SPARSE, PLAN_MASKED = 0, 1, 2

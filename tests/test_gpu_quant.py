@@ -567,10 +567,20 @@ def chunk_lens(w, qmax, seed):
     return n
 
 
+@pytest.fixture
+def split(request):
+    """dsa_set_prefill_split for one test: 1 whole units, n >= 2 units in n parts."""
+    saved = dsa.dsa_get_prefill_split()
+    dsa.dsa_set_prefill_split(request.param)
+    yield request.param
+    dsa.dsa_set_prefill_split(saved)
+
+
+@pytest.mark.parametrize("split", [0, 1, 3], indirect=True)
 @pytest.mark.parametrize("qmax", [1, 7, 16, 70])
 @pytest.mark.parametrize("g", [1, 2, 4, 8])
 @pytest.mark.parametrize("d", [64, 128])
-def test_chunk_every_build(d, g, qmax):
+def test_chunk_every_build(d, g, qmax, split):
     w = wl.generate(case(d, g, seed=d + g + qmax), spare_pages=3)
     qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
     run_chunk(qb, w, qmax, chunk_lens(w, qmax, g), seed=qmax)
@@ -578,13 +588,15 @@ def test_chunk_every_build(d, g, qmax):
 
 @pytest.mark.parametrize("name,batch,qmax", [("janus-pro-7b", 5, 32), ("llamagen-xl", 6, 24),
                                              ("emu3-8b", 2, 40)])
-def test_chunk_workload_shapes(name, batch, qmax):
+@pytest.mark.parametrize("split", [0, 1], indirect=True)
+def test_chunk_workload_shapes(name, batch, qmax, split):
     w = wl.generate(wl.scaled(wl.WORKLOADS[name], batch=batch))
     qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
     run_chunk(qb, w, qmax, chunk_lens(w, qmax, 1))
 
 
-def test_chunk_whole_sequences_and_edges():
+@pytest.mark.parametrize("split", [0, 1], indirect=True)
+def test_chunk_whole_sequences_and_edges(split):
     """Every row a query, no query, a window of 0, empty and full masks, a prompt longer
     than the request."""
     w = wl.generate(case(128, 4, batch=6, lo=30, hi=150, prompt=(0, 40), W=64, seed=5))
@@ -597,7 +609,8 @@ def test_chunk_whole_sequences_and_edges():
     run_chunk(qb, w, int(L.max()), [int(L[0]), 0, int(L[2]), min(17, int(L[3])), 1, int(L[5])], seed=6)
 
 
-def test_chunk_long_window():
+@pytest.mark.parametrize("split", [0, 1], indirect=True)
+def test_chunk_long_window(split):
     w = wl.generate(case(128, 2, batch=3, lo=1500, hi=2200, prompt=(0, 60), W=1500, seed=11))
     qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
     run_chunk(qb, w, 40, chunk_lens(w, 40, 12))
@@ -627,7 +640,8 @@ def test_chunk_of_one_is_a_decode_step():
     assert torch.allclose(l2[:, 0], lse, atol=1e-5)
 
 
-def test_chunk_ignores_unread_rows():
+@pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
+def test_chunk_ignores_unread_rows(split):
     w = wl.generate(case(128, 4, batch=4, lo=100, hi=400, prompt=(20, 60), W=64, seed=17), spare_pages=4)
     qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
     n = np.minimum(9, w["seq_len"])
@@ -654,11 +668,13 @@ def test_chunk_ignores_unread_rows():
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
-def test_chunk_flags_bad_requests():
-    w = wl.generate(case(64, 2, batch=3, lo=100, hi=200, seed=19))
+@pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_flags_bad_requests(d, split):
+    w = wl.generate(case(d, 2, batch=3, lo=100, hi=200, seed=19))
     qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
     bt = qb.batch
-    q = torch.randn(3, 5, w["hq"], 64, device="cuda").to(torch.bfloat16)
+    q = torch.randn(3, 5, w["hq"], d, device="cuda").to(torch.bfloat16)
     for n, code in (((5, -1, 5), 11), ((5, 6, 5), 11), ((5, 5, 5), 0)):
         out = torch.full_like(q, SENTINEL)
         qb.prefill_sparse(q, torch.tensor(n, dtype=torch.int32, device="cuda"), out, None)

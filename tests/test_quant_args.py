@@ -136,4 +136,4 @@ def test_binding_checks():
     with pytest.raises(TypeError):
         dsa.quant_cache(t, t, torch.ones(4, 2), torch.ones(4, 2))  # CUDA tensors wanted
     with pytest.raises(TypeError):
-        dsa._cache(dims(), object())
+        dsa._cache(dims(), object(), 0)
