@@ -30,6 +30,7 @@
 #include "internal.h"
 #include "mma.cuh"
 #include "quant.cuh"
+#include "quant_redo.cuh"
 
 namespace dsa {
 namespace {
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
     }
   }
   if (kg != 0 || !active) return;
+  float nan_probe = 0.f;
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -456,14 +458,27 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
       const float r = 1.f / l;
       uint32_t o[NK];
 #pragma unroll
-      for (int mt = 0; mt < NK; ++mt)
+      for (int mt = 0; mt < NK; ++mt) {
         o[mt] = bf16x2_rn(st.acc[nt][mt][h] * r, st.acc[nt][mt][2 + h] * r);
+        nan_probe += st.acc[nt][mt][h] + st.acc[nt][mt][2 + h];
+      }
       uint4* to = reinterpret_cast<uint4*>(a.out + qh * D + g * (D / 8));
 #pragma unroll
       for (int i = 0; i < NK / 4; ++i)
         to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       if (a.lse != nullptr && g == 0)
         a.lse[qh] = (st.ref[nt][h] - kCHead + log2f(l)) * kLn2;
+    }
+  // A NaN may come from a row of V that other queries of the tile keep (weight 0 times
+  // NaN): the warp's columns are done again from the rows each one keeps.
+  if (__any_sync(0xffffffffu, nan_probe != nan_probe))
+    for (int col = 0; col < kCols; ++col) {
+      const int t = gt0 + (col >> lg);
+      if (t >= gt1) break;
+      quant_redo_query<D>(a, b, hk, L - n + t, P, W,
+                          (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << lg) +
+                              (col & ((1 << lg) - 1)),
+                          lane);
     }
 }
 

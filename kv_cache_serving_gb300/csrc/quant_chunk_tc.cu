@@ -30,6 +30,7 @@
 #include "internal.h"
 #include "mma.cuh"
 #include "quant.cuh"
+#include "quant_redo.cuh"
 #include "tcgen05.cuh"
 
 namespace dsa {
@@ -52,10 +53,11 @@ struct TcShape {
   static constexpr int kRef = kInfo + 2 * kTPages * 16;    // ref, head - ref, factor: N each
   static constexpr int kMax = kRef + 3 * N * 4;            // 4 x N column maxima / sums
   static constexpr int kRed = kMax + 4 * N * 4;            // 8 floats
-  static constexpr int kBar = kRed + 32;                   // two barriers, address, flag
+  static constexpr int kBar = kRed + 32;                   // two barriers, address, flags
   static constexpr int kMask = kBar + 32;
   static constexpr int kSlack = 1024;                      // the base is rounded up to 1024
-  static constexpr int kTmem = 2 * N;                      // S, then O^T
+  // tensor memory: S, O^T, and two copies of every row's part of the columns' sums
+  static constexpr int kS = 0, kO = N, kL = 2 * N, kTmem = 4 * N;
   static int smem(int words) { return kSlack + kMask + 4 * words; }
 };
 
@@ -65,17 +67,10 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                : "memory");
 }
 
-// 16 codes as two 16-byte pieces of fp16.
-__device__ __forceinline__ void codes16(const uint4& v, uint4& lo, uint4& hi) {
-  lo = make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2_hi(v.x), e4m3x2_f16x2(v.y), e4m3x2_f16x2_hi(v.y));
-  hi = make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2_hi(v.z), e4m3x2_f16x2(v.w), e4m3x2_f16x2_hi(v.w));
-}
-
-// Maximum over the warp of each of W values: lane l ends with value l * W / 32.
-template <int W>
-__device__ __forceinline__ float scatter_max(float (&v)[W], int lane) {
+// Maximum over the warp of each of 16 values: lane l ends with value l / 2.
+__device__ __forceinline__ float scatter_max(float (&v)[16], int lane) {
 #pragma unroll
-  for (int n = W, off = 16; n > 1; n >>= 1, off >>= 1) {
+  for (int n = 16, off = 16; n > 1; n >>= 1, off >>= 1) {
     const bool hi = (lane & off) != 0;
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) {
@@ -83,17 +78,15 @@ __device__ __forceinline__ float scatter_max(float (&v)[W], int lane) {
       v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, off));
     }
   }
-  float m = v[0];
-#pragma unroll
-  for (int off = 32 / W / 2; off >= 1; off >>= 1)
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  return m;
+  return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-template <int N>
+template <int N, int LG>
 __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const QuantChunkLaunch a) {
   using Sh = TcShape<N>;
-  constexpr int W = N / 2;  // columns per warp
+  constexpr int W = N / 2;              // columns per warp ...
+  constexpr int kChunks = W / 16;       // ... in pieces of 16
+  constexpr int per_cta = N >> LG;      // query tokens per CTA
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sm = smem_addr(smem);
@@ -101,16 +94,19 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wq = warp & 3, cg = warp >> 2;  // lane quarter of tensor memory, column half
-  const int unit = blockIdx.x;
-  const int qt = a.q_tiles - 1 - unit % a.q_tiles;
-  const int hk = unit / a.q_tiles % a.hkv, bpos = unit / (a.q_tiles * a.hkv);
+  // the last query tokens, which see the most rows, first
+  const int qt = gridDim.x - 1 - blockIdx.x, hk = blockIdx.y, bpos = blockIdx.z;
   const int b = a.order != nullptr ? __ldg(a.order + bpos) : bpos;
   if (static_cast<unsigned>(b) >= static_cast<unsigned>(a.batch)) {
     if (qt == 0 && hk == 0 && tid == 0) set_error(a.err, DSA_DEV_BAD_ORDER);
     return;
   }
-  const int lg = a.group_log2, per_cta = N >> lg, t0 = qt * per_cta;
+  const int t0 = qt * per_cta;
   const int L = a.seq_len[b], n = a.q_len[b], P = a.prompt_len[b], Wn = a.window[b];
+  const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.max_pages;
+  // page ids of the first two blocks, should they be the request's first pages
+  const int spec0 = warp < a.max_pages ? __ldg(pt + warp) : 0;
+  const int spec1 = warp + kTPages < a.max_pages ? __ldg(pt + warp + kTPages) : 0;
   int code = 0;
   if (L < 1 || L > a.max_pages * kPage) code = DSA_DEV_BAD_SEQ_LEN;
   else if (n < 0 || n > L || n > a.max_q) code = DSA_DEV_BAD_QLEN;
@@ -119,12 +115,11 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   if (code != 0) {
     // q_len is not trusted: NaN into every slot of the unit
     if (qt == 0 && hk == 0 && tid == 0) set_error(a.err, code);
-    const int heads = 1 << lg;
     for (int x = tid; x < N * kTD; x += kTThreads) {
-      const int t = t0 + x / (heads * kTD);
+      const int t = t0 + x / (kTD << LG);
       if (t >= a.max_q) break;
-      const size_t qh =
-          (static_cast<size_t>(b) * a.max_q + t) * a.hq + hk * heads + x / kTD % heads;
+      const size_t qh = (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << LG) +
+                        (x / kTD & ((1 << LG) - 1));
       a.out[qh * kTD + x % kTD] = 0x7fc0;
       if (a.lse != nullptr && x % kTD == 0) a.lse[qh] = __int_as_float(0x7fc00000);
     }
@@ -133,12 +128,18 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   if (t0 >= n) return;
   const int t1 = min(t0 + per_cta, n);
   const int i_first = L - n + t0, i_last = L - n + t1 - 1;
+  // pages scanned: those of the prompt rows [0, pa), then those from the window's start
   const int n_prompt = min(P, i_last + 1);
   const int pa = (n_prompt + 15) >> 4;
   const int pb = max(pa, max(i_first - Wn, 0) >> 4), pe = i_last >> 4;
   const int pages = pa + max(0, pe - pb + 1);
   const int nblocks = (pages + kTPages - 1) / kTPages;
   auto page_of = [&](int x) { return x < pa ? x : pb + (x - pa); };
+  // row of q and out of column c
+  const size_t qh0 = (static_cast<size_t>(b) * a.max_q + t0) * a.hq + (hk << LG);
+  auto qh_of = [&](int c) {
+    return qh0 + static_cast<size_t>(c >> LG) * a.hq + (c & ((1 << LG) - 1));
+  };
 
   int4* info = reinterpret_cast<int4*>(smem + Sh::kInfo);
   float* ref = reinterpret_cast<float*>(smem + Sh::kRef);
@@ -150,13 +151,19 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   uint64_t* o_done = s_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_done + 2);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* redo = failed + 1;
   uint32_t* msk = reinterpret_cast<uint32_t*>(smem + Sh::kMask);
-  if (warp == 0) tmem_alloc<Sh::kTmem>(tmem_slot);
-  if (tid == 0) {
-    mbar_init(s_done, 1);
-    mbar_init(o_done, 1);
-    fence_mbar_init();
-    *failed = 0;
+
+  // q: a thread holds 128 N / 256 elements of one column
+  constexpr int kTpc = kTThreads / N;       // threads per column
+  constexpr int kQE = kTD / kTpc;           // elements per thread
+  const int qcol = tid / kTpc, qd0 = (tid % kTpc) * kQE;
+  uint4 qv[kQE / 8];
+  {
+    const bool in = t0 + (qcol >> LG) < t1;
+    const uint4* p = reinterpret_cast<const uint4*>(a.q + qh_of(qcol) * kTD + qd0);
+#pragma unroll
+    for (int i = 0; i < kQE / 8; ++i) qv[i] = in ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
   }
   // the mask shifted by one: bit o keeps offset o, 0 (the query itself) and 1 .. window
   {
@@ -170,38 +177,120 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
       msk[x] = v;
     }
   }
+  if (warp == 0) tmem_alloc<Sh::kTmem>(tmem_slot);
+  if (tid == 0) {
+    mbar_init(s_done, 1);
+    mbar_init(o_done, 1);
+    fence_mbar_init();
+    *failed = 0;
+    *redo = 0;
+  }
   if (tid < N) {
     ref[tid] = -INFINITY;
     nref[tid] = INFINITY;
   }
 
-  // q: a thread holds 128 N / 256 elements of one column
-  constexpr int kTpc = kTThreads / N;       // threads per column
-  constexpr int kQE = kTD / kTpc;           // elements per thread
-  const int qcol = tid / kTpc, qd0 = (tid % kTpc) * kQE;
-  uint4 qv[kQE / 8];
-  {
-    const int t = t0 + (qcol >> lg);
-    const size_t qh =
-        (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << lg) + (qcol & ((1 << lg) - 1));
-    const uint4* p = reinterpret_cast<const uint4*>(a.q + qh * kTD + qd0);
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < kQE / 8; ++i) {
-      qv[i] = t < t1 ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+  auto load_page = [&](int blk) {
+    const int x = blk * kTPages + warp;
+    return x < pages ? __ldg(pt + page_of(x)) : 0;
+  };
+  // Rows of this warp's page of block blk that some query of the CTA keeps.
+  auto rows_needed = [&](int blk) -> unsigned {
+    const int x = blk * kTPages + warp;
+    if (x >= pages) return 0u;
+    const int j0 = page_of(x) * 16;
+    if (j0 + 15 <= i_last && (j0 + 15 < P || j0 >= i_first)) return 0xffffu;
+    const int j = j0 + (lane & 15);
+    bool need = j <= i_last;
+    if (need && j >= P && j < i_first) {
+      const int lo = i_first - j, hi = min(Wn, i_last - j);
+      need = false;
+      for (int w = lo >> 5; w <= (hi >> 5) && lo <= hi; ++w) {
+        uint32_t v = msk[w];
+        if (w == (lo >> 5)) v &= 0xffffffffu << (lo & 31);
+        if (w == (hi >> 5) && (hi & 31) != 31) v &= (2u << (hi & 31)) - 1u;
+        need |= v != 0u;
+      }
     }
-    amax = warp_max(amax);
-    if (lane == 0) red[warp] = amax;
-  }
-  __syncthreads();  // mask, references, maxima, tensor-memory address
-  const uint32_t tmem = *tmem_slot;
-  float amax = red[0];
+    return __ballot_sync(0xffffffffu, need) & 0xffffu;
+  };
+  // One page of a block on its way to a warp: the rows needed, the page's index in the
+  // pool, its scales (lane 0).
+  struct Page {
+    unsigned need;
+    size_t ph;
+    float ks, vs;
+  };
+  auto open_page = [&](int blk, int pg) -> Page {
+    Page p{rows_needed(blk), 0, 1.f, 1.f};
+    if (p.need != 0u && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
+      set_error(a.err, DSA_DEV_BAD_PAGE);
+      p.need = 0u;
+    }
+    if (p.need != 0u) {
+      p.ph = static_cast<size_t>(pg) * a.hkv + hk;
+      p.ks = __ldg(a.k_scale + p.ph);
+      p.vs = __ldg(a.v_scale + p.ph);
+    }
+    return p;
+  };
+  // Its codes: this lane's 8 of rows 2 i + lane / 16, piece lane % 16.
+  auto load_codes = [&](const uint8_t* base, const Page& p, uint2 (&v)[8]) {
+    const uint2* src = reinterpret_cast<const uint2*>(base + p.ph * (16 * kTD)) + lane;
+    if (p.need == 0xffffu) {
 #pragma unroll
-  for (int i = 1; i < 8; ++i) amax = fmaxf(amax, red[i]);
+      for (int i = 0; i < 8; ++i) v[i] = __ldg(src + 32 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = (p.need >> (2 * i + (lane >> 4))) & 1u ? __ldg(src + 32 * i) : make_uint2(0u, 0u);
+    }
+  };
+  // The same as fp16 into a block's tile (rows 16 warp .. + 15): 64-dim halves of 128
+  // rows of 128 bytes, 16-byte pieces swizzled by the row (conflict-free: 8 lanes write
+  // the 8 pieces of one line).
+  uint32_t f16_at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 2 * i + (lane >> 4);
+    f16_at[i] = sm + ((lane >> 3) & 1) * Sh::kHalf + (16 * warp + r) * 128 +
+                (((lane & 7) ^ r) << 4);
+  }
+  auto store_f16 = [&](int tile, const uint2 (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      sts128(f16_at[i & 3] + tile + (i >> 2) * 1024,
+             make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2_hi(v[i].x), e4m3x2_f16x2(v[i].y),
+                        e4m3x2_f16x2_hi(v[i].y)));
+  };
+  auto put_info = [&](int blk, const Page& p) {
+    if (lane == 0) {
+      const uint32_t ks = __float_as_uint(p.ks), vs = __float_as_uint(p.vs);
+      if (!scale_ok(ks) || !scale_ok(vs)) set_error(a.err, DSA_DEV_BAD_SCALE);
+      info[(blk & 1) * kTPages + warp] =
+          make_int4(static_cast<int>(p.need), static_cast<int>(ks), static_cast<int>(vs), 0);
+    }
+  };
+
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kQE / 8; ++i) {
+    const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+  }
+  amax = warp_max(amax);
+  if (lane == 0) red[warp] = amax;
+  __syncthreads();  // mask, references, maxima, tensor-memory address
+  uint2 kreg[8], vreg[8];
+  Page cur = open_page(0, page_of(warp) == warp ? spec0 : load_page(0));
+  load_codes(a.k, cur, kreg);
+  load_codes(a.v, cur, vreg);
+  int pg = page_of(kTPages + warp) == kTPages + warp ? spec1 : load_page(1);
+  const uint32_t tmem = *tmem_slot;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, red[i]);
   const int qe = q_exponent(amax);
   const float f = a.scale_log2 * pow2i(qe);
   {
@@ -217,105 +306,35 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
              make_uint4(h[0], h[1], h[2], h[3]));
     }
   }
-
-  const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.max_pages;
-  auto load_page = [&](int blk) {
-    const int x = blk * kTPages + warp;
-    return x < pages ? __ldg(pt + page_of(x)) : 0;
-  };
-  // Rows of this warp's page of block blk that some query of the CTA keeps.
-  auto rows_needed = [&](int blk) -> unsigned {
-    const int x = blk * kTPages + warp;
-    if (x >= pages) return 0u;
-    const int j = page_of(x) * 16 + (lane & 15);
-    bool need = j <= i_last;
-    if (need && j >= P && j < i_first) {
-      const int lo = i_first - j, hi = min(Wn, i_last - j);
-      need = false;
-      for (int w = lo >> 5; w <= (hi >> 5) && lo <= hi; ++w) {
-        uint32_t v = msk[w];
-        if (w == (lo >> 5)) v &= 0xffffffffu << (lo & 31);
-        if (w == (hi >> 5) && (hi & 31) != 31) v &= (2u << (hi & 31)) - 1u;
-        need |= v != 0u;
-      }
-    }
-    return __ballot_sync(0xffffffffu, need) & 0xffffu;
-  };
-  const int ch = lane & 7, r8 = lane >> 3;
-  // Codes of this lane: rows 4 i + lane / 8 of the page, piece lane % 8.
-  auto load_codes = [&](const uint8_t* base, size_t ph, unsigned need, uint4 (&v)[4]) {
-    const uint4* p = reinterpret_cast<const uint4*>(base + ph * (16 * kTD)) + lane;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = (need >> (4 * i + r8)) & 1u ? __ldg(p + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-  };
-  // The same as fp16 into a block's tile (rows 16 warp .. + 15): 64-dim halves of 128
-  // rows, 16-byte pieces swizzled by the row.  The lanes of the second half write their
-  // odd piece first, so that the 8 lanes of a row cover all banks.
-  auto store_f16 = [&](uint32_t tile, const uint4 (&v)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint4 lo, hi;
-      codes16(v[i], lo, hi);
-      const int r = 16 * warp + 4 * i + r8, c16 = 2 * (ch & 3);
-      const uint32_t row = tile + (ch >> 2) * Sh::kHalf + r * 128;
-      const uint32_t at0 = row + ((c16 ^ (r & 7)) << 4), at1 = row + (((c16 + 1) ^ (r & 7)) << 4);
-      const bool odd = ch >= 4;
-      sts128(odd ? at1 : at0, odd ? hi : lo);
-      sts128(odd ? at0 : at1, odd ? lo : hi);
-    }
-  };
-  auto check_page = [&](unsigned& need, int pg) -> size_t {
-    if (need != 0u && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
-      set_error(a.err, DSA_DEV_BAD_PAGE);
-      need = 0u;
-    }
-    return need != 0u ? static_cast<size_t>(pg) * a.hkv + hk : 0;
-  };
-  auto put_info = [&](int blk, unsigned need, size_t ph) {
-    if (lane == 0) {
-      // rows nobody needs: scales of one
-      uint32_t ks = 0x3f800000u, vs = 0x3f800000u;
-      if (need != 0u) {
-        ks = __float_as_uint(__ldg(a.k_scale + ph));
-        vs = __float_as_uint(__ldg(a.v_scale + ph));
-        if (!scale_ok(ks) || !scale_ok(vs)) set_error(a.err, DSA_DEV_BAD_SCALE);
-      }
-      info[(blk & 1) * kTPages + warp] =
-          make_int4(static_cast<int>(need), static_cast<int>(ks), static_cast<int>(vs), 0);
-    }
-  };
   constexpr uint32_t kIdS = tc_idesc(128, N, false), kIdO = tc_idesc(128, N, true);
   auto issue_s = [&]() {  // S = K Q^T
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      tc_mma_f16(tmem,
+      tc_mma_f16(tmem + Sh::kS,
                  tc_desc(sm + Sh::kK + (k >> 2) * Sh::kHalf + (k & 3) * 32, 16, 1024, kSwizzle128),
                  tc_desc(sm + Sh::kQ + (k >> 2) * (N * 128) + (k & 3) * 32, 16, 1024, kSwizzle128),
                  kIdS, k > 0);
     tc_commit(s_done);
   };
-  auto issue_o = [&](bool first) {  // O^T += V^T P
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      tc_mma_f16(tmem + N, tc_desc(sm + Sh::kV + k * 2048, Sh::kHalf, 1024, kSwizzle128),
+  auto issue_o = [&](bool first, int present) {  // O^T += V^T P, a step for each page
+    for (int k = 0; k < present; ++k)
+      tc_mma_f16(tmem + Sh::kO, tc_desc(sm + Sh::kV + k * 2048, Sh::kHalf, 1024, kSwizzle128),
                  tc_desc(sm + Sh::kP + k * (16 * Sh::kPRow), 16, 8 * Sh::kPRow,
                          N == 64 ? kSwizzle128 : kSwizzle64),
                  kIdO, !first || k > 0);
     tc_commit(o_done);
   };
 
-  uint4 kreg[4], vreg[4];
-  int pg = load_page(0);
-  {
-    unsigned need = rows_needed(0);
-    const size_t ph = check_page(need, pg);
-    load_codes(a.k, ph, need, kreg);
-    load_codes(a.v, ph, need, vreg);
-    put_info(0, need, ph);
+  if (warp < pages) store_f16(Sh::kK, kreg);
+  put_info(0, cur);
+  // the next block's K and V leave as soon as their registers are free, an iteration
+  // before they are wanted
+  Page nxt = cur;
+  if (nblocks > 1) {
+    nxt = open_page(1, pg);
+    load_codes(a.k, nxt, kreg);
+    pg = load_page(2);
   }
-  pg = load_page(1);
-  store_f16(sm + Sh::kK, kreg);
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
@@ -326,123 +345,185 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   // this thread's row of a block: lane 32 wq + lane of tensor memory
   const int row = 32 * wq + lane;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * wq) << 16) + cg * W;
-  f32x2 l[W / 2];
-#pragma unroll
-  for (int i = 0; i < W / 2; ++i) l[i] = pack2(0.f, 0.f);
   bool ok = true;
   for (int blk = 0; blk < nblocks && ok; ++blk) {
-    // next block's K on its way, then this block's V into shared memory
-    unsigned need = 0;
-    size_t ph = 0;
-    if (blk + 1 < nblocks) {
-      need = rows_needed(blk + 1);
-      ph = check_page(need, pg);
-      load_codes(a.k, ph, need, kreg);
-    }
-    if (blk > 0) ok = mbar_wait(o_done, (blk - 1) & 1);
-    store_f16(sm + Sh::kV, vreg);
-    if (blk + 1 < nblocks) {
-      load_codes(a.v, ph, need, vreg);
-      put_info(blk + 1, need, ph);
-      pg = load_page(blk + 2);
-    }
-    ok = mbar_wait(s_done, blk & 1) && ok;
+    if (blk > 0) ok = mbar_wait(o_done, (blk - 1) & 1);  // V and the weights are free
+    if (blk * kTPages + warp < pages) store_f16(Sh::kV, vreg);
+    if (blk + 1 < nblocks) load_codes(a.v, nxt, vreg);
+    ok = mbar_wait(s_done, blk & 1) && ok;               // S is there, K is free
     if (!ok) *failed = 1;
     tc_fence_after();
+    if (blk + 1 < nblocks) {
+      if ((blk + 1) * kTPages + warp < pages) store_f16(Sh::kK, kreg);
+      put_info(blk + 1, nxt);
+      if (blk + 2 < nblocks) {
+        nxt = open_page(blk + 2, pg);
+        load_codes(a.k, nxt, kreg);
+        pg = load_page(blk + 3);
+      }
+    }
 
     // softmax of the block: this thread's row, W columns
     const int x = blk * kTPages + (row >> 4);
     const int4 in = info[(blk & 1) * kTPages + (row >> 4)];
     const int j = x < pages ? page_of(x) * 16 + (row & 15) : 0;
-    const bool here = (in.x >> (row & 15)) & 1;
+    const bool here = x < pages && ((in.x >> (row & 15)) & 1);
     const float c1 = f * __uint_as_float(static_cast<uint32_t>(in.y));
     const float lv = static_cast<float>(scale_exp(static_cast<uint32_t>(in.z)));
     const float inv = __uint_as_float((254u << 23) - static_cast<uint32_t>(in.z));
-    const int tok0 = (cg * W) >> lg;  // token of the warp's first column
     uint32_t keep = here ? 0xffffffffu : 0u;  // bit c: column cg W + c keeps this row
+    const bool some = __any_sync(0xffffffffu, here);  // else: nothing in this warp's rows
     const bool all = __all_sync(0xffffffffu, here && j < P && j <= i_first);
     if (!all && here) {
-      // bit t of `win`: token tok0 + t keeps the row, for the tokens of W columns
-      const int o0 = i_first + tok0 - j;  // offset of the first of them
-      uint32_t win;
-      if (j < P) {
-        win = 0xffffffffu;
-      } else {
+      // bit t of `win`: the warp's t-th token keeps the row
+      const int o0 = i_first + ((cg * W) >> LG) - j;  // offset of the first token
+      uint32_t win = 0xffffffffu;
+      if (j >= P) {
         const int w0 = max(o0, 0) >> 5, sh = max(o0, 0) & 31, last = a.max_window / 32;
         const uint32_t lo = w0 <= last ? msk[w0] : 0u, hi = w0 < last ? msk[w0 + 1] : 0u;
         win = __funnelshift_r(lo, hi, sh);
       }
       if (o0 < 0) win = o0 <= -32 ? 0u : win << -o0;
-      if (lg == 0) {
+      if (LG == 0) {
         keep = win;
       } else {
         keep = 0u;
-        const uint32_t ones = (1u << (1 << lg)) - 1u;
+        constexpr uint32_t ones = (1u << (1 << LG)) - 1u;
 #pragma unroll
-        for (int t = 0; t < W / 2; ++t)
-          if (t < (W >> lg)) keep |= ((win >> t) & 1u) ? ones << (t << lg) : 0u;
+        for (int t = 0; t < (W >> LG); ++t) keep |= ((win >> t) & 1u) ? ones << (t << LG) : 0u;
       }
     }
-    float p[W];
-    uint32_t h[W / 2];
-    auto softmax = [&]() -> bool {
-      uint32_t s[W];
-      tmem_load<W>(t_lane, s);
-      tc_wait_ld();
-      const f32x2 c2 = pack2(c1, c1), lv2 = pack2(lv, lv);
-      uint32_t top = 0u;
+    // The first block: a column's reference is its score with the block's first row
+    // if it keeps that row (a maximum would need a reduction over the rows; a
+    // reference too low is found out like any other).
+    if (blk == 0) {
+      if (wq == 0) {
 #pragma unroll
-      for (int i = 0; i < W / 2; i += 2) {
-        const float4 r = *reinterpret_cast<const float4*>(nref + cg * W + 2 * i);
+        for (int q = 0; q < kChunks; ++q) {
+          uint32_t s[16];
+          tmem_load<16>(t_lane + Sh::kS + 16 * q, s);
+          tc_wait_ld();
+          if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int c = 2 * (i + k);
-          const f32x2 z2 = fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2,
-                                add2(k == 0 ? pack2(r.x, r.y) : pack2(r.z, r.w), lv2));
-          unpack2(z2, p[c], p[c + 1]);
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(ref + cg * W + 16 * q + 4 * i) =
+                  make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+          }
+        }
+        __syncwarp();
+        const uint32_t keep0 = __shfl_sync(0xffffffffu, keep, 0);
+        const float c10 = __shfl_sync(0xffffffffu, c1, 0), lv0 = __shfl_sync(0xffffffffu, lv, 0);
+        if (lane < W) {
+          const float y = fmaf(ref[cg * W + lane], c10, lv0);
+          const bool use = ((keep0 >> lane) & 1u) && fabsf(y) < INFINITY;
+          ref[cg * W + lane] = use ? y : -INFINITY;
+          nref[cg * W + lane] = use ? kTHead - y : INFINITY;
         }
       }
-      if (!all) {
+      __syncthreads();
+    }
+    // weights of the row, stored as the B operand; the row's part of the columns' sums,
+    // from copy blk % 2 to the other one
+    const float wsum = here ? inv : 0.f;
+    const uint32_t l_old = t_lane + Sh::kL + (blk & 1) * N, l_new = t_lane + Sh::kL + (~blk & 1) * N;
+    const uint32_t p_at = sm + Sh::kP + row * Sh::kPRow;
+    auto p_piece = [&](int i) {  // 16-byte piece i of the warp's columns
+      const int piece = cg * (W / 8) + i;
+      return p_at + ((N == 64 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3)) << 4);
+    };
+    auto softmax = [&](bool rescale) -> bool {
+      const f32x2 c2 = pack2(c1, c1), lv2 = pack2(lv, lv), inv2 = pack2(wsum, wsum);
+      uint32_t top = 0u;
 #pragma unroll
-        for (int c = 0; c < W; ++c) p[c] = (keep >> c) & 1u ? p[c] : -INFINITY;
-      }
+      for (int q = 0; q < kChunks; ++q) {
+        uint32_t s[16], lr[16];
+        tmem_load<16>(t_lane + Sh::kS + 16 * q, s);
+        if (blk > 0) tmem_load<16>(l_old + 16 * q, lr);
+        tc_wait_ld();
+        float p[16];
 #pragma unroll
-      for (int i = 0; i < W / 2; ++i) {
-        p[2 * i] = ex2_approx(p[2 * i]);
-        p[2 * i + 1] = ex2_approx(p[2 * i + 1]);
-        h[i] = f16x2_rn(p[2 * i], p[2 * i + 1]);
-        top = hmax2(top, h[i]);
+        for (int i = 0; i < 4; ++i) {
+          const float4 r = *reinterpret_cast<const float4*>(nref + cg * W + 16 * q + 4 * i);
+          const f32x2 z0 = fma2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), c2,
+                                add2(pack2(r.x, r.y), lv2));
+          const f32x2 z1 = fma2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])),
+                                c2, add2(pack2(r.z, r.w), lv2));
+          unpack2(z0, p[4 * i], p[4 * i + 1]);
+          unpack2(z1, p[4 * i + 2], p[4 * i + 3]);
+        }
+        if (!all) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) p[c] = (keep >> (16 * q + c)) & 1u ? p[c] : -INFINITY;
+        }
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[2 * i] = ex2_approx(p[2 * i]);
+          p[2 * i + 1] = ex2_approx(p[2 * i + 1]);
+          h[i] = f16x2_rn(p[2 * i], p[2 * i + 1]);
+          top = hmax2(top, h[i]);
+        }
+        sts128(p_piece(2 * q), make_uint4(h[0], h[1], h[2], h[3]));
+        sts128(p_piece(2 * q + 1), make_uint4(h[4], h[5], h[6], h[7]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f32x2 l = blk > 0 ? pack2(__uint_as_float(lr[2 * i]), __uint_as_float(lr[2 * i + 1]))
+                            : pack2(0.f, 0.f);
+          if (rescale)
+            l = mul2(l, *reinterpret_cast<const f32x2*>(fac + cg * W + 16 * q + 2 * i));
+          l = fma2(pack2(p[2 * i], p[2 * i + 1]), inv2, l);
+          float u, v;
+          unpack2(l, u, v);
+          lr[2 * i] = __float_as_uint(u);
+          lr[2 * i + 1] = __float_as_uint(v);
+        }
+        tmem_store16(l_new + 16 * q, lr);
       }
+      tc_wait_st();
       // weights of 2^15 and more (0x7800 as fp16): the reference has to move
       return (top & 0xffffu) >= 0x7800u || (top >> 16) >= 0x7800u;
     };
-    auto store_p = [&]() {
-      const uint32_t at = sm + Sh::kP + row * Sh::kPRow;
+    // a warp none of whose rows is there: no weights, and its sums move on as they are
+    auto nothing = [&](bool rescale) {
 #pragma unroll
-      for (int i = 0; i < W / 8; ++i) {
-        const int piece = cg * (W / 8) + i;
-        const int sw = N == 64 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3);
-        sts128(at + (sw << 4), make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]));
+      for (int q = 0; q < kChunks; ++q) {
+        uint32_t lr[16];
+        if (blk > 0) {
+          tmem_load<16>(l_old + 16 * q, lr);
+          tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (rescale)
+              lr[c] = __float_as_uint(__uint_as_float(lr[c]) * fac[cg * W + 16 * q + c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) lr[c] = 0u;
+        }
+        tmem_store16(l_new + 16 * q, lr);
+        sts128(p_piece(2 * q), make_uint4(0u, 0u, 0u, 0u));
+        sts128(p_piece(2 * q + 1), make_uint4(0u, 0u, 0u, 0u));
       }
+      tc_wait_st();
     };
-    const bool over = softmax();
-    store_p();
-    if (blk + 1 < nblocks) store_f16(sm + Sh::kK, kreg);  // S of this block is done with K
+    bool over = false;
+    if (some) over = softmax(false);
+    else nothing(false);
     fence_proxy_async_smem();
     tc_fence_before();
     if (__syncthreads_or(over)) {
       // column maxima over the block, new references, everything so far rescaled
       tc_fence_after();
-      {
-        uint32_t s[W];
-        tmem_load<W>(t_lane, s);
-        tc_wait_ld();
-        float y[W];
 #pragma unroll
-        for (int c = 0; c < W; ++c)
-          y[c] = (keep >> c) & 1u ? fmaf(__uint_as_float(s[c]), c1, lv) : -INFINITY;
-        const float m = scatter_max<W>(y, lane);
-        if (lane % (32 / W) == 0) cmax[wq * N + cg * W + lane / (32 / W)] = m;
+      for (int q = 0; q < kChunks; ++q) {
+        uint32_t s[16];
+        tmem_load<16>(t_lane + Sh::kS + 16 * q, s);
+        tc_wait_ld();
+        float y[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          y[c] = (keep >> (16 * q + c)) & 1u ? fmaf(__uint_as_float(s[c]), c1, lv) : -INFINITY;
+        const float m = scatter_max(y, lane);
+        if ((lane & 1) == 0) cmax[wq * N + cg * W + 16 * q + (lane >> 1)] = m;
       }
       __syncthreads();
       if (tid < N) {
@@ -455,78 +536,81 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
         nref[tid] = kTHead - m;
       }
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < W / 2; ++i)
-        l[i] = mul2(l[i], *reinterpret_cast<const f32x2*>(fac + cg * W + 2 * i));
       if (blk > 0) {
-        uint32_t o[W];
-        tmem_load<W>(t_lane + N, o);
-        tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < W; ++c)
-          o[c] = __float_as_uint(__uint_as_float(o[c]) * fac[cg * W + c]);
+        for (int q = 0; q < kChunks; ++q) {
+          uint32_t o[16];
+          tmem_load<16>(t_lane + Sh::kO + 16 * q, o);
+          tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < W; c += 16) tmem_store16(t_lane + N + c, o + c);
+          for (int c = 0; c < 16; ++c)
+            o[c] = __float_as_uint(__uint_as_float(o[c]) * fac[cg * W + 16 * q + c]);
+          tmem_store16(t_lane + Sh::kO + 16 * q, o);
+        }
         tc_wait_st();
       }
-      softmax();
-      store_p();
+      if (some) softmax(true);
+      else nothing(true);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncthreads();
     }
-    const f32x2 inv2 = pack2(here ? inv : 0.f, here ? inv : 0.f);
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) l[i] = fma2(pack2(p[2 * i], p[2 * i + 1]), inv2, l[i]);
     ok = *failed == 0;
     if (tid == 0 && ok) {
       tc_fence_after();
-      issue_o(blk == 0);
+      issue_o(blk == 0, min(kTPages, pages - blk * kTPages));
       if (blk + 1 < nblocks) issue_s();
     }
   }
+  // sums of the columns over all rows
+#pragma unroll
+  for (int q = 0; q < kChunks; ++q) {
+    uint32_t lr[16];
+    tmem_load<16>(t_lane + Sh::kL + (nblocks & 1) * N + 16 * q, lr);
+    tc_wait_ld();
+    float v[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(lr[c]);
+    const float t = reduce_scatter<16>(v, lane);
+    if ((lane & 1) == 0) cmax[wq * N + cg * W + 16 * q + (lane >> 1)] = t;
+  }
   if (ok) ok = mbar_wait(o_done, (nblocks - 1) & 1);
   if (!ok) *failed = 1;
-  // sums of the columns over all rows
-  {
-    float v[W];
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) unpack2(l[i], v[2 * i], v[2 * i + 1]);
-    const float t = reduce_scatter<W>(v, lane);
-    if (lane % (32 / W) == 0) cmax[wq * N + cg * W + lane / (32 / W)] = t;
-  }
   __syncthreads();
   ok = *failed == 0;
   if (ok) {
     if (tid < N) {
       const float t = cmax[tid] + cmax[N + tid] + cmax[2 * N + tid] + cmax[3 * N + tid];
       fac[tid] = 1.f / t;
-      const int tk = t0 + (tid >> lg);
-      if (a.lse != nullptr && tk < t1)
-        a.lse[(static_cast<size_t>(b) * a.max_q + tk) * a.hq + (hk << lg) +
-              (tid & ((1 << lg) - 1))] = (ref[tid] - kTHead + log2f(t)) * kLn2;
+      if (a.lse != nullptr && t0 + (tid >> LG) < t1)
+        a.lse[qh_of(tid)] = (ref[tid] - kTHead + log2f(t)) * kLn2;
     }
     __syncthreads();
     tc_fence_after();
-    uint32_t o[W];
-    tmem_load<W>(t_lane + N, o);
-    tc_wait_ld();
     // lane pairs exchange columns: an even lane stores column c, dims row and row + 1,
     // its neighbour column c + 1
     const int odd = lane & 1;
+    float nan_probe = 0.f;
 #pragma unroll
-    for (int c = 0; c < W; c += 2) {
-      const float u = __uint_as_float(o[c]) * fac[cg * W + c];
-      const float v = __uint_as_float(o[c + 1]) * fac[cg * W + c + 1];
-      const float got = __shfl_xor_sync(0xffffffffu, odd ? u : v, 1);
-      const uint32_t w = odd ? bf16x2_rn(got, v) : bf16x2_rn(u, got);
-      const int col = cg * W + c + odd, tk = t0 + (col >> lg);
-      if (tk < t1) {
-        const size_t qh =
-            (static_cast<size_t>(b) * a.max_q + tk) * a.hq + (hk << lg) + (col & ((1 << lg) - 1));
-        *reinterpret_cast<uint32_t*>(a.out + qh * kTD + (row & ~1)) = w;
+    for (int q = 0; q < kChunks; ++q) {
+      uint32_t o[16];
+      tmem_load<16>(t_lane + Sh::kO + 16 * q, o);
+      tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 16; c += 2) {
+        const float2 r = *reinterpret_cast<const float2*>(fac + cg * W + 16 * q + c);
+        const float u = __uint_as_float(o[c]) * r.x, v = __uint_as_float(o[c + 1]) * r.y;
+        nan_probe += u + v;
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? u : v, 1);
+        const uint32_t w = odd ? bf16x2_rn(got, v) : bf16x2_rn(u, got);
+        const int col = cg * W + 16 * q + c + odd;
+        if (t0 + (col >> LG) < t1)
+          *reinterpret_cast<uint32_t*>(a.out + qh_of(col) * kTD + (row & ~1)) = w;
       }
     }
+    // A NaN may come from a row of V that other queries of the CTA keep (weight 0 times
+    // NaN): such a tile is done again query by query, from the rows each one keeps.
+    if (nan_probe != nan_probe) *redo = 1;
     tc_fence_before();
   } else {
     // give products in flight a bounded time to finish before the memory goes back
@@ -539,23 +623,23 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     tc_fence_after();
     tmem_dealloc<Sh::kTmem>(tmem);
   }
+  if (ok && *redo != 0)
+    for (int col = warp; col < N; col += kTThreads / 32)
+      if (t0 + (col >> LG) < t1)
+        quant_redo_query<kTD>(a, b, hk, L - n + t0 + (col >> LG), P, Wn, qh_of(col), lane);
 }
 
-template <int N>
-cudaError_t launch_one(QuantChunkLaunch a, cudaStream_t s) {
-  auto kern = quant_chunk_tc_kernel<N>;
+template <int N, int LG>
+cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
+  auto kern = quant_chunk_tc_kernel<N, LG>;
   const int smem = TcShape<N>::smem(a.max_window / 32 + 1);
   static KernelSlots cache;
   int per_sm = 0;
   const cudaError_t e =
       cache.get(reinterpret_cast<const void*>(kern), kTThreads, smem, &per_sm);
   if (e != cudaSuccess) return e;
-  const int per_cta = N >> a.group_log2;
-  a.q_tiles = (a.max_q + per_cta - 1) / per_cta;
-  a.parts = 1;
-  const int64_t units = static_cast<int64_t>(a.q_tiles) * a.hkv * a.batch;
-  if (units > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(kTThreads),
+  constexpr int per_cta = N >> LG;
+  return launch_pdl(kern, dim3((a.max_q + per_cta - 1) / per_cta, a.hkv, a.batch), dim3(kTThreads),
                     static_cast<size_t>(smem), s, a);
 }
 
@@ -569,6 +653,7 @@ int columns(const QuantChunkLaunch& a) {
 // A unit here is never cut along its pages, so this kernel needs as many units as
 // fill the GPU at least in part.
 bool quant_chunk_tc_fits(const QuantChunkLaunch& a) {
+  if (a.batch > 65535 || a.hkv > 65535) return false;  // grid axes
   if (a.split_setting != 0) return a.split_setting == 1;
   const int per_cta = columns(a) >> a.group_log2;
   const int64_t units =
@@ -577,7 +662,13 @@ bool quant_chunk_tc_fits(const QuantChunkLaunch& a) {
 }
 
 cudaError_t launch_quant_chunk_tc(const QuantChunkLaunch& a, cudaStream_t s) {
-  return columns(a) == 32 ? launch_one<32>(a, s) : launch_one<64>(a, s);
+  const bool few = columns(a) == 32;
+  switch (a.group_log2) {
+    case 0: return few ? launch_one<32, 0>(a, s) : launch_one<64, 0>(a, s);
+    case 1: return few ? launch_one<32, 1>(a, s) : launch_one<64, 1>(a, s);
+    case 2: return few ? launch_one<32, 2>(a, s) : launch_one<64, 2>(a, s);
+    default: return few ? launch_one<32, 3>(a, s) : launch_one<64, 3>(a, s);
+  }
 }
 
 }  // namespace dsa

@@ -669,6 +669,53 @@ def test_chunk_ignores_unread_rows(split):
 
 
 @pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
+@pytest.mark.parametrize("d,g", [(64, 2), (128, 1), (128, 4)])
+def test_chunk_nan_rows_reach_only_their_queries(d, g, split):
+    """NaN in V (and in K) of a row of the chunk: queries before it, and queries whose mask
+    skips it, keep their bits' worth; the others get the NaN where it belongs."""
+    w = wl.generate(case(d, g, batch=2, hkv=2, lo=200, hi=260, prompt=(40, 60), W=64, seed=23))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    bt, n = qb.batch, 20
+    gen = torch.Generator().manual_seed(0)
+    q = torch.randn(2, n, w["hq"], d, generator=gen).to(torch.bfloat16).cuda()
+    ql = torch.full((2,), n, dtype=torch.int32, device="cuda")
+
+    def run():
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+        qb.prefill_sparse(q, ql, out, lse)
+        torch.cuda.synchronize()
+        assert bt.device_error() == 0
+        return out.float().cpu(), lse.cpu()
+
+    base, base_lse = run()
+    for what in ("v", "k"):
+        codes = (qb.v if what == "v" else qb.k).view(torch.uint8)
+        for b, back in ((0, 8), (1, 30)):  # a row of the chunk, a window row before it
+            j = int(w["seq_len"][b]) - 1 - back
+            page = int(w["page_table"][b, j // 16])
+            keepers = torch.zeros(n, dtype=torch.bool)
+            for t in range(n):
+                i = int(w["seq_len"][b]) - n + t
+                keepers[t] = j in oracle.kept_set(i + 1, int(w["prompt_len"][b]), int(w["window"][b]),
+                                                  w["keep_mask"][b, 1]) if i >= j else False
+            assert keepers.any() and not keepers.all()
+            saved = codes[page, 1, j % 16, 5].clone()
+            codes[page, 1, j % 16, 5] = 127
+            out, lse = run()
+            codes[page, 1, j % 16, 5] = saved
+            mine = slice(g, 2 * g)  # the heads of kv head 1
+            hit = torch.isnan(out[b, :, mine])
+            want = torch.zeros_like(hit)
+            want[keepers, :, 5 if what == "v" else slice(None)] = True
+            assert torch.equal(hit, want)
+            assert torch.equal(torch.isnan(lse[b, :, mine]),
+                               keepers[:, None].expand(-1, g) & (what == "k"))
+            ok = ~hit
+            assert torch.allclose(out[b, :, mine][ok], base[b, :, mine][ok], rtol=2 ** -7, atol=4e-3)
+            assert torch.equal(out[b, :, :g], base[b, :, :g]) and torch.equal(out[1 - b], base[1 - b])
+
+
+@pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
 @pytest.mark.parametrize("d", [64, 128])
 def test_chunk_flags_bad_requests(d, split):
     w = wl.generate(case(d, 2, batch=3, lo=100, hi=200, seed=19))
