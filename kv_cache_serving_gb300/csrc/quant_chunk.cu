@@ -25,6 +25,8 @@
 // the last part to arrive sums in order.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "host.h"
 #include "internal.h"
@@ -39,7 +41,10 @@ constexpr int kCW = 4;          // warps per CTA
 constexpr int kCols = 32;       // columns per warp
 constexpr int kNT = kCols / 8;  // 8-column tiles per warp
 constexpr int kCStages = 3;
-constexpr float kCHead = 4.f, kCSlack = 10.f;  // as in quant_decode.cu
+// Weights are 2^(y - ref); ref follows the largest y so that it stands for 2^kCHead, once a
+// y passes it by kCSlack (as in quant_decode.cu).  Before its first row it is far below
+// every score, and finite: -inf - ref stays -inf.
+constexpr float kCHead = 4.f, kCSlack = 10.f, kNoRef = -1e30f;
 
 template <int D, int KG>
 struct ChunkShape {
@@ -68,7 +73,7 @@ struct ChunkState {
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        ref[nt][j] = -INFINITY;
+        ref[nt][j] = kNoRef;
         l[nt][j] = 0.f;
       }
 #pragma unroll
@@ -105,8 +110,8 @@ struct ChunkState {
       for (int j = 0; j < 2; ++j) {
         const float r = get(p + (NK * 4 + j) * 32);
         const float to = fmaxf(ref[nt][j], r);
-        wa[j] = ref[nt][j] == to ? 1.f : ex2_approx(ref[nt][j] - to);
-        wb[j] = r == to ? 1.f : ex2_approx(r - to);
+        wa[j] = ex2_approx(ref[nt][j] - to);
+        wb[j] = ex2_approx(r - to);
         ref[nt][j] = to;
         l[nt][j] = l[nt][j] * wa[j] + get(p + (NK * 4 + 2 + j) * 32) * wb[j];
       }
@@ -338,11 +343,58 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
           for (int nt = 0; nt < kNT; ++nt) mma_f16(z[nt], a0, a1, a2, a3, q[nt][i][0], q[nt][i][1]);
         }
       }
-      // which (row, column) pairs are kept: all of a page of prompt rows before the
-      // group's first query, else by the mask
-      uint32_t keep = 0xffffffffu;  // bit 4 nt + v
-      if (!(j0 + 15 < P && j0 + 15 <= i_lo)) {
-        keep = 0u;
+      // Scores to weights.  A page of prompt rows before the group's first query is kept
+      // whole and carries no mask arithmetic; else bit 4 nt + v of `keep` tells.
+      uint32_t p[kNT][2];
+      auto weigh = [&](auto masked, uint32_t keep) {
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float c1 = f[nt][h] * kscale;
+#pragma unroll
+            for (int v = h; v < 4; v += 2) {
+              z[nt][v] = fmaf(z[nt][v], c1, lv);
+              if (decltype(masked)::value && !((keep >> (4 * nt + v)) & 1u)) z[nt][v] = -INFINITY;
+            }
+            over |= fmaxf(z[nt][h], z[nt][2 + h]) > st.ref[nt][h] + (kCHead + kCSlack);
+          }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float mx = fmaxf(z[nt][h], z[nt][2 + h]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float to = fmaxf(st.ref[nt][h], mx - kCHead);
+              const float down = ex2_approx(st.ref[nt][h] - to);
+              st.ref[nt][h] = to;
+              st.l[nt][h] *= down;
+#pragma unroll
+              for (int mt = 0; mt < NK; ++mt) {
+                st.acc[nt][mt][h] *= down;
+                st.acc[nt][mt][2 + h] *= down;
+              }
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            z[nt][v] = ex2_approx(z[nt][v] - st.ref[nt][v & 1]);
+            st.l[nt][v & 1] = fmaf(z[nt][v], inv, st.l[nt][v & 1]);
+          }
+          p[nt][0] = movmatrix_trans(f16x2_rn(z[nt][0], z[nt][1]));
+          p[nt][1] = movmatrix_trans(f16x2_rn(z[nt][2], z[nt][3]));
+        }
+      };
+      if (j0 + 15 < P && j0 + 15 <= i_lo) {
+        weigh(std::false_type{}, 0u);
+      } else {
+        uint32_t keep = 0u;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -353,47 +405,7 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
             if (on && j >= P) on = o <= W && ((msk[o >> 5] >> (o & 31)) & 1u);
             keep |= on ? 1u << (4 * nt + v) : 0u;
           }
-      }
-      bool over = false;
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          z[nt][v] = fmaf(z[nt][v], f[nt][v & 1] * kscale, lv);
-          over |= ((keep >> (4 * nt + v)) & 1u) && z[nt][v] > st.ref[nt][v & 1] + kCSlack;
-        }
-      if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float mx = (keep >> (4 * nt + h)) & 1u ? z[nt][h] : -INFINITY;
-            mx = fmaxf(mx, (keep >> (4 * nt + 2 + h)) & 1u ? z[nt][2 + h] : -INFINITY);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float to = fmaxf(st.ref[nt][h], mx);
-            const float down = to == st.ref[nt][h] ? 1.f : ex2_approx(st.ref[nt][h] - to);
-            st.ref[nt][h] = to;
-            st.l[nt][h] *= down;
-#pragma unroll
-            for (int mt = 0; mt < NK; ++mt) {
-              st.acc[nt][mt][h] *= down;
-              st.acc[nt][mt][2 + h] *= down;
-            }
-          }
-      }
-      uint32_t p[kNT][2];
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float w = ex2_approx(z[nt][v] - (st.ref[nt][v & 1] - kCHead));
-          z[nt][v] = (keep >> (4 * nt + v)) & 1u ? w : 0.f;
-          st.l[nt][v & 1] = fmaf(z[nt][v], inv, st.l[nt][v & 1]);
-        }
-        p[nt][0] = movmatrix_trans(f16x2_rn(z[nt][0], z[nt][1]));
-        p[nt][1] = movmatrix_trans(f16x2_rn(z[nt][2], z[nt][3]));
+        weigh(std::true_type{}, keep);
       }
       uint32_t w[4][Tile::kVW];
       Tile::load_v(tile + Tile::kBytes, lane, w);
@@ -467,7 +479,7 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
       for (int i = 0; i < NK / 4; ++i)
         to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       if (a.lse != nullptr && g == 0)
-        a.lse[qh] = (st.ref[nt][h] - kCHead + log2f(l)) * kLn2;
+        a.lse[qh] = (st.ref[nt][h] + log2f(l)) * kLn2;
     }
   // A NaN may come from a row of V that other queries of the tile keep (weight 0 times
   // NaN): the warp's columns are done again from the rows each one keeps.

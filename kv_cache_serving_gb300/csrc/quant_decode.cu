@@ -38,15 +38,15 @@
 namespace dsa {
 namespace {
 
-constexpr int kQW = 4;                 // warps per CTA
-constexpr int kSlack = 10;             // a score may pass the reference by 2^10 ...
-constexpr float kHeadroom = 4.f;       // ... which itself stands for 2^4
+// Weights are 2^(y - ref).  ref follows the largest y so that it stands for 2^kHead, once
+// a y passes it by kSlack; before the first row it is far below every score, and finite.
+constexpr float kHead = 4.f, kSlack = 10.f, kNoRef = -1e30f;
 
-template <int D>
+template <int D, int NW>
 struct QuantRing {
-  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kWarp = kStages * QuantTile<D>::kStage;
-  static constexpr int kSmem = kQW * kWarp;
+  static constexpr int kSmem = NW * kWarp;
   // a warp's end state, 8 heads of [acc(D), m, l], fits the start of its ring
   static_assert(8 * (D + 2) * 4 <= kWarp, "state fits the ring");
 };
@@ -62,7 +62,7 @@ struct QuantWarp {
   bool bad;
 
   __device__ __forceinline__ void reset() {
-    ref[0] = ref[1] = -INFINITY;
+    ref[0] = ref[1] = kNoRef;
     l[0] = l[1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < NK; ++mt)
@@ -70,36 +70,32 @@ struct QuantWarp {
       for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
   }
 
-  // Heads qrow0 .. qrow0 + group - 1; columns past the group are zero.
-  __device__ __forceinline__ void load_q(const void* q, size_t qrow0, int group, float scale_log2,
-                                         int lane) {
+  // This thread's part (dims c*D/4 .. of head g) of heads qrow0 .. qrow0 + group - 1, as it
+  // is in memory: asked for before anything else, converted when the copies are out.
+  // Columns past the group are zero.
+  static constexpr int kQV = D / (XQ ? 16 : 32);
+  __device__ __forceinline__ static void fetch_q(const void* q, size_t qrow0, int group, int lane,
+                                                 uint4 (&v)[kQV]) {
     const int g = lane >> 2, c = lane & 3;
+    const size_t at = (qrow0 + g) * D + c * (D / 4);
+    const uint4* p = reinterpret_cast<const uint4*>(
+        reinterpret_cast<const unsigned char*>(q) + at * (XQ ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < kQV; ++i) v[i] = g < group ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void take_q(const uint4 (&v)[kQV], float scale_log2, int lane) {
+    const int c = lane & 3;
     float x[D / 4];
 #pragma unroll
-    for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
-    if (g < group) {
-      const size_t at = (qrow0 + g) * D + c * (D / 4);
-      if (XQ) {
-        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(q) + at);
+    for (int i = 0; i < kQV; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const float4 v = __ldg(p + i);
-          x[4 * i] = v.x;
-          x[4 * i + 1] = v.y;
-          x[4 * i + 2] = v.z;
-          x[4 * i + 3] = v.w;
-        }
-      } else {
-        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(q) + at);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 v = __ldg(p + i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[8 * i + 2 * k] = bf16_lo(w[k]);
-            x[8 * i + 2 * k + 1] = bf16_hi(w[k]);
-          }
+      for (int k = 0; k < 4; ++k) {
+        if (XQ) {
+          x[4 * i + k] = __uint_as_float(w[k]);
+        } else {
+          x[8 * i + 2 * k] = bf16_lo(w[k]);
+          x[8 * i + 2 * k + 1] = bf16_hi(w[k]);
         }
       }
     }
@@ -123,7 +119,9 @@ struct QuantWarp {
     f[1] = __shfl_sync(0xffffffffu, up, (2 * c + 1) * 4);
   }
 
-  // Rows 0 .. nrows - 1 of the tile at shared address `tile`.
+  // Rows 0 .. nrows - 1 of the tile at shared address `tile`.  PAGE: the rows are those of
+  // one page (one K and one V scale), else every row has its own.
+  template <bool PAGE>
   __device__ __forceinline__ void tile(uint32_t tile, int nrows, int lane) {
     const int g = lane >> 2;
     float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
@@ -138,24 +136,30 @@ struct QuantWarp {
         if constexpr (XQ) mma_f16((i & 1) ? s : s2, a0, a1, a2, a3, ql[i][0], ql[i][1]);
       }
     }
-    const uint32_t sc = tile + Tile::kScaleOff + 4 * g;
+    const uint32_t sc = tile + Tile::kScaleOff;
     float y[4];  // rows g (0, 1) and g + 8 (2, 3), heads 2c and 2c + 1
     float inv[2];
-    bool over = false;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint32_t ks = lds32(sc + 32 * r), vs = lds32(sc + 64 + 32 * r);
-      const bool in = g + 8 * r < nrows;
-      bad |= in && !(scale_ok(ks) && scale_ok(vs));
+      const uint32_t ks = lds32(sc + (PAGE ? 0 : 4 * g + 32 * r));
+      const uint32_t vs = lds32(sc + 64 + (PAGE ? 0 : 4 * g + 32 * r));
+      bad |= (PAGE || g + 8 * r < nrows) && !(scale_ok(ks) && scale_ok(vs));
       inv[r] = __uint_as_float((254u << 23) - vs);
       const float lv = static_cast<float>(scale_exp(vs));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float x = (s[2 * r + j] + s2[2 * r + j]) * (f[j] * __uint_as_float(ks));
-        y[2 * r + j] = in ? x + lv : -INFINITY;
-        over |= y[2 * r + j] > ref[j] + kSlack;
-      }
+      for (int j = 0; j < 2; ++j)
+        y[2 * r + j] = fmaf(s[2 * r + j] + s2[2 * r + j], f[j] * __uint_as_float(ks), lv);
     }
+    if (nrows < 16) {  // rows that are not there: no weight, and finite in the sum
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (g + 8 * r >= nrows) {
+          y[2 * r] = y[2 * r + 1] = -INFINITY;
+          inv[r] = 0.f;
+        }
+    }
+    const bool over = fmaxf(y[0], y[2]) > ref[0] + (kHead + kSlack) ||
+                      fmaxf(y[1], y[3]) > ref[1] + (kHead + kSlack);
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -163,9 +167,8 @@ struct QuantWarp {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float to = fmaxf(ref[j], mx);
-        // -inf - -inf (nothing seen yet, nothing here) must not become NaN
-        const float down = to == ref[j] ? 1.f : ex2_approx(ref[j] - to);
+        const float to = fmaxf(ref[j], mx - kHead);
+        const float down = ex2_approx(ref[j] - to);
         ref[j] = to;
         l[j] *= down;
 #pragma unroll
@@ -177,9 +180,8 @@ struct QuantWarp {
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      // a row that is not there has weight 0 whatever the reference is
-      y[e] = g + 8 * (e >> 1) < nrows ? ex2_approx(y[e] - (ref[e & 1] - kHeadroom)) : 0.f;
-      l[e & 1] = fmaf(y[e], g + 8 * (e >> 1) < nrows ? inv[e >> 1] : 0.f, l[e & 1]);
+      y[e] = ex2_approx(y[e] - ref[e & 1]);
+      l[e & 1] = fmaf(y[e], inv[e >> 1], l[e & 1]);
     }
     const uint32_t p0 = f16x2_rn(y[0], y[1]), p1 = f16x2_rn(y[2], y[3]);
     const uint32_t b0 = movmatrix_trans(p0), b1 = movmatrix_trans(p1);
@@ -199,8 +201,8 @@ struct QuantWarp {
     }
   }
 
-  // State as [head][acc(D), m, l] for the heads of the group; m stands for the
-  // reference the weights were taken against.
+  // State as [head][acc(D), m, l] for the heads of the group; m is the reference the
+  // weights were taken against.
   __device__ __forceinline__ void flush(float* to, int group, int lane) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -218,7 +220,7 @@ struct QuantWarp {
           row[g * (D / 8) + 2 * mt + 1] = acc[mt][2 + j];
         }
         if (g == 0) {
-          row[D] = ref[j] - kHeadroom;
+          row[D] = ref[j];
           row[D + 1] = sum;
         }
       }
@@ -226,15 +228,27 @@ struct QuantWarp {
   }
 };
 
+__device__ __forceinline__ int arrive(int32_t* p) {
+  int v;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// x / d; tile counts almost always fit 32 bits, where a division costs a third.
+__device__ __forceinline__ uint64_t div(uint64_t x, uint64_t d) {
+  return ((x | d) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(d) : x / d;
+}
+
 // One CTA's piece of a unit: tiles t0 .. t1 - 1 of the unit's row list.
 struct Segment {
   int b, hk, L, n, t0, t1;
 };
 
-template <int D, int MODE, bool XQ>
+template <int D, int MODE, bool XQ, int NW>
 struct QuantDecode {
   using Tile = QuantTile<D>;
-  using Ring = QuantRing<D>;
+  using Ring = QuantRing<D, NW>;
+  using Warp = QuantWarp<D, XQ>;
   static constexpr int S = Ring::kStages;
   const QuantDecodeLaunch& a;
   unsigned char* smem;
@@ -250,7 +264,7 @@ struct QuantDecode {
 
   // NaN into every output of unit (b, hk).
   __device__ void poison(int b, int hk) {
-    for (int x = threadIdx.x; x < a.group * D; x += kQW * 32) {
+    for (int x = threadIdx.x; x < a.group * D; x += NW * 32) {
       const size_t qh = static_cast<size_t>(b) * a.hq + hk * a.group + x / D;
       if (XQ)
         reinterpret_cast<float*>(a.out)[qh * D + x % D] = __int_as_float(0x7fc00000);
@@ -262,17 +276,20 @@ struct QuantDecode {
 
   // Every warp's state over its tiles of the segment, in shared memory; ends with
   // a barrier.
-  __device__ __forceinline__ void scan(const Segment& sg) {
-    QuantWarp<D, XQ> w;
+  // spec[t]: page ids loaded before the row set was known, as if tile t were rows of the
+  // prompt (kModeMask; they are used where that turns out so).
+  __device__ __forceinline__ void scan(const Segment& sg, const int (&spec)[S],
+                                       const uint4 (&qv)[Warp::kQV]) {
+    Warp w;
     const int nt = sg.t1 - sg.t0;
-    const int my_tiles = warp < nt ? (nt - warp + kQW - 1) / kQW : 0;
+    const int my_tiles = warp < nt ? (nt - warp + NW - 1) / NW : 0;
     const int32_t* pt = a.page_table + static_cast<size_t>(sg.b) * a.max_pages;
     const int32_t* list =
         MODE == kModeList ? a.kept_idx + (static_cast<size_t>(sg.b) * a.hkv + sg.hk) * a.max_kept
                           : nullptr;
     const uint32_t ring = smem_addr(smem + warp * Ring::kWarp);
     const int my_r = lane & 15;
-    auto tile_of = [&](int t) { return sg.t0 + warp + t * kQW; };
+    auto tile_of = [&](int t) { return sg.t0 + warp + t * NW; };
     auto rows_of = [&](int t) { return min(16, sg.n - 16 * tile_of(t)); };
 
     // Logical row of this lane's row (lane % 16) of local tile t.
@@ -297,6 +314,7 @@ struct QuantDecode {
       }
       return __ldg(pt + (j >> 4));
     };
+    // Copies of local tile t into stage s: this lane's row (lane % 16) is row j, in page pg.
     auto issue = [&](int t, int s, int j, int pg) {
       if (t < my_tiles) {
         const int nrows = rows_of(t);
@@ -307,23 +325,37 @@ struct QuantDecode {
           pg = 0;
         }
         const uint32_t ph = static_cast<uint32_t>(pg) * a.hkv + sg.hk;
-        const uint32_t row = ph * 16u + (j & 15);
-        const unsigned okm = __ballot_sync(0xffffffffu, ok);
         const uint32_t dst = ring + s * Tile::kStage;
+        const unsigned okm = __ballot_sync(0xffffffffu, ok);
+        if constexpr (MODE == kModeDense) {
+          const size_t at = static_cast<size_t>(ph) * (16 * D) + 16 * lane;
+          const uint8_t *kp = a.k + at, *vp = a.v + at;
 #pragma unroll
-        for (int i = 0; i < Tile::kCopies; ++i) {
-          const int r = Tile::copy_row(i, lane);
-          const uint32_t gr = MODE == kModeDense
-                                  ? ph * 16u + r
-                                  : __shfl_sync(0xffffffffu, row, r);
-          const size_t off = static_cast<size_t>(gr) * D + 16 * Tile::copy_piece(lane);
-          const uint32_t to = dst + Tile::offset(r, Tile::copy_piece(lane));
-          const bool in = (okm >> r) & 1u;
-          cp_async16_zfill(to, a.k + off, in);
-          cp_async16_zfill(to + Tile::kBytes, a.v + off, in);
+          for (int i = 0; i < Tile::kCopies; ++i) {
+            const int r = Tile::copy_row(i, lane);
+            const uint32_t to = dst + Tile::offset(r, Tile::copy_piece(lane));
+            const bool in = (okm >> r) & 1u;
+            cp_async16_zfill(to, kp + 512 * i, in);
+            cp_async16_zfill(to + Tile::kBytes, vp + 512 * i, in);
+          }
+          if (lane < 2)  // the page's scales
+            cp_async4_zfill(dst + Tile::kScaleOff + 64 * lane,
+                            (lane == 0 ? a.k_scale : a.v_scale) + ph, okm != 0u);
+        } else {
+          const uint32_t row = ph * 16u + (j & 15);
+#pragma unroll
+          for (int i = 0; i < Tile::kCopies; ++i) {
+            const int r = Tile::copy_row(i, lane);
+            const uint32_t gr = __shfl_sync(0xffffffffu, row, r);
+            const size_t off = static_cast<size_t>(gr) * D + 16 * Tile::copy_piece(lane);
+            const uint32_t to = dst + Tile::offset(r, Tile::copy_piece(lane));
+            const bool in = (okm >> r) & 1u;
+            cp_async16_zfill(to, a.k + off, in);
+            cp_async16_zfill(to + Tile::kBytes, a.v + off, in);
+          }
+          cp_async4_zfill(dst + Tile::kScaleOff + 4 * lane,
+                          (lane < 16 ? a.k_scale : a.v_scale) + ph, ok);
         }
-        cp_async4_zfill(dst + Tile::kScaleOff + 4 * lane,
-                        (lane < 16 ? a.k_scale : a.v_scale) + ph, ok);
       }
       cp_async_commit();
     };
@@ -345,7 +377,10 @@ struct QuantDecode {
       for (int t = 0; t < S; ++t) js[t] = load_j(t);
       jn2 = load_j(S);
 #pragma unroll
-      for (int t = 0; t < S; ++t) ps[t] = load_page(t, js[t]);
+      for (int t = 0; t < S; ++t)
+        ps[t] = MODE == kModeMask && my_r < rows_of(t) && js[t] == 16 * (warp + t * NW) + my_r
+                    ? spec[t]
+                    : load_page(t, js[t]);
 #pragma unroll
       for (int t = 0; t < S - 1; ++t) issue(t, t, js[t], ps[t]);
       jn = js[S - 1];
@@ -358,7 +393,7 @@ struct QuantDecode {
     }
     w.reset();
     w.bad = false;
-    w.load_q(a.q, static_cast<size_t>(sg.b) * a.hq + sg.hk * a.group, a.group, a.scale_log2, lane);
+    w.take_q(qv, a.scale_log2, lane);
     int s = 0, s_fill = S - 1;
     for (int t = 0; t < my_tiles; ++t) {
       const int tf = t + S - 1;  // tile whose copies go out now
@@ -376,7 +411,7 @@ struct QuantDecode {
       }
       cp_async_wait<S - 1>();
       __syncwarp();
-      w.tile(ring + s * Tile::kStage, rows_of(t), lane);
+      w.template tile<MODE == kModeDense>(ring + s * Tile::kStage, rows_of(t), lane);
       __syncwarp();  // every lane has read the stage before it is refilled
       s = s + 1 == S ? 0 : s + 1;
       s_fill = s_fill + 1 == S ? 0 : s_fill + 1;
@@ -390,13 +425,13 @@ struct QuantDecode {
 
   // The CTA's state (summed over its warps) of head h: weight of each warp's state,
   // and the combined m and l.
-  __device__ __forceinline__ void weights(int h, float (&wt)[kQW], float& m, float& l) {
+  __device__ __forceinline__ void weights(int h, float (&wt)[NW], float& m, float& l) {
     m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kQW; ++w) m = fmaxf(m, state(w)[h * (D + 2) + D]);
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, state(w)[h * (D + 2) + D]);
     l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kQW; ++w) {
+    for (int w = 0; w < NW; ++w) {
       wt[w] = ex2_approx(state(w)[h * (D + 2) + D] - m);
       l += state(w)[h * (D + 2) + D + 1] * wt[w];
     }
@@ -421,13 +456,13 @@ struct QuantDecode {
     const size_t qh0 = static_cast<size_t>(sg.b) * a.hq + sg.hk * a.group;
     const int part_floats = quant_part_floats(a.group, D);
     float* part = slot < 0 ? nullptr : a.part + static_cast<size_t>(slot) * part_floats;
-    for (int x = threadIdx.x; x < a.group * (D / 4); x += kQW * 32) {
+    for (int x = threadIdx.x; x < a.group * (D / 4); x += NW * 32) {
       const int h = x / (D / 4), d = 4 * (x % (D / 4));
-      float wt[kQW], m, l;
+      float wt[NW], m, l;
       weights(h, wt, m, l);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kQW; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const float2 u = *reinterpret_cast<const float2*>(state(w) + h * (D + 2) + d);
         const float2 v = *reinterpret_cast<const float2*>(state(w) + h * (D + 2) + d + 2);
         o.x = fmaf(u.x, wt[w], o.x);
@@ -450,22 +485,22 @@ struct QuantDecode {
       __syncthreads();  // the states are read before the rings are refilled
       return;
     }
+    // the CTA's stores, ordered by the barrier, are released by one thread's arrival; the
+    // last arrival acquires those of the others
     __shared__ int last;
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-      last = atomicAdd(a.count + cnt, 1) == nparts - 1;
+      last = arrive(a.count + cnt) == nparts - 1;
       if (last) a.count[cnt] = 0;  // every part has arrived
     }
     __syncthreads();
     if (!last) return;
-    __threadfence();
     auto slot_of = [&](int p) {
       return a.part + static_cast<size_t>(p == 0 ? first : later + p * stride) * part_floats;
     };
     // combined m and l of each head, one warp per head
     float* ml = state(0);
-    for (int h = warp; h < a.group; h += kQW) {
+    for (int h = warp; h < a.group; h += NW) {
       float m = -INFINITY, l = 0.f;
       for (int p = lane; p < nparts; p += 32)
         m = fmaxf(m, __ldcg(slot_of(p) + a.group * D + 2 * h));
@@ -482,7 +517,7 @@ struct QuantDecode {
       }
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < a.group * (D / 4); x += kQW * 32) {
+    for (int x = threadIdx.x; x < a.group * (D / 4); x += NW * 32) {
       const int h = x / (D / 4), d = 4 * (x % (D / 4));
       const float m = ml[2 * h];
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -502,86 +537,83 @@ struct QuantDecode {
     __syncthreads();
   }
 
-  // Dense rows: this CTA's share of all tiles of the batch.
+  // Dense rows: this CTA's share of all tiles of the batch, in unit order.  Every warp finds
+  // the share by itself, from a prefix sum over the requests' tiles (lane l: requests
+  // l * per .. l * per + per - 1).
   __device__ __forceinline__ void run_dense() {
-    const int tid = threadIdx.x, nth = kQW * 32;
     auto valid = [&](int L) { return L >= 1 && L <= a.max_pages * kPage; };
     auto tiles_of = [&](int L) { return valid(L) ? (L + 15) >> 4 : 0; };
-    // requests with a bad length: flagged, NaN outputs
-    for (int b = blockIdx.x; b < a.batch; b += gridDim.x)
-      if (!valid(a.seq_len[b])) {
-        if (tid == 0) set_error(a.err, DSA_DEV_BAD_SEQ_LEN);
-        for (int hk = 0; hk < a.hkv; ++hk) poison(b, hk);
-      }
-    // prefix sums of the requests' tiles: thread t holds requests t*per .. t*per+per-1
-    __shared__ long long wsum[kQW];
-    __shared__ long long s_base;
-    __shared__ int s_b;
-    const int per = (a.batch + nth - 1) / nth;
-    const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(a.seq_len[b]);
-    long long incl = mine;
+    const int per = (a.batch + 31) / 32;
+    const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
+    int64_t mine = 0;
+    bool any_bad = false;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) {
+      const int L = __ldg(a.seq_len + b);
+      mine += tiles_of(L);
+      any_bad |= !valid(L);
+    }
+    int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    long long before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kQW; ++w) {
-      if (w < warp) before += wsum[w];
-      total += wsum[w];
-    }
-    const long long T = total * a.hkv;
-    // no more CTAs than leave each its least share
-    const long long most = (T + a.min_tiles - 1) / a.min_tiles;
-    const long long N = most < gridDim.x ? most : gridDim.x;
-    if (static_cast<long long>(blockIdx.x) >= N) return;
-    auto border = [&](long long i) { return i * T / N; };
-    auto owner = [&](long long x) { return static_cast<int>(((x + 1) * N + T - 1) / T - 1); };
-    long long x = border(blockIdx.x);
-    const long long x1 = border(blockIdx.x + 1);
-    if (x >= before * a.hkv && x < (before + mine) * a.hkv) {
-      long long base = before * a.hkv;
-      for (int b = b0; b < b1; ++b) {
-        const long long nb = static_cast<long long>(tiles_of(a.seq_len[b])) * a.hkv;
-        if (x < base + nb) {
-          s_b = b;
-          s_base = base;
-          break;
+    if (__any_sync(0xffffffffu, any_bad)) {
+      // requests with a bad length are flagged and get NaN (by one CTA each)
+      for (int b = blockIdx.x; b < a.batch; b += gridDim.x)
+        if (!valid(a.seq_len[b])) {
+          if (threadIdx.x == 0) set_error(a.err, DSA_DEV_BAD_SEQ_LEN);
+          for (int hk = 0; hk < a.hkv; ++hk) poison(b, hk);
         }
+    }
+    // T tiles over N CTAs (no more than leave each its least share): CTA i takes tiles
+    // floor(i T / N) .. floor((i+1) T / N) - 1
+    const uint64_t T = static_cast<uint64_t>(__shfl_sync(0xffffffffu, incl, 31)) * a.hkv;
+    const uint64_t most = div(T + a.min_tiles - 1, a.min_tiles);
+    const uint64_t N = most < gridDim.x ? most : gridDim.x;
+    if (blockIdx.x >= N) return;
+    auto owner = [&](uint64_t x) { return static_cast<int>(div((x + 1) * N + T - 1, T) - 1); };
+    uint64_t x = div(blockIdx.x * T, N);
+    const uint64_t x1 = div((blockIdx.x + 1) * T, N);
+    // the request of tile x: its lane by vote, then that lane's walk over its requests
+    uint64_t base = static_cast<uint64_t>(incl - mine) * a.hkv;
+    int b = b0;
+    const bool have = x >= base && x < base + static_cast<uint64_t>(mine) * a.hkv;
+    if (have)
+      for (; b < b1; ++b) {
+        const uint64_t nb = static_cast<uint64_t>(tiles_of(__ldg(a.seq_len + b))) * a.hkv;
+        if (x < base + nb) break;
         base += nb;
       }
-    }
-    __syncthreads();
-    int b = s_b;
-    long long base = s_base;
+    const int src = __ffs(__ballot_sync(0xffffffffu, have)) - 1;
+    b = __shfl_sync(0xffffffffu, b, src);
+    base = __shfl_sync(0xffffffffu, base, src);
     while (x < x1) {
-      int L = a.seq_len[b];
-      while (!valid(L)) L = a.seq_len[++b];  // a tile x < T lies ahead
+      int L = __ldg(a.seq_len + b);
+      while (!valid(L)) L = __ldg(a.seq_len + ++b);  // a tile x < T lies ahead
       const int nb = tiles_of(L);
-      const int hk = static_cast<int>((x - base) / nb);
-      const int tl = static_cast<int>((x - base) % nb);
-      const long long left = x1 - x;
-      const int t1 = left < nb - tl ? tl + static_cast<int>(left) : nb;
+      const int hk = static_cast<int>(div(x - base, nb));
+      const int tl = static_cast<int>(x - base - static_cast<uint64_t>(hk) * nb);
+      const uint64_t left = x1 - x;
+      const int t1 = left < static_cast<uint64_t>(nb - tl) ? tl + static_cast<int>(left) : nb;
       const Segment sg{b, hk, L, L, tl, t1};
-      scan(sg);
-      if (tl == 0 && t1 == nb) {
-        finish(sg, -1, 0, 1, 0, 0, 0);
-      } else {
-        // CTA i leaves the unit it began before i's share in slot 2i, the unit
-        // that goes on after it in slot 2i + 1
-        const long long u0 = x - tl;
-        const int i0 = owner(u0), i1 = owner(u0 + nb - 1);
-        const int slot = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == i0);
-        finish(sg, slot, i0, i1 - i0 + 1, 2 * i0 + 1, 2 * i0, 2);
+      uint4 qv[Warp::kQV];
+      Warp::fetch_q(a.q, static_cast<size_t>(b) * a.hq + hk * a.group, a.group, lane, qv);
+      scan(sg, {}, qv);
+      // CTA i leaves the unit it began before i's share in slot 2i, the unit that goes on
+      // after it in slot 2i + 1; the counter is that of the unit's first CTA
+      int slot = -1, i0 = 0, nparts = 1;
+      if (tl != 0 || t1 != nb) {
+        const uint64_t u0 = x - tl;
+        i0 = owner(u0);
+        nparts = owner(u0 + nb - 1) - i0 + 1;
+        slot = 2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == i0);
       }
+      finish(sg, slot, i0, nparts, 2 * i0 + 1, 2 * i0, 2);
       x += t1 - tl;
       if (t1 == nb && hk == a.hkv - 1) {
-        base += static_cast<long long>(nb) * a.hkv;
+        base += static_cast<uint64_t>(nb) * a.hkv;
         ++b;
       }
     }
@@ -600,7 +632,16 @@ struct QuantDecode {
       if (part == 0 && hk == 0 && threadIdx.x == 0) set_error(a.err, DSA_DEV_BAD_ORDER);
       return;
     }
+    uint4 qv[Warp::kQV];
+    Warp::fetch_q(a.q, static_cast<size_t>(b) * a.hq + hk * a.group, a.group, lane, qv);
     const int L = a.seq_len[b];
+    int spec[S] = {};
+    if constexpr (MODE == kModeMask) {
+#pragma unroll
+      for (int t = 0; t < S; ++t)
+        if (warp + t * NW < a.max_pages)
+          spec[t] = __ldg(a.page_table + static_cast<size_t>(b) * a.max_pages + warp + t * NW);
+    }
     int n;
     if constexpr (MODE == kModeMask) {
       const uint32_t* mrow = a.keep_mask + (static_cast<size_t>(b) * a.hkv + hk) * a.mask_words;
@@ -623,20 +664,25 @@ struct QuantDecode {
     const int per = (nt + a.parts - 1) / a.parts, nparts = (nt + per - 1) / per;
     if (part >= nparts) return;
     const Segment sg{b, hk, L, n, part * per, min(nt, (part + 1) * per)};
-    scan(sg);
+    scan(sg, spec, qv);
     const int slot0 = unit * a.parts;
-    if (nparts == 1) finish(sg, -1, 0, 1, 0, 0, 0);
-    else finish(sg, slot0 + part, unit, nparts, slot0, slot0, 1);
+    finish(sg, nparts == 1 ? -1 : slot0 + part, unit, nparts, slot0, slot0, 1);
   }
 };
 
-template <int D, int MODE, bool XQ>
-__global__ void __launch_bounds__(kQW * 32, D == 128 ? (XQ ? 3 : 4) : (XQ ? 4 : 6))
+// Resident CTAs per SM the register budget allows for: 16 warps of the bf16 builds at D = 128
+// (128 registers a thread), 12 with fp32 q (its second halves), more at D = 64.
+constexpr int resident_ctas(int d, bool xq, int nw) {
+  return (d == 128 ? (xq ? 12 : 16) : (xq ? 16 : 24)) / nw;
+}
+
+template <int D, int MODE, bool XQ, int NW>
+__global__ void __launch_bounds__(NW * 32, (resident_ctas(D, XQ, NW)))
     quant_decode_kernel(const QuantDecodeLaunch a) {
   extern __shared__ __align__(128) unsigned char smem[];
   griddep_wait();
   griddep_launch_dependents();
-  QuantDecode<D, MODE, XQ> k(a, smem);
+  QuantDecode<D, MODE, XQ, NW> k(a, smem);
   if constexpr (MODE == kModeDense) k.run_dense();
   else k.run_sparse();
 }
@@ -646,19 +692,19 @@ __global__ void __launch_bounds__(kQW * 32, D == 128 ? (XQ ? 3 : 4) : (XQ ? 4 : 
 int sparse_parts(int64_t units, int64_t slots, int max_kept) {
   if (units < 1 || units * 2 > slots || units > kMultiCounters) return 1;
   int64_t parts = slots / units;
-  const int64_t most = (static_cast<int64_t>(max_kept) + 16 * kQW - 1) / (16 * kQW);
+  const int64_t most = (max_kept + 63) / 64;
   if (parts > most) parts = most;
   if (parts > kQuantMaxParts) parts = kQuantMaxParts;
   return parts < 1 ? 1 : static_cast<int>(parts);
 }
 
-template <int D, int MODE, bool XQ>
+template <int D, int MODE, bool XQ, int NW>
 cudaError_t launch_one(QuantDecodeLaunch a, cudaStream_t s) {
-  auto kern = quant_decode_kernel<D, MODE, XQ>;
-  constexpr int smem = QuantRing<D>::kSmem;
+  auto kern = quant_decode_kernel<D, MODE, XQ, NW>;
+  constexpr int smem = QuantRing<D, NW>::kSmem;
   static KernelSlots cache;
   int per_sm = 0;
-  const cudaError_t e = cache.get(reinterpret_cast<const void*>(kern), kQW * 32, smem, &per_sm);
+  const cudaError_t e = cache.get(reinterpret_cast<const void*>(kern), NW * 32, smem, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t slots = static_cast<int64_t>(per_sm) * a.sms;
   const int64_t units = static_cast<int64_t>(a.batch) * a.hkv;
@@ -667,25 +713,40 @@ cudaError_t launch_one(QuantDecodeLaunch a, cudaStream_t s) {
     a.min_tiles = kQuantMinTiles;
     const int64_t most = (units * a.max_pages + kQuantMinTiles - 1) / kQuantMinTiles;
     grid = slots < most ? slots : most;
-    // two slots of partials and one counter per CTA
-    if (grid > kMultiCounters) grid = kMultiCounters;
+    // two slots of partials and one counter for each CTA
     const int64_t fit = a.part_cap / (2 * quant_part_floats(a.group, D));
     if (grid > fit) grid = fit;
+    if (grid > kMultiCounters) grid = kMultiCounters;
     if (grid < 1) grid = 1;
   } else {
     a.parts = sparse_parts(units, slots, a.max_kept);
     if (units * a.parts * quant_part_floats(a.group, D) > a.part_cap) a.parts = 1;
     grid = units * a.parts;
   }
-  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kQW * 32),
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(NW * 32),
                     static_cast<size_t>(smem), s, a);
+}
+
+// Sparse rows: a unit in a CTA of 2 warps when there is more than one unit for every two
+// SMs' worth of ... slots (a warp's start -- sizes, mask, first pages, about 4 us under load -- is
+// then paid by fewer warps per unit), else of 4.
+template <int D, int MODE, bool XQ>
+cudaError_t launch_warps(const QuantDecodeLaunch& a, cudaStream_t s) {
+  if constexpr (MODE == kModeDense) {
+    return launch_one<D, MODE, XQ, 4>(a, s);
+  } else {
+    const int64_t units = static_cast<int64_t>(a.batch) * a.hkv;
+    return units * 2 > static_cast<int64_t>(resident_ctas(D, XQ, 4)) * a.sms
+               ? launch_one<D, MODE, XQ, 2>(a, s)
+               : launch_one<D, MODE, XQ, 4>(a, s);
+  }
 }
 
 template <int D, bool XQ>
 cudaError_t launch_mode(const QuantDecodeLaunch& a, int mode, cudaStream_t s) {
-  if (mode == kModeDense) return launch_one<D, kModeDense, XQ>(a, s);
-  if (mode == kModeList) return launch_one<D, kModeList, XQ>(a, s);
-  return launch_one<D, kModeMask, XQ>(a, s);
+  if (mode == kModeDense) return launch_warps<D, kModeDense, XQ>(a, s);
+  if (mode == kModeList) return launch_warps<D, kModeList, XQ>(a, s);
+  return launch_warps<D, kModeMask, XQ>(a, s);
 }
 
 }  // namespace
