@@ -138,9 +138,9 @@ dsa_status dsa_rope_axes(const dsa_dims* dims, const dsa_rope* rope, int32_t tok
     const double f = rope->inv_freq[i];
     if (!std::isfinite(f) || std::fabs(f) > 6.283185307179587 || rope->pair_axis[i] >= rope->axes)
       return DSA_ERR_INVALID_ARG;
-    // turns per position as a 64-bit fraction: at most one turn, and a whole turn is none
-    const double turns = std::fabs(f) / 6.283185307179586476925;
-    const double scaled = std::ldexp(turns, 64);
+    // turns per position as a 64-bit fraction (2^64 / 2 pi units per radian): at most one
+    // turn, and a whole turn is none
+    const double scaled = std::fabs(f) * 2935890503282001226.5;
     const uint64_t t = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
     a.turn[i] = f < 0 ? 0 - t : t;
     a.pair_axis[i] = rope->pair_axis[i];

@@ -498,41 +498,45 @@ struct QuantDecode {
     auto slot_of = [&](int p) {
       return a.part + static_cast<size_t>(p == 0 ? first : later + p * stride) * part_floats;
     };
-    // combined m and l of each head, one warp per head
-    float* ml = state(0);
-    for (int h = warp; h < a.group; h += NW) {
-      float m = -INFINITY, l = 0.f;
-      for (int p = lane; p < nparts; p += 32)
-        m = fmaxf(m, __ldcg(slot_of(p) + a.group * D + 2 * h));
-      m = warp_max(m);
-      for (int p = lane; p < nparts; p += 32) {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(slot_of(p) + a.group * D + 2 * h));
-        l += v.y * ex2_approx(v.x - m);
-      }
-      l = warp_sum(l);
-      if (lane == 0) {
-        ml[2 * h] = m;
-        ml[2 * h + 1] = l;
-        if (a.lse != nullptr) a.lse[qh0 + h] = (m + log2f(l)) * kLn2;
-      }
-    }
-    __syncthreads();
+    // one pass over the parts in order, eight in flight: running maximum, sum and
+    // accumulator of this thread's head and dims
     for (int x = threadIdx.x; x < a.group * (D / 4); x += NW * 32) {
       const int h = x / (D / 4), d = 4 * (x % (D / 4));
-      const float m = ml[2 * h];
+      float m = kNoRef, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int p = 0; p < nparts; ++p) {
-        const float* src = slot_of(p);
-        const float wt = ex2_approx(__ldcg(src + a.group * D + 2 * h) - m);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + h * D + d));
-        o.x = fmaf(v.x, wt, o.x);
-        o.y = fmaf(v.y, wt, o.y);
-        o.z = fmaf(v.z, wt, o.z);
-        o.w = fmaf(v.w, wt, o.w);
+      for (int p0 = 0; p0 < nparts; p0 += 8) {
+        float2 ml[8];
+        float4 v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const float* src = slot_of(min(p0 + p, nparts - 1));
+          ml[p] = __ldcg(reinterpret_cast<const float2*>(src + a.group * D + 2 * h));
+          v[p] = __ldcg(reinterpret_cast<const float4*>(src + h * D + d));
+        }
+        float to = m;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) to = fmaxf(to, ml[p].x);
+        const float keep = ex2_approx(m - to);
+        m = to;
+        l *= keep;
+        o.x *= keep;
+        o.y *= keep;
+        o.z *= keep;
+        o.w *= keep;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          if (p0 + p >= nparts) break;
+          const float wt = ex2_approx(ml[p].x - m);
+          l = fmaf(ml[p].y, wt, l);
+          o.x = fmaf(v[p].x, wt, o.x);
+          o.y = fmaf(v[p].y, wt, o.y);
+          o.z = fmaf(v[p].z, wt, o.z);
+          o.w = fmaf(v[p].w, wt, o.w);
+        }
       }
-      const float r = 1.f / ml[2 * h + 1];
+      const float r = 1.f / l;
       store(qh0 + h, d, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+      if (d == 0 && a.lse != nullptr) a.lse[qh0 + h] = (m + log2f(l)) * kLn2;
     }
     __syncthreads();
   }

@@ -458,9 +458,10 @@ def _arg(t, dtype, dev, what):
     return t.data_ptr()
 
 
-def _rows_arg(t, heads, head_dim, dtype, dev, what):
-    """Address and row stride of [..., heads, head_dim] whose rows are evenly spaced (the
-    last two dimensions contiguous: slices of a fused projection are fine)."""
+def _rows_arg(t, want, dtype, dev, what):
+    """Address and row stride of a tensor of shape `want` = (..., heads, head_dim) whose rows
+    are evenly spaced (the last two dimensions contiguous: slices of a fused projection are
+    fine)."""
     if t is None:
         return None, 0
     if t.get_device() != dev:
@@ -468,20 +469,23 @@ def _rows_arg(t, heads, head_dim, dtype, dev, what):
                         f"{t.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{what} has dtype {t.dtype}, expected {dtype}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) < 3 or shape[-2] != heads or shape[-1] != head_dim:
-        raise ValueError(f"{what} must be [..., {heads}, {head_dim}]")
+    if t.shape != want:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(want)}")
+    heads, head_dim = want[-2:]
+    if t.is_contiguous():
+        return t.data_ptr(), heads * head_dim
+    stride = t.stride()
     if stride[-1] != 1 or (stride[-2] != head_dim and heads > 1):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
     row = None  # elements between rows, from the innermost row dimension that has several
-    for i in range(len(shape) - 3, -1, -1):
-        if shape[i] == 1:
+    for i in range(len(want) - 3, -1, -1):
+        if want[i] == 1:
             continue
         if row is None:
             row = stride[i]
         elif stride[i] != span:
             raise ValueError(f"{what}: rows must be evenly spaced")
-        span = stride[i] * shape[i]
+        span = stride[i] * want[i]
     return t.data_ptr(), heads * head_dim if row is None else row
 
 
@@ -513,15 +517,15 @@ def dsa_rope_axes(dims, rope, positions, q, k, q_out, k_out, stream=None):
     if getattr(rope, "pairs", hd // 2) != hd // 2:
         raise ValueError(f"rope has {rope.pairs} pairs, head_dim {hd}")
     dev, st = _launch_on(stream)
-    n, hq, hkv = positions.shape[0], dims.hq, dims.hkv
+    n = positions.shape[0]
+    qw, kw = (n, dims.hq, hd), (n, dims.hkv, hd)
     qt, kt = _TYPE.get(dims.q_dtype), _TYPE.get(dims.kv_dtype)
-    for t, heads, what in ((q, hq, "q"), (k, hkv, "k"), (q_out, hq, "q_out"), (k_out, hkv, "k_out")):
-        _shape(t, (n, heads, hd), what)
-    _check(_load().dsa_rope_axes(
-        dims, rope, n, _arg(positions, _I32, dev, "positions"),
-        *_rows_arg(q, hq, hd, qt, dev, "q"), *_rows_arg(k, hkv, hd, kt, dev, "k"),
-        *_rows_arg(q_out, hq, hd, qt, dev, "q_out"), *_rows_arg(k_out, hkv, hd, kt, dev, "k_out"),
-        st), "dsa_rope_axes")
+    qp, qs = _rows_arg(q, qw, qt, dev, "q")
+    kp, ks = _rows_arg(k, kw, kt, dev, "k")
+    qo, qos = _rows_arg(q_out, qw, qt, dev, "q_out")
+    ko, kos = _rows_arg(k_out, kw, kt, dev, "k_out")
+    _check(_load().dsa_rope_axes(dims, rope, n, _arg(positions, _I32, dev, "positions"), qp, qs, kp,
+                                 ks, qo, qos, ko, kos, st), "dsa_rope_axes")
 
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -542,6 +546,7 @@ def quant_cache(k_codes, v_codes, k_scale, v_scale) -> dsa_quant_cache:
                         _arg(k_scale, torch.float32, dev, "k_scale"),
                         _arg(v_scale, torch.float32, dev, "v_scale"))
     c.tensors = (k_codes, v_codes, k_scale, v_scale)
+    c.facts = (dev, *k_codes.shape)
     return c
 
 
@@ -549,28 +554,28 @@ def _cache(dims, cache, dev):
     """The cache, checked against dims."""
     if cache.__class__ is not dsa_quant_cache:
         raise TypeError("cache must be a dsa_quant_cache (see quant_cache)")
-    codes = cache.tensors[0] if hasattr(cache, "tensors") else None
-    if codes is not None:
-        _shape(codes, (dims.num_pages, dims.hkv, PAGE, dims.head_dim), "cache codes")
-        if codes.get_device() != dev:
-            raise TypeError(f"cache on {codes.device}, current device cuda:{dev}")
+    facts = getattr(cache, "facts", None)  # of the tensors it was made over
+    if facts is not None and facts != (dev, dims.num_pages, dims.hkv, PAGE, dims.head_dim):
+        raise ValueError(f"cache is [num_pages, hkv, 16, head_dim] = {facts[1:]} on cuda:{facts[0]}; "
+                         f"the call wants {(dims.num_pages, dims.hkv, PAGE, dims.head_dim)} on "
+                         f"cuda:{dev}")
     return cache
 
 
 def dsa_quant_write(dims, cache, k_new, v_new, page_table, seq_len, new_len, ws, stream=None):
     """Quantise k_new / v_new [batch, max_new, hkv, head_dim] into the cache as the last
     new_len[b] rows of each request (new_len None: all max_new slots)."""
-    if k_new.dim() != 4 or k_new.shape[0] != dims.batch:
-        raise ValueError("k_new must be [batch, max_new, hkv, head_dim]")
-    _shape(v_new, k_new.shape, "v_new")
     dev, st = _launch_on(stream)
-    kt = _TYPE.get(dims.kv_dtype)
-    k, ks = _rows_arg(k_new, dims.hkv, dims.head_dim, kt, dev, "k_new")
-    v, vs = _rows_arg(v_new, dims.hkv, dims.head_dim, kt, dev, "v_new")
+    kt, shape = _TYPE.get(dims.kv_dtype), k_new.shape
+    if len(shape) != 4:
+        raise ValueError("k_new must be [batch, max_new, hkv, head_dim]")
+    want = (dims.batch, shape[1], dims.hkv, dims.head_dim)
+    k, ks = _rows_arg(k_new, want, kt, dev, "k_new")
+    v, vs = _rows_arg(v_new, want, kt, dev, "v_new")
     if ks != vs:
         raise ValueError("k_new and v_new must have the same row stride")
     _check(_load().dsa_quant_write(
-        dims, _cache(dims, cache, dev), k_new.shape[1], k, v, ks,
+        dims, _cache(dims, cache, dev), shape[1], k, v, ks,
         _arg(page_table, _I32, dev, "page_table"), _arg(seq_len, _I32, dev, "seq_len"),
         _arg(new_len, _I32, dev, "new_len"), _arg(ws, torch.uint8, dev, "ws"), st), "dsa_quant_write")
 
@@ -596,9 +601,13 @@ def dsa_quant_read(dims, cache, page_table, seq_len, row_start, row_count, k_out
 
 def _q_out(dims, q, out, lse, dev, rows):
     """Addresses of q, out (q's type) and lse, their shapes checked."""
-    _shape(q, rows + (dims.hq, dims.head_dim), "q")
-    _shape(out, q.shape, "out")
-    _shape(lse, rows + (dims.hq,), "lse")
+    shape = q.shape
+    if shape != rows + (dims.hq, dims.head_dim):
+        raise ValueError(f"q has shape {tuple(shape)}, expected {rows + (dims.hq, dims.head_dim)}")
+    if out.shape != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    if lse is not None and lse.shape != shape[:-1]:
+        raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {tuple(shape[:-1])}")
     qt = _TYPE.get(dims.q_dtype)
     return _arg(q, qt, dev, "q"), _arg(out, qt, dev, "out"), _arg(lse, torch.float32, dev, "lse")
 

@@ -176,10 +176,11 @@ def test_write_bit_exact(d, hkv, dtype):
     pool.check()
 
 
-def test_write_special_values():
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_write_special_values(dtype):
     """Zeros of both signs, infinities, NaN, the largest and smallest magnitudes, and
     values on the border between two codes."""
-    pool = Pool(1, 4, 64, "f32", 3)
+    pool = Pool(1, 4, 64, dtype, 3)
     x = torch.zeros(1, 40, 4, 64, dtype=torch.float64)
     x[0, :, 0] = -0.0                                            # head 0: zeros alone
     x[0, :16, 1] = torch.linspace(-500, 500, 64).double()          # over 448: the scale is 2
@@ -189,7 +190,7 @@ def test_write_special_values():
     ties = torch.as_tensor((POSITIVE[:-1] + POSITIVE[1:]) / 2)[-64:]
     x[0, :, 3] = ties                                            # halfway between codes
     x[0, 3, 3] = -ties
-    x = x.float()
+    x = x.to(pool.dt)
     assert pool.write(x, -x, [40], [40]) == 0
     pool.ref.write({"k": x, "v": -x}, pool.table, [40], [40])
     pool.check()
