@@ -19,10 +19,15 @@
 // (a vote at the barrier the block has anyway); then the sums and the accumulators in
 // tensor memory are rescaled.
 //
-// What bounds it: instruction issue in the conversion and the softmax (about 2100
-// instructions per block of 128 rows x 64 columns against 512 cycles of MMA).  Two CTAs
-// per SM, so that one converts while the other's products run; loads of the next block
-// are in flight during the softmax.
+// What bounds it: latency and instruction issue between the products, not the products (6%
+// of the tensor pipe): a block's chain is V into shared memory, S awaited, K, softmax,
+// barrier, products, about 700 instructions per warp at 16 warps per SM, of which the
+// conversions are 130 and the softmax 300.  Two CTAs per SM, so that one converts while the
+// other's products run; the next block's K and V are loaded an iteration ahead, past the
+// L1 (whose 20 KB keep page ids, masks and spills).  Measured: 32 tokens of 64 requests of 320 ..
+// 1280 rows under the mask, 32/32 heads: 90 us (136 with quant_chunk.cu).  A persistent
+// form (tiles of several units in one CTA, the next tile's q and first block ahead)
+// measured slower: 141 us, its second set of tile values spills.
 #include <math.h>
 
 #include "common.cuh"
@@ -67,6 +72,13 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+// Read once: past the L1, whose few kilobytes beside the tiles hold the page ids and masks.
+__device__ __forceinline__ uint2 ld_stream(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 // Maximum over the warp of each of 16 values: lane l ends with value l / 2.
 __device__ __forceinline__ float scatter_max(float (&v)[16], int lane) {
 #pragma unroll
@@ -94,8 +106,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wq = warp & 3, cg = warp >> 2;  // lane quarter of tensor memory, column half
-  // the last query tokens, which see the most rows, first
-  const int qt = gridDim.x - 1 - blockIdx.x, hk = blockIdx.y, bpos = blockIdx.z;
+  const int qt = blockIdx.x, hk = blockIdx.y, bpos = blockIdx.z;
   const int b = a.order != nullptr ? __ldg(a.order + bpos) : bpos;
   if (static_cast<unsigned>(b) >= static_cast<unsigned>(a.batch)) {
     if (qt == 0 && hk == 0 && tid == 0) set_error(a.err, DSA_DEV_BAD_ORDER);
@@ -239,11 +250,11 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     const uint2* src = reinterpret_cast<const uint2*>(base + p.ph * (16 * kTD)) + lane;
     if (p.need == 0xffffu) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __ldg(src + 32 * i);
+      for (int i = 0; i < 8; ++i) v[i] = ld_stream(src + 32 * i);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i] = (p.need >> (2 * i + (lane >> 4))) & 1u ? __ldg(src + 32 * i) : make_uint2(0u, 0u);
+        v[i] = (p.need >> (2 * i + (lane >> 4))) & 1u ? ld_stream(src + 32 * i) : make_uint2(0u, 0u);
     }
   };
   // The same as fp16 into a block's tile (rows 16 warp .. + 15): 64-dim halves of 128
@@ -307,21 +318,26 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     }
   }
   constexpr uint32_t kIdS = tc_idesc(128, N, false), kIdO = tc_idesc(128, N, true);
+  // Operand descriptors differ by whole multiples of their address unit (16 bytes) from one
+  // step of a product to the next, so a step is an addition.
+  const uint64_t k_desc = tc_desc(sm + Sh::kK, 16, 1024, kSwizzle128);
+  const uint64_t q_desc = tc_desc(sm + Sh::kQ, 16, 1024, kSwizzle128);
+  const uint64_t v_desc = tc_desc(sm + Sh::kV, Sh::kHalf, 1024, kSwizzle128);
+  const uint64_t p_desc =
+      tc_desc(sm + Sh::kP, 16, 8 * Sh::kPRow, N == 64 ? kSwizzle128 : kSwizzle64);
   auto issue_s = [&]() {  // S = K Q^T
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      tc_mma_f16(tmem + Sh::kS,
-                 tc_desc(sm + Sh::kK + (k >> 2) * Sh::kHalf + (k & 3) * 32, 16, 1024, kSwizzle128),
-                 tc_desc(sm + Sh::kQ + (k >> 2) * (N * 128) + (k & 3) * 32, 16, 1024, kSwizzle128),
-                 kIdS, k > 0);
+      tc_mma_f16(tmem + Sh::kS, k_desc + (((k >> 2) * Sh::kHalf + (k & 3) * 32) >> 4),
+                 q_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS, k > 0);
     tc_commit(s_done);
   };
   auto issue_o = [&](bool first, int present) {  // O^T += V^T P, a step for each page
-    for (int k = 0; k < present; ++k)
-      tc_mma_f16(tmem + Sh::kO, tc_desc(sm + Sh::kV + k * 2048, Sh::kHalf, 1024, kSwizzle128),
-                 tc_desc(sm + Sh::kP + k * (16 * Sh::kPRow), 16, 8 * Sh::kPRow,
-                         N == 64 ? kSwizzle128 : kSwizzle64),
-                 kIdO, !first || k > 0);
+#pragma unroll
+    for (int k = 0; k < kTPages; ++k)
+      if (k < present)
+        tc_mma_f16(tmem + Sh::kO, v_desc + (k * 2048 >> 4), p_desc + (k * (16 * Sh::kPRow) >> 4),
+                   kIdO, !first || k > 0);
     tc_commit(o_done);
   };
 
@@ -643,26 +659,22 @@ cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
                     static_cast<size_t>(smem), s, a);
 }
 
-// Columns per CTA, and the CTAs of a call.
-int columns(const QuantChunkLaunch& a) {
-  return (static_cast<int64_t>(a.max_q) << a.group_log2) <= 32 ? 32 : 64;
-}
-
 }  // namespace
 
-// A unit here is never cut along its pages, so this kernel needs as many units as
-// fill the GPU at least in part.
+// Which calls this kernel takes: those whose (request, kv head) is one tile, when there are
+// enough of them to fill half the GPU (a tile is never cut along its pages).  Measured
+// against quant_chunk.cu, which serves the others (us, this kernel / that one, batch x kv
+// heads x group, tokens, rows): 64x32x1, 32, 300: 84 / 114; 128x8x4, 8, 500: 59 / 82;
+// 128x8x4, 16, 300: 74 / 80; 128x8x4, 64, 300: 241 / 193; 64x8x4, 128, 256: 191 / 151;
+// 128x8x4, 512, 512: 1659 / 1299.
 bool quant_chunk_tc_fits(const QuantChunkLaunch& a) {
-  if (a.batch > 65535 || a.hkv > 65535) return false;  // grid axes
-  if (a.split_setting != 0) return a.split_setting == 1;
-  const int per_cta = columns(a) >> a.group_log2;
-  const int64_t units =
-      static_cast<int64_t>((a.max_q + per_cta - 1) / per_cta) * a.hkv * a.batch;
-  return units * 2 >= a.sms;
+  const int64_t columns = static_cast<int64_t>(a.max_q) << a.group_log2;
+  if (columns > 64 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
+  return a.split_setting == 1 || static_cast<int64_t>(a.batch) * a.hkv * 2 >= a.sms;
 }
 
 cudaError_t launch_quant_chunk_tc(const QuantChunkLaunch& a, cudaStream_t s) {
-  const bool few = columns(a) == 32;
+  const bool few = (static_cast<int64_t>(a.max_q) << a.group_log2) <= 32;
   switch (a.group_log2) {
     case 0: return few ? launch_one<32, 0>(a, s) : launch_one<64, 0>(a, s);
     case 1: return few ? launch_one<32, 1>(a, s) : launch_one<64, 1>(a, s);

@@ -13,19 +13,25 @@
 // is rounded to fp16 (2^-12 relative, below the bf16 output's own 2^-9); with fp32 q
 // both q and p_j are split into two fp16 halves (2^-23).
 //
-// What bounds it: HBM.  A row is 2 D bytes for 4 D G flops (<= 8 flops per byte and
-// the 8 columns of an mma cost the same for G = 1 .. 8), so the design keeps bytes in
-// flight: each warp owns a ring of 16-row tiles filled by cp.async (256 bytes of K
-// and V per row at D = 128; 16 warps per SM hold about 190 KB), and nothing but its
-// own copies ever stops a warp.  A tile costs about 200 instructions per warp for its
-// 4 KB, a third of the issue slots the copy rate leaves.
+// What bounds it: HBM, and for short calls the chain of dependent loads at a CTA's start.  A
+// row is 2 D bytes for 4 D G flops (<= 8 flops per byte; the 8 columns of an mma cost the
+// same for G = 1 .. 8), so the design keeps bytes in flight: each warp owns a ring of two
+// 16-row tiles filled by cp.async (4 KB of K and V each at D = 128; 16 warps per SM hold 128
+// KB; a third stage measured 2% slower, more warps with fewer registers 8%), and nothing
+// but its own copies ever stops a warp.  q, the page ids of a kept set's first tiles and the
+// sizes are asked for together.
+// Measured (GB300, back-to-back calls): 128 requests of 33 .. 4608 rows, 32/8 heads, dense 102
+// us = 5.7 TB/s, 0.83 of the copy rate; 8 requests of 8000 rows 32 us (10 us of it start and
+// joining); 2048 units of 290 kept rows 33 us.  The copies alone, without the arithmetic,
+// take 99.5, 30.8 and 29.4 us.
 //
 // Work split.  Dense rows: a persistent grid of one CTA per resident slot takes equal
-// shares of all tiles of the batch, in unit order (a unit is a request and kv head);
-// the shares' borders come from a prefix sum over seq_len that every CTA makes itself.
-// Sparse rows: one CTA per unit, or a few when there are too few units.  A unit cut
-// over several CTAs leaves partial states in the workspace, and the last one to
-// arrive sums them in order.
+// shares of all tiles of the batch, in unit order (a unit is a request and kv head); the
+// shares' borders come from a prefix sum over seq_len that every warp makes itself (handing
+// out the last quarter in small pieces as CTAs get done measured 2-5% slower: a piece's start
+// costs what the balance gains).  Sparse rows: one CTA per unit, or a few when there are
+// too few units.  A unit cut over several CTAs leaves partial states in the workspace, and
+// the last one to arrive sums them in order.
 #include <math.h>
 
 #include "common.cuh"
@@ -40,11 +46,11 @@ namespace {
 
 // Weights are 2^(y - ref).  ref follows the largest y so that it stands for 2^kHead, once
 // a y passes it by kSlack; before the first row it is far below every score, and finite.
-constexpr float kHead = 4.f, kSlack = 10.f, kNoRef = -1e30f;
+constexpr float kHead = 4.f, kSlack = 10.f, kNoRef = -3e38f;
 
 template <int D, int NW>
 struct QuantRing {
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kStages = 2;
   static constexpr int kWarp = kStages * QuantTile<D>::kStage;
   static constexpr int kSmem = NW * kWarp;
   // a warp's end state, 8 heads of [acc(D), m, l], fits the start of its ring
@@ -731,9 +737,12 @@ cudaError_t launch_one(QuantDecodeLaunch a, cudaStream_t s) {
                     static_cast<size_t>(smem), s, a);
 }
 
-// Sparse rows: a unit in a CTA of 2 warps when there is more than one unit for every two
-// SMs' worth of ... slots (a warp's start -- sizes, mask, first pages, about 4 us under load -- is
-// then paid by fewer warps per unit), else of 4.
+// Warps per CTA.  Dense rows: 4 (2 warps leave twice the partial states to join, 8 drain
+// together at every unit's end; mixed batch 102 us against 101 and 106, 64 units of 8000
+// rows 32 us against 40 and 31).  Sparse rows: a unit per CTA, and 2 warps once the units
+// fill half of the resident slots -- a CTA's start (sizes, mask, first pages: 3 us under load)
+// is then paid by half as many warps per unit; 2048 units of 290 rows 33.3 us against 36.5,
+// 640 units of 140 rows 9.1 against 9.9 -- else 4.
 template <int D, int MODE, bool XQ>
 cudaError_t launch_warps(const QuantDecodeLaunch& a, cudaStream_t s) {
   if constexpr (MODE == kModeDense) {
