@@ -540,6 +540,7 @@ cudaError_t launch_cols(const QuantChunkLaunch& a, cudaStream_t s) {
 
 cudaError_t launch_quant_chunk(const QuantChunkLaunch& a, cudaStream_t s) {
   if (a.head_dim == 128 && quant_chunk_tc_fits(a)) return launch_quant_chunk_tc(a, s);
+  if (a.head_dim == 128 && quant_chunk_rows_fits(a)) return launch_quant_chunk_rows(a, s);
   return a.head_dim == 128 ? launch_cols<128>(a, s) : launch_cols<64>(a, s);
 }
 

@@ -1,0 +1,562 @@
+// quant_chunk_rows.cu -- several query tokens per request over the 8-bit paged K/V cache
+// on the 5th-generation tensor cores, for chunks of many (query token, head) rows
+// (head_dim 128).
+//
+// Mathematics as in quant_chunk.cu, with the queries on the lanes of tensor memory: a CTA
+// holds 128 rows (query token, head of the kv head's group) of one (request, kv head) and
+// walks its pages in blocks of 8 (128 cache rows):
+//   S (128 x 128) = Q K^T,   P = weights of S,   O (128 x 128) += P V
+// so a thread owns a query: its running reference and sum are two registers, a page's
+// scales are constants of 16 of its scores, its mask is one shifted word per page, and P
+// goes back to tensor memory (over S, 16 columns read for 8 written) as the left operand
+// of the second product.  The reference follows the row's maximum (taken over the raw
+// scores of a page, then scaled once) when that passes it by 2^10.
+//
+// Two groups of 4 warps: one converts (K and V codes to fp16 in shared memory, 4 pages
+// sides per warp and block, loads a block ahead; one of its threads issues the products),
+// the other weighs.  A block's scores, weights and second product follow each other
+// within a CTA, its conversions run beside them, and two CTAs per SM fill the gaps.
+//
+// What bounds it: see the figures at quant_chunk_rows_fits.
+#include <math.h>
+
+#include "common.cuh"
+#include "host.h"
+#include "internal.h"
+#include "mma.cuh"
+#include "quant.cuh"
+#include "quant_redo.cuh"
+#include "tcgen05.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kRD = 128;            // head_dim
+constexpr int kRRows = 128;         // query rows per CTA, and cache rows per block
+constexpr int kRPages = 8;
+constexpr int kRThreads = 256;
+constexpr int kRHalf = 128 * 128;   // bytes of 64 dims of 128 rows, fp16
+constexpr float kRHead = 4.f, kRSlack = 10.f, kRNoRef = -3e38f;  // as in quant_chunk.cu
+
+struct RowsShape {
+  static constexpr int kQ = 0, kK = 2 * kRHalf, kV = 4 * kRHalf;
+  static constexpr int kInfo = 6 * kRHalf;             // 2 x 8 int4: rows needed, scales
+  static constexpr int kRed = kInfo + 2 * kRPages * 16;  // 8 floats
+  static constexpr int kBar = kRed + 32;               // four barriers, address, flags
+  static constexpr int kMask = kBar + 48;
+  static constexpr int kSlack = 1024;                  // the base is rounded up to 1024
+  static constexpr int kS = 0, kO = 128, kTmem = 256;  // tensor memory: S and P, O
+  static int smem(int words) { return kSlack + kMask + 4 * words; }
+};
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// Read once: past the L1, whose few kilobytes beside the tiles hold page ids and masks.
+__device__ __forceinline__ uint2 ld_stream(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+// Barrier of the 128 converting threads; true when every one of them came with ok.
+__device__ __forceinline__ bool converters_sync(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return all != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+template <int LG>
+__global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const QuantChunkLaunch a) {
+  using Sh = RowsShape;
+  constexpr int per_cta = kRRows >> LG;  // query tokens per CTA
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sm = smem_addr(smem);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the last query tokens, which see the most rows, first
+  const int qt = gridDim.x - 1 - blockIdx.x, hk = blockIdx.y, bpos = blockIdx.z;
+  const int b = a.order != nullptr ? __ldg(a.order + bpos) : bpos;
+  if (static_cast<unsigned>(b) >= static_cast<unsigned>(a.batch)) {
+    if (qt == 0 && hk == 0 && tid == 0) set_error(a.err, DSA_DEV_BAD_ORDER);
+    return;
+  }
+  const int t0 = qt * per_cta;
+  const int L = a.seq_len[b], n = a.q_len[b], P = a.prompt_len[b], Wn = a.window[b];
+  int code = 0;
+  if (L < 1 || L > a.max_pages * kPage) code = DSA_DEV_BAD_SEQ_LEN;
+  else if (n < 0 || n > L || n > a.max_q) code = DSA_DEV_BAD_QLEN;
+  else if (P < 0) code = DSA_DEV_BAD_PROMPT;
+  else if (Wn < 0 || Wn > a.max_window) code = DSA_DEV_BAD_WINDOW;
+  if (code != 0) {
+    // q_len is not trusted: NaN into every slot of the unit
+    if (qt == 0 && hk == 0 && tid == 0) set_error(a.err, code);
+    for (int x = tid; x < kRRows * kRD; x += kRThreads) {
+      const int t = t0 + x / (kRD << LG);
+      if (t >= a.max_q) break;
+      const size_t qh = (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << LG) +
+                        (x / kRD & ((1 << LG) - 1));
+      a.out[qh * kRD + x % kRD] = 0x7fc0;
+      if (a.lse != nullptr && x % kRD == 0) a.lse[qh] = __int_as_float(0x7fc00000);
+    }
+    return;
+  }
+  if (t0 >= n) return;
+  const int t1 = min(t0 + per_cta, n);
+  const int i_first = L - n + t0, i_last = L - n + t1 - 1;
+  // pages scanned: those of the prompt rows [0, pa), then those from the window's start
+  const int pa = (min(P, i_last + 1) + 15) >> 4;
+  const int pb = max(pa, max(i_first - Wn, 0) >> 4), pe = i_last >> 4;
+  const int pages = pa + max(0, pe - pb + 1);
+  const int nblocks = (pages + kRPages - 1) / kRPages;
+  auto page_of = [&](int x) { return x < pa ? x : pb + (x - pa); };
+  // row of q and out of query row r
+  const size_t qh0 = (static_cast<size_t>(b) * a.max_q + t0) * a.hq + (hk << LG);
+  auto qh_of = [&](int r) {
+    return qh0 + static_cast<size_t>(r >> LG) * a.hq + (r & ((1 << LG) - 1));
+  };
+
+  int4* info = reinterpret_cast<int4*>(smem + Sh::kInfo);
+  float* red = reinterpret_cast<float*>(smem + Sh::kRed);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Sh::kBar);  // a block's scales are there
+  uint64_t* s_done = k_full + 1;                                    // scores are there
+  uint64_t* p_full = k_full + 2;                                    // weights are there
+  uint64_t* o_done = k_full + 3;                                    // second product is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 4);
+  volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* redo = failed + 1;
+  uint32_t* msk = reinterpret_cast<uint32_t*>(smem + Sh::kMask);
+
+  // ---- q, mask, barriers, tensor memory
+  const int qrow = tid >> 1, qd0 = (tid & 1) * 64;  // half a row per thread
+  uint4 qv[8];
+  {
+    const bool in = t0 + (qrow >> LG) < t1;
+    const uint4* p = reinterpret_cast<const uint4*>(a.q + qh_of(qrow) * kRD + qd0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) qv[i] = in ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  {
+    // the mask shifted by one: bit o keeps offset o, 0 (the query itself) and 1 .. window
+    const uint32_t* mrow = a.keep_mask + (static_cast<size_t>(b) * a.hkv + hk) * a.mask_words;
+    for (int x = tid; x < a.max_window / 32 + 1; x += kRThreads) {
+      const uint32_t lo = x == 0 ? 0x80000000u : __ldg(mrow + x - 1);
+      const uint32_t hi = x < a.mask_words ? __ldg(mrow + x) : 0u;
+      uint32_t v = (hi << 1) | (lo >> 31);
+      const int live = Wn + 1 - 32 * x;
+      if (live < 32) v = live <= 0 ? 0u : v & ((1u << live) - 1u);
+      msk[x] = v;
+    }
+  }
+  if (warp == 0) tmem_alloc<Sh::kTmem>(tmem_slot);
+  if (tid == 0) {
+    mbar_init(k_full, 4);
+    mbar_init(s_done, 1);
+    mbar_init(p_full, 128);
+    mbar_init(o_done, 1);
+    fence_mbar_init();
+    *failed = 0;
+    *redo = 0;
+  }
+  {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7fff7fffu));
+    }
+    const float v = warp_max(fmaxf(bf16_lo(m), bf16_hi(m)));
+    if (lane == 0) red[warp] = v;
+  }
+  __syncthreads();  // mask, maxima, barriers, tensor-memory address
+  const uint32_t tmem = *tmem_slot;
+  float amax = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) amax = fmaxf(amax, red[i]);
+  const int qe = q_exponent(amax);
+  // scores are taken with the scale's sign in q, so that a page's largest score is its
+  // largest product
+  const float f = fabsf(a.scale_log2) * pow2i(qe);
+  {
+    const float down = a.scale_log2 < 0.f ? -pow2i(-qe) : pow2i(-qe);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = f16x2_rn(bf16_lo(w[k]) * down, bf16_hi(w[k]) * down);
+      sts128(sm + Sh::kQ + (tid & 1) * kRHalf + qrow * 128 + ((i ^ (qrow & 7)) << 4),
+             make_uint4(h[0], h[1], h[2], h[3]));
+    }
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+
+  bool ok = true;
+  if (warp >= 4) {
+    // ================= converters =================
+    const int cw = warp - 4;
+    struct Page {
+      unsigned need;
+      size_t ph;
+      float ks, vs;
+    };
+    const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.max_pages;
+    // Page x of the scan: the rows of it that some query of the CTA keeps, its place in
+    // the pool, its scales.
+    auto open_page = [&](int x) -> Page {
+      Page p{0u, 0, 1.f, 1.f};
+      if (x >= pages) return p;
+      const int j0 = page_of(x) * 16, pg = __ldg(pt + page_of(x));
+      if (j0 + 15 <= i_last && (j0 + 15 < P || j0 >= i_first)) {
+        p.need = 0xffffu;
+      } else {
+        const int j = j0 + (lane & 15);
+        bool need = j <= i_last;
+        if (need && j >= P && j < i_first) {
+          const int lo = i_first - j, hi = min(Wn, i_last - j);
+          need = false;
+          for (int w = lo >> 5; lo <= hi && w <= (hi >> 5); ++w) {
+            uint32_t v = msk[w];
+            if (w == (lo >> 5)) v &= 0xffffffffu << (lo & 31);
+            if (w == (hi >> 5) && (hi & 31) != 31) v &= (2u << (hi & 31)) - 1u;
+            need |= v != 0u;
+          }
+        }
+        p.need = __ballot_sync(0xffffffffu, need) & 0xffffu;
+      }
+      if (p.need != 0u && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
+        set_error(a.err, DSA_DEV_BAD_PAGE);
+        p.need = 0u;
+      }
+      if (p.need != 0u) {
+        p.ph = static_cast<size_t>(pg) * a.hkv + hk;
+        p.ks = __ldg(a.k_scale + p.ph);
+        p.vs = __ldg(a.v_scale + p.ph);
+      }
+      return p;
+    };
+    // This lane's 8 codes of rows 2 i + lane / 16 of a page, piece lane % 16; rows nobody
+    // needs are zeros.
+    auto load_codes = [&](const uint8_t* base, const Page& p, uint2 (&v)[8]) {
+      const uint2* src = reinterpret_cast<const uint2*>(base + p.ph * (16 * kRD)) + lane;
+      if (p.need == 0xffffu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ld_stream(src + 32 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = (p.need >> (2 * i + (lane >> 4))) & 1u ? ld_stream(src + 32 * i)
+                                                        : make_uint2(0u, 0u);
+      }
+    };
+    // The same as fp16 into rows 16 (2 cw + e) .. of a tile: 64-dim halves of 128 rows of
+    // 128 bytes, 16-byte pieces swizzled by the row.
+    uint32_t f16_at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      f16_at[i] = sm + ((lane >> 3) & 1) * kRHalf + (32 * cw + r) * 128 + (((lane & 7) ^ r) << 4);
+    }
+    auto store_f16 = [&](int tile, int e, const uint2 (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sts128(f16_at[i & 3] + tile + e * 2048 + (i >> 2) * 1024,
+               make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2_hi(v[i].x), e4m3x2_f16x2(v[i].y),
+                          e4m3x2_f16x2_hi(v[i].y)));
+    };
+    const uint64_t q_desc = tc_desc(sm + Sh::kQ, 16, 1024, kSwizzle128);
+    const uint64_t k_desc = tc_desc(sm + Sh::kK, 16, 1024, kSwizzle128);
+    const uint64_t v_desc = tc_desc(sm + Sh::kV, kRHalf, 1024, kSwizzle128);
+    const bool issuer = tid == 128;
+
+    uint2 k[2][8], v[2][8];
+    Page pg[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      pg[e] = open_page(2 * cw + e);
+      load_codes(a.k, pg[e], k[e]);
+      load_codes(a.v, pg[e], v[e]);
+    }
+    for (int blk = 0; blk < nblocks; ++blk) {
+      const int present = min(kRPages, pages - blk * kRPages);
+      const bool more = blk + 1 < nblocks;
+      // K of this block (the scores of the last one are done with it), its scales
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (2 * cw + e < present) store_f16(Sh::kK, e, k[e]);
+        if (lane == 0) {
+          const uint32_t ks = __float_as_uint(pg[e].ks), vs = __float_as_uint(pg[e].vs);
+          if (!scale_ok(ks) || !scale_ok(vs)) set_error(a.err, DSA_DEV_BAD_SCALE);
+          info[(blk & 1) * kRPages + 2 * cw + e] =
+              make_int4(static_cast<int>(pg[e].need), static_cast<int>(ks), static_cast<int>(vs), 0);
+        }
+      }
+      if (lane == 0) mbar_arrive(k_full);
+      if (more) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          pg[e] = open_page((blk + 1) * kRPages + 2 * cw + e);
+          load_codes(a.k, pg[e], k[e]);
+        }
+      }
+      fence_proxy_async_smem();
+      ok = converters_sync(ok);
+      if (!ok) break;
+      if (blk > 0) ok = mbar_wait(o_done, (blk - 1) & 1);  // S / P and V are free
+      if (issuer && ok) {
+        tc_fence_after();
+        const uint32_t id = tc_idesc(128, 16 * present, false);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const uint64_t step = ((s >> 2) * kRHalf + (s & 3) * 32) >> 4;
+          tc_mma_f16(tmem + Sh::kS, q_desc + step, k_desc + step, id, s > 0);
+        }
+        tc_commit(s_done);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (2 * cw + e < present) store_f16(Sh::kV, e, v[e]);
+        if (more) load_codes(a.v, pg[e], v[e]);
+      }
+      fence_proxy_async_smem();
+      ok = converters_sync(ok);
+      if (!ok) break;
+      if (issuer) {
+        ok = mbar_wait(p_full, blk & 1);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t id = tc_idesc_b_rows(128, kRD);
+          for (int s = 0; s < present; ++s)
+            tc_mma_f16_ta(tmem + Sh::kO, tmem + Sh::kS + 8 * s, v_desc + (s * 2048 >> 4), id,
+                          blk > 0 || s > 0);
+          tc_commit(o_done);
+        }
+      }
+      ok = mbar_wait(s_done, blk & 1) && ok;  // K is free
+    }
+    if (!ok) *failed = 1;
+  } else {
+    // ================= weighing: one query row per thread =================
+    const int r = tid;
+    const int i = i_first + (r >> LG);
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    float ref = kRNoRef, l = 0.f;
+    for (int blk = 0; blk < nblocks; ++blk) {
+      const int present = min(kRPages, pages - blk * kRPages);
+      ok = mbar_wait(k_full, blk & 1) && mbar_wait(s_done, blk & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const int4* in = info + (blk & 1) * kRPages;
+      // pass 1: the row's largest score; which of a page's rows it keeps (16 bits each)
+      uint32_t keep[kRPages / 2];
+      float top = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < kRPages / 2; ++h) {
+        keep[h] = 0xffffffffu;
+        if (2 * h < present) {
+          uint32_t s[32];
+          tmem_load<32>(t_lane + Sh::kS + 32 * h, s);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int x = blk * kRPages + 2 * h + e, j0 = page_of(x) * 16;
+            if (2 * h + e >= present) {
+              keep[h] &= 0xffffu;
+            } else if (!(j0 + 15 < P && j0 + 15 <= i_first)) {
+              // columns up to the query's own row, and of those prompt rows and kept offsets
+              const int c = i - j0;  // column of the query itself
+              uint32_t on = c < 0 ? 0u : c >= 15 ? 0xffffu : (2u << c) - 1u;
+              if (j0 + 15 >= P) {
+                const int base = c - 15;  // offset of column 15
+                const int w0 = max(base, 0) >> 5, sh = max(base, 0) & 31;
+                const int words = a.max_window / 32 + 1;
+                const uint32_t lo = w0 < words ? msk[w0] : 0u, hi = w0 + 1 < words ? msk[w0 + 1] : 0u;
+                uint32_t win = __funnelshift_r(lo, hi, sh);
+                if (base < 0) win = base <= -32 ? 0u : win << -base;
+                win = __brev(win) >> 16;  // bit of column 15 - k to bit k's place
+                const int np = P - j0;    // prompt rows of the page
+                on &= win | (np <= 0 ? 0u : (1u << min(np, 16)) - 1u);
+              }
+              keep[h] &= e == 0 ? on | 0xffff0000u : (on << 16) | 0xffffu;
+            }
+          }
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t on = (keep[h] >> (16 * e)) & 0xffffu;
+            float m = -INFINITY;
+            if (__all_sync(0xffffffffu, on == 0xffffu)) {
+#pragma unroll
+              for (int q = 0; q < 16; q += 2)
+                m = max3(m, __uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1]));
+            } else {
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                if ((on >> q) & 1u) m = fmaxf(m, __uint_as_float(s[16 * e + q]));
+            }
+            const int4 pgi = in[2 * h + e];
+            const float lv = static_cast<float>(scale_exp(static_cast<uint32_t>(pgi.z)));
+            if (2 * h + e < present)
+              top = fmaxf(top, fmaf(m, f * __uint_as_float(static_cast<uint32_t>(pgi.y)), lv));
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, top > ref + (kRHead + kRSlack))) {
+        const float to = top > ref + (kRHead + kRSlack) ? top - kRHead : ref;
+        const float down = ex2_approx(ref - to);
+        ref = to;
+        l *= down;
+        if (blk > 0) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t o[32];
+            tmem_load<32>(t_lane + Sh::kO + 32 * h, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * down);
+            tmem_store16(t_lane + Sh::kO + 32 * h, o);
+            tmem_store16(t_lane + Sh::kO + 32 * h + 16, o + 16);
+          }
+        }
+      }
+      // pass 2: weights, packed over the scores already read
+#pragma unroll
+      for (int h = 0; h < kRPages / 2; ++h) {
+        if (2 * h < present) {
+          uint32_t s[32], w[16];
+          tmem_load<32>(t_lane + Sh::kS + 32 * h, s);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int4 pgi = in[2 * h + e];
+            const uint32_t vs = static_cast<uint32_t>(pgi.z);
+            const float c1 = f * __uint_as_float(static_cast<uint32_t>(pgi.y));
+            const float c2 = static_cast<float>(scale_exp(vs)) - ref;
+            const f32x2 a1 = pack2(c1, c1), a2 = pack2(c2, c2);
+            const uint32_t on = (keep[h] >> (16 * e)) & 0xffffu;
+            float z[16];
+#pragma unroll
+            for (int q = 0; q < 16; q += 2)
+              unpack2(fma2(pack2(__uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1])),
+                           a1, a2),
+                      z[q], z[q + 1]);
+            if (!__all_sync(0xffffffffu, on == 0xffffu)) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) z[q] = (on >> q) & 1u ? z[q] : -INFINITY;
+            }
+            f32x2 sum = pack2(0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < 16; q += 2) {
+              z[q] = ex2_approx(z[q]);
+              z[q + 1] = ex2_approx(z[q + 1]);
+              sum = add2(sum, pack2(z[q], z[q + 1]));
+              w[8 * e + q / 2] = f16x2_rn(z[q], z[q + 1]);
+            }
+            float u, t;
+            unpack2(sum, u, t);
+            if (2 * h + e < present) l = fmaf(u + t, __uint_as_float((254u << 23) - vs), l);
+          }
+          tmem_store16(t_lane + Sh::kS + 16 * h, w);
+        }
+      }
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_full);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_done, (nblocks - 1) & 1));
+    if (!ok) *failed = 1;
+    if (ok) {
+      tc_fence_after();
+      const float inv = 1.f / l;
+      const bool in = t0 + (r >> LG) < t1;
+      const size_t qh = qh_of(r);
+      if (a.lse != nullptr && in) a.lse[qh] = (ref + log2f(l)) * kLn2;
+      float probe = 0.f;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t o[32];
+        tmem_load<32>(t_lane + Sh::kO + 32 * h, o);
+        tc_wait_ld();
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const float u = __uint_as_float(o[2 * q]) * inv, t = __uint_as_float(o[2 * q + 1]) * inv;
+          probe += u + t;
+          w[q] = bf16x2_rn(u, t);
+        }
+        if (in) {
+          uint4* to = reinterpret_cast<uint4*>(a.out + qh * kRD + 32 * h);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            to[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        }
+      }
+      // a NaN may come from a row of V that other queries of the CTA keep (weight 0 times
+      // NaN): the CTA's queries are done again below, from the rows each one keeps
+      if (in && probe != probe) *redo = 1;
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (*failed != 0) {
+    // give products in flight a bounded time to finish before the memory goes back
+    if (tid == 0) set_error(a.err, DSA_DEV_TIMEOUT);
+    mbar_wait(s_done, (nblocks - 1) & 1);
+    mbar_wait(o_done, (nblocks - 1) & 1);
+    __syncthreads();
+  }
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc<Sh::kTmem>(tmem);
+  }
+  if (*failed == 0 && *redo != 0)
+    for (int r = warp; r < kRRows; r += kRThreads / 32)
+      if (t0 + (r >> LG) < t1)
+        quant_redo_query<kRD>(a, b, hk, i_first + (r >> LG), P, Wn, qh_of(r), lane);
+}
+
+template <int LG>
+cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
+  auto kern = quant_chunk_rows_kernel<LG>;
+  const int smem = RowsShape::smem(a.max_window / 32 + 1);
+  static KernelSlots cache;
+  int per_sm = 0;
+  const cudaError_t e =
+      cache.get(reinterpret_cast<const void*>(kern), kRThreads, smem, &per_sm);
+  if (e != cudaSuccess) return e;
+  constexpr int per_cta = kRRows >> LG;
+  return launch_pdl(kern, dim3((a.max_q + per_cta - 1) / per_cta, a.hkv, a.batch), dim3(kRThreads),
+                    static_cast<size_t>(smem), s, a);
+}
+
+}  // namespace
+
+bool quant_chunk_rows_fits(const QuantChunkLaunch& a) {
+  const int64_t rows = static_cast<int64_t>(a.max_q) << a.group_log2;
+  if (rows <= 64 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
+  return a.split_setting == 1 ||
+         (rows + kRRows - 1) / kRRows * a.batch * a.hkv * 2 >= a.sms;
+}
+
+cudaError_t launch_quant_chunk_rows(const QuantChunkLaunch& a, cudaStream_t s) {
+  switch (a.group_log2) {
+    case 0: return launch_one<0>(a, s);
+    case 1: return launch_one<1>(a, s);
+    case 2: return launch_one<2>(a, s);
+    default: return launch_one<3>(a, s);
+  }
+}
+
+}  // namespace dsa
