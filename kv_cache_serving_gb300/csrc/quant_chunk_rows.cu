@@ -12,13 +12,17 @@
 // of the second product.  The reference follows the row's maximum (taken over the raw
 // scores of a page, then scaled once) when that passes it by 2^10.
 //
-// Two groups of 4 warps: one converts (K and V codes to fp16 in shared memory, 4 pages
-// sides per warp and block, loads a block ahead; one of its threads issues the products),
-// the other weighs.  A block's scores, weights and second product follow each other
-// within a CTA, its conversions run beside them, and two CTAs per SM fill the gaps.
+// Two groups of 4 warps: one converts (K and V codes to fp16 in shared memory, four page
+// sides per warp and block, loads a block ahead), the other weighs, and one thread of it
+// issues the products (as a converter it would wait for the weights with the next block's
+// K unconverted: 175 -> XXX us on 128 tokens over 4096 rows).  A block's scores, weights and
+// second product follow each other within a CTA, its conversions run beside them, and two
+// CTAs per SM fill the gaps.
 //
 // What bounds it: see the figures at quant_chunk_rows_fits.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "host.h"
@@ -40,10 +44,10 @@ constexpr float kRHead = 4.f, kRSlack = 10.f, kRNoRef = -3e38f;  // as in quant_
 
 struct RowsShape {
   static constexpr int kQ = 0, kK = 2 * kRHalf, kV = 4 * kRHalf;
-  static constexpr int kInfo = 6 * kRHalf;             // 2 x 8 int4: rows needed, scales
+  static constexpr int kInfo = 6 * kRHalf;             // 2 x 8 float4 of a page: see below
   static constexpr int kRed = kInfo + 2 * kRPages * 16;  // 8 floats
-  static constexpr int kBar = kRed + 32;               // four barriers, address, flags
-  static constexpr int kMask = kBar + 48;
+  static constexpr int kBar = kRed + 32;               // five barriers, address, flags
+  static constexpr int kMask = kBar + 64;
   static constexpr int kSlack = 1024;                  // the base is rounded up to 1024
   static constexpr int kS = 0, kO = 128, kTmem = 256;  // tensor memory: S and P, O
   static int smem(int words) { return kSlack + kMask + 4 * words; }
@@ -60,8 +64,8 @@ __device__ __forceinline__ uint2 ld_stream(const uint2* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
-// Barrier of the 128 converting threads; true when every one of them came with ok.
-__device__ __forceinline__ bool converters_sync(bool ok) {
+// Barrier of the 128 weighing threads; true when every one of them came with ok.
+__device__ __forceinline__ bool group_sync(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
@@ -125,18 +129,103 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     return qh0 + static_cast<size_t>(r >> LG) * a.hq + (r & ((1 << LG) - 1));
   };
 
-  int4* info = reinterpret_cast<int4*>(smem + Sh::kInfo);
+  float4* info = reinterpret_cast<float4*>(smem + Sh::kInfo);
   float* red = reinterpret_cast<float*>(smem + Sh::kRed);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Sh::kBar);  // a block's scales are there
-  uint64_t* s_done = k_full + 1;                                    // scores are there
-  uint64_t* p_full = k_full + 2;                                    // weights are there
-  uint64_t* o_done = k_full + 3;                                    // second product is done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 4);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Sh::kBar);  // K and scales of a block
+  uint64_t* v_full = k_full + 1;                                    // its V
+  uint64_t* s_done = k_full + 2;                                    // its scores
+  uint64_t* o_done = k_full + 3;                                    // its second product
+  // k_full as the issuing thread passes it on to its group: its next phase waits for the
+  // group, so that no thread can miss one (k_full's next phase waits for s_done alone)
+  uint64_t* i_full = k_full + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 5);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* redo = failed + 1;
   uint32_t* msk = reinterpret_cast<uint32_t*>(smem + Sh::kMask);
 
-  // ---- q, mask, barriers, tensor memory
+  const int cw = warp & 3;  // of the converting warps
+  struct Page {
+    unsigned need;
+    size_t ph;
+    float ks, vs;
+  };
+  const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.max_pages;
+  // Page x of the scan: the rows of it that some query of the CTA keeps, its place in
+  // the pool, its scales.
+  auto open_page = [&](int x) -> Page {
+    Page p{0u, 0, 1.f, 1.f};
+    if (x >= pages) return p;
+    const int j0 = page_of(x) * 16, pg = __ldg(pt + page_of(x));
+    if (j0 + 15 <= i_last && (j0 + 15 < P || j0 >= i_first)) {
+      p.need = 0xffffu;
+    } else {
+      const int j = j0 + (lane & 15);
+      bool need = j <= i_last;
+      if (need && j >= P && j < i_first) {
+        // kept by some query: a set bit among offsets lo + 1 .. hi + 1
+        const uint32_t* mrow = a.keep_mask + (static_cast<size_t>(b) * a.hkv + hk) * a.mask_words;
+        const int lo = i_first - j - 1, hi = min(Wn, i_last - j) - 1;
+        need = false;
+        for (int w = lo >> 5; lo <= hi && w <= (hi >> 5); ++w) {
+          uint32_t v = __ldg(mrow + w);
+          if (w == (lo >> 5)) v &= 0xffffffffu << (lo & 31);
+          if (w == (hi >> 5) && (hi & 31) != 31) v &= (2u << (hi & 31)) - 1u;
+          need |= v != 0u;
+        }
+      }
+      p.need = __ballot_sync(0xffffffffu, need) & 0xffffu;
+    }
+    if (p.need != 0u && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
+      set_error(a.err, DSA_DEV_BAD_PAGE);
+      p.need = 0u;
+    }
+    if (p.need != 0u) {
+      p.ph = static_cast<size_t>(pg) * a.hkv + hk;
+      p.ks = __ldg(a.k_scale + p.ph);
+      p.vs = __ldg(a.v_scale + p.ph);
+    }
+    return p;
+  };
+  // This lane's 8 codes of rows 2 i + lane / 16 of a page, piece lane % 16; rows nobody
+  // needs are zeros.
+  auto load_codes = [&](const uint8_t* base, const Page& p, uint2 (&v)[8]) {
+    const uint2* src = reinterpret_cast<const uint2*>(base + p.ph * (16 * kRD)) + lane;
+    if (p.need == 0xffffu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = ld_stream(src + 32 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = (p.need >> (2 * i + (lane >> 4))) & 1u ? ld_stream(src + 32 * i)
+                                                      : make_uint2(0u, 0u);
+    }
+  };
+  // The same as fp16 into rows 16 (2 cw + e) .. of a tile: 64-dim halves of 128 rows of
+  // 128 bytes, 16-byte pieces swizzled by the row.
+  uint32_t f16_at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 2 * i + (lane >> 4);
+    f16_at[i] = sm + ((lane >> 3) & 1) * kRHalf + (32 * cw + r) * 128 + (((lane & 7) ^ r) << 4);
+  }
+  auto store_f16 = [&](int tile, int e, const uint2 (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      sts128(f16_at[i & 3] + tile + e * 2048 + (i >> 2) * 1024,
+             make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2_hi(v[i].x), e4m3x2_f16x2(v[i].y),
+                        e4m3x2_f16x2_hi(v[i].y)));
+  };
+  // ---- first block's codes on their way; q, mask, barriers, tensor memory
+  uint2 k[2][8], v[2][8];
+  Page pg[2];
+  if (warp >= 4) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      pg[e] = open_page(2 * cw + e);
+      load_codes(a.k, pg[e], k[e]);
+      load_codes(a.v, pg[e], v[e]);
+    }
+  }
   const int qrow = tid >> 1, qd0 = (tid & 1) * 64;  // half a row per thread
   uint4 qv[8];
   {
@@ -160,9 +249,10 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   if (warp == 0) tmem_alloc<Sh::kTmem>(tmem_slot);
   if (tid == 0) {
     mbar_init(k_full, 4);
+    mbar_init(v_full, 4);
     mbar_init(s_done, 1);
-    mbar_init(p_full, 128);
     mbar_init(o_done, 1);
+    mbar_init(i_full, 1);
     fence_mbar_init();
     *failed = 0;
     *redo = 0;
@@ -206,93 +296,12 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   bool ok = true;
   if (warp >= 4) {
     // ================= converters =================
-    const int cw = warp - 4;
-    struct Page {
-      unsigned need;
-      size_t ph;
-      float ks, vs;
-    };
-    const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.max_pages;
-    // Page x of the scan: the rows of it that some query of the CTA keeps, its place in
-    // the pool, its scales.
-    auto open_page = [&](int x) -> Page {
-      Page p{0u, 0, 1.f, 1.f};
-      if (x >= pages) return p;
-      const int j0 = page_of(x) * 16, pg = __ldg(pt + page_of(x));
-      if (j0 + 15 <= i_last && (j0 + 15 < P || j0 >= i_first)) {
-        p.need = 0xffffu;
-      } else {
-        const int j = j0 + (lane & 15);
-        bool need = j <= i_last;
-        if (need && j >= P && j < i_first) {
-          const int lo = i_first - j, hi = min(Wn, i_last - j);
-          need = false;
-          for (int w = lo >> 5; lo <= hi && w <= (hi >> 5); ++w) {
-            uint32_t v = msk[w];
-            if (w == (lo >> 5)) v &= 0xffffffffu << (lo & 31);
-            if (w == (hi >> 5) && (hi & 31) != 31) v &= (2u << (hi & 31)) - 1u;
-            need |= v != 0u;
-          }
-        }
-        p.need = __ballot_sync(0xffffffffu, need) & 0xffffu;
-      }
-      if (p.need != 0u && static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
-        set_error(a.err, DSA_DEV_BAD_PAGE);
-        p.need = 0u;
-      }
-      if (p.need != 0u) {
-        p.ph = static_cast<size_t>(pg) * a.hkv + hk;
-        p.ks = __ldg(a.k_scale + p.ph);
-        p.vs = __ldg(a.v_scale + p.ph);
-      }
-      return p;
-    };
-    // This lane's 8 codes of rows 2 i + lane / 16 of a page, piece lane % 16; rows nobody
-    // needs are zeros.
-    auto load_codes = [&](const uint8_t* base, const Page& p, uint2 (&v)[8]) {
-      const uint2* src = reinterpret_cast<const uint2*>(base + p.ph * (16 * kRD)) + lane;
-      if (p.need == 0xffffu) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = ld_stream(src + 32 * i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = (p.need >> (2 * i + (lane >> 4))) & 1u ? ld_stream(src + 32 * i)
-                                                        : make_uint2(0u, 0u);
-      }
-    };
-    // The same as fp16 into rows 16 (2 cw + e) .. of a tile: 64-dim halves of 128 rows of
-    // 128 bytes, 16-byte pieces swizzled by the row.
-    uint32_t f16_at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 2 * i + (lane >> 4);
-      f16_at[i] = sm + ((lane >> 3) & 1) * kRHalf + (32 * cw + r) * 128 + (((lane & 7) ^ r) << 4);
-    }
-    auto store_f16 = [&](int tile, int e, const uint2 (&v)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        sts128(f16_at[i & 3] + tile + e * 2048 + (i >> 2) * 1024,
-               make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2_hi(v[i].x), e4m3x2_f16x2(v[i].y),
-                          e4m3x2_f16x2_hi(v[i].y)));
-    };
-    const uint64_t q_desc = tc_desc(sm + Sh::kQ, 16, 1024, kSwizzle128);
-    const uint64_t k_desc = tc_desc(sm + Sh::kK, 16, 1024, kSwizzle128);
-    const uint64_t v_desc = tc_desc(sm + Sh::kV, kRHalf, 1024, kSwizzle128);
-    const bool issuer = tid == 128;
-
-    uint2 k[2][8], v[2][8];
-    Page pg[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      pg[e] = open_page(2 * cw + e);
-      load_codes(a.k, pg[e], k[e]);
-      load_codes(a.v, pg[e], v[e]);
-    }
     for (int blk = 0; blk < nblocks; ++blk) {
       const int present = min(kRPages, pages - blk * kRPages);
       const bool more = blk + 1 < nblocks;
-      // K of this block (the scores of the last one are done with it), its scales
+      // K of this block (the last one's scores are done with it), and its scales as the
+      // weighing group uses them
+      if (blk > 0) ok = mbar_wait(s_done, (blk - 1) & 1) && ok;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (2 * cw + e < present) store_f16(Sh::kK, e, k[e]);
@@ -300,9 +309,12 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           const uint32_t ks = __float_as_uint(pg[e].ks), vs = __float_as_uint(pg[e].vs);
           if (!scale_ok(ks) || !scale_ok(vs)) set_error(a.err, DSA_DEV_BAD_SCALE);
           info[(blk & 1) * kRPages + 2 * cw + e] =
-              make_int4(static_cast<int>(pg[e].need), static_cast<int>(ks), static_cast<int>(vs), 0);
+              make_float4(f * pg[e].ks, static_cast<float>(scale_exp(vs)),
+                          __uint_as_float((254u << 23) - vs), 0.f);
         }
       }
+      fence_proxy_async_smem();
+      __syncwarp();
       if (lane == 0) mbar_arrive(k_full);
       if (more) {
 #pragma unroll
@@ -311,40 +323,16 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           load_codes(a.k, pg[e], k[e]);
         }
       }
-      fence_proxy_async_smem();
-      ok = converters_sync(ok);
-      if (!ok) break;
-      if (blk > 0) ok = mbar_wait(o_done, (blk - 1) & 1);  // S / P and V are free
-      if (issuer && ok) {
-        tc_fence_after();
-        const uint32_t id = tc_idesc(128, 16 * present, false);
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const uint64_t step = ((s >> 2) * kRHalf + (s & 3) * 32) >> 4;
-          tc_mma_f16(tmem + Sh::kS, q_desc + step, k_desc + step, id, s > 0);
-        }
-        tc_commit(s_done);
-      }
+      if (blk > 0) ok = mbar_wait(o_done, (blk - 1) & 1) && ok;  // V is free
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (2 * cw + e < present) store_f16(Sh::kV, e, v[e]);
         if (more) load_codes(a.v, pg[e], v[e]);
       }
       fence_proxy_async_smem();
-      ok = converters_sync(ok);
-      if (!ok) break;
-      if (issuer) {
-        ok = mbar_wait(p_full, blk & 1);
-        if (ok) {
-          tc_fence_after();
-          const uint32_t id = tc_idesc_b_rows(128, kRD);
-          for (int s = 0; s < present; ++s)
-            tc_mma_f16_ta(tmem + Sh::kO, tmem + Sh::kS + 8 * s, v_desc + (s * 2048 >> 4), id,
-                          blk > 0 || s > 0);
-          tc_commit(o_done);
-        }
-      }
-      ok = mbar_wait(s_done, blk & 1) && ok;  // K is free
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_full);
+      if (!__all_sync(0xffffffffu, ok)) break;
     }
     if (!ok) *failed = 1;
   } else {
@@ -352,64 +340,91 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     const int r = tid;
     const int i = i_first + (r >> LG);
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-    float ref = kRNoRef, l = 0.f;
-    for (int blk = 0; blk < nblocks; ++blk) {
+    const uint64_t q_desc = tc_desc(sm + Sh::kQ, 16, 1024, kSwizzle128);
+    const uint64_t k_desc = tc_desc(sm + Sh::kK, 16, 1024, kSwizzle128);
+    const uint64_t v_desc = tc_desc(sm + Sh::kV, kRHalf, 1024, kSwizzle128);
+    auto issue_s = [&](int blk) {  // S = Q K^T over the block's pages
+      const uint32_t id = tc_idesc(128, 16 * min(kRPages, pages - blk * kRPages), false);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const uint64_t step = ((s >> 2) * kRHalf + (s & 3) * 32) >> 4;
+        tc_mma_f16(tmem + Sh::kS, q_desc + step, k_desc + step, id, s > 0);
+      }
+      tc_commit(s_done);
+    };
+    auto issue_o = [&](int blk) {  // O += P V, a step for each page
+      constexpr uint32_t id = tc_idesc_b_rows(128, kRD);
       const int present = min(kRPages, pages - blk * kRPages);
-      ok = mbar_wait(k_full, blk & 1) && mbar_wait(s_done, blk & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+#pragma unroll
+      for (int s = 0; s < kRPages; ++s)
+        if (s < present)
+          tc_mma_f16_ta(tmem + Sh::kO, tmem + Sh::kS + 8 * s, v_desc + (s * 2048 >> 4), id,
+                        blk > 0 || s > 0);
+      tc_commit(o_done);
+    };
+    if (tid == 0) {
+      ok = mbar_wait(k_full, 0);
       tc_fence_after();
-      const int4* in = info + (blk & 1) * kRPages;
-      // pass 1: the row's largest score; which of a page's rows it keeps (16 bits each)
+      if (ok) {
+        mbar_arrive(i_full);
+        issue_s(0);
+      }
+    }
+    __syncwarp();
+    float ref = kRNoRef, l = 0.f;
+    // The weights of a block; MASKED: some query of the CTA does not keep some row of it.
+    auto weigh = [&](auto masked, int blk, int present) {
+      constexpr bool kMasked = decltype(masked)::value;
+      const float4* in = info + (blk & 1) * kRPages;
+      // which of a page's rows this query keeps: 16 bits each
       uint32_t keep[kRPages / 2];
+      if constexpr (kMasked) {
+        const int words = a.max_window / 32 + 1;
+#pragma unroll
+        for (int x = 0; x < kRPages; ++x) {
+          uint32_t on = 0u;
+          if (x < present) {
+            const int j0 = page_of(blk * kRPages + x) * 16;
+            // columns up to the query's own row, and of those prompt rows and kept offsets
+            const int c = i - j0;  // column of the query itself
+            on = c < 0 ? 0u : c >= 15 ? 0xffffu : (2u << c) - 1u;
+            if (j0 + 15 >= P) {
+              const int base = c - 15;  // offset of column 15
+              const int w0 = max(base, 0) >> 5, sh = max(base, 0) & 31;
+              const uint32_t lo = w0 < words ? msk[w0] : 0u, hi = w0 + 1 < words ? msk[w0 + 1] : 0u;
+              uint32_t win = __funnelshift_r(lo, hi, sh);
+              if (base < 0) win = base <= -32 ? 0u : win << -base;
+              win = __brev(win) >> 16;  // the bit of column 15 - k to bit 15 - k
+              const int np = P - j0;    // prompt rows of the page
+              on &= win | (np <= 0 ? 0u : (1u << min(np, 16)) - 1u);
+            }
+          }
+          if (x & 1) keep[x / 2] |= on << 16;
+          else keep[x / 2] = on;
+        }
+      }
+      // pass 1: the row's largest score
       float top = -INFINITY;
 #pragma unroll
       for (int h = 0; h < kRPages / 2; ++h) {
-        keep[h] = 0xffffffffu;
         if (2 * h < present) {
           uint32_t s[32];
           tmem_load<32>(t_lane + Sh::kS + 32 * h, s);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int x = blk * kRPages + 2 * h + e, j0 = page_of(x) * 16;
-            if (2 * h + e >= present) {
-              keep[h] &= 0xffffu;
-            } else if (!(j0 + 15 < P && j0 + 15 <= i_first)) {
-              // columns up to the query's own row, and of those prompt rows and kept offsets
-              const int c = i - j0;  // column of the query itself
-              uint32_t on = c < 0 ? 0u : c >= 15 ? 0xffffu : (2u << c) - 1u;
-              if (j0 + 15 >= P) {
-                const int base = c - 15;  // offset of column 15
-                const int w0 = max(base, 0) >> 5, sh = max(base, 0) & 31;
-                const int words = a.max_window / 32 + 1;
-                const uint32_t lo = w0 < words ? msk[w0] : 0u, hi = w0 + 1 < words ? msk[w0 + 1] : 0u;
-                uint32_t win = __funnelshift_r(lo, hi, sh);
-                if (base < 0) win = base <= -32 ? 0u : win << -base;
-                win = __brev(win) >> 16;  // bit of column 15 - k to bit k's place
-                const int np = P - j0;    // prompt rows of the page
-                on &= win | (np <= 0 ? 0u : (1u << min(np, 16)) - 1u);
-              }
-              keep[h] &= e == 0 ? on | 0xffff0000u : (on << 16) | 0xffffu;
-            }
-          }
           tc_wait_ld();
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t on = (keep[h] >> (16 * e)) & 0xffffu;
-            float m = -INFINITY;
-            if (__all_sync(0xffffffffu, on == 0xffffu)) {
-#pragma unroll
-              for (int q = 0; q < 16; q += 2)
-                m = max3(m, __uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1]));
-            } else {
+            if (kMasked) {
 #pragma unroll
               for (int q = 0; q < 16; ++q)
-                if ((on >> q) & 1u) m = fmaxf(m, __uint_as_float(s[16 * e + q]));
+                if (!((keep[h] >> (16 * e + q)) & 1u)) s[16 * e + q] = 0xff800000u;  // -inf
             }
-            const int4 pgi = in[2 * h + e];
-            const float lv = static_cast<float>(scale_exp(static_cast<uint32_t>(pgi.z)));
-            if (2 * h + e < present)
-              top = fmaxf(top, fmaf(m, f * __uint_as_float(static_cast<uint32_t>(pgi.y)), lv));
+            float m = __uint_as_float(s[16 * e]);
+#pragma unroll
+            for (int q = 1; q < 15; q += 2)
+              m = max3(m, __uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1]));
+            m = fmaxf(m, __uint_as_float(s[16 * e + 15]));
+            const float2 pgi = *reinterpret_cast<const float2*>(in + 2 * h + e);
+            if (2 * h + e < present) top = fmaxf(top, fmaf(m, pgi.x, pgi.y));
           }
         }
       }
@@ -440,42 +455,64 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           tc_wait_ld();
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int4 pgi = in[2 * h + e];
-            const uint32_t vs = static_cast<uint32_t>(pgi.z);
-            const float c1 = f * __uint_as_float(static_cast<uint32_t>(pgi.y));
-            const float c2 = static_cast<float>(scale_exp(vs)) - ref;
-            const f32x2 a1 = pack2(c1, c1), a2 = pack2(c2, c2);
-            const uint32_t on = (keep[h] >> (16 * e)) & 0xffffu;
-            float z[16];
-#pragma unroll
-            for (int q = 0; q < 16; q += 2)
-              unpack2(fma2(pack2(__uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1])),
-                           a1, a2),
-                      z[q], z[q + 1]);
-            if (!__all_sync(0xffffffffu, on == 0xffffu)) {
-#pragma unroll
-              for (int q = 0; q < 16; ++q) z[q] = (on >> q) & 1u ? z[q] : -INFINITY;
-            }
+            const float4 pgi = in[2 * h + e];
+            const float c2 = pgi.y - ref;
+            const f32x2 a1 = pack2(pgi.x, pgi.x), a2 = pack2(c2, c2);
             f32x2 sum = pack2(0.f, 0.f);
 #pragma unroll
             for (int q = 0; q < 16; q += 2) {
-              z[q] = ex2_approx(z[q]);
-              z[q + 1] = ex2_approx(z[q + 1]);
-              sum = add2(sum, pack2(z[q], z[q + 1]));
-              w[8 * e + q / 2] = f16x2_rn(z[q], z[q + 1]);
+              float z0, z1;
+              unpack2(fma2(pack2(__uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1])),
+                           a1, a2),
+                      z0, z1);
+              if (kMasked) {
+                z0 = (keep[h] >> (16 * e + q)) & 1u ? z0 : -INFINITY;
+                z1 = (keep[h] >> (16 * e + q + 1)) & 1u ? z1 : -INFINITY;
+              }
+              z0 = ex2_approx(z0);
+              z1 = ex2_approx(z1);
+              sum = add2(sum, pack2(z0, z1));
+              w[8 * e + q / 2] = f16x2_rn(z0, z1);
             }
             float u, t;
             unpack2(sum, u, t);
-            if (2 * h + e < present) l = fmaf(u + t, __uint_as_float((254u << 23) - vs), l);
+            if (2 * h + e < present) l = fmaf(u + t, pgi.z, l);
           }
           tmem_store16(t_lane + Sh::kS + 16 * h, w);
         }
       }
+    };
+    for (int blk = 0; blk < nblocks; ++blk) {
+      const int present = min(kRPages, pages - blk * kRPages);
+      ok = mbar_wait(i_full, blk & 1) && mbar_wait(s_done, blk & 1) && ok;
+      __syncwarp();
+      tc_fence_after();
+      const int j_last = page_of(blk * kRPages + present - 1) * 16 + 15;
+      if (j_last < P && j_last <= i_first) weigh(std::false_type{}, blk, present);
+      else weigh(std::true_type{}, blk, present);
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(p_full);
+      ok = group_sync(ok);
+      if (!ok) break;
+      if (warp == 0) {
+        if (lane == 0) {
+          ok = mbar_wait(v_full, blk & 1);
+          tc_fence_after();
+          if (ok) issue_o(blk);
+          if (blk + 1 < nblocks) {  // P lies over S: the next scores wait for this product
+            ok = mbar_wait(o_done, blk & 1) && mbar_wait(k_full, (blk + 1) & 1) && ok;
+            tc_fence_after();
+            if (ok) {
+              mbar_arrive(i_full);
+              issue_s(blk + 1);
+            }
+          }
+        }
+        __syncwarp();
+      }
     }
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_done, (nblocks - 1) & 1));
+    if (ok) ok = mbar_wait(o_done, (nblocks - 1) & 1);
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) *failed = 1;
     if (ok) {
       tc_fence_after();
@@ -496,12 +533,12 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           probe += u + t;
           w[q] = bf16x2_rn(u, t);
         }
-        if (in) {
-          uint4* to = reinterpret_cast<uint4*>(a.out + qh * kRD + 32 * h);
+        // by way of q's place in shared memory (its products are done): pieces of 16 bytes,
+        // swizzled by the row
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            to[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-        }
+        for (int q = 0; q < 4; ++q)
+          sts128(sm + Sh::kQ + r * 256 + (((4 * h + q) ^ (r & 15)) << 4),
+                 make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
       }
       // a NaN may come from a row of V that other queries of the CTA keep (weight 0 times
       // NaN): the CTA's queries are done again below, from the rows each one keeps
@@ -510,6 +547,16 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     }
   }
   __syncthreads();
+  if (*failed == 0) {
+    // whole rows out: 16 lanes a row
+#pragma unroll
+    for (int q = 0; q < kRRows / 16; ++q) {
+      const int r = 16 * q + (tid >> 4), ch = tid & 15;
+      if (t0 + (r >> LG) < t1)
+        *reinterpret_cast<uint4*>(a.out + qh_of(r) * kRD + 8 * ch) =
+            *reinterpret_cast<const uint4*>(smem + Sh::kQ + r * 256 + ((ch ^ (r & 15)) << 4));
+    }
+  }
   if (*failed != 0) {
     // give products in flight a bounded time to finish before the memory goes back
     if (tid == 0) set_error(a.err, DSA_DEV_TIMEOUT);
@@ -521,10 +568,12 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     tc_fence_after();
     tmem_dealloc<Sh::kTmem>(tmem);
   }
-  if (*failed == 0 && *redo != 0)
+  if (*failed == 0 && *redo != 0) {
+    __syncthreads();  // after every row's first output
     for (int r = warp; r < kRRows; r += kRThreads / 32)
       if (t0 + (r >> LG) < t1)
         quant_redo_query<kRD>(a, b, hk, i_first + (r >> LG), P, Wn, qh_of(r), lane);
+  }
 }
 
 template <int LG>
