@@ -15,7 +15,8 @@
 // Two groups of 4 warps: one converts (K and V codes to fp16 in shared memory, four page
 // sides per warp and block, loads a block ahead), the other weighs, and one thread of it
 // issues the products (as a converter it would wait for the weights with the next block's
-// K unconverted: 175 -> XXX us on 128 tokens over 4096 rows).  A block's scores, weights and
+// K unconverted: 128 tokens over 4096 rows of 8 requests,
+// 32/8 heads, take 108 us instead of 175).  A block's scores, weights and
 // second product follow each other within a CTA, its conversions run beside them, and two
 // CTAs per SM fill the gaps.
 //
@@ -45,8 +46,8 @@ constexpr float kRHead = 4.f, kRSlack = 10.f, kRNoRef = -3e38f;  // as in quant_
 struct RowsShape {
   static constexpr int kQ = 0, kK = 2 * kRHalf, kV = 4 * kRHalf;
   static constexpr int kInfo = 6 * kRHalf;             // 2 x 8 float4 of a page: see below
-  static constexpr int kRed = kInfo + 2 * kRPages * 16;  // 8 floats
-  static constexpr int kBar = kRed + 32;               // five barriers, address, flags
+  static constexpr int kUp = kInfo + 2 * kRPages * 16;   // score factor of a row: 128 floats
+  static constexpr int kBar = kUp + 4 * kRRows;              // five barriers, address, flags
   static constexpr int kMask = kBar + 64;
   static constexpr int kSlack = 1024;                  // the base is rounded up to 1024
   static constexpr int kS = 0, kO = 128, kTmem = 256;  // tensor memory: S and P, O
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   };
 
   float4* info = reinterpret_cast<float4*>(smem + Sh::kInfo);
-  float* red = reinterpret_cast<float*>(smem + Sh::kRed);
+  float* up = reinterpret_cast<float*>(smem + Sh::kUp);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Sh::kBar);  // K and scales of a block
   uint64_t* v_full = k_full + 1;                                    // its V
   uint64_t* s_done = k_full + 2;                                    // its scores
@@ -257,6 +258,9 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     *failed = 0;
     *redo = 0;
   }
+  // q as fp16, a row (query token, head) scaled by its own power of two: a query's result
+  // does not hang on the others of its tile.  The scale's sign goes into q, so that a
+  // page's largest score is its largest product.
   {
     uint32_t m = 0u;
 #pragma unroll
@@ -266,20 +270,11 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       for (int k = 0; k < 4; ++k)
         asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7fff7fffu));
     }
-    const float v = warp_max(fmaxf(bf16_lo(m), bf16_hi(m)));
-    if (lane == 0) red[warp] = v;
-  }
-  __syncthreads();  // mask, maxima, barriers, tensor-memory address
-  const uint32_t tmem = *tmem_slot;
-  float amax = red[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) amax = fmaxf(amax, red[i]);
-  const int qe = q_exponent(amax);
-  // scores are taken with the scale's sign in q, so that a page's largest score is its
-  // largest product
-  const float f = fabsf(a.scale_log2) * pow2i(qe);
-  {
+    float amax = fmaxf(bf16_lo(m), bf16_hi(m));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const int qe = q_exponent(amax);
     const float down = a.scale_log2 < 0.f ? -pow2i(-qe) : pow2i(-qe);
+    if ((tid & 1) == 0) up[qrow] = fabsf(a.scale_log2) * pow2i(qe);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
@@ -291,7 +286,8 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     }
   }
   fence_proxy_async_smem();
-  __syncthreads();
+  __syncthreads();  // q, mask, barriers, tensor-memory address
+  const uint32_t tmem = *tmem_slot;
 
   bool ok = true;
   if (warp >= 4) {
@@ -309,7 +305,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           const uint32_t ks = __float_as_uint(pg[e].ks), vs = __float_as_uint(pg[e].vs);
           if (!scale_ok(ks) || !scale_ok(vs)) set_error(a.err, DSA_DEV_BAD_SCALE);
           info[(blk & 1) * kRPages + 2 * cw + e] =
-              make_float4(f * pg[e].ks, static_cast<float>(scale_exp(vs)),
+              make_float4(pg[e].ks, static_cast<float>(scale_exp(vs)),
                           __uint_as_float((254u << 23) - vs), 0.f);
         }
       }
@@ -371,6 +367,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       }
     }
     __syncwarp();
+    const float f = up[r];
     float ref = kRNoRef, l = 0.f;
     // The weights of a block; MASKED: some query of the CTA does not keep some row of it.
     auto weigh = [&](auto masked, int blk, int present) {
@@ -424,7 +421,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
               m = max3(m, __uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1]));
             m = fmaxf(m, __uint_as_float(s[16 * e + 15]));
             const float2 pgi = *reinterpret_cast<const float2*>(in + 2 * h + e);
-            if (2 * h + e < present) top = fmaxf(top, fmaf(m, pgi.x, pgi.y));
+            if (2 * h + e < present) top = fmaxf(top, fmaf(m, f * pgi.x, pgi.y));
           }
         }
       }
@@ -456,8 +453,8 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float4 pgi = in[2 * h + e];
-            const float c2 = pgi.y - ref;
-            const f32x2 a1 = pack2(pgi.x, pgi.x), a2 = pack2(c2, c2);
+            const float c1 = f * pgi.x, c2 = pgi.y - ref;
+            const f32x2 a1 = pack2(c1, c1), a2 = pack2(c2, c2);
             f32x2 sum = pack2(0.f, 0.f);
 #pragma unroll
             for (int q = 0; q < 16; q += 2) {

@@ -57,8 +57,8 @@ struct TcShape {
   static constexpr int kInfo = kQ + 2 * N * 128;           // 2 x 8 int4: needed rows, scales
   static constexpr int kRef = kInfo + 2 * kTPages * 16;    // ref, head - ref, factor: N each
   static constexpr int kMax = kRef + 3 * N * 4;            // 4 x N column maxima / sums
-  static constexpr int kRed = kMax + 4 * N * 4;            // 8 floats
-  static constexpr int kBar = kRed + 32;                   // two barriers, address, flags
+  static constexpr int kUp = kMax + 4 * N * 4;             // score factor of a column: N floats
+  static constexpr int kBar = kUp + 4 * N;                  // two barriers, address, flags
   static constexpr int kMask = kBar + 32;
   static constexpr int kSlack = 1024;                      // the base is rounded up to 1024
   // tensor memory: S, O^T, and two copies of every row's part of the columns' sums
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   float* nref = ref + N;
   float* fac = ref + 2 * N;
   float* cmax = reinterpret_cast<float*>(smem + Sh::kMax);
-  float* red = reinterpret_cast<float*>(smem + Sh::kRed);
+  float* up = reinterpret_cast<float*>(smem + Sh::kUp);
   uint64_t* s_done = reinterpret_cast<uint64_t*>(smem + Sh::kBar);
   uint64_t* o_done = s_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_done + 2);
@@ -283,29 +283,23 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     }
   };
 
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kQE / 8; ++i) {
-    const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
-  }
-  amax = warp_max(amax);
-  if (lane == 0) red[warp] = amax;
-  __syncthreads();  // mask, references, maxima, tensor-memory address
-  uint2 kreg[8], vreg[8];
-  Page cur = open_page(0, page_of(warp) == warp ? spec0 : load_page(0));
-  load_codes(a.k, cur, kreg);
-  load_codes(a.v, cur, vreg);
-  int pg = page_of(kTPages + warp) == kTPages + warp ? spec1 : load_page(1);
-  const uint32_t tmem = *tmem_slot;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, red[i]);
-  const int qe = q_exponent(amax);
-  const float f = a.scale_log2 * pow2i(qe);
+  // q as fp16, a column (query token, head) scaled by its own power of two: a query's result
+  // does not hang on the others of its tile.
   {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kQE / 8; ++i) {
+      const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+    }
+#pragma unroll
+    for (int o = kTpc / 2; o >= 1; o >>= 1)
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int qe = q_exponent(amax);
     const float down = pow2i(-qe);
+    if (tid % kTpc == 0) up[qcol] = a.scale_log2 * pow2i(qe);
 #pragma unroll
     for (int i = 0; i < kQE / 8; ++i) {
       const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
@@ -317,6 +311,13 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
              make_uint4(h[0], h[1], h[2], h[3]));
     }
   }
+  __syncthreads();  // mask, references, tensor-memory address
+  uint2 kreg[8], vreg[8];
+  Page cur = open_page(0, page_of(warp) == warp ? spec0 : load_page(0));
+  load_codes(a.k, cur, kreg);
+  load_codes(a.v, cur, vreg);
+  int pg = page_of(kTPages + warp) == kTPages + warp ? spec1 : load_page(1);
+  const uint32_t tmem = *tmem_slot;
   constexpr uint32_t kIdS = tc_idesc(128, N, false), kIdO = tc_idesc(128, N, true);
   // Operand descriptors differ by whole multiples of their address unit (16 bytes) from one
   // step of a product to the next, so a step is an addition.
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     const int4 in = info[(blk & 1) * kTPages + (row >> 4)];
     const int j = x < pages ? page_of(x) * 16 + (row & 15) : 0;
     const bool here = x < pages && ((in.x >> (row & 15)) & 1);
-    const float c1 = f * __uint_as_float(static_cast<uint32_t>(in.y));
+    const float c1 = __uint_as_float(static_cast<uint32_t>(in.y));
     const float lv = static_cast<float>(scale_exp(static_cast<uint32_t>(in.z)));
     const float inv = __uint_as_float((254u << 23) - static_cast<uint32_t>(in.z));
     uint32_t keep = here ? 0xffffffffu : 0u;  // bit c: column cg W + c keeps this row
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
         const uint32_t keep0 = __shfl_sync(0xffffffffu, keep, 0);
         const float c10 = __shfl_sync(0xffffffffu, c1, 0), lv0 = __shfl_sync(0xffffffffu, lv, 0);
         if (lane < W) {
-          const float y = fmaf(ref[cg * W + lane], c10, lv0);
+          const float y = fmaf(ref[cg * W + lane], c10 * up[cg * W + lane], lv0);
           const bool use = ((keep0 >> lane) & 1u) && fabsf(y) < INFINITY;
           ref[cg * W + lane] = use ? y : -INFINITY;
           nref[cg * W + lane] = use ? kTHead - y : INFINITY;
@@ -460,10 +461,11 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 r = *reinterpret_cast<const float4*>(nref + cg * W + 16 * q + 4 * i);
-          const f32x2 z0 = fma2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), c2,
-                                add2(pack2(r.x, r.y), lv2));
+          const float4 f = *reinterpret_cast<const float4*>(up + cg * W + 16 * q + 4 * i);
+          const f32x2 z0 = fma2(pack2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
+                                mul2(c2, pack2(f.x, f.y)), add2(pack2(r.x, r.y), lv2));
           const f32x2 z1 = fma2(pack2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])),
-                                c2, add2(pack2(r.z, r.w), lv2));
+                                mul2(c2, pack2(f.z, f.w)), add2(pack2(r.z, r.w), lv2));
           unpack2(z0, p[4 * i], p[4 * i + 1]);
           unpack2(z1, p[4 * i + 2], p[4 * i + 3]);
         }
@@ -537,7 +539,9 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
         float y[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c)
-          y[c] = (keep >> (16 * q + c)) & 1u ? fmaf(__uint_as_float(s[c]), c1, lv) : -INFINITY;
+          y[c] = (keep >> (16 * q + c)) & 1u
+                     ? fmaf(__uint_as_float(s[c]), c1 * up[cg * W + 16 * q + c], lv)
+                     : -INFINITY;
         const float m = scatter_max(y, lane);
         if ((lane & 1) == 0) cmax[wq * N + cg * W + 16 * q + (lane >> 1)] = m;
       }

@@ -670,6 +670,41 @@ def test_chunk_ignores_unread_rows(split):
 
 
 @pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
+@pytest.mark.parametrize("d,g,n", [(64, 2, 20), (128, 1, 20), (128, 4, 9), (128, 4, 40), (128, 2, 80)])
+def test_chunk_queries_of_unlike_sizes(d, g, n, split):
+    """A query far larger, far smaller, infinite or NaN beside others of its tile: the others
+    keep their results.  Not their bits: the references of a tile may move together, and the
+    weights (fp16, 2^-11 each) and the output (bf16, 2^-8 against 2^-8) are rounded anew, so
+    two runs lie within 2^-7 of the value and 2 * 2^-11 of the largest |V| (about 4)."""
+    w = wl.generate(case(d, g, batch=2, hkv=2, lo=200, hi=260, prompt=(40, 60), W=64, seed=29))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    gen = torch.Generator().manual_seed(1)
+    q = torch.randn(2, n, w["hq"], d, generator=gen).to(torch.bfloat16).cuda()
+    ql = torch.full((2,), n, dtype=torch.int32, device="cuda")
+
+    def run(x):
+        out, lse = torch.empty_like(x), torch.empty(x.shape[:3], device="cuda")
+        qb.prefill_sparse(x, ql, out, lse)
+        torch.cuda.synchronize()
+        assert qb.batch.device_error() == 0
+        return out, lse
+
+    out, lse = run(q)
+    others = torch.ones(n, dtype=torch.bool, device="cuda")
+    others[[2, n - 1]] = False
+    for factor in (2.0 ** 50, 2.0 ** -50, float("inf"), float("nan")):
+        x = q.clone()
+        x[:, [2, n - 1]] *= factor
+        o, l = run(x)
+        assert torch.allclose(o[:, others].float(), out[:, others].float(), rtol=2 ** -7, atol=4e-3)
+        assert torch.allclose(l[:, others], lse[:, others], rtol=0, atol=1e-5)
+        if factor == 2.0 ** -50:  # scores of nothing: lse is the log of the rows kept
+            assert torch.allclose(l[:, ~others].exp(), l[:, ~others].exp().round(), rtol=1e-5)
+        if factor == 2.0 ** 50:
+            assert torch.isfinite(o).all() and torch.isfinite(l).all()
+
+
+@pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
 @pytest.mark.parametrize("d,g", [(64, 2), (128, 1), (128, 4)])
 def test_chunk_nan_rows_reach_only_their_queries(d, g, split):
     """NaN in V (and in K) of a row of the chunk: queries before it, and queries whose mask
