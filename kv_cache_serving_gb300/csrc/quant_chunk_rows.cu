@@ -37,20 +37,22 @@ namespace dsa {
 namespace {
 
 constexpr int kRD = 128;            // head_dim
-constexpr int kRRows = 128;         // query rows per CTA, and cache rows per block
-constexpr int kRPages = 8;
-constexpr int kRThreads = 256;
-constexpr int kRHalf = 128 * 128;   // bytes of 64 dims of 128 rows, fp16
+constexpr int kRRows = 128;         // query rows per CTA
+constexpr int kRPages = 4;          // pages per block ...
+constexpr int kRBlock = 64;         // ... and cache rows
+constexpr int kRThreads = 288;      // 4 weighing warps, 4 converting ones, an issuing one
+constexpr int kRQHalf = kRRows * 128, kRHalf = kRBlock * 128;  // bytes of 64 dims, fp16
+constexpr int kRInfos = 4;          // blocks whose scales are held
 constexpr float kRHead = 4.f, kRSlack = 10.f, kRNoRef = -3e38f;  // as in quant_chunk.cu
 
 struct RowsShape {
-  static constexpr int kQ = 0, kK = 2 * kRHalf, kV = 4 * kRHalf;
-  static constexpr int kInfo = 6 * kRHalf;             // 2 x 8 float4 of a page: see below
-  static constexpr int kUp = kInfo + 2 * kRPages * 16;   // score factor of a row: 128 floats
-  static constexpr int kBar = kUp + 4 * kRRows;              // five barriers, address, flags
-  static constexpr int kMask = kBar + 64;
+  static constexpr int kQ = 0, kK = 2 * kRQHalf, kV = kK + 4 * kRHalf;  // K and V twice
+  static constexpr int kInfo = kV + 4 * kRHalf;        // 4 x 4 float4 of a page: see below
+  static constexpr int kUp = kInfo + kRInfos * kRPages * 16;  // score factor of a row: 128 floats
+  static constexpr int kBar = kUp + 4 * kRRows;        // thirteen barriers, address, flag
+  static constexpr int kMask = kBar + 112;
   static constexpr int kSlack = 1024;                  // the base is rounded up to 1024
-  static constexpr int kS = 0, kO = 128, kTmem = 256;  // tensor memory: S and P, O
+  static constexpr int kS = 0, kO = 128, kTmem = 256;  // tensor memory: S and P twice, O
   static int smem(int words) { return kSlack + kMask + 4 * words; }
 };
 
@@ -65,16 +67,11 @@ __device__ __forceinline__ uint2 ld_stream(const uint2* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
-// Barrier of the 128 weighing threads; true when every one of them came with ok.
-__device__ __forceinline__ bool group_sync(bool ok) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"(static_cast<uint32_t>(ok))
-      : "memory");
-  return all != 0;
+// 32 bytes in one store: a whole sector.
+__device__ __forceinline__ void stg256(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
@@ -87,7 +84,8 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   const uint32_t sm = smem_addr(smem);
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the warp's
   // the last query tokens, which see the most rows, first
   const int qt = gridDim.x - 1 - blockIdx.x, hk = blockIdx.y, bpos = blockIdx.z;
   const int b = a.order != nullptr ? __ldg(a.order + bpos) : bpos;
@@ -132,31 +130,37 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
 
   float4* info = reinterpret_cast<float4*>(smem + Sh::kInfo);
   float* up = reinterpret_cast<float*>(smem + Sh::kUp);
+  // Barriers, one for even blocks and one for odd ones of each kind.
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Sh::kBar);  // K and scales of a block
-  uint64_t* v_full = k_full + 1;                                    // its V
-  uint64_t* s_done = k_full + 2;                                    // its scores
-  uint64_t* o_done = k_full + 3;                                    // its second product
-  // k_full as the issuing thread passes it on to its group: its next phase waits for the
-  // group, so that no thread can miss one (k_full's next phase waits for s_done alone)
-  uint64_t* i_full = k_full + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 5);
+  uint64_t* v_full = k_full + 2;                                    // its V
+  uint64_t* s_done = k_full + 4;                                    // its scores
+  uint64_t* o_done = k_full + 6;                                    // its second product
+  uint64_t* p_full = k_full + 8;                                    // its weights
+  // k_full as the issuing warp passes it on to the weighing ones: its next phase waits for
+  // their weights, so that none can miss one (k_full's next phase waits for s_done alone)
+  uint64_t* i_full = k_full + 10;
+  uint64_t* q_full = k_full + 12;  // q, its factors and the mask
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + 13);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* redo = failed + 1;
   uint32_t* msk = reinterpret_cast<uint32_t*>(smem + Sh::kMask);
 
-  const int cw = warp & 3;  // of the converting warps
+  const int cw = warp & 3;  // of the converting warps: its page of a block
   struct Page {
     unsigned need;
     size_t ph;
     float ks, vs;
   };
   const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.max_pages;
-  // Page x of the scan: the rows of it that some query of the CTA keeps, its place in
-  // the pool, its scales.
-  auto open_page = [&](int x) -> Page {
+  auto load_id = [&](int blk) {  // this warp's page of a block
+    const int x = blk * kRPages + cw;
+    return x < pages ? __ldg(pt + page_of(x)) : 0;
+  };
+  // The rows of it that some query of the CTA keeps, its place in the pool, its scales.
+  auto open_page = [&](int blk, int pg) -> Page {
     Page p{0u, 0, 1.f, 1.f};
+    const int x = blk * kRPages + cw;
     if (x >= pages) return p;
-    const int j0 = page_of(x) * 16, pg = __ldg(pt + page_of(x));
+    const int j0 = page_of(x) * 16;
     if (j0 + 15 <= i_last && (j0 + 15 < P || j0 >= i_first)) {
       p.need = 0xffffu;
     } else {
@@ -201,134 +205,123 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
                                                       : make_uint2(0u, 0u);
     }
   };
-  // The same as fp16 into rows 16 (2 cw + e) .. of a tile: 64-dim halves of 128 rows of
+  // The same as fp16 into rows 16 cw .. of a block's tile: 64-dim halves of 64 rows of
   // 128 bytes, 16-byte pieces swizzled by the row.
-  uint32_t f16_at[4];
+  const uint32_t f16_at = sm + ((lane >> 3) & 1) * kRHalf + (16 * cw + (lane >> 4)) * 128 +
+                          (((lane & 7) ^ (lane >> 4)) << 4);
+  auto store_f16 = [&](int tile, const uint2 (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 2 * i + (lane >> 4);
-    f16_at[i] = sm + ((lane >> 3) & 1) * kRHalf + (32 * cw + r) * 128 + (((lane & 7) ^ r) << 4);
-  }
-  auto store_f16 = [&](int tile, int e, const uint2 (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      sts128(f16_at[i & 3] + tile + e * 2048 + (i >> 2) * 1024,
+    for (int i = 0; i < 8; ++i)  // row 2 i + lane / 16
+      sts128((f16_at ^ ((i & 3) << 5)) + tile + i * 256,
              make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2_hi(v[i].x), e4m3x2_f16x2(v[i].y),
                         e4m3x2_f16x2_hi(v[i].y)));
   };
-  // ---- first block's codes on their way; q, mask, barriers, tensor memory
-  uint2 k[2][8], v[2][8];
-  Page pg[2];
-  if (warp >= 4) {
+  if (warp == 8) tmem_alloc<Sh::kTmem>(tmem_slot);
+  if (tid == 256) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      pg[e] = open_page(2 * cw + e);
-      load_codes(a.k, pg[e], k[e]);
-      load_codes(a.v, pg[e], v[e]);
+      mbar_init(k_full + e, 4);
+      mbar_init(v_full + e, 4);
+      mbar_init(s_done + e, 1);
+      mbar_init(o_done + e, 1);
+      mbar_init(p_full + e, 4);
+      mbar_init(i_full + e, 1);
     }
-  }
-  const int qrow = tid >> 1, qd0 = (tid & 1) * 64;  // half a row per thread
-  uint4 qv[8];
-  {
-    const bool in = t0 + (qrow >> LG) < t1;
-    const uint4* p = reinterpret_cast<const uint4*>(a.q + qh_of(qrow) * kRD + qd0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) qv[i] = in ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  {
-    // the mask shifted by one: bit o keeps offset o, 0 (the query itself) and 1 .. window
-    const uint32_t* mrow = a.keep_mask + (static_cast<size_t>(b) * a.hkv + hk) * a.mask_words;
-    for (int x = tid; x < a.max_window / 32 + 1; x += kRThreads) {
-      const uint32_t lo = x == 0 ? 0x80000000u : __ldg(mrow + x - 1);
-      const uint32_t hi = x < a.mask_words ? __ldg(mrow + x) : 0u;
-      uint32_t v = (hi << 1) | (lo >> 31);
-      const int live = Wn + 1 - 32 * x;
-      if (live < 32) v = live <= 0 ? 0u : v & ((1u << live) - 1u);
-      msk[x] = v;
-    }
-  }
-  if (warp == 0) tmem_alloc<Sh::kTmem>(tmem_slot);
-  if (tid == 0) {
-    mbar_init(k_full, 4);
-    mbar_init(v_full, 4);
-    mbar_init(s_done, 1);
-    mbar_init(o_done, 1);
-    mbar_init(i_full, 1);
+    mbar_init(q_full, 4);
     fence_mbar_init();
     *failed = 0;
-    *redo = 0;
   }
-  // q as fp16, a row (query token, head) scaled by its own power of two: a query's result
-  // does not hang on the others of its tile.  The scale's sign goes into q, so that a
-  // page's largest score is its largest product.
-  {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7fff7fffu));
-    }
-    float amax = fmaxf(bf16_lo(m), bf16_hi(m));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    const int qe = q_exponent(amax);
-    const float down = a.scale_log2 < 0.f ? -pow2i(-qe) : pow2i(-qe);
-    if ((tid & 1) == 0) up[qrow] = fabsf(a.scale_log2) * pow2i(qe);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-      uint32_t h[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = f16x2_rn(bf16_lo(w[k]) * down, bf16_hi(w[k]) * down);
-      sts128(sm + Sh::kQ + (tid & 1) * kRHalf + qrow * 128 + ((i ^ (qrow & 7)) << 4),
-             make_uint4(h[0], h[1], h[2], h[3]));
-    }
-  }
-  fence_proxy_async_smem();
-  __syncthreads();  // q, mask, barriers, tensor-memory address
-  const uint32_t tmem = *tmem_slot;
+  const bool converts = warp >= 4 && warp < 8;
+  const int id0 = converts ? load_id(0) : 0;
+  __syncthreads();  // barriers, tensor-memory address
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   bool ok = true;
-  if (warp >= 4) {
-    // ================= converters =================
+  if (converts) {
+    // ================= converters: a page of every block, codes loaded a block ahead =========
+    uint2 k[8], v[8];
+    Page pg = open_page(0, id0);
+    load_codes(a.k, pg, k);
+    load_codes(a.v, pg, v);
+    int id = load_id(1);
     for (int blk = 0; blk < nblocks; ++blk) {
-      const int present = min(kRPages, pages - blk * kRPages);
-      const bool more = blk + 1 < nblocks;
-      // K of this block (the last one's scores are done with it), and its scales as the
-      // weighing group uses them
-      if (blk > 0) ok = mbar_wait(s_done, (blk - 1) & 1) && ok;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (2 * cw + e < present) store_f16(Sh::kK, e, k[e]);
-        if (lane == 0) {
-          const uint32_t ks = __float_as_uint(pg[e].ks), vs = __float_as_uint(pg[e].vs);
-          if (!scale_ok(ks) || !scale_ok(vs)) set_error(a.err, DSA_DEV_BAD_SCALE);
-          info[(blk & 1) * kRPages + 2 * cw + e] =
-              make_float4(pg[e].ks, static_cast<float>(scale_exp(vs)),
-                          __uint_as_float((254u << 23) - vs), 0.f);
-        }
+      const int e = blk & 1;
+      const bool here = blk * kRPages + cw < pages, more = blk + 1 < nblocks;
+      const uint32_t was = (static_cast<uint32_t>(blk >> 1) - 1u) & 1u;  // of block blk - 2
+      if (blk > 1) ok = mbar_wait(s_done + e, was) && ok;  // its K is free
+      if (here) store_f16(Sh::kK + 2 * e * kRHalf, k);
+      if (lane == 0) {
+        // a page's K scale, log2 and reciprocal of its V scale
+        const uint32_t ks = __float_as_uint(pg.ks), vs = __float_as_uint(pg.vs);
+        if (!scale_ok(ks) || !scale_ok(vs)) set_error(a.err, DSA_DEV_BAD_SCALE);
+        info[(blk & (kRInfos - 1)) * kRPages + cw] =
+            make_float4(pg.ks, static_cast<float>(scale_exp(vs)),
+                        __uint_as_float((254u << 23) - vs), 0.f);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(k_full);
+      if (lane == 0) mbar_arrive(k_full + e);
       if (more) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          pg[e] = open_page((blk + 1) * kRPages + 2 * cw + e);
-          load_codes(a.k, pg[e], k[e]);
-        }
+        pg = open_page(blk + 1, id);
+        load_codes(a.k, pg, k);
+        id = load_id(blk + 2);
       }
-      if (blk > 0) ok = mbar_wait(o_done, (blk - 1) & 1) && ok;  // V is free
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (2 * cw + e < present) store_f16(Sh::kV, e, v[e]);
-        if (more) load_codes(a.v, pg[e], v[e]);
-      }
+      if (blk > 1) ok = mbar_wait(o_done + e, was) && ok;  // its V is free
+      if (here) store_f16(Sh::kV + 2 * e * kRHalf, v);
+      if (more) load_codes(a.v, pg, v);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(v_full);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) mbar_arrive(v_full + e);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+    }
+    if (!ok) *failed = 1;
+  } else if (warp == 8) {
+    // ================= issuing =================
+    const uint64_t q_desc = tc_desc(sm + Sh::kQ, 16, 1024, kSwizzle128);
+    const uint64_t k_desc = tc_desc(sm + Sh::kK, 16, 1024, kSwizzle128);
+    const uint64_t v_desc = tc_desc(sm + Sh::kV, kRHalf, 1024, kSwizzle128);
+    auto issue_s = [&](int blk) {  // S = Q K^T over the block's pages, when K is there
+      ok = mbar_wait(k_full + (blk & 1), static_cast<uint32_t>(blk >> 1) & 1u) && ok;
+      tc_fence_after();
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const uint32_t id_s = tc_idesc(128, 16 * min(kRPages, pages - blk * kRPages), false);
+      const uint32_t to = tmem + Sh::kS + (blk & 1) * kRBlock;
+      const uint64_t kd = k_desc + ((blk & 1) * 2 * kRHalf >> 4);
+      if (elect_one()) {
+        mbar_arrive(i_full + (blk & 1));
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          tc_mma_f16(to, q_desc + (((s >> 2) * kRQHalf + (s & 3) * 32) >> 4),
+                     kd + (((s >> 2) * kRHalf + (s & 3) * 32) >> 4), id_s, s > 0);
+        tc_commit(s_done + (blk & 1));
+      }
+      __syncwarp();
+    };
+    ok = mbar_wait(q_full, 0);
+    for (int blk = 0; blk < min(2, nblocks); ++blk) issue_s(blk);
+    for (int blk = 0; blk < nblocks; ++blk) {
+      const int e = blk & 1, present = min(kRPages, pages - blk * kRPages);
+      const uint32_t phase = static_cast<uint32_t>(blk >> 1) & 1u;
+      ok = mbar_wait(v_full + e, phase) && mbar_wait(p_full + e, phase) && ok;
+      tc_fence_after();
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t from = tmem + Sh::kS + e * kRBlock;
+      const uint64_t vd = v_desc + (e * 2 * kRHalf >> 4);
+      if (elect_one()) {  // O += P V, a step for each page
+        constexpr uint32_t id_o = tc_idesc_b_rows(128, kRD);
+#pragma unroll
+        for (int s = 0; s < kRPages; ++s)
+          if (s < present)
+            tc_mma_f16_ta(tmem + Sh::kO, from + 8 * s, vd + (s * 2048 >> 4), id_o, blk > 0 || s > 0);
+        tc_commit(o_done + e);
+      }
+      __syncwarp();
+      if (blk + 2 < nblocks) {  // into the place of these weights
+        ok = mbar_wait(o_done + e, phase) && ok;
+        issue_s(blk + 2);
+      }
     }
     if (!ok) *failed = 1;
   } else {
@@ -336,56 +329,89 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     const int r = tid;
     const int i = i_first + (r >> LG);
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-    const uint64_t q_desc = tc_desc(sm + Sh::kQ, 16, 1024, kSwizzle128);
-    const uint64_t k_desc = tc_desc(sm + Sh::kK, 16, 1024, kSwizzle128);
-    const uint64_t v_desc = tc_desc(sm + Sh::kV, kRHalf, 1024, kSwizzle128);
-    auto issue_s = [&](int blk) {  // S = Q K^T over the block's pages
-      const uint32_t id = tc_idesc(128, 16 * min(kRPages, pages - blk * kRPages), false);
+    // q as fp16, a row (query token, head) scaled by its own power of two: a query's result
+    // does not hang on the others of its tile.  The scale's sign goes into q, so that a
+    // page's largest score is its largest product.  16 lanes a row.
+    {
+      const int piece = lane & 15, r0 = 32 * warp + (lane >> 4);
+      uint4 x[16];
+      uint32_t m[16];
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const uint64_t step = ((s >> 2) * kRHalf + (s & 3) * 32) >> 4;
-        tc_mma_f16(tmem + Sh::kS, q_desc + step, k_desc + step, id, s > 0);
+      for (int y = 0; y < 16; ++y)
+        x[y] = t0 + ((r0 + 2 * y) >> LG) < t1
+                    ? __ldg(reinterpret_cast<const uint4*>(a.q + qh_of(r0 + 2 * y) * kRD) + piece)
+                    : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int y = 0; y < 16; ++y) {
+        m[y] = x[y].x & 0x7fff7fffu;
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].y & 0x7fff7fffu));
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].z & 0x7fff7fffu));
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].w & 0x7fff7fffu));
       }
-      tc_commit(s_done);
-    };
-    auto issue_o = [&](int blk) {  // O += P V, a step for each page
-      constexpr uint32_t id = tc_idesc_b_rows(128, kRD);
-      const int present = min(kRPages, pages - blk * kRPages);
 #pragma unroll
-      for (int s = 0; s < kRPages; ++s)
-        if (s < present)
-          tc_mma_f16_ta(tmem + Sh::kO, tmem + Sh::kS + 8 * s, v_desc + (s * 2048 >> 4), id,
-                        blk > 0 || s > 0);
-      tc_commit(o_done);
-    };
-    if (tid == 0) {
-      ok = mbar_wait(k_full, 0);
-      tc_fence_after();
-      if (ok) {
-        mbar_arrive(i_full);
-        issue_s(0);
+      for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, m[y], o);
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(other));
+        }
+#pragma unroll
+      for (int y = 0; y < 16; ++y) {
+        const int row = r0 + 2 * y;
+        const int qe = q_exponent(fmaxf(bf16_lo(m[y]), bf16_hi(m[y])));
+        const float down = a.scale_log2 < 0.f ? -pow2i(-qe) : pow2i(-qe);
+        // at least 2^-105, so that a masked score (-inf) times it and a page's scale (2^-40
+        // and more) stays one; a score so scaled is below 2^-40
+        if (piece == 0) up[row] = fmaxf(fabsf(a.scale_log2) * pow2i(qe), 0x1p-105f);
+        sts128(sm + Sh::kQ + (piece >> 3) * kRQHalf + row * 128 + (((piece & 7) ^ (row & 7)) << 4),
+               make_uint4(f16x2_rn(bf16_lo(x[y].x) * down, bf16_hi(x[y].x) * down),
+                          f16x2_rn(bf16_lo(x[y].y) * down, bf16_hi(x[y].y) * down),
+                          f16x2_rn(bf16_lo(x[y].z) * down, bf16_hi(x[y].z) * down),
+                          f16x2_rn(bf16_lo(x[y].w) * down, bf16_hi(x[y].w) * down)));
       }
     }
+    {
+      // the mask shifted by one: bit o keeps offset o, 0 (the query itself) and 1 .. window
+      const uint32_t* mrow = a.keep_mask + (static_cast<size_t>(b) * a.hkv + hk) * a.mask_words;
+      for (int x = tid; x < a.max_window / 32 + 1; x += 128) {
+        const uint32_t lo = x == 0 ? 0x80000000u : __ldg(mrow + x - 1);
+        const uint32_t hi = x < a.mask_words ? __ldg(mrow + x) : 0u;
+        uint32_t m = (hi << 1) | (lo >> 31);
+        const int live = Wn + 1 - 32 * x;
+        if (live < 32) m = live <= 0 ? 0u : m & ((1u << live) - 1u);
+        msk[x] = m;
+      }
+    }
+    fence_proxy_async_smem();
     __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+    ok = mbar_wait(q_full, 0);  // the other warps' part of the mask
     const float f = up[r];
     float ref = kRNoRef, l = 0.f;
-    // The weights of a block; MASKED: some query of the CTA does not keep some row of it.
-    auto weigh = [&](auto masked, int blk, int present) {
-      constexpr bool kMasked = decltype(masked)::value;
-      const float4* in = info + (blk & 1) * kRPages;
-      // which of a page's rows this query keeps: 16 bits each
-      uint32_t keep[kRPages / 2];
-      if constexpr (kMasked) {
-        const int words = a.max_window / 32 + 1;
+    for (int blk = 0; blk < nblocks; ++blk) {
+      const int e = blk & 1, present = min(kRPages, pages - blk * kRPages);
+      const uint32_t phase = static_cast<uint32_t>(blk >> 1) & 1u;
+      ok = mbar_wait(i_full + e, phase) && mbar_wait(s_done + e, phase) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_s = t_lane + Sh::kS + e * kRBlock;
+      const float4* in = info + (blk & (kRInfos - 1)) * kRPages;
+      // Which rows of two pages this query keeps, 16 bits each; only looked at where some
+      // query of the CTA does not keep some row of the block.
+      uint32_t keep[kRPages / 2] = {0xffffffffu, 0xffffffffu};
+      const int j_last = page_of(blk * kRPages + present - 1) * 16 + 15;
+      const bool masked = j_last >= P || j_last > i_first;
+      if (masked) {
 #pragma unroll
         for (int x = 0; x < kRPages; ++x) {
-          uint32_t on = 0u;
           if (x < present) {
             const int j0 = page_of(blk * kRPages + x) * 16;
             // columns up to the query's own row, and of those prompt rows and kept offsets
             const int c = i - j0;  // column of the query itself
-            on = c < 0 ? 0u : c >= 15 ? 0xffffu : (2u << c) - 1u;
+            uint32_t on = c < 0 ? 0u : c >= 15 ? 0xffffu : (2u << c) - 1u;
             if (j0 + 15 >= P) {
+              const int words = a.max_window / 32 + 1;
               const int base = c - 15;  // offset of column 15
               const int w0 = max(base, 0) >> 5, sh = max(base, 0) & 31;
               const uint32_t lo = w0 < words ? msk[w0] : 0u, hi = w0 + 1 < words ? msk[w0 + 1] : 0u;
@@ -395,33 +421,37 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
               const int np = P - j0;    // prompt rows of the page
               on &= win | (np <= 0 ? 0u : (1u << min(np, 16)) - 1u);
             }
+            keep[x / 2] &= x & 1 ? (on << 16) | 0xffffu : on | 0xffff0000u;
           }
-          if (x & 1) keep[x / 2] |= on << 16;
-          else keep[x / 2] = on;
         }
       }
-      // pass 1: the row's largest score
-      float top = -INFINITY;
+      // The scores of two pages; -inf where the query does not keep the row.
+      auto scores = [&](int h, uint32_t (&s)[32]) {
+        tmem_load<32>(t_s + 32 * h, s);
+        tc_wait_ld();
+        if (masked && !__all_sync(0xffffffffu, keep[h] == 0xffffffffu)) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            if (!((keep[h] >> q) & 1u)) s[q] = 0xff800000u;
+        }
+      };
+      float top = -INFINITY;  // the row's largest score
 #pragma unroll
       for (int h = 0; h < kRPages / 2; ++h) {
         if (2 * h < present) {
           uint32_t s[32];
-          tmem_load<32>(t_lane + Sh::kS + 32 * h, s);
-          tc_wait_ld();
+          scores(h, s);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (kMasked) {
+          for (int y = 0; y < 2; ++y) {
+            float m[4];
 #pragma unroll
-              for (int q = 0; q < 16; ++q)
-                if (!((keep[h] >> (16 * e + q)) & 1u)) s[16 * e + q] = 0xff800000u;  // -inf
-            }
-            float m = __uint_as_float(s[16 * e]);
-#pragma unroll
-            for (int q = 1; q < 15; q += 2)
-              m = max3(m, __uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1]));
-            m = fmaxf(m, __uint_as_float(s[16 * e + 15]));
-            const float2 pgi = *reinterpret_cast<const float2*>(in + 2 * h + e);
-            if (2 * h + e < present) top = fmaxf(top, fmaf(m, f * pgi.x, pgi.y));
+            for (int q = 0; q < 4; ++q)
+              m[q] = fmaxf(max3(__uint_as_float(s[16 * y + q]), __uint_as_float(s[16 * y + 4 + q]),
+                                __uint_as_float(s[16 * y + 8 + q])),
+                           __uint_as_float(s[16 * y + 12 + q]));
+            const float2 pgi = *reinterpret_cast<const float2*>(in + 2 * h + y);
+            if (2 * h + y < present)
+              top = fmaxf(top, fmaf(fmaxf(max3(m[0], m[1], m[2]), m[3]), f * pgi.x, pgi.y));
           }
         }
       }
@@ -431,92 +461,64 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
         ref = to;
         l *= down;
         if (blk > 0) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t o[32];
-            tmem_load<32>(t_lane + Sh::kO + 32 * h, o);
+          ok = mbar_wait(o_done + (e ^ 1), static_cast<uint32_t>((blk - 1) >> 1) & 1u) && ok;
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int h = 0; h < 8; ++h) {
+            uint32_t o[16];
+            tmem_load<16>(t_lane + Sh::kO + 16 * h, o);
             tc_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * down);
-            tmem_store16(t_lane + Sh::kO + 32 * h, o);
-            tmem_store16(t_lane + Sh::kO + 32 * h + 16, o + 16);
+            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * down);
+            tmem_store16(t_lane + Sh::kO + 16 * h, o);
           }
         }
       }
-      // pass 2: weights, packed over the scores already read
+      // weights, packed over the scores already read
 #pragma unroll
       for (int h = 0; h < kRPages / 2; ++h) {
         if (2 * h < present) {
           uint32_t s[32], w[16];
-          tmem_load<32>(t_lane + Sh::kS + 32 * h, s);
-          tc_wait_ld();
+          scores(h, s);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 pgi = in[2 * h + e];
+          for (int y = 0; y < 2; ++y) {
+            const float4 pgi = in[2 * h + y];
             const float c1 = f * pgi.x, c2 = pgi.y - ref;
             const f32x2 a1 = pack2(c1, c1), a2 = pack2(c2, c2);
             f32x2 sum = pack2(0.f, 0.f);
 #pragma unroll
-            for (int q = 0; q < 16; q += 2) {
+            for (int q = 16 * y; q < 16 * y + 16; q += 2) {
               float z0, z1;
-              unpack2(fma2(pack2(__uint_as_float(s[16 * e + q]), __uint_as_float(s[16 * e + q + 1])),
-                           a1, a2),
-                      z0, z1);
-              if (kMasked) {
-                z0 = (keep[h] >> (16 * e + q)) & 1u ? z0 : -INFINITY;
-                z1 = (keep[h] >> (16 * e + q + 1)) & 1u ? z1 : -INFINITY;
-              }
+              unpack2(fma2(pack2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), a1, a2), z0, z1);
               z0 = ex2_approx(z0);
               z1 = ex2_approx(z1);
               sum = add2(sum, pack2(z0, z1));
-              w[8 * e + q / 2] = f16x2_rn(z0, z1);
+              w[q / 2] = f16x2_rn(z0, z1);
             }
             float u, t;
             unpack2(sum, u, t);
-            if (2 * h + e < present) l = fmaf(u + t, pgi.z, l);
+            if (2 * h + y < present) l = fmaf(u + t, pgi.z, l);
           }
-          tmem_store16(t_lane + Sh::kS + 16 * h, w);
+          tmem_store16(t_s + 16 * h, w);
         }
       }
-    };
-    for (int blk = 0; blk < nblocks; ++blk) {
-      const int present = min(kRPages, pages - blk * kRPages);
-      ok = mbar_wait(i_full, blk & 1) && mbar_wait(s_done, blk & 1) && ok;
-      __syncwarp();
-      tc_fence_after();
-      const int j_last = page_of(blk * kRPages + present - 1) * 16 + 15;
-      if (j_last < P && j_last <= i_first) weigh(std::false_type{}, blk, present);
-      else weigh(std::true_type{}, blk, present);
       tc_wait_st();
       tc_fence_before();
-      ok = group_sync(ok);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (warp == 0) {
-        if (lane == 0) {
-          ok = mbar_wait(v_full, blk & 1);
-          tc_fence_after();
-          if (ok) issue_o(blk);
-          if (blk + 1 < nblocks) {  // P lies over S: the next scores wait for this product
-            ok = mbar_wait(o_done, blk & 1) && mbar_wait(k_full, (blk + 1) & 1) && ok;
-            tc_fence_after();
-            if (ok) {
-              mbar_arrive(i_full);
-              issue_s(blk + 1);
-            }
-          }
-        }
-        __syncwarp();
-      }
+      if (lane == 0) mbar_arrive(p_full + e);
     }
-    if (ok) ok = mbar_wait(o_done, (nblocks - 1) & 1);
+    if (ok)
+      ok = mbar_wait(o_done + ((nblocks - 1) & 1), static_cast<uint32_t>((nblocks - 1) >> 1) & 1u);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *failed = 1;
     if (ok) {
       tc_fence_after();
       const float inv = 1.f / l;
-      const bool in = t0 + (r >> LG) < t1;
-      const size_t qh = qh_of(r);
-      if (a.lse != nullptr && in) a.lse[qh] = (ref + log2f(l)) * kLn2;
+      const bool mine = t0 + (r >> LG) < t1;
+      if (a.lse != nullptr && mine) a.lse[qh_of(r)] = (ref + log2f(l)) * kLn2;
+      uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + qh_of(r) * kRD;
       float probe = 0.f;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -530,46 +532,36 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           probe += u + t;
           w[q] = bf16x2_rn(u, t);
         }
-        // by way of q's place in shared memory (its products are done): pieces of 16 bytes,
-        // swizzled by the row
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          sts128(sm + Sh::kQ + r * 256 + (((4 * h + q) ^ (r & 15)) << 4),
-                 make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+        if (mine) {
+          stg256(to + 32 * h, w);
+          stg256(to + 32 * h + 16, w + 8);
+        }
       }
-      // a NaN may come from a row of V that other queries of the CTA keep (weight 0 times
-      // NaN): the CTA's queries are done again below, from the rows each one keeps
-      if (in && probe != probe) *redo = 1;
       tc_fence_before();
+      // A NaN may come from a row of V that other queries of the CTA keep (weight 0 times
+      // NaN): such a query is done again, from the rows it keeps.
+      unsigned nan = __ballot_sync(0xffffffffu, mine && probe != probe);
+      __syncwarp();  // after the rows' first output
+      while (nan != 0u) {
+        const int rr = 32 * warp + __ffs(nan) - 1;
+        nan &= nan - 1u;
+        quant_redo_query<kRD>(a, b, hk, i_first + (rr >> LG), P, Wn, qh_of(rr), lane);
+      }
     }
   }
   __syncthreads();
-  if (*failed == 0) {
-    // whole rows out: 16 lanes a row
-#pragma unroll
-    for (int q = 0; q < kRRows / 16; ++q) {
-      const int r = 16 * q + (tid >> 4), ch = tid & 15;
-      if (t0 + (r >> LG) < t1)
-        *reinterpret_cast<uint4*>(a.out + qh_of(r) * kRD + 8 * ch) =
-            *reinterpret_cast<const uint4*>(smem + Sh::kQ + r * 256 + ((ch ^ (r & 15)) << 4));
-    }
-  }
   if (*failed != 0) {
     // give products in flight a bounded time to finish before the memory goes back
     if (tid == 0) set_error(a.err, DSA_DEV_TIMEOUT);
-    mbar_wait(s_done, (nblocks - 1) & 1);
-    mbar_wait(o_done, (nblocks - 1) & 1);
+    for (int blk = max(0, nblocks - 2); blk < nblocks; ++blk) {
+      mbar_wait(s_done + (blk & 1), static_cast<uint32_t>(blk >> 1) & 1u);
+      mbar_wait(o_done + (blk & 1), static_cast<uint32_t>(blk >> 1) & 1u);
+    }
     __syncthreads();
   }
-  if (warp == 0) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc<Sh::kTmem>(tmem);
-  }
-  if (*failed == 0 && *redo != 0) {
-    __syncthreads();  // after every row's first output
-    for (int r = warp; r < kRRows; r += kRThreads / 32)
-      if (t0 + (r >> LG) < t1)
-        quant_redo_query<kRD>(a, b, hk, i_first + (r >> LG), P, Wn, qh_of(r), lane);
   }
 }
 
