@@ -46,8 +46,9 @@ constexpr int kRInfos = 4;          // blocks whose scales are held
 constexpr float kRHead = 4.f, kRSlack = 10.f, kRNoRef = -3e38f;  // as in quant_chunk.cu
 
 struct RowsShape {
-  static constexpr int kQ = 0, kK = 2 * kRQHalf, kV = kK + 4 * kRHalf;  // K and V twice
-  static constexpr int kInfo = kV + 4 * kRHalf;        // 4 x 4 float4 of a page: see below
+  static constexpr int kQ = 0, kK = 2 * kRQHalf, kV = kK + 4 * kRHalf;  // K twice, V once
+  static constexpr int kCodes = kV + 2 * kRHalf;       // a block's codes: K, V of each page
+  static constexpr int kInfo = kCodes + kRPages * 2 * 16 * kRD;        // 4 x 4 float4 of a page: see below
   static constexpr int kUp = kInfo + kRInfos * kRPages * 16;  // score factor of a row: 128 floats
   static constexpr int kBar = kUp + 4 * kRRows;        // thirteen barriers, address, flag
   static constexpr int kMask = kBar + 112;
@@ -60,12 +61,6 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w)
                : "memory");
-}
-// Read once: past the L1, whose few kilobytes beside the tiles hold page ids and masks.
-__device__ __forceinline__ uint2 ld_stream(const uint2* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
 }
 // 32 bytes in one store: a whole sector.
 __device__ __forceinline__ void stg256(void* p, const uint32_t* w) {
@@ -191,27 +186,28 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     }
     return p;
   };
-  // This lane's 8 codes of rows 2 i + lane / 16 of a page, piece lane % 16; rows nobody
-  // needs are zeros.
-  auto load_codes = [&](const uint8_t* base, const Page& p, uint2 (&v)[8]) {
-    const uint2* src = reinterpret_cast<const uint2*>(base + p.ph * (16 * kRD)) + lane;
-    if (p.need == 0xffffu) {
+  // The codes of a page on their way to shared memory (not through registers: what an SM can
+  // have in flight there is bounded by the few KB of L1 beside the tiles); rows that nobody
+  // needs become zeros.
+  auto load_codes = [&](const uint8_t* base, const Page& p, uint32_t to) {
+    const uint8_t* src = base + p.ph * (16 * kRD) + 16 * lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = ld_stream(src + 32 * i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = (p.need >> (2 * i + (lane >> 4))) & 1u ? ld_stream(src + 32 * i)
-                                                      : make_uint2(0u, 0u);
-    }
+    for (int i = 0; i < 4; ++i)  // 4 rows of 8 pieces
+      cp_async16_zfill(to + 512 * i + 16 * lane, src + 512 * i,
+                       (p.need >> (4 * i + (lane >> 3))) & 1u);
   };
-  // The same as fp16 into rows 16 cw .. of a block's tile: 64-dim halves of 64 rows of
-  // 128 bytes, 16-byte pieces swizzled by the row.
+  // Its fp16 values into rows 16 cw .. of a block's tile: 64-dim halves of 64 rows of 128
+  // bytes, 16-byte pieces swizzled by the row; a lane has the 8 codes of rows 2 i + lane / 16,
+  // piece lane % 16.
   const uint32_t f16_at = sm + ((lane >> 3) & 1) * kRHalf + (16 * cw + (lane >> 4)) * 128 +
                           (((lane & 7) ^ (lane >> 4)) << 4);
+  auto take_codes = [&](uint32_t from, uint2 (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = lds64(from + 256 * i + 8 * lane);
+  };
   auto store_f16 = [&](int tile, const uint2 (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)  // row 2 i + lane / 16
+    for (int i = 0; i < 8; ++i)
       sts128((f16_at ^ ((i & 3) << 5)) + tile + i * 256,
              make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2_hi(v[i].x), e4m3x2_f16x2(v[i].y),
                         e4m3x2_f16x2_hi(v[i].y)));
@@ -239,17 +235,18 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   bool ok = true;
   if (converts) {
     // ================= converters: a page of every block, codes loaded a block ahead =========
-    uint2 k[8], v[8];
+    const uint32_t at_k = sm + Sh::kCodes + cw * 2 * 16 * kRD, at_v = at_k + 16 * kRD;
     Page pg = open_page(0, id0);
-    load_codes(a.k, pg, k);
-    load_codes(a.v, pg, v);
+    load_codes(a.k, pg, at_k);
+    cp_async_commit();
+    load_codes(a.v, pg, at_v);
+    cp_async_commit();
     int id = load_id(1);
     for (int blk = 0; blk < nblocks; ++blk) {
       const int e = blk & 1;
       const bool here = blk * kRPages + cw < pages, more = blk + 1 < nblocks;
-      const uint32_t was = (static_cast<uint32_t>(blk >> 1) - 1u) & 1u;  // of block blk - 2
-      if (blk > 1) ok = mbar_wait(s_done + e, was) && ok;  // its K is free
-      if (here) store_f16(Sh::kK + 2 * e * kRHalf, k);
+      const uint32_t half = static_cast<uint32_t>(blk >> 1);
+      uint2 x[8];
       if (lane == 0) {
         // a page's K scale, log2 and reciprocal of its V scale
         const uint32_t ks = __float_as_uint(pg.ks), vs = __float_as_uint(pg.vs);
@@ -258,23 +255,35 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
             make_float4(pg.ks, static_cast<float>(scale_exp(vs)),
                         __uint_as_float((254u << 23) - vs), 0.f);
       }
+      cp_async_wait<1>();  // its K
+      __syncwarp();
+      take_codes(at_k, x);
+      if (blk > 1) ok = mbar_wait(s_done + e, (half - 1u) & 1u) && ok;  // its place is free
+      if (here) store_f16(Sh::kK + 2 * e * kRHalf, x);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full + e);
       if (more) {
         pg = open_page(blk + 1, id);
-        load_codes(a.k, pg, k);
+        load_codes(a.k, pg, at_k);
         id = load_id(blk + 2);
       }
-      if (blk > 1) ok = mbar_wait(o_done + e, was) && ok;  // its V is free
-      if (here) store_f16(Sh::kV + 2 * e * kRHalf, v);
-      if (more) load_codes(a.v, pg, v);
+      cp_async_commit();
+      cp_async_wait<1>();  // its V
+      __syncwarp();
+      take_codes(at_v, x);
+      if (blk > 0)  // the last block's second product is done with its place
+        ok = mbar_wait(o_done + (e ^ 1), static_cast<uint32_t>((blk - 1) >> 1) & 1u) && ok;
+      if (here) store_f16(Sh::kV, x);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full + e);
+      if (more) load_codes(a.v, pg, at_v);
+      cp_async_commit();
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
     }
+    cp_async_wait<0>();
     if (!ok) *failed = 1;
   } else if (warp == 8) {
     // ================= issuing =================
@@ -308,13 +317,12 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t from = tmem + Sh::kS + e * kRBlock;
-      const uint64_t vd = v_desc + (e * 2 * kRHalf >> 4);
       if (elect_one()) {  // O += P V, a step for each page
         constexpr uint32_t id_o = tc_idesc_b_rows(128, kRD);
 #pragma unroll
         for (int s = 0; s < kRPages; ++s)
           if (s < present)
-            tc_mma_f16_ta(tmem + Sh::kO, from + 8 * s, vd + (s * 2048 >> 4), id_o, blk > 0 || s > 0);
+            tc_mma_f16_ta(tmem + Sh::kO, from + 8 * s, v_desc + (s * 2048 >> 4), id_o, blk > 0 || s > 0);
         tc_commit(o_done + e);
       }
       __syncwarp();
@@ -334,40 +342,51 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     // page's largest score is its largest product.  16 lanes a row.
     {
       const int piece = lane & 15, r0 = 32 * warp + (lane >> 4);
-      uint4 x[16];
-      uint32_t m[16];
+      auto load_q = [&](int g, uint4 (&x)[4]) {
 #pragma unroll
-      for (int y = 0; y < 16; ++y)
-        x[y] = t0 + ((r0 + 2 * y) >> LG) < t1
-                    ? __ldg(reinterpret_cast<const uint4*>(a.q + qh_of(r0 + 2 * y) * kRD) + piece)
-                    : make_uint4(0u, 0u, 0u, 0u);
+        for (int y = 0; y < 4; ++y) {
+          const int row = r0 + 8 * g + 2 * y;
+          x[y] = t0 + (row >> LG) < t1
+                     ? __ldg(reinterpret_cast<const uint4*>(a.q + qh_of(row) * kRD) + piece)
+                     : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      uint4 x[4], ahead[4];
+      load_q(0, x);
+      load_q(1, ahead);
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        uint32_t m[4];
 #pragma unroll
-      for (int y = 0; y < 16; ++y) {
-        m[y] = x[y].x & 0x7fff7fffu;
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].y & 0x7fff7fffu));
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].z & 0x7fff7fffu));
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].w & 0x7fff7fffu));
-      }
-#pragma unroll
-      for (int o = 8; o >= 1; o >>= 1)
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, m[y], o);
-          asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(other));
+        for (int y = 0; y < 4; ++y) {
+          m[y] = x[y].x & 0x7fff7fffu;
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].y & 0x7fff7fffu));
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].z & 0x7fff7fffu));
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].w & 0x7fff7fffu));
         }
 #pragma unroll
-      for (int y = 0; y < 16; ++y) {
-        const int row = r0 + 2 * y;
-        const int qe = q_exponent(fmaxf(bf16_lo(m[y]), bf16_hi(m[y])));
-        const float down = a.scale_log2 < 0.f ? -pow2i(-qe) : pow2i(-qe);
-        // at least 2^-105, so that a masked score (-inf) times it and a page's scale (2^-40
-        // and more) stays one; a score so scaled is below 2^-40
-        if (piece == 0) up[row] = fmaxf(fabsf(a.scale_log2) * pow2i(qe), 0x1p-105f);
-        sts128(sm + Sh::kQ + (piece >> 3) * kRQHalf + row * 128 + (((piece & 7) ^ (row & 7)) << 4),
-               make_uint4(f16x2_rn(bf16_lo(x[y].x) * down, bf16_hi(x[y].x) * down),
-                          f16x2_rn(bf16_lo(x[y].y) * down, bf16_hi(x[y].y) * down),
-                          f16x2_rn(bf16_lo(x[y].z) * down, bf16_hi(x[y].z) * down),
-                          f16x2_rn(bf16_lo(x[y].w) * down, bf16_hi(x[y].w) * down)));
+        for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, m[y], o);
+            asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(other));
+          }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int row = r0 + 8 * g + 2 * y;
+          const int qe = q_exponent(fmaxf(bf16_lo(m[y]), bf16_hi(m[y])));
+          const float down = a.scale_log2 < 0.f ? -pow2i(-qe) : pow2i(-qe);
+          // at least 2^-105, so that a masked score (-inf) times it and a page's scale (2^-40
+          // and more) stays one; a score so scaled is below 2^-40
+          if (piece == 0) up[row] = fmaxf(fabsf(a.scale_log2) * pow2i(qe), 0x1p-105f);
+          sts128(sm + Sh::kQ + (piece >> 3) * kRQHalf + row * 128 + (((piece & 7) ^ (row & 7)) << 4),
+                 make_uint4(f16x2_rn(bf16_lo(x[y].x) * down, bf16_hi(x[y].x) * down),
+                            f16x2_rn(bf16_lo(x[y].y) * down, bf16_hi(x[y].y) * down),
+                            f16x2_rn(bf16_lo(x[y].z) * down, bf16_hi(x[y].z) * down),
+                            f16x2_rn(bf16_lo(x[y].w) * down, bf16_hi(x[y].w) * down)));
+          x[y] = ahead[y];
+        }
+        if (g < 2) load_q(g + 2, ahead);
       }
     }
     {
@@ -397,12 +416,14 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       tc_fence_after();
       const uint32_t t_s = t_lane + Sh::kS + e * kRBlock;
       const float4* in = info + (blk & (kRInfos - 1)) * kRPages;
-      // Which rows of two pages this query keeps, 16 bits each; only looked at where some
-      // query of the CTA does not keep some row of the block.
-      uint32_t keep[kRPages / 2] = {0xffffffffu, 0xffffffffu};
+      uint32_t s[kRPages][16];
+#pragma unroll
+      for (int x = 0; x < kRPages; ++x)
+        if (x < present) tmem_load<16>(t_s + 16 * x, s[x]);
+      tc_wait_ld();
       const int j_last = page_of(blk * kRPages + present - 1) * 16 + 15;
-      const bool masked = j_last >= P || j_last > i_first;
-      if (masked) {
+      if (j_last >= P || j_last > i_first) {
+        // some query does not keep some row: scores that this one does not keep become -inf
 #pragma unroll
         for (int x = 0; x < kRPages; ++x) {
           if (x < present) {
@@ -421,38 +442,26 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
               const int np = P - j0;    // prompt rows of the page
               on &= win | (np <= 0 ? 0u : (1u << min(np, 16)) - 1u);
             }
-            keep[x / 2] &= x & 1 ? (on << 16) | 0xffffu : on | 0xffff0000u;
+            if (!__all_sync(0xffffffffu, on == 0xffffu)) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                if (!((on >> q) & 1u)) s[x][q] = 0xff800000u;
+            }
           }
         }
       }
-      // The scores of two pages; -inf where the query does not keep the row.
-      auto scores = [&](int h, uint32_t (&s)[32]) {
-        tmem_load<32>(t_s + 32 * h, s);
-        tc_wait_ld();
-        if (masked && !__all_sync(0xffffffffu, keep[h] == 0xffffffffu)) {
-#pragma unroll
-          for (int q = 0; q < 32; ++q)
-            if (!((keep[h] >> q) & 1u)) s[q] = 0xff800000u;
-        }
-      };
       float top = -INFINITY;  // the row's largest score
 #pragma unroll
-      for (int h = 0; h < kRPages / 2; ++h) {
-        if (2 * h < present) {
-          uint32_t s[32];
-          scores(h, s);
+      for (int x = 0; x < kRPages; ++x) {
+        if (x < present) {
+          float m[4];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float m[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              m[q] = fmaxf(max3(__uint_as_float(s[16 * y + q]), __uint_as_float(s[16 * y + 4 + q]),
-                                __uint_as_float(s[16 * y + 8 + q])),
-                           __uint_as_float(s[16 * y + 12 + q]));
-            const float2 pgi = *reinterpret_cast<const float2*>(in + 2 * h + y);
-            if (2 * h + y < present)
-              top = fmaxf(top, fmaf(fmaxf(max3(m[0], m[1], m[2]), m[3]), f * pgi.x, pgi.y));
-          }
+          for (int q = 0; q < 4; ++q)
+            m[q] = fmaxf(max3(__uint_as_float(s[x][q]), __uint_as_float(s[x][4 + q]),
+                              __uint_as_float(s[x][8 + q])),
+                         __uint_as_float(s[x][12 + q]));
+          const float2 pgi = *reinterpret_cast<const float2*>(in + x);
+          top = fmaxf(top, fmaf(fmaxf(max3(m[0], m[1], m[2]), m[3]), f * pgi.x, pgi.y));
         }
       }
       if (__any_sync(0xffffffffu, top > ref + (kRHead + kRSlack))) {
@@ -475,32 +484,28 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           }
         }
       }
-      // weights, packed over the scores already read
+      // weights, packed over the scores
 #pragma unroll
-      for (int h = 0; h < kRPages / 2; ++h) {
-        if (2 * h < present) {
-          uint32_t s[32], w[16];
-          scores(h, s);
+      for (int x = 0; x < kRPages; ++x) {
+        if (x < present) {
+          const float4 pgi = in[x];
+          const float c1 = f * pgi.x, c2 = pgi.y - ref;
+          const f32x2 a1 = pack2(c1, c1), a2 = pack2(c2, c2);
+          f32x2 sum = pack2(0.f, 0.f);
+          uint32_t w[8];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float4 pgi = in[2 * h + y];
-            const float c1 = f * pgi.x, c2 = pgi.y - ref;
-            const f32x2 a1 = pack2(c1, c1), a2 = pack2(c2, c2);
-            f32x2 sum = pack2(0.f, 0.f);
-#pragma unroll
-            for (int q = 16 * y; q < 16 * y + 16; q += 2) {
-              float z0, z1;
-              unpack2(fma2(pack2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), a1, a2), z0, z1);
-              z0 = ex2_approx(z0);
-              z1 = ex2_approx(z1);
-              sum = add2(sum, pack2(z0, z1));
-              w[q / 2] = f16x2_rn(z0, z1);
-            }
-            float u, t;
-            unpack2(sum, u, t);
-            if (2 * h + y < present) l = fmaf(u + t, pgi.z, l);
+          for (int q = 0; q < 16; q += 2) {
+            float z0, z1;
+            unpack2(fma2(pack2(__uint_as_float(s[x][q]), __uint_as_float(s[x][q + 1])), a1, a2), z0, z1);
+            z0 = ex2_approx(z0);
+            z1 = ex2_approx(z1);
+            sum = add2(sum, pack2(z0, z1));
+            w[q / 2] = f16x2_rn(z0, z1);
           }
-          tmem_store16(t_s + 16 * h, w);
+          tmem_store8(t_s + 8 * x, w);
+          float u, t;
+          unpack2(sum, u, t);
+          l = fmaf(u + t, pgi.z, l);
         }
       }
       tc_wait_st();
@@ -519,8 +524,9 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       const bool mine = t0 + (r >> LG) < t1;
       if (a.lse != nullptr && mine) a.lse[qh_of(r)] = (ref + log2f(l)) * kLn2;
       uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + qh_of(r) * kRD;
+      const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;  // rows are 256 bytes
       float probe = 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 4; ++h) {
         uint32_t o[32];
         tmem_load<32>(t_lane + Sh::kO + 32 * h, o);
@@ -532,9 +538,14 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           probe += u + t;
           w[q] = bf16x2_rn(u, t);
         }
-        if (mine) {
+        if (mine && wide) {
           stg256(to + 32 * h, w);
           stg256(to + 32 * h + 16, w + 8);
+        } else if (mine) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            reinterpret_cast<uint4*>(to + 32 * h)[q] =
+                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         }
       }
       tc_fence_before();
