@@ -17,8 +17,11 @@
 // columns and 16 warps measured a third slower).  The accumulators hold the output
 // transposed (dims x columns), which lets the weights go from the score accumulators to
 // the second product by movmatrix alone.
-// Measured: prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 694 us = 169 TFLOP/s of kept
-// pairs; quant_chunk_tc.cu serves the calls whose columns fit one of its tiles.
+// This kernel serves head_dim 64, calls with too few tiles to fill the GPU and calls whose
+// units are to be cut along their pages; the others go to quant_chunk_tc.cu (up to 32
+// columns) and quant_chunk_rows.cu.  Measured: 40 tokens over 3000 rows of one request,
+// 32/8 heads, head_dim 128: 36 us in 8 parts, 54 whole in quant_chunk_rows.cu.  (Prompts of 32 .. 512 rows of 128 requests, 32/8
+// heads, take 694 us here, 440 in quant_chunk_rows.cu.)
 //
 // Work split.  A CTA of 4 warps covers 32 KC columns (KC = 4 / KG column groups) of one
 // (request, kv head); KG warps share a column group and take its pages in turn, joined
@@ -521,7 +524,8 @@ cudaError_t launch_one(QuantChunkLaunch a, cudaStream_t s) {
     if (parts > most) parts = most;
     if (parts > kQuantMaxParts) parts = kQuantMaxParts;
   }
-  if (units > kMultiCounters || units * parts * Sh::KC * Sh::kStateWords * 32 > a.part_cap) parts = 1;
+  const int64_t hold = units > kMultiCounters ? 1 : a.part_cap / (units * Sh::KC * Sh::kStateWords * 32);
+  if (parts > hold) parts = hold;
   a.parts = parts < 1 ? 1 : static_cast<int32_t>(parts);
   if (units * a.parts > INT32_MAX) return cudaErrorInvalidValue;
   return launch_pdl(kern, dim3(static_cast<unsigned>(units * a.parts)), dim3(kCW * 32),

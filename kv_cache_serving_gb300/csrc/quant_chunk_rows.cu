@@ -4,23 +4,31 @@
 //
 // Mathematics as in quant_chunk.cu, with the queries on the lanes of tensor memory: a CTA
 // holds 128 rows (query token, head of the kv head's group) of one (request, kv head) and
-// walks its pages in blocks of 8 (128 cache rows):
-//   S (128 x 128) = Q K^T,   P = weights of S,   O (128 x 128) += P V
+// walks its pages in blocks of 4 (64 cache rows):
+//   S (128 x 64) = Q K^T,   P = weights of S,   O (128 x 128) += P V
 // so a thread owns a query: its running reference and sum are two registers, a page's
 // scales are constants of 16 of its scores, its mask is one shifted word per page, and P
-// goes back to tensor memory (over S, 16 columns read for 8 written) as the left operand
-// of the second product.  The reference follows the row's maximum (taken over the raw
-// scores of a page, then scaled once) when that passes it by 2^10.
+// goes back to tensor memory over S as the left operand of the second product.  The
+// reference follows the row's maximum (taken over the raw scores of a page, then scaled
+// once) when that passes it by 2^10.  A block that every query keeps whole is not masked.
 //
-// Two groups of 4 warps: one converts (K and V codes to fp16 in shared memory, four page
-// sides per warp and block, loads a block ahead), the other weighs, and one thread of it
-// issues the products (as a converter it would wait for the weights with the next block's
-// K unconverted: 128 tokens over 4096 rows of 8 requests,
-// 32/8 heads, take 108 us instead of 175).  A block's scores, weights and
-// second product follow each other within a CTA, its conversions run beside them, and two
-// CTAs per SM fill the gaps.
+// Nine warps: four weigh, four convert (K and V codes of a page each to fp16 in shared
+// memory), one issues the products.  S, P and K exist twice, so the scores of a block are
+// ready when the weights of the one before it are done; V once (its place is free again
+// before the next weights are).  Codes reach the converters by asynchronous copies into
+// shared memory: loads to registers are held up by the few KB of L1 that the tiles leave
+// (128 tokens over 4096 rows of 8 requests, 32/8 heads: 107 -> 97 us).  The issuing warp
+// elects its lane, which keeps the products' descriptors in uniform registers: issuing a
+// product took 150 cycles from a weighing thread and takes 60.  The unrolled prologue was an instruction-cache
+// miss per tile; as loops of four rows it brought prompts from 485 to 447 us.
 //
-// What bounds it: see the figures at quant_chunk_rows_fits.
+// What bounds it: latency and instruction issue of the weighing and the prologue, not the
+// products (11% of the tensor pipe) and not HBM.  Of a tile of prompts (3.5 blocks on
+// average) 2.3 K cycles go by until its sizes and tensor memory are there, 7 K until q is
+// converted and the first scores exist, 3 K per block, 4 K for the output; two CTAs per SM
+// fill each other's gaps to 1.3 instructions per cycle.
+// Measured: prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 440 us = 267 TFLOP/s of kept
+// pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 406 us (1017).
 #include <math.h>
 
 #include <type_traits>
@@ -592,11 +600,20 @@ cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
 
 }  // namespace
 
+// Which calls this kernel takes: more than 32 rows (fewer are quant_chunk_tc.cu's), when
+// their tiles are a quarter of the SMs or more: a tile is never cut along its pages, and
+// quant_chunk.cu, which cuts them, was ahead at 32 tiles of 4000 rows (62 / 70 us) and
+// behind at 48 (78 / 70).  Measured against the other two (us, this kernel / quant_chunk_tc.cu or
+// quant_chunk.cu, batch x kv heads x group, tokens, rows):
+//   up to 32 rows of a tile:  128x8x4, 8, 500: 71 / 57;  64x32x1, 32, 1000: 195 / 168
+//   33 .. 64:                 128x8x4, 16, 300: 54 / 77 and 80;  64x32x1, 40, 200: 82 / 98
+//   more:                     64x8x4, 128, 256: 90 / 150;  8x8x4, 128, 4096: 97 / 271;
+//                             8x8x4, 2048, 2048: 406 / 1017
 bool quant_chunk_rows_fits(const QuantChunkLaunch& a) {
   const int64_t rows = static_cast<int64_t>(a.max_q) << a.group_log2;
-  if (rows <= 64 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
+  if (rows <= 32 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
   return a.split_setting == 1 ||
-         (rows + kRRows - 1) / kRRows * a.batch * a.hkv * 2 >= a.sms;
+         (rows + kRRows - 1) / kRRows * a.batch * a.hkv * 4 >= a.sms;
 }
 
 cudaError_t launch_quant_chunk_rows(const QuantChunkLaunch& a, cudaStream_t s) {

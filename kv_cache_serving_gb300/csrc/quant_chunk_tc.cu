@@ -1,19 +1,19 @@
 // quant_chunk_tc.cu -- several query tokens per request over the 8-bit paged K/V cache
-// on the 5th-generation tensor cores (head_dim 128).
+// on the 5th-generation tensor cores (head_dim 128), for chunks of up to 32 (query token,
+// head) columns: speculative steps, the rows of an image.
 //
-// Mathematics as in quant_chunk.cu.  A CTA holds N = 32 or 64 columns (query token,
-// head of the kv head's group) of one (request, kv head) and walks its pages in blocks
-// of 8 (128 rows).  Per block, both products have the rows or the head's dims on the 128
-// lanes of tensor memory and the columns along it:
-//   S  (128 rows x N) = K (128 x 128) Q^T,      O^T (128 dims x N) += V^T (128 x 128 rows) P
-// so any number of columns fits without waste, a row's scales and its place in the
-// mask are constants of a thread, and the weights (rows x columns) are written as they
-// are held: a thread stores its row's columns side by side, which is the B operand with
-// the contraction in the rows.
+// Mathematics as in quant_chunk.cu.  A CTA holds the 32 columns of one (request, kv head)
+// and walks its pages in blocks of 8 (128 rows).  Per block, both products have the rows
+// or the head's dims on the 128 lanes of tensor memory and the columns along it:
+//   S  (128 rows x 32) = K (128 x 128) Q^T,    O^T (128 dims x 32) += V^T (128 x 128 rows) P
+// so few columns fit without the waste of queries on 128 lanes, a row's scales and its
+// place in the mask are constants of a thread, and the weights (rows x columns) are written
+// as they are held: a thread stores its row's columns side by side, which is the B operand
+// with the contraction in the rows.
 //
 // K and V become fp16 on the way into shared memory (a warp converts one page: 4 loads
-// of 512 bytes, swizzled 16-byte stores), once for all N columns.  q enters as fp16
-// scaled by one power of two per CTA.  The softmax of a block is 128 N elements over 256
+// of 512 bytes, swizzled 16-byte stores), once for all columns.  q enters as fp16, a column
+// scaled by its own power of two.  The softmax of a block is 128 x 32 elements over 256
 // threads: z = s * (q and K scale) + (log2 of the V scale - reference), weight 2^z, sum +=
 // weight / V scale.  The reference of a column moves only when a weight would pass 2^15
 // (a vote at the barrier the block has anyway); then the sums and the accumulators in
@@ -25,7 +25,7 @@
 // conversions are 130 and the softmax 300.  Two CTAs per SM, so that one converts while the
 // other's products run; the next block's K and V are loaded an iteration ahead, past the
 // L1 (whose 20 KB keep page ids, masks and spills).  Measured: 32 tokens of 64 requests of 320 ..
-// 1280 rows under the mask, 32/32 heads: 90 us (136 with quant_chunk.cu).  A persistent
+// 1280 rows under the mask, 32/32 heads: 85 us (136 with quant_chunk.cu).  A persistent
 // form (tiles of several units in one CTA, the next tile's q and first block ahead)
 // measured slower: 141 us, its second set of tile values spills.
 #include <math.h>
@@ -44,25 +44,25 @@ namespace {
 constexpr int kTD = 128;           // head_dim
 constexpr int kTRows = 128;        // rows per block
 constexpr int kTPages = 8;         // pages per block: one per warp
+constexpr int kTCols = 32;         // columns: (query token, head of the group)
 constexpr int kTThreads = 256;
 constexpr float kTHead = 4.f;      // the reference stands for 2^4
 
-template <int N>
 struct TcShape {
   static constexpr int kHalf = kTRows * 128;             // 64 dims of a block, fp16
   static constexpr int kK = 0, kV = 2 * kHalf;
-  static constexpr int kPRow = N * 2;                      // bytes of a row of weights
+  static constexpr int kPRow = kTCols * 2;                      // bytes of a row of weights
   static constexpr int kP = 4 * kHalf;
-  static constexpr int kQ = kP + kTRows * kPRow;           // two halves of N rows x 128 B
-  static constexpr int kInfo = kQ + 2 * N * 128;           // 2 x 8 int4: needed rows, scales
-  static constexpr int kRef = kInfo + 2 * kTPages * 16;    // ref, head - ref, factor: N each
-  static constexpr int kMax = kRef + 3 * N * 4;            // 4 x N column maxima / sums
-  static constexpr int kUp = kMax + 4 * N * 4;             // score factor of a column: N floats
-  static constexpr int kBar = kUp + 4 * N;                  // two barriers, address, flags
+  static constexpr int kQ = kP + kTRows * kPRow;           // two halves of kTCols rows x 128 B
+  static constexpr int kInfo = kQ + 2 * kTCols * 128;           // 2 x 8 int4: needed rows, scales
+  static constexpr int kRef = kInfo + 2 * kTPages * 16;    // ref, head - ref, factor: kTCols each
+  static constexpr int kMax = kRef + 3 * kTCols * 4;            // 4 x kTCols column maxima / sums
+  static constexpr int kUp = kMax + 4 * kTCols * 4;             // score factor of a column: kTCols floats
+  static constexpr int kBar = kUp + 4 * kTCols;                  // two barriers, address, flags
   static constexpr int kMask = kBar + 32;
   static constexpr int kSlack = 1024;                      // the base is rounded up to 1024
   // tensor memory: S, O^T, and two copies of every row's part of the columns' sums
-  static constexpr int kS = 0, kO = N, kL = 2 * N, kTmem = 4 * N;
+  static constexpr int kS = 0, kO = kTCols, kL = 2 * kTCols, kTmem = 4 * kTCols;
   static int smem(int words) { return kSlack + kMask + 4 * words; }
 };
 
@@ -93,18 +93,19 @@ __device__ __forceinline__ float scatter_max(float (&v)[16], int lane) {
   return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-template <int N, int LG>
+template <int LG>
 __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const QuantChunkLaunch a) {
-  using Sh = TcShape<N>;
-  constexpr int W = N / 2;              // columns per warp ...
+  using Sh = TcShape;
+  constexpr int W = kTCols / 2;              // columns per warp ...
   constexpr int kChunks = W / 16;       // ... in pieces of 16
-  constexpr int per_cta = N >> LG;      // query tokens per CTA
+  constexpr int per_cta = kTCols >> LG;      // query tokens per CTA
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sm = smem_addr(smem);
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the warp's
   const int wq = warp & 3, cg = warp >> 2;  // lane quarter of tensor memory, column half
   const int qt = blockIdx.x, hk = blockIdx.y, bpos = blockIdx.z;
   const int b = a.order != nullptr ? __ldg(a.order + bpos) : bpos;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   if (code != 0) {
     // q_len is not trusted: NaN into every slot of the unit
     if (qt == 0 && hk == 0 && tid == 0) set_error(a.err, code);
-    for (int x = tid; x < N * kTD; x += kTThreads) {
+    for (int x = tid; x < kTCols * kTD; x += kTThreads) {
       const int t = t0 + x / (kTD << LG);
       if (t >= a.max_q) break;
       const size_t qh = (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << LG) +
@@ -154,8 +155,8 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
 
   int4* info = reinterpret_cast<int4*>(smem + Sh::kInfo);
   float* ref = reinterpret_cast<float*>(smem + Sh::kRef);
-  float* nref = ref + N;
-  float* fac = ref + 2 * N;
+  float* nref = ref + kTCols;
+  float* fac = ref + 2 * kTCols;
   float* cmax = reinterpret_cast<float*>(smem + Sh::kMax);
   float* up = reinterpret_cast<float*>(smem + Sh::kUp);
   uint64_t* s_done = reinterpret_cast<uint64_t*>(smem + Sh::kBar);
@@ -165,8 +166,8 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   volatile int* redo = failed + 1;
   uint32_t* msk = reinterpret_cast<uint32_t*>(smem + Sh::kMask);
 
-  // q: a thread holds 128 N / 256 elements of one column
-  constexpr int kTpc = kTThreads / N;       // threads per column
+  // q: a thread holds 128 kTCols / 256 elements of one column
+  constexpr int kTpc = kTThreads / kTCols;       // threads per column
   constexpr int kQE = kTD / kTpc;           // elements per thread
   const int qcol = tid / kTpc, qd0 = (tid % kTpc) * kQE;
   uint4 qv[kQE / 8];
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     *failed = 0;
     *redo = 0;
   }
-  if (tid < N) {
+  if (tid < kTCols) {
     ref[tid] = -INFINITY;
     nref[tid] = INFINITY;
   }
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[k] = f16x2_rn(bf16_lo(w[k]) * down, bf16_hi(w[k]) * down);
       const int d = qd0 + 8 * i, piece = (d & 63) >> 3;
-      sts128(sm + Sh::kQ + (d >> 6) * (N * 128) + qcol * 128 + ((piece ^ (qcol & 7)) << 4),
+      sts128(sm + Sh::kQ + (d >> 6) * (kTCols * 128) + qcol * 128 + ((piece ^ (qcol & 7)) << 4),
              make_uint4(h[0], h[1], h[2], h[3]));
     }
   }
@@ -317,20 +318,20 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   load_codes(a.k, cur, kreg);
   load_codes(a.v, cur, vreg);
   int pg = page_of(kTPages + warp) == kTPages + warp ? spec1 : load_page(1);
-  const uint32_t tmem = *tmem_slot;
-  constexpr uint32_t kIdS = tc_idesc(128, N, false), kIdO = tc_idesc(128, N, true);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  constexpr uint32_t kIdS = tc_idesc(128, kTCols, false), kIdO = tc_idesc(128, kTCols, true);
   // Operand descriptors differ by whole multiples of their address unit (16 bytes) from one
   // step of a product to the next, so a step is an addition.
   const uint64_t k_desc = tc_desc(sm + Sh::kK, 16, 1024, kSwizzle128);
   const uint64_t q_desc = tc_desc(sm + Sh::kQ, 16, 1024, kSwizzle128);
   const uint64_t v_desc = tc_desc(sm + Sh::kV, Sh::kHalf, 1024, kSwizzle128);
   const uint64_t p_desc =
-      tc_desc(sm + Sh::kP, 16, 8 * Sh::kPRow, N == 64 ? kSwizzle128 : kSwizzle64);
+      tc_desc(sm + Sh::kP, 16, 8 * Sh::kPRow, kSwizzle64);
   auto issue_s = [&]() {  // S = K Q^T
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       tc_mma_f16(tmem + Sh::kS, k_desc + (((k >> 2) * Sh::kHalf + (k & 3) * 32) >> 4),
-                 q_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS, k > 0);
+                 q_desc + (((k >> 2) * (kTCols * 128) + (k & 3) * 32) >> 4), kIdS, k > 0);
     tc_commit(s_done);
   };
   auto issue_o = [&](bool first, int present) {  // O^T += V^T P, a step for each page
@@ -354,9 +355,10 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   }
   fence_proxy_async_smem();
   __syncthreads();
-  if (tid == 0) {
+  if (warp == 0) {
     tc_fence_after();
-    issue_s();
+    if (elect_one()) issue_s();
+    __syncwarp();
   }
 
   // this thread's row of a block: lane 32 wq + lane of tensor memory
@@ -442,11 +444,12 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     // weights of the row, stored as the B operand; the row's part of the columns' sums,
     // from copy blk % 2 to the other one
     const float wsum = here ? inv : 0.f;
-    const uint32_t l_old = t_lane + Sh::kL + (blk & 1) * N, l_new = t_lane + Sh::kL + (~blk & 1) * N;
+    const uint32_t l_old = t_lane + Sh::kL + (blk & 1) * kTCols;
+    const uint32_t l_new = t_lane + Sh::kL + (~blk & 1) * kTCols;
     const uint32_t p_at = sm + Sh::kP + row * Sh::kPRow;
     auto p_piece = [&](int i) {  // 16-byte piece i of the warp's columns
       const int piece = cg * (W / 8) + i;
-      return p_at + ((N == 64 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3)) << 4);
+      return p_at + ((piece ^ ((row >> 1) & 3)) << 4);
     };
     auto softmax = [&](bool rescale) -> bool {
       const f32x2 c2 = pack2(c1, c1), lv2 = pack2(lv, lv), inv2 = pack2(wsum, wsum);
@@ -543,14 +546,14 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
                      ? fmaf(__uint_as_float(s[c]), c1 * up[cg * W + 16 * q + c], lv)
                      : -INFINITY;
         const float m = scatter_max(y, lane);
-        if ((lane & 1) == 0) cmax[wq * N + cg * W + 16 * q + (lane >> 1)] = m;
+        if ((lane & 1) == 0) cmax[wq * kTCols + cg * W + 16 * q + (lane >> 1)] = m;
       }
       __syncthreads();
-      if (tid < N) {
+      if (tid < kTCols) {
         float m = ref[tid];
         const float was = m;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) m = fmaxf(m, cmax[q * N + tid]);
+        for (int q = 0; q < 4; ++q) m = fmaxf(m, cmax[q * kTCols + tid]);
         fac[tid] = m == was ? 1.f : ex2_approx(was - m);
         ref[tid] = m;
         nref[tid] = kTHead - m;
@@ -576,31 +579,34 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
       __syncthreads();
     }
     ok = *failed == 0;
-    if (tid == 0 && ok) {
+    if (warp == 0 && ok) {
       tc_fence_after();
-      issue_o(blk == 0, min(kTPages, pages - blk * kTPages));
-      if (blk + 1 < nblocks) issue_s();
+      if (elect_one()) {
+        issue_o(blk == 0, min(kTPages, pages - blk * kTPages));
+        if (blk + 1 < nblocks) issue_s();
+      }
+      __syncwarp();
     }
   }
   // sums of the columns over all rows
 #pragma unroll
   for (int q = 0; q < kChunks; ++q) {
     uint32_t lr[16];
-    tmem_load<16>(t_lane + Sh::kL + (nblocks & 1) * N + 16 * q, lr);
+    tmem_load<16>(t_lane + Sh::kL + (nblocks & 1) * kTCols + 16 * q, lr);
     tc_wait_ld();
     float v[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(lr[c]);
     const float t = reduce_scatter<16>(v, lane);
-    if ((lane & 1) == 0) cmax[wq * N + cg * W + 16 * q + (lane >> 1)] = t;
+    if ((lane & 1) == 0) cmax[wq * kTCols + cg * W + 16 * q + (lane >> 1)] = t;
   }
   if (ok) ok = mbar_wait(o_done, (nblocks - 1) & 1);
   if (!ok) *failed = 1;
   __syncthreads();
   ok = *failed == 0;
   if (ok) {
-    if (tid < N) {
-      const float t = cmax[tid] + cmax[N + tid] + cmax[2 * N + tid] + cmax[3 * N + tid];
+    if (tid < kTCols) {
+      const float t = cmax[tid] + cmax[kTCols + tid] + cmax[2 * kTCols + tid] + cmax[3 * kTCols + tid];
       fac[tid] = 1.f / t;
       if (a.lse != nullptr && t0 + (tid >> LG) < t1)
         a.lse[qh_of(tid)] = (ref[tid] - kTHead + log2f(t)) * kLn2;
@@ -644,21 +650,21 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     tmem_dealloc<Sh::kTmem>(tmem);
   }
   if (ok && *redo != 0)
-    for (int col = warp; col < N; col += kTThreads / 32)
+    for (int col = warp; col < kTCols; col += kTThreads / 32)
       if (t0 + (col >> LG) < t1)
         quant_redo_query<kTD>(a, b, hk, L - n + t0 + (col >> LG), P, Wn, qh_of(col), lane);
 }
 
-template <int N, int LG>
+template <int LG>
 cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
-  auto kern = quant_chunk_tc_kernel<N, LG>;
-  const int smem = TcShape<N>::smem(a.max_window / 32 + 1);
+  auto kern = quant_chunk_tc_kernel<LG>;
+  const int smem = TcShape::smem(a.max_window / 32 + 1);
   static KernelSlots cache;
   int per_sm = 0;
   const cudaError_t e =
       cache.get(reinterpret_cast<const void*>(kern), kTThreads, smem, &per_sm);
   if (e != cudaSuccess) return e;
-  constexpr int per_cta = N >> LG;
+  constexpr int per_cta = kTCols >> LG;
   return launch_pdl(kern, dim3((a.max_q + per_cta - 1) / per_cta, a.hkv, a.batch), dim3(kTThreads),
                     static_cast<size_t>(smem), s, a);
 }
@@ -667,23 +673,21 @@ cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
 
 // Which calls this kernel takes: those whose (request, kv head) is one tile, when there are
 // enough of them to fill half the GPU (a tile is never cut along its pages).  Measured
-// against quant_chunk.cu, which serves the others (us, this kernel / that one, batch x kv
-// heads x group, tokens, rows): 64x32x1, 32, 300: 84 / 114; 128x8x4, 8, 500: 59 / 82;
-// 128x8x4, 16, 300: 74 / 80; 128x8x4, 64, 300: 241 / 193; 64x8x4, 128, 256: 191 / 151;
-// 128x8x4, 512, 512: 1659 / 1299.
+// against quant_chunk.cu (us, this kernel / that one, batch x kv heads x group, tokens,
+// rows): 64x32x1, 32, 300: 80 / 114; 128x8x4, 8, 500: 57 / 82; 128x8x4, 8, 2000: 169 / 235;
+// 128x8x4, 4, 1000: 94 / 121.  Against quant_chunk_rows.cu: see there.
 bool quant_chunk_tc_fits(const QuantChunkLaunch& a) {
   const int64_t columns = static_cast<int64_t>(a.max_q) << a.group_log2;
-  if (columns > 64 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
+  if (columns > 32 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
   return a.split_setting == 1 || static_cast<int64_t>(a.batch) * a.hkv * 2 >= a.sms;
 }
 
 cudaError_t launch_quant_chunk_tc(const QuantChunkLaunch& a, cudaStream_t s) {
-  const bool few = (static_cast<int64_t>(a.max_q) << a.group_log2) <= 32;
   switch (a.group_log2) {
-    case 0: return few ? launch_one<32, 0>(a, s) : launch_one<64, 0>(a, s);
-    case 1: return few ? launch_one<32, 1>(a, s) : launch_one<64, 1>(a, s);
-    case 2: return few ? launch_one<32, 2>(a, s) : launch_one<64, 2>(a, s);
-    default: return few ? launch_one<32, 3>(a, s) : launch_one<64, 3>(a, s);
+    case 0: return launch_one<0>(a, s);
+    case 1: return launch_one<1>(a, s);
+    case 2: return launch_one<2>(a, s);
+    default: return launch_one<3>(a, s);
   }
 }
 

@@ -669,6 +669,28 @@ def test_chunk_ignores_unread_rows(split):
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("split", [1, 2], indirect=True)
+@pytest.mark.parametrize("d,n", [(64, 20), (128, 6), (128, 20)])
+def test_chunk_of_16_byte_alignment(d, n, split):
+    """q and out that begin 16 bytes into their memory: the same bits as whole ones."""
+    w = wl.generate(case(d, 4, batch=2, hkv=2, lo=100, hi=160, prompt=(40, 60), W=64, seed=31))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    gen = torch.Generator().manual_seed(2)
+    q = torch.randn(2, n, w["hq"], d, generator=gen).to(torch.bfloat16).cuda()
+    ql = torch.full((2,), n, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    qb.prefill_sparse(q, ql, out, None)
+    flat = [torch.full((q.numel() + 16,), SENTINEL, dtype=q.dtype, device="cuda") for _ in range(2)]
+    q2, out2 = (f[8:8 + q.numel()].view(q.shape) for f in flat)
+    q2.copy_(q)
+    qb.prefill_sparse(q2, ql, out2, None)
+    torch.cuda.synchronize()
+    assert qb.batch.device_error() == 0
+    assert torch.equal(out, out2)
+    edge = torch.cat([flat[1][:8], flat[1][8 + q.numel():]])
+    assert (edge == torch.tensor(SENTINEL, dtype=q.dtype, device="cuda")).all()
+
+
 @pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
 @pytest.mark.parametrize("d,g,n", [(64, 2, 20), (128, 1, 20), (128, 4, 9), (128, 4, 40), (128, 2, 80)])
 def test_chunk_queries_of_unlike_sizes(d, g, n, split):
