@@ -8,9 +8,11 @@
 // top 32 bits (error 2^-32 turns) with sincospi.
 //
 // Bound by HBM: each element is read and written once.  A CTA computes the table of
-// its tokens' sines and cosines in shared memory once for all heads, then streams the
-// heads; a thread handles 8 pairs (two 16-byte loads and stores with bf16).  Measured: q
-// and k of 65 K tokens, 32/8 heads of 128, two axes: 223 us = 0.88 of the copy rate.
+// its tokens' cosines and sines in shared memory once for all heads, then streams the
+// heads; a thread handles 8 pairs (two 16-byte loads and stores with bf16, each in a line
+// of its lanes' own; the table is swizzled against bank conflicts).  Measured: q and k of
+// 65 K tokens, 32/8 heads of 128, two axes: 201 us = 0.98 of the copy rate (227 with 8 pairs
+// side by side and a plain table, whose conflicts kept the L1 pipe 91% busy).
 #include <math.h>
 
 #include "common.cuh"
@@ -52,22 +54,31 @@ __device__ __forceinline__ void store8(void* p, size_t at, const float (&x)[8]) 
   }
 }
 
-// 8 pairs p0 .. p0 + 7 of the head at element `at`.
+// Place of 16-byte unit u (the cosines and sines of two pairs) in a token's table: 8 lanes
+// that read units 4 l + j, or 2 l + j, then find 8 different banks.
+__device__ __forceinline__ int table_unit(int u) { return u ^ ((u >> 3) & 3); }
+
+// The l-th 8 pairs of the head at element `at`: pairs 8 l .., or (NEAR) 4 l .. and
+// D / 4 + 4 l .., so that either way 8 lanes read and write whole lines.
 template <int D, bool BF16, bool NEAR>
 __device__ __forceinline__ void rotate8(const void* in, size_t at_in, void* out, size_t at_out,
-                                        int p0, const float2* cs) {
-  const int lo = NEAR ? 2 * p0 : p0, hi = NEAR ? 2 * p0 + 8 : p0 + D / 2;
+                                        int l, const float4* cs) {
+  const int lo = 8 * l, hi = 8 * l + D / 2;
   float u[8], v[8];
   load8<BF16>(in, at_in + lo, u);
   load8<BF16>(in, at_in + hi, v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 t = cs[p0 + i];
-    float& x = NEAR ? (i < 4 ? u[2 * i] : v[2 * i - 8]) : u[i];
-    float& y = NEAR ? (i < 4 ? u[2 * i + 1] : v[2 * i - 7]) : v[i];
-    const float rx = x * t.x - y * t.y, ry = y * t.x + x * t.y;
-    x = rx;
-    y = ry;
+  for (int i = 0; i < 4; ++i) {  // pairs 2 i and 2 i + 1 of the eight
+    const float4 t = cs[table_unit(!NEAR ? 4 * l + i : i < 2 ? 2 * l + i : D / 8 + 2 * l + i - 2)];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float c = k ? t.z : t.x, n = k ? t.w : t.y;
+      float& x = !NEAR ? u[2 * i + k] : i < 2 ? u[4 * i + 2 * k] : v[4 * i - 8 + 2 * k];
+      float& y = !NEAR ? v[2 * i + k] : i < 2 ? u[4 * i + 2 * k + 1] : v[4 * i - 7 + 2 * k];
+      const float rx = x * c - y * n, ry = y * c + x * n;
+      x = rx;
+      y = ry;
+    }
   }
   store8<BF16>(out, at_out + lo, u);
   store8<BF16>(out, at_out + hi, v);
@@ -76,7 +87,7 @@ __device__ __forceinline__ void rotate8(const void* in, size_t at_in, void* out,
 template <int D, bool QBF, bool KBF, bool NEAR, int TT>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeLaunch a) {
   constexpr int kPairs = D / 2, kGroups = kPairs / 8;
-  __shared__ float2 cs[TT][kPairs];
+  __shared__ float4 cs[TT][kPairs / 2];
   griddep_wait();
   griddep_launch_dependents();
   const int t0 = blockIdx.x * TT, nt = min(TT, a.tokens - t0);
@@ -88,21 +99,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeLaunch a) 
     const float half = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
     float s, c;
     sincospif(half, &s, &c);
-    cs[t][i] = make_float2(c, s);
+    reinterpret_cast<float2*>(&cs[t][table_unit(i >> 1)])[i & 1] = make_float2(c, s);
   }
   __syncthreads();
   const int nq = a.q != nullptr ? a.hq : 0, nk = a.k != nullptr ? a.hkv : 0;
   const int per = (nq + nk) * kGroups;
   for (int x = threadIdx.x; x < nt * per; x += kRopeThreads) {
     const int t = x / per, y = x % per;
-    const int h = y / kGroups, p0 = 8 * (y % kGroups);
+    const int h = y / kGroups, l = y % kGroups;
     const size_t tok = static_cast<size_t>(t0 + t);
     if (h < nq)
       rotate8<D, QBF, NEAR>(a.q, tok * a.q_stride + static_cast<size_t>(h) * D, a.q_out,
-                            tok * a.q_out_stride + static_cast<size_t>(h) * D, p0, cs[t]);
+                            tok * a.q_out_stride + static_cast<size_t>(h) * D, l, cs[t]);
     else
       rotate8<D, KBF, NEAR>(a.k, tok * a.k_stride + static_cast<size_t>(h - nq) * D, a.k_out,
-                            tok * a.k_out_stride + static_cast<size_t>(h - nq) * D, p0, cs[t]);
+                            tok * a.k_out_stride + static_cast<size_t>(h - nq) * D, l, cs[t]);
   }
 }
 
