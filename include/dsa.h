@@ -656,8 +656,8 @@ dsa_status dsa_decode_sparse_masked_quant(const dsa_dims* dims, const void* q,
  * query tokens per request, each over its own causal kept set (their rows
  * already written with dsa_quant_write).  Arguments and errors as there; q and out
  * are bf16 (q_dtype), else DSA_ERR_UNSUPPORTED.  dsa_set_prefill_split applies: with 1
- * no unit is cut along its rows, with n >= 2 every unit the workspace holds is cut into
- * n parts, with 0 each call picks.
+ * no unit is cut along its rows, with n >= 2 every unit is cut into n parts (fewer where
+ * the workspace does not hold them), with 0 each call picks.
  */
 dsa_status dsa_prefill_sparse_quant(const dsa_dims* dims, int32_t max_q, const void* q,
                                     const dsa_quant_cache* cache, const int32_t* page_table,

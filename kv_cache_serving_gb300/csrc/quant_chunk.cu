@@ -21,7 +21,7 @@
 // units are to be cut along their pages; the others go to quant_chunk_tc.cu (up to 32
 // columns) and quant_chunk_rows.cu.  Measured: 40 tokens over 3000 rows of one request,
 // 32/8 heads, head_dim 128: 36 us in 8 parts, 54 whole in quant_chunk_rows.cu.  (Prompts of 32 .. 512 rows of 128 requests, 32/8
-// heads, take 694 us here, 440 in quant_chunk_rows.cu.)
+// heads, take 694 us here, 432 in quant_chunk_rows.cu.)
 //
 // Work split.  A CTA of 4 warps covers 32 KC columns (KC = 4 / KG column groups) of one
 // (request, kv head); KG warps share a column group and take its pages in turn, joined

@@ -27,7 +27,7 @@
 // average) 2.3 K cycles go by until its sizes and tensor memory are there, 7 K until q is
 // converted and the first scores exist, 3 K per block, 4 K for the output; two CTAs per SM
 // fill each other's gaps to 1.3 instructions per cycle.
-// Measured: prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 440 us = 267 TFLOP/s of kept
+// Measured: prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 432 us = 271 TFLOP/s of kept
 // pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 406 us (1017).
 #include <math.h>
 
@@ -348,7 +348,10 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     // q as fp16, a row (query token, head) scaled by its own power of two: a query's result
     // does not hang on the others of its tile.  The scale's sign goes into q, so that a
     // page's largest score is its largest product.  16 lanes a row.
-    {
+    // A warp without a query has nothing to weigh (what its rows of S and O hold is theirs
+    // alone): it keeps the blocks' count and no more.
+    const bool idle = t0 + (32 * warp >> LG) >= t1;
+    if (!idle) {
       const int piece = lane & 15, r0 = 32 * warp + (lane >> 4);
       auto load_q = [&](int g, uint4 (&x)[4]) {
 #pragma unroll
@@ -418,9 +421,13 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     for (int blk = 0; blk < nblocks; ++blk) {
       const int e = blk & 1, present = min(kRPages, pages - blk * kRPages);
       const uint32_t phase = static_cast<uint32_t>(blk >> 1) & 1u;
-      ok = mbar_wait(i_full + e, phase) && mbar_wait(s_done + e, phase) && ok;
+      ok = mbar_wait(i_full + e, phase) && (idle || mbar_wait(s_done + e, phase)) && ok;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      if (idle) {
+        if (lane == 0) mbar_arrive(p_full + e);
+        continue;
+      }
       tc_fence_after();
       const uint32_t t_s = t_lane + Sh::kS + e * kRBlock;
       const float4* in = info + (blk & (kRInfos - 1)) * kRPages;
@@ -522,11 +529,11 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       if (!ok) break;
       if (lane == 0) mbar_arrive(p_full + e);
     }
-    if (ok)
+    if (ok && !idle)
       ok = mbar_wait(o_done + ((nblocks - 1) & 1), static_cast<uint32_t>((nblocks - 1) >> 1) & 1u);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *failed = 1;
-    if (ok) {
+    if (ok && !idle) {
       tc_fence_after();
       const float inv = 1.f / l;
       const bool mine = t0 + (r >> LG) < t1;
