@@ -900,6 +900,94 @@ def test_two_streams_with_their_own_workspaces():
             assert torch.equal(got[0], exp[0]) and torch.equal(got[1], exp[1])
 
 
+@pytest.mark.parametrize("n", [4, 20, 70])
+def test_chunks_in_a_graph_and_on_two_streams(n):
+    """Chunk calls of two batches, captured together and replayed, and issued on two streams
+    at once: the bits of eager calls made one after the other."""
+    runs = []
+    for seed in (1, 2):
+        w = wl.generate(case(128, 4, batch=12, hkv=2, lo=90, hi=400, prompt=(30, 60), W=64, seed=seed))
+        qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+        gen = torch.Generator().manual_seed(seed)
+        q = torch.randn(12, n, w["hq"], 128, generator=gen).to(torch.bfloat16).cuda()
+        runs.append((qb, q, torch.as_tensor(chunk_lens(w, n, seed).astype(np.int32)).cuda(),
+                     torch.full_like(q, SENTINEL), torch.full(q.shape[:3], SENTINEL, device="cuda")))
+    for r in runs:
+        r[0].prefill_sparse(*r[1:])
+    torch.cuda.synchronize()
+    want = [(r[3].clone(), r[4].clone()) for r in runs]
+    same = lambda: all(torch.equal(r[3], x) and torch.equal(r[4], y) for r, (x, y) in zip(runs, want))
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        for r in runs:
+            r[0].prefill_sparse(*r[1:], stream=stream)
+    for _ in range(3):
+        for r in runs:
+            r[3].fill_(SENTINEL), r[4].fill_(SENTINEL)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(10):
+        for r, s in zip(runs, streams):
+            r[0].prefill_sparse(*r[1:], stream=s)
+    torch.cuda.synchronize()
+    assert same() and all(r[0].batch.device_error() == 0 for r in runs)
+
+
+def test_offsets_past_32_bits():
+    """The same pages at the far end of a pool whose codes pass 2^32 bytes: the same bits."""
+    w = wl.generate(case(128, 4, batch=4, hkv=2, lo=60, hi=200, prompt=(30, 60), W=64, seed=37))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    bt = qb.batch
+    pages = bt.dims.num_pages
+    far = 2 ** 32 // (2 * 16 * 128) + 5
+    total = far + pages
+    k, v = (torch.empty(total, 2, 16, 128, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((total, 2), float("nan"), device="cuda") for _ in range(2))
+    for big, small in ((k, qb.k.view(torch.uint8)), (v, qb.v.view(torch.uint8)), (ks, qb.k_scale),
+                       (vs, qb.v_scale)):
+        big[far:] = small
+    cache = dsa.quant_cache(k, v, ks, vs)
+    dims = dsa.dsa_dims.from_buffer_copy(bt.dims)
+    dims.num_pages = total
+    table = torch.where(bt.page_table >= 0, bt.page_table + far, bt.page_table)
+    ws = dsa.alloc_workspace(dims, "cuda")
+    out = torch.empty_like(qb.out)
+    want = qb.decode_dense()[0].clone()
+    dsa.dsa_decode_dense_quant(dims, bt.q, cache, table, bt.seq_len, bt.scale, out, None, ws)
+    assert torch.equal(out, want)
+    want = qb.decode_sparse_masked()[0].clone()
+    dsa.dsa_decode_sparse_masked_quant(dims, bt.q, cache, table, bt.seq_len, bt.prompt_len, bt.window,
+                                       bt.keep_mask, bt.scale, out, None, ws)
+    assert torch.equal(out, want)
+    saved = dsa.dsa_get_prefill_split()
+    try:
+        for n, split in ((4, 1), (20, 1), (20, 2)):
+            dsa.dsa_set_prefill_split(split)
+            gen = torch.Generator().manual_seed(n)
+            q = torch.randn(4, n, w["hq"], 128, generator=gen).to(torch.bfloat16).cuda()
+            ql = torch.full((4,), n, dtype=torch.int32, device="cuda")
+            a, b = torch.empty_like(q), torch.empty_like(q)
+            qb.prefill_sparse(q, ql, a, None)
+            dsa.dsa_prefill_sparse_quant(dims, q, cache, table, bt.seq_len, ql, bt.prompt_len, bt.window,
+                                         bt.keep_mask, bt.scale, b, None, ws)
+            assert torch.equal(a, b)
+    finally:
+        dsa.dsa_set_prefill_split(saved)
+    rows = torch.randn(4, 3, 2, 128, device="cuda").to(torch.bfloat16)
+    dsa.dsa_quant_write(dims, cache, rows, -rows, table, bt.seq_len, None, ws)
+    qb.write(rows, -rows)
+    start, count = bt.seq_len - 40, torch.full_like(bt.seq_len, 40)
+    got = [torch.empty(4, 40, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    dsa.dsa_quant_read(dims, cache, table, bt.seq_len, start, count, got[0], got[1], ws)
+    dsa.dsa_quant_read(bt.dims, qb.cache, bt.page_table, bt.seq_len, start, count, got[2], got[3], bt.ws)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+    assert bt.device_error() == 0
+    dsa.check_device_error(ws, "far pages")
+
+
 def test_empty_batches():
     dims = dsa.make_dims(0, 8, 2, 64, 4, 2, 32, 1, 8, "bf16", "bf16")
     real = dsa.make_dims(1, 8, 2, 64, 4, 2, 32, 1, 8, "bf16", "bf16")
