@@ -64,19 +64,19 @@ FALLBACK_HBM_GBS = 6800.0
 # decode-kernel sources whose digest is `digest` and are reported as null
 # otherwise.
 NCU_TRAFFIC = {
-    "digest": "9f7d16093e2dc428",
+    "digest": "49f9c5ad99382229",
     "bytes": {
-        "mixed-serving-gqa4": 167971840,
-        "janus-pro-7b-like-32x32": 316328960,
+        "mixed-serving-gqa4": 167713536,
+        "janus-pro-7b-like-32x32": 316329472,
         "llamagen-xl-like-24x24": 21440768,
         "emu3-8b-like-90x90-gqa4": 3281408,
     },
 }
 
 # Sources the timed decode kernel (and its launch plan) is built from.
-DECODE_SOURCES = ("common.cuh", "decode.cuh", "warp_attn.cuh", "mma.cuh", "internal.h",
-                  "decode_bf16.cu", "decode_bf16_list.cu", "decode_bf16_mask.cu", "decode_f32.cu",
-                  "dsa_api.cu")
+DECODE_SOURCES = ("common.cuh", "decode.cuh", "rows.cuh", "warp_attn.cuh", "mma.cuh", "internal.h",
+                  "host.h", "decode_bf16.cu", "decode_bf16_list.cu", "decode_bf16_mask.cu",
+                  "decode_f32.cu", "dsa_api.cu")
 
 
 def kernel_digest() -> str:
