@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
 #pragma unroll
       for (int mt = 0; mt < NK; ++mt) {
         o[mt] = bf16x2_rn(st.acc[nt][mt][h] * r, st.acc[nt][mt][2 + h] * r);
-        nan_probe += st.acc[nt][mt][h] + st.acc[nt][mt][2 + h];
+        if (quant_redo_needed(l, st.ref[nt][h])) nan_probe += st.acc[nt][mt][h] + st.acc[nt][mt][2 + h];
       }
       uint4* to = reinterpret_cast<uint4*>(a.out + qh * D + g * (D / 8));
 #pragma unroll

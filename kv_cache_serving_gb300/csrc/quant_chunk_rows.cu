@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       tc_fence_before();
       // A NaN may come from a row of V that other queries of the CTA keep (weight 0 times
       // NaN): such a query is done again, from the rows it keeps.
-      unsigned nan = __ballot_sync(0xffffffffu, mine && probe != probe);
+      unsigned nan =
+          __ballot_sync(0xffffffffu, mine && probe != probe && quant_redo_needed(l, ref));
       __syncwarp();  // after the rows' first output
       while (nan != 0u) {
         const int rr = 32 * warp + __ffs(nan) - 1;

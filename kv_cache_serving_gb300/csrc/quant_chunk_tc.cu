@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   }
   if (ok && *redo != 0)
     for (int col = warp; col < kTCols; col += kTThreads / 32)
-      if (t0 + (col >> LG) < t1)
+      if (t0 + (col >> LG) < t1 && quant_redo_needed(fac[col], ref[col]))
         quant_redo_query<kTD>(a, b, hk, L - n + t0 + (col >> LG), P, Wn, qh_of(col), lane);
 }
 

@@ -15,6 +15,14 @@
 
 namespace dsa {
 
+// Whether a query whose output holds a NaN is to be done again, by its sum and reference.  Not
+// one whose sum is NaN too: a score of its own is NaN (or infinite), so all of its output is
+// -- unless its scores pass 2^20, where the rounding of the reference alone, up to half a
+// unit of its last place, can carry a weight past fp16.
+__device__ __forceinline__ bool quant_redo_needed(float l, float ref) {
+  return l == l || (fabsf(ref) >= 0x1p20f && fabsf(ref) < 1e38f);
+}
+
 // Query token at row i of request b, head row qh of q and out.
 template <int D>
 __device__ __noinline__ void quant_redo_query(const QuantChunkLaunch& a, int b, int hk, int i, int P,
