@@ -28,7 +28,7 @@
 // converted and the first scores exist, 3 K per block, 4 K for the output; two CTAs per SM
 // fill each other's gaps to 1.3 instructions per cycle.
 // Measured: prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 432 us = 271 TFLOP/s of kept
-// pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 406 us (1017).
+// pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 396 us (1017).
 #include <math.h>
 
 #include <type_traits>
@@ -243,51 +243,60 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   bool ok = true;
   if (converts) {
     // ================= converters: a page of every block, codes loaded a block ahead =========
+    // K goes a block ahead of V, so that the scores after next wait for no V.
     const uint32_t at_k = sm + Sh::kCodes + cw * 2 * 16 * kRD, at_v = at_k + 16 * kRD;
-    Page pg = open_page(0, id0);
-    load_codes(a.k, pg, at_k);
-    cp_async_commit();
-    load_codes(a.v, pg, at_v);
-    cp_async_commit();
-    int id = load_id(1);
-    for (int blk = 0; blk < nblocks; ++blk) {
+    auto put_k = [&](int blk, const Page& p) {  // codes of the block are there
       const int e = blk & 1;
-      const bool here = blk * kRPages + cw < pages, more = blk + 1 < nblocks;
-      const uint32_t half = static_cast<uint32_t>(blk >> 1);
       uint2 x[8];
+      take_codes(at_k, x);
       if (lane == 0) {
         // a page's K scale, log2 and reciprocal of its V scale
-        const uint32_t ks = __float_as_uint(pg.ks), vs = __float_as_uint(pg.vs);
+        const uint32_t ks = __float_as_uint(p.ks), vs = __float_as_uint(p.vs);
         if (!scale_ok(ks) || !scale_ok(vs)) set_error(a.err, DSA_DEV_BAD_SCALE);
         info[(blk & (kRInfos - 1)) * kRPages + cw] =
-            make_float4(pg.ks, static_cast<float>(scale_exp(vs)),
+            make_float4(p.ks, static_cast<float>(scale_exp(vs)),
                         __uint_as_float((254u << 23) - vs), 0.f);
       }
-      cp_async_wait<1>();  // its K
-      __syncwarp();
-      take_codes(at_k, x);
-      if (blk > 1) ok = mbar_wait(s_done + e, (half - 1u) & 1u) && ok;  // its place is free
-      if (here) store_f16(Sh::kK + 2 * e * kRHalf, x);
+      if (blk > 1)  // its place is free
+        ok = mbar_wait(s_done + e, (static_cast<uint32_t>(blk >> 1) - 1u) & 1u) && ok;
+      if (blk * kRPages + cw < pages) store_f16(Sh::kK + 2 * e * kRHalf, x);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full + e);
-      if (more) {
-        pg = open_page(blk + 1, id);
-        load_codes(a.k, pg, at_k);
-        id = load_id(blk + 2);
+    };
+    Page page = open_page(0, id0);  // of the block whose K comes next
+    load_codes(a.k, page, at_k);
+    cp_async_commit();
+    load_codes(a.v, page, at_v);
+    cp_async_commit();
+    int id = load_id(1);
+    for (int blk = -1; blk < nblocks; ++blk) {
+      // K of block blk + 1 (before block 1's there are block 0's V and block 1's K to wait for)
+      if (blk == 0) cp_async_wait<0>();
+      else cp_async_wait<1>();
+      __syncwarp();
+      if (blk + 1 < nblocks) put_k(blk + 1, page);
+      const Page held = page;
+      if (blk + 2 < nblocks) {
+        page = open_page(blk + 2, id);
+        load_codes(a.k, page, at_k);
+        id = load_id(blk + 3);
       }
       cp_async_commit();
-      cp_async_wait<1>();  // its V
-      __syncwarp();
-      take_codes(at_v, x);
-      if (blk > 0)  // the last block's second product is done with its place
-        ok = mbar_wait(o_done + (e ^ 1), static_cast<uint32_t>((blk - 1) >> 1) & 1u) && ok;
-      if (here) store_f16(Sh::kV, x);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_full + e);
-      if (more) load_codes(a.v, pg, at_v);
-      cp_async_commit();
+      if (blk >= 0) {  // V of block blk
+        uint2 x[8];
+        cp_async_wait<1>();
+        __syncwarp();
+        take_codes(at_v, x);
+        if (blk > 0)  // the last block's second product is done with its place
+          ok = mbar_wait(o_done + (~blk & 1), static_cast<uint32_t>((blk - 1) >> 1) & 1u) && ok;
+        if (blk * kRPages + cw < pages) store_f16(Sh::kV, x);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + (blk & 1));
+        if (blk + 1 < nblocks) load_codes(a.v, held, at_v);
+        cp_async_commit();
+      }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
     }
@@ -615,8 +624,8 @@ cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
 // quant_chunk.cu, batch x kv heads x group, tokens, rows):
 //   up to 32 rows of a tile:  128x8x4, 8, 500: 71 / 57;  64x32x1, 32, 1000: 195 / 168
 //   33 .. 64:                 128x8x4, 16, 300: 54 / 77 and 80;  64x32x1, 40, 200: 82 / 98
-//   more:                     64x8x4, 128, 256: 90 / 150;  8x8x4, 128, 4096: 97 / 271;
-//                             8x8x4, 2048, 2048: 406 / 1017
+//   more:                     64x8x4, 128, 256: 90 / 150;  8x8x4, 128, 4096: 95 / 271;
+//                             8x8x4, 2048, 2048: 396 / 1017
 bool quant_chunk_rows_fits(const QuantChunkLaunch& a) {
   const int64_t rows = static_cast<int64_t>(a.max_q) << a.group_log2;
   if (rows <= 32 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
