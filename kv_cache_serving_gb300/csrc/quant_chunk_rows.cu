@@ -19,8 +19,9 @@
 // shared memory: loads to registers are held up by the few KB of L1 that the tiles leave
 // (128 tokens over 4096 rows of 8 requests, 32/8 heads: 107 -> 97 us).  The issuing warp
 // elects its lane, which keeps the products' descriptors in uniform registers: issuing a
-// product took 150 cycles from a weighing thread and takes 60.  The unrolled prologue was an instruction-cache
-// miss per tile; as loops of four rows it brought prompts from 485 to 447 us.
+// product took 150 cycles from a weighing thread and takes 60.  The unrolled prologue was
+// a run of instruction-cache misses for every tile; as loops of four rows it brought prompts
+// from 485 to 447 us.
 //
 // What bounds it: latency and instruction issue of the weighing and the prologue, not the
 // products (11% of the tensor pipe) and not HBM.  Of a tile of prompts (3.5 blocks on
