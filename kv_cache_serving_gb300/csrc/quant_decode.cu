@@ -577,10 +577,12 @@ struct QuantDecode {
           for (int hk = 0; hk < a.hkv; ++hk) poison(b, hk);
         }
     }
-    // T tiles over N CTAs (no more than leave each its least share): CTA i takes tiles
-    // floor(i T / N) .. floor((i+1) T / N) - 1
+    // T tiles over N CTAs (no more than leave each its least share, or a unit): CTA i takes
+    // tiles floor(i T / N) .. floor((i+1) T / N) - 1
     const uint64_t T = static_cast<uint64_t>(__shfl_sync(0xffffffffu, incl, 31)) * a.hkv;
-    const uint64_t most = div(T + a.min_tiles - 1, a.min_tiles);
+    const uint64_t units = static_cast<uint64_t>(a.batch) * a.hkv;
+    uint64_t most = div(T + a.min_tiles - 1, a.min_tiles);
+    if (most < units) most = units < T ? units : T;
     const uint64_t N = most < gridDim.x ? most : gridDim.x;
     if (blockIdx.x >= N) return;
     auto owner = [&](uint64_t x) { return static_cast<int>(div((x + 1) * N + T - 1, T) - 1); };
@@ -721,7 +723,8 @@ cudaError_t launch_one(QuantDecodeLaunch a, cudaStream_t s) {
   int64_t grid;
   if (MODE == kModeDense) {
     a.min_tiles = kQuantMinTiles;
-    const int64_t most = (units * a.max_pages + kQuantMinTiles - 1) / kQuantMinTiles;
+    int64_t most = (units * a.max_pages + kQuantMinTiles - 1) / kQuantMinTiles;
+    if (most < units) most = units;
     grid = slots < most ? slots : most;
     // two slots of partials and one counter for each CTA
     const int64_t fit = a.part_cap / (2 * quant_part_floats(a.group, D));
@@ -737,22 +740,20 @@ cudaError_t launch_one(QuantDecodeLaunch a, cudaStream_t s) {
                     static_cast<size_t>(smem), s, a);
 }
 
-// Warps per CTA.  Dense rows: 4 (2 warps leave twice the partial states to join, 8 drain
-// together at every unit's end; mixed batch 102 us against 101 and 106, 64 units of 8000
-// rows 32 us against 40 and 31).  Sparse rows: a unit per CTA, and 2 warps once the units
-// fill half of the resident slots -- a CTA's start (sizes, mask, first pages: 3 us under load)
-// is then paid by half as many warps per unit; 2048 units of 290 rows 33.3 us against 36.5,
-// 640 units of 140 rows 9.1 against 9.9 -- else 4.
+// Warps per CTA: 2 once there are units enough, else 4.  A unit's start and end (sizes, mask,
+// first pages, the join of the warps: 3 us under load) are then paid by half as many warps,
+// but a unit cut over CTAs leaves twice the partial states.  Sparse rows, a unit per CTA:
+// enough is half of the resident slots; 2048 units of 290 rows 33.3 us against 36.5, 640
+// units of 140 rows 9.1 against 9.9.  Dense rows, equal shares: all of the slots; 960 units
+// of 1 .. 165 rows 15.4 us against 20.8, 2048 of 100 .. 300 24.0 against 28.6, the mixed
+// batch's 1024 of 33 .. 4608 100.5 either way -- but 512 of 1 .. 40 11.5 against 10.5, 256 of
+// 200 .. 600 15.3 against 13.8, 64 of 8000 39 against 30.  (8 warps: 106 on the mixed batch.)
 template <int D, int MODE, bool XQ>
 cudaError_t launch_warps(const QuantDecodeLaunch& a, cudaStream_t s) {
-  if constexpr (MODE == kModeDense) {
-    return launch_one<D, MODE, XQ, 4>(a, s);
-  } else {
-    const int64_t units = static_cast<int64_t>(a.batch) * a.hkv;
-    return units * 2 > static_cast<int64_t>(resident_ctas(D, XQ, 4)) * a.sms
-               ? launch_one<D, MODE, XQ, 2>(a, s)
-               : launch_one<D, MODE, XQ, 4>(a, s);
-  }
+  const int64_t units = static_cast<int64_t>(a.batch) * a.hkv;
+  return units * (MODE == kModeDense ? 1 : 2) > static_cast<int64_t>(resident_ctas(D, XQ, 4)) * a.sms
+             ? launch_one<D, MODE, XQ, 2>(a, s)
+             : launch_one<D, MODE, XQ, 4>(a, s);
 }
 
 template <int D, bool XQ>

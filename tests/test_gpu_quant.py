@@ -376,6 +376,16 @@ def test_decode_many_short_requests():
     run_modes(QuantBatch.from_batch(DecodeBatch.from_workload(w)), w)
 
 
+@pytest.mark.parametrize("batch,hkv,g,d,lo,hi", [(3, 2, 2, 64, 1, 3), (48, 8, 1, 128, 1, 40),
+                                                 (130, 8, 2, 128, 1, 165), (90, 16, 1, 64, 100, 200)])
+def test_decode_dense_short_units(batch, hkv, g, d, lo, hi):
+    """Dense shares of a unit or less: fewer tiles than the CTAs' least share, more units than
+    resident CTAs."""
+    w = wl.generate(case(d, g, batch=batch, hkv=hkv, lo=lo, hi=hi, prompt=(1, 2), W=16, seed=batch))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    run_modes(qb, w, ("dense",))
+
+
 def test_decode_long_prompts_share_units():
     """Sparse rows of few units with long prompts: several CTAs per unit."""
     w = wl.generate(case(128, 8, batch=2, hkv=1, lo=3000, hi=4000, prompt=(1500, 2900), W=200, seed=9))
