@@ -241,6 +241,9 @@ constexpr __host__ __device__ int quant_part_floats(int group, int head_dim) {
 constexpr int kQuantMaxParts = 8;
 constexpr int kQuantMinTiles = 16;
 
+// Pages of a request up to which the tcgen05 chunk kernels take few tiles too (2048 rows).
+constexpr int kQuantWholePages = 128;
+
 // Several query tokens per request over the 8-bit cache: q and out bf16.
 struct QuantChunkLaunch {
   const uint16_t* q;  // [batch][max_q][hq][head_dim] bf16

@@ -28,7 +28,7 @@
 // average) 2.3 K cycles go by until its sizes and tensor memory are there, 7 K until q is
 // converted and the first scores exist, 3 K per block, 4 K for the output; two CTAs per SM
 // fill each other's gaps to 1.3 instructions per cycle.
-// Measured: prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 432 us = 271 TFLOP/s of kept
+// Measured: prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 430 us = 273 TFLOP/s of kept
 // pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 396 us (1017).
 #include <math.h>
 
@@ -619,9 +619,10 @@ cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
 }  // namespace
 
 // Which calls this kernel takes: more than 32 rows (fewer are quant_chunk_tc.cu's), when
-// their tiles are a quarter of the SMs or more: a tile is never cut along its pages, and
-// quant_chunk.cu, which cuts them, was ahead at 32 tiles of 4000 rows (62 / 70 us) and
-// behind at 48 (78 / 70).  Measured against the other two (us, this kernel / quant_chunk_tc.cu or
+// their tiles are a quarter of the SMs or more, or no request passes 2048 rows: a tile is
+// never cut along its pages, and quant_chunk.cu, which cuts them, was ahead at 32 tiles of
+// 4000 rows (62 / 70 us) and behind at 48 (78 / 70); at 8 tiles of 2000 rows 32 / 38, of 1000
+// 26 / 22, of 500 19 / 14, and of 2000 rows of which prompt and window leave 110, 18 / 9.  Measured against the other two (us, this kernel / quant_chunk_tc.cu or
 // quant_chunk.cu, batch x kv heads x group, tokens, rows):
 //   up to 32 rows of a tile:  128x8x4, 8, 500: 71 / 57;  64x32x1, 32, 1000: 195 / 168
 //   33 .. 64:                 128x8x4, 16, 300: 54 / 77 and 80;  64x32x1, 40, 200: 82 / 98
@@ -630,7 +631,7 @@ cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
 bool quant_chunk_rows_fits(const QuantChunkLaunch& a) {
   const int64_t rows = static_cast<int64_t>(a.max_q) << a.group_log2;
   if (rows <= 32 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
-  return a.split_setting == 1 ||
+  return a.split_setting == 1 || a.max_pages <= kQuantWholePages ||
          (rows + kRRows - 1) / kRRows * a.batch * a.hkv * 4 >= a.sms;
 }
 

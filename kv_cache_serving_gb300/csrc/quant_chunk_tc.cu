@@ -25,7 +25,7 @@
 // conversions are 130 and the softmax 300.  Two CTAs per SM, so that one converts while the
 // other's products run; the next block's K and V are loaded an iteration ahead, past the
 // L1 (whose 20 KB keep page ids, masks and spills).  Measured: 32 tokens of 64 requests of 320 ..
-// 1280 rows under the mask, 32/32 heads: 85 us (136 with quant_chunk.cu).  A persistent
+// 1280 rows under the mask, 32/32 heads: 85 us (88 with a flushed L2; 136 with quant_chunk.cu).  A persistent
 // form (tiles of several units in one CTA, the next tile's q and first block ahead)
 // measured slower: 141 us, its second set of tile values spills.
 #include <math.h>
@@ -672,14 +672,18 @@ cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
 }  // namespace
 
 // Which calls this kernel takes: those whose (request, kv head) is one tile, when there are
-// enough of them to fill half the GPU (a tile is never cut along its pages).  Measured
+// enough of them to fill half the GPU or no request passes 2048 rows (a tile is never cut
+// along its pages; 8 tiles, cut in quant_chunk.cu / whole here: of 4000 rows 28 / 58 us, of
+// 2000 23 / 31, of 1000 21 / 18, of 500 15 / 12, and of 1900 rows of which prompt and window
+// leave 60, 16 / 6).  Measured
 // against quant_chunk.cu (us, this kernel / that one, batch x kv heads x group, tokens,
 // rows): 64x32x1, 32, 300: 80 / 114; 128x8x4, 8, 500: 57 / 82; 128x8x4, 8, 2000: 169 / 235;
 // 128x8x4, 4, 1000: 94 / 121.  Against quant_chunk_rows.cu: see there.
 bool quant_chunk_tc_fits(const QuantChunkLaunch& a) {
   const int64_t columns = static_cast<int64_t>(a.max_q) << a.group_log2;
   if (columns > 32 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
-  return a.split_setting == 1 || static_cast<int64_t>(a.batch) * a.hkv * 2 >= a.sms;
+  return a.split_setting == 1 || a.max_pages <= kQuantWholePages ||
+         static_cast<int64_t>(a.batch) * a.hkv * 2 >= a.sms;
 }
 
 cudaError_t launch_quant_chunk_tc(const QuantChunkLaunch& a, cudaStream_t s) {

@@ -11,7 +11,7 @@
 // its tokens' cosines and sines in shared memory once for all heads, then streams the
 // heads; a thread handles 8 pairs (two 16-byte loads and stores with bf16, each in a line
 // of its lanes' own; the table is swizzled against bank conflicts).  Measured: q and k of
-// 65 K tokens, 32/8 heads of 128, two axes: 201 us = 0.98 of the copy rate (227 with 8 pairs
+// 65 K tokens, 32/8 heads of 128, two axes: 195 us, the copy rate (223 with 8 pairs
 // side by side and a plain table, whose conflicts kept the L1 pipe 91% busy).
 #include <math.h>
 
