@@ -307,7 +307,7 @@ struct RopeLaunch {
 
 cudaError_t launch_quant_decode(const QuantDecodeLaunch& a, int mode, cudaStream_t s);
 cudaError_t launch_quant_chunk(const QuantChunkLaunch& a, cudaStream_t s);
-// The tcgen05 kernels of the call (head_dim 128), and whether one takes a call: _tc with the
+// The tcgen05 kernels of the call (_tc: head_dim 128), and whether one takes a call: _tc with the
 // queries as columns (few of them per request), _rows with the queries as rows.
 bool quant_chunk_rows_fits(const QuantChunkLaunch& a);
 cudaError_t launch_quant_chunk_rows(const QuantChunkLaunch& a, cudaStream_t s);

@@ -17,11 +17,11 @@
 // columns and 16 warps measured a third slower).  The accumulators hold the output
 // transposed (dims x columns), which lets the weights go from the score accumulators to
 // the second product by movmatrix alone.
-// This kernel serves head_dim 64, calls of few tiles over long caches and calls whose units
-// are to be cut along their pages; the others go to quant_chunk_tc.cu (up to 32 columns) and
-// quant_chunk_rows.cu.  Measured: 40 tokens over 3000 rows of one request, 32/8 heads,
-// head_dim 128: 36 us in 8 parts (54 whole in quant_chunk_rows.cu).  Prompts of 32 .. 512 rows
-// of 128 requests, 32/8 heads, take 694 us here, 430 in quant_chunk_rows.cu.
+// This kernel serves head_dim 64 up to 32 columns, calls of few tiles over long caches and
+// calls whose units are to be cut along their pages; the others go to quant_chunk_tc.cu
+// (head_dim 128 up to 32 columns) and quant_chunk_rows.cu.  Measured: 40 tokens over 3000
+// rows of one request, 32/8 heads of 128: 36 us in 8 parts (54 whole in quant_chunk_rows.cu).
+// Prompts of 32 .. 512 rows of 128 requests, 32/8 heads, take 694 us here, 430 there.
 //
 // Work split.  A CTA of 4 warps covers 32 KC columns (KC = 4 / KG column groups) of one
 // (request, kv head); KG warps share a column group and take its pages in turn, joined
@@ -544,7 +544,7 @@ cudaError_t launch_cols(const QuantChunkLaunch& a, cudaStream_t s) {
 
 cudaError_t launch_quant_chunk(const QuantChunkLaunch& a, cudaStream_t s) {
   if (a.head_dim == 128 && quant_chunk_tc_fits(a)) return launch_quant_chunk_tc(a, s);
-  if (a.head_dim == 128 && quant_chunk_rows_fits(a)) return launch_quant_chunk_rows(a, s);
+  if (quant_chunk_rows_fits(a)) return launch_quant_chunk_rows(a, s);
   return a.head_dim == 128 ? launch_cols<128>(a, s) : launch_cols<64>(a, s);
 }
 

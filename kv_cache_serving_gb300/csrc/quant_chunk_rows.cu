@@ -1,11 +1,10 @@
 // quant_chunk_rows.cu -- several query tokens per request over the 8-bit paged K/V cache
-// on the 5th-generation tensor cores, for chunks of many (query token, head) rows
-// (head_dim 128).
+// on the 5th-generation tensor cores, for chunks of many (query token, head) rows.
 //
 // Mathematics as in quant_chunk.cu, with the queries on the lanes of tensor memory: a CTA
 // holds 128 rows (query token, head of the kv head's group) of one (request, kv head) and
 // walks its pages in blocks of 4 (64 cache rows):
-//   S (128 x 64) = Q K^T,   P = weights of S,   O (128 x 128) += P V
+//   S (128 x 64) = Q K^T,   P = weights of S,   O (128 x head_dim) += P V
 // so a thread owns a query: its running reference and sum are two registers, a page's
 // scales are constants of 16 of its scores, its mask is one shifted word per page, and P
 // goes back to tensor memory over S as the left operand of the second product.  The
@@ -28,8 +27,9 @@
 // average) 2.3 K cycles go by until its sizes and tensor memory are there, 7 K until q is
 // converted and the first scores exist, 3 K per block, 4 K for the output; two CTAs per SM
 // fill each other's gaps to 1.3 instructions per cycle.
-// Measured: prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 430 us = 273 TFLOP/s of kept
-// pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 396 us (1017).
+// Measured (head_dim 128): prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 430 us =
+// 273 TFLOP/s of kept pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 396 us
+// (1017).
 #include <math.h>
 
 #include <type_traits>
@@ -45,7 +45,6 @@
 namespace dsa {
 namespace {
 
-constexpr int kRD = 128;            // head_dim
 constexpr int kRRows = 128;         // query rows per CTA
 constexpr int kRPages = 4;          // pages per block ...
 constexpr int kRBlock = 64;         // ... and cache rows
@@ -54,10 +53,14 @@ constexpr int kRQHalf = kRRows * 128, kRHalf = kRBlock * 128;  // bytes of 64 di
 constexpr int kRInfos = 4;          // blocks whose scales are held
 constexpr float kRHead = 4.f, kRSlack = 10.f, kRNoRef = -3e38f;  // as in quant_chunk.cu
 
+template <int D>
 struct RowsShape {
-  static constexpr int kQ = 0, kK = 2 * kRQHalf, kV = kK + 4 * kRHalf;  // K twice, V once
-  static constexpr int kCodes = kV + 2 * kRHalf;       // a block's codes: K, V of each page
-  static constexpr int kInfo = kCodes + kRPages * 2 * 16 * kRD;        // 4 x 4 float4 of a page: see below
+  static constexpr int kHalves = D / 64;               // of a row of a tile
+  static constexpr int kQ = 0, kK = kHalves * kRQHalf;
+  static constexpr int kV = kK + 2 * kHalves * kRHalf;  // K twice, V once
+  static constexpr int kCodes = kV + kHalves * kRHalf;  // a block's codes: K, V of each page
+  // 4 x 4 float4 of a page: see below
+  static constexpr int kInfo = kCodes + kRPages * 2 * 16 * D;
   static constexpr int kUp = kInfo + kRInfos * kRPages * 16;  // score factor of a row: 128 floats
   static constexpr int kBar = kUp + 4 * kRRows;        // thirteen barriers, address, flag
   static constexpr int kMask = kBar + 112;
@@ -79,9 +82,10 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t* w) {
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-template <int LG>
+template <int D, int LG>
 __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const QuantChunkLaunch a) {
-  using Sh = RowsShape;
+  using Sh = RowsShape<D>;
+  constexpr int kHalves = Sh::kHalves;
   constexpr int per_cta = kRRows >> LG;  // query tokens per CTA
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -107,13 +111,13 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   if (code != 0) {
     // q_len is not trusted: NaN into every slot of the unit
     if (qt == 0 && hk == 0 && tid == 0) set_error(a.err, code);
-    for (int x = tid; x < kRRows * kRD; x += kRThreads) {
-      const int t = t0 + x / (kRD << LG);
+    for (int x = tid; x < kRRows * D; x += kRThreads) {
+      const int t = t0 + x / (D << LG);
       if (t >= a.max_q) break;
       const size_t qh = (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << LG) +
-                        (x / kRD & ((1 << LG) - 1));
-      a.out[qh * kRD + x % kRD] = 0x7fc0;
-      if (a.lse != nullptr && x % kRD == 0) a.lse[qh] = __int_as_float(0x7fc00000);
+                        (x / D & ((1 << LG) - 1));
+      a.out[qh * D + x % D] = 0x7fc0;
+      if (a.lse != nullptr && x % D == 0) a.lse[qh] = __int_as_float(0x7fc00000);
     }
     return;
   }
@@ -199,25 +203,25 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   // have in flight there is bounded by the few KB of L1 beside the tiles); rows that nobody
   // needs become zeros.
   auto load_codes = [&](const uint8_t* base, const Page& p, uint32_t to) {
-    const uint8_t* src = base + p.ph * (16 * kRD) + 16 * lane;
+    const uint8_t* src = base + p.ph * (16 * D) + 16 * lane;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // 4 rows of 8 pieces
+    for (int i = 0; i < D / 32; ++i)  // 512 bytes
       cp_async16_zfill(to + 512 * i + 16 * lane, src + 512 * i,
-                       (p.need >> (4 * i + (lane >> 3))) & 1u);
+                       (p.need >> ((512 * i + 16 * lane) / D)) & 1u);
   };
   // Its fp16 values into rows 16 cw .. of a block's tile: 64-dim halves of 64 rows of 128
-  // bytes, 16-byte pieces swizzled by the row; a lane has the 8 codes of rows 2 i + lane / 16,
-  // piece lane % 16.
-  const uint32_t f16_at = sm + ((lane >> 3) & 1) * kRHalf + (16 * cw + (lane >> 4)) * 128 +
-                          (((lane & 7) ^ (lane >> 4)) << 4);
-  auto take_codes = [&](uint32_t from, uint2 (&v)[8]) {
+  // bytes, 16-byte pieces swizzled by the row; a lane has 8 codes of every kStep-th row.
+  constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+  const uint32_t f16_at = sm + (D == 128 ? (lane >> 3) & 1 : 0) * kRHalf +
+                          (16 * cw + lane / kLanes) * 128 + (((lane & 7) ^ (lane / kLanes)) << 4);
+  auto take_codes = [&](uint32_t from, uint2 (&v)[D / 16]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = lds64(from + 256 * i + 8 * lane);
+    for (int i = 0; i < D / 16; ++i) v[i] = lds64(from + 256 * i + 8 * lane);
   };
-  auto store_f16 = [&](int tile, const uint2 (&v)[8]) {
+  auto store_f16 = [&](int tile, const uint2 (&v)[D / 16]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      sts128((f16_at ^ ((i & 3) << 5)) + tile + i * 256,
+    for (int i = 0; i < D / 16; ++i)
+      sts128((f16_at ^ ((kStep * i & 7) << 4)) + tile + i * kStep * 128,
              make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2_hi(v[i].x), e4m3x2_f16x2(v[i].y),
                         e4m3x2_f16x2_hi(v[i].y)));
   };
@@ -245,10 +249,10 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   if (converts) {
     // ================= converters: a page of every block, codes loaded a block ahead =========
     // K goes a block ahead of V, so that the scores after next wait for no V.
-    const uint32_t at_k = sm + Sh::kCodes + cw * 2 * 16 * kRD, at_v = at_k + 16 * kRD;
+    const uint32_t at_k = sm + Sh::kCodes + cw * 2 * 16 * D, at_v = at_k + 16 * D;
     auto put_k = [&](int blk, const Page& p) {  // codes of the block are there
       const int e = blk & 1;
-      uint2 x[8];
+      uint2 x[D / 16];
       take_codes(at_k, x);
       if (lane == 0) {
         // a page's K scale, log2 and reciprocal of its V scale
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       }
       if (blk > 1)  // its place is free
         ok = mbar_wait(s_done + e, (static_cast<uint32_t>(blk >> 1) - 1u) & 1u) && ok;
-      if (blk * kRPages + cw < pages) store_f16(Sh::kK + 2 * e * kRHalf, x);
+      if (blk * kRPages + cw < pages) store_f16(Sh::kK + kHalves * e * kRHalf, x);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full + e);
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       }
       cp_async_commit();
       if (blk >= 0) {  // V of block blk
-        uint2 x[8];
+        uint2 x[D / 16];
         cp_async_wait<1>();
         __syncwarp();
         take_codes(at_v, x);
@@ -314,11 +318,11 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       if (!__all_sync(0xffffffffu, ok)) return;
       const uint32_t id_s = tc_idesc(128, 16 * min(kRPages, pages - blk * kRPages), false);
       const uint32_t to = tmem + Sh::kS + (blk & 1) * kRBlock;
-      const uint64_t kd = k_desc + ((blk & 1) * 2 * kRHalf >> 4);
+      const uint64_t kd = k_desc + ((blk & 1) * kHalves * kRHalf >> 4);
       if (elect_one()) {
         mbar_arrive(i_full + (blk & 1));
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+        for (int s = 0; s < D / 16; ++s)
           tc_mma_f16(to, q_desc + (((s >> 2) * kRQHalf + (s & 3) * 32) >> 4),
                      kd + (((s >> 2) * kRHalf + (s & 3) * 32) >> 4), id_s, s > 0);
         tc_commit(s_done + (blk & 1));
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       if (!ok) break;
       const uint32_t from = tmem + Sh::kS + e * kRBlock;
       if (elect_one()) {  // O += P V, a step for each page
-        constexpr uint32_t id_o = tc_idesc_b_rows(128, kRD);
+        constexpr uint32_t id_o = tc_idesc_b_rows(128, D);
 #pragma unroll
         for (int s = 0; s < kRPages; ++s)
           if (s < present)
@@ -357,18 +361,19 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     // q as fp16, a row (query token, head) scaled by its own power of two: a query's result
     // does not hang on the others of its tile.  The scale's sign goes into q, so that a
-    // page's largest score is its largest product.  16 lanes a row.
+    // page's largest score is its largest product.
     // A warp without a query has nothing to weigh (what its rows of S and O hold is theirs
     // alone): it keeps the blocks' count and no more.
     const bool idle = t0 + (32 * warp >> LG) >= t1;
     if (!idle) {
-      const int piece = lane & 15, r0 = 32 * warp + (lane >> 4);
+      constexpr int kPass = 4 * kStep;  // rows a pass
+      const int piece = lane % kLanes, r0 = 32 * warp + lane / kLanes;
       auto load_q = [&](int g, uint4 (&x)[4]) {
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const int row = r0 + 8 * g + 2 * y;
+          const int row = r0 + kPass * g + kStep * y;
           x[y] = t0 + (row >> LG) < t1
-                     ? __ldg(reinterpret_cast<const uint4*>(a.q + qh_of(row) * kRD) + piece)
+                     ? __ldg(reinterpret_cast<const uint4*>(a.q + qh_of(row) * D) + piece)
                      : make_uint4(0u, 0u, 0u, 0u);
         }
       };
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       load_q(0, x);
       load_q(1, ahead);
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < 32 / kPass; ++g) {
         uint32_t m[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           asm("max.bf16x2 %0, %0, %1;" : "+r"(m[y]) : "r"(x[y].w & 0x7fff7fffu));
         }
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1)
+        for (int o = kLanes / 2; o >= 1; o >>= 1)
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const uint32_t other = __shfl_xor_sync(0xffffffffu, m[y], o);
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           }
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const int row = r0 + 8 * g + 2 * y;
+          const int row = r0 + kPass * g + kStep * y;
           const int qe = q_exponent(fmaxf(bf16_lo(m[y]), bf16_hi(m[y])));
           const float down = a.scale_log2 < 0.f ? -pow2i(-qe) : pow2i(-qe);
           // at least 2^-105, so that a masked score (-inf) times it and a page's scale (2^-40
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
                             f16x2_rn(bf16_lo(x[y].w) * down, bf16_hi(x[y].w) * down)));
           x[y] = ahead[y];
         }
-        if (g < 2) load_q(g + 2, ahead);
+        if (g + 2 < 32 / kPass) load_q(g + 2, ahead);
       }
     }
     {
@@ -499,7 +504,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
-          for (int h = 0; h < 8; ++h) {
+          for (int h = 0; h < D / 16; ++h) {
             uint32_t o[16];
             tmem_load<16>(t_lane + Sh::kO + 16 * h, o);
             tc_wait_ld();
@@ -548,11 +553,11 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       const float inv = 1.f / l;
       const bool mine = t0 + (r >> LG) < t1;
       if (a.lse != nullptr && mine) a.lse[qh_of(r)] = (ref + log2f(l)) * kLn2;
-      uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + qh_of(r) * kRD;
+      uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + qh_of(r) * D;
       const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;  // rows are 256 bytes
       float probe = 0.f;
 #pragma unroll 1
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h < D / 32; ++h) {
         uint32_t o[32];
         tmem_load<32>(t_lane + Sh::kO + 32 * h, o);
         tc_wait_ld();
@@ -582,7 +587,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       while (nan != 0u) {
         const int rr = 32 * warp + __ffs(nan) - 1;
         nan &= nan - 1u;
-        quant_redo_query<kRD>(a, b, hk, i_first + (rr >> LG), P, Wn, qh_of(rr), lane);
+        quant_redo_query<D>(a, b, hk, i_first + (rr >> LG), P, Wn, qh_of(rr), lane);
       }
     }
   }
@@ -602,10 +607,10 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
   }
 }
 
-template <int LG>
+template <int D, int LG>
 cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
-  auto kern = quant_chunk_rows_kernel<LG>;
-  const int smem = RowsShape::smem(a.max_window / 32 + 1);
+  auto kern = quant_chunk_rows_kernel<D, LG>;
+  const int smem = RowsShape<D>::smem(a.max_window / 32 + 1);
   static KernelSlots cache;
   int per_sm = 0;
   const cudaError_t e =
@@ -616,18 +621,32 @@ cudaError_t launch_one(const QuantChunkLaunch& a, cudaStream_t s) {
                     static_cast<size_t>(smem), s, a);
 }
 
+template <int D>
+cudaError_t launch_group(const QuantChunkLaunch& a, cudaStream_t s) {
+  switch (a.group_log2) {
+    case 0: return launch_one<D, 0>(a, s);
+    case 1: return launch_one<D, 1>(a, s);
+    case 2: return launch_one<D, 2>(a, s);
+    default: return launch_one<D, 3>(a, s);
+  }
+}
+
 }  // namespace
 
 // Which calls this kernel takes: more than 32 rows (fewer are quant_chunk_tc.cu's), when
 // their tiles are a quarter of the SMs or more, or no request passes 2048 rows: a tile is
 // never cut along its pages, and quant_chunk.cu, which cuts them, was ahead at 32 tiles of
 // 4000 rows (62 / 70 us) and behind at 48 (78 / 70); at 8 tiles of 2000 rows 32 / 38, of 1000
-// 26 / 22, of 500 19 / 14, and of 2000 rows of which prompt and window leave 110, 18 / 9.  Measured against the other two (us, this kernel / quant_chunk_tc.cu or
-// quant_chunk.cu, batch x kv heads x group, tokens, rows):
+// 26 / 22, of 500 19 / 14, and of 2000 rows of which prompt and window leave 110, 18 / 9.
+// Measured against the other two (us, this kernel / quant_chunk_tc.cu or quant_chunk.cu,
+// batch x kv heads x group, tokens, rows):
 //   up to 32 rows of a tile:  128x8x4, 8, 500: 71 / 57;  64x32x1, 32, 1000: 195 / 168
 //   33 .. 64:                 128x8x4, 16, 300: 54 / 77 and 80;  64x32x1, 40, 200: 82 / 98
 //   more:                     64x8x4, 128, 256: 90 / 150;  8x8x4, 128, 4096: 95 / 271;
 //                             8x8x4, 2048, 2048: 396 / 1017
+// and with head_dim 64 against quant_chunk.cu: 64x20x1, 8, 300: 46 / 38;  128x8x4, 8, 2000:
+// 162 / 141;  64x20x1, 48, 600: 79 / 87;  128x20x1, 400, 400: 341 / 514;  8x8x4, 128, 4096:
+// 80 / 224.
 bool quant_chunk_rows_fits(const QuantChunkLaunch& a) {
   const int64_t rows = static_cast<int64_t>(a.max_q) << a.group_log2;
   if (rows <= 32 || a.split_setting >= 2 || a.batch > 65535 || a.hkv > 65535) return false;
@@ -636,12 +655,7 @@ bool quant_chunk_rows_fits(const QuantChunkLaunch& a) {
 }
 
 cudaError_t launch_quant_chunk_rows(const QuantChunkLaunch& a, cudaStream_t s) {
-  switch (a.group_log2) {
-    case 0: return launch_one<0>(a, s);
-    case 1: return launch_one<1>(a, s);
-    case 2: return launch_one<2>(a, s);
-    default: return launch_one<3>(a, s);
-  }
+  return a.head_dim == 128 ? launch_group<128>(a, s) : launch_group<64>(a, s);
 }
 
 }  // namespace dsa
