@@ -64,12 +64,12 @@ FALLBACK_HBM_GBS = 6800.0
 # decode-kernel sources whose digest is `digest` and are reported as null
 # otherwise.
 NCU_TRAFFIC = {
-    "digest": "49f9c5ad99382229",
+    "digest": "afac391cd849058f",
     "bytes": {
-        "mixed-serving-gqa4": 167713536,
-        "janus-pro-7b-like-32x32": 316329472,
-        "llamagen-xl-like-24x24": 21440768,
-        "emu3-8b-like-90x90-gqa4": 3281408,
+        "mixed-serving-gqa4": 168038912,
+        "janus-pro-7b-like-32x32": 316020736,
+        "llamagen-xl-like-24x24": 21442816,
+        "emu3-8b-like-90x90-gqa4": 3281664,
     },
 }
 
