@@ -132,7 +132,6 @@ def _lengths(case):
     out = dict(L=L)
     if "new_lo" in case:
         out["n"] = np.minimum(between("new"), L)
-        out["n"][0] = max(out["n"][0], 1)                       # some row in every case
     if "rows_lo" in case:
         out["n"] = np.minimum(between("rows"), L)
         out["start"] = rng.integers(0, L - out["n"] + 1)
