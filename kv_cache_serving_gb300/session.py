@@ -43,6 +43,21 @@ def schedule_order(lengths, spread: float = 1.25):
     return longest_first_order(lengths)
 
 
+def page_rows(page_table, seq_len, num_pages) -> np.ndarray:
+    """Rows that each page of a pool holds: of the requests that map it, the most (host arrays;
+    entries of -1 and entries past a request's rows are not looked at)."""
+    table, L = np.asarray(page_table), np.asarray(seq_len, dtype=np.int64)
+    if L.size and L.max() > table.shape[1] * dsa.PAGE:
+        raise ValueError(f"seq_len {L.max()} passes the page table's {table.shape[1]} pages")
+    n = np.clip(L[:, None] - dsa.PAGE * np.arange(table.shape[1]), 0, dsa.PAGE)
+    used = (n > 0) & (table >= 0)
+    if used.any() and table[used].max() >= num_pages:
+        raise ValueError(f"page id {table[used].max()} outside the pool of {num_pages}")
+    rows = np.zeros(num_pages, np.int32)
+    np.maximum.at(rows, table[used], n[used])
+    return rows
+
+
 class PackedIO:
     """One pinned host buffer and one device buffer per direction, so that a
     step's inputs go up in one copy and its results come back in one.  The
@@ -273,16 +288,12 @@ class QuantBatch:
 
     @classmethod
     def from_batch(cls, batch: DecodeBatch) -> "QuantBatch":
-        """The batch's own pages quantised: every page is written like a request of its
-        own, with as many rows as its request has there."""
+        """The batch's own pages quantised, with the lengths and the page table that are on the
+        device now: every page is written like a request of its own, with as many rows as the
+        longest request that maps it has there."""
         self = cls(batch)
         d = batch.dims
-        table = batch.page_table.cpu().numpy()
-        rows = np.zeros(d.num_pages, np.int32)
-        for b, L in enumerate(batch._host_lengths[0]):
-            for p in range((int(L) + dsa.PAGE - 1) // dsa.PAGE):
-                if table[b, p] >= 0:
-                    rows[table[b, p]] = min(dsa.PAGE, int(L) - p * dsa.PAGE)
+        rows = page_rows(batch.page_table.cpu().numpy(), batch.seq_len.cpu().numpy(), d.num_pages)
         used = np.flatnonzero(rows)
         dims = dsa.make_dims(len(used), d.hkv, d.hkv, d.head_dim, d.num_pages, 1, 0, 1, 1,
                              d.kv_dtype, d.kv_dtype)
