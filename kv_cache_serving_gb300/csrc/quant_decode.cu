@@ -9,9 +9,13 @@
 // p_j / t_j (exact) enters the sum.  So the weights of that product share one range
 // however much the pages' scales differ, and no V element is ever scaled.  r follows
 // the running maximum with a slack of 2^10: one vote per tile instead of a reduction
-// over its rows, and the accumulators are rescaled only when it moves.  p_j <= 2^14
-// is rounded to fp16 (2^-12 relative, below the bf16 output's own 2^-9); with fp32 q
-// both q and p_j are split into two fp16 halves (2^-23).
+// over its rows, and the accumulators are rescaled only when it moves.
+// bf16 q: p_j <= 2^14 is rounded to fp16 (2^-11 relative, below the bf16 output's own 2^-8;
+// the largest is 2^4 or more, so below 2^-18 of it, where fp16's normal range ends, by steps of
+// 2^-28 of the largest).  fp32 q: q in two fp16 halves (2^-22 relative, 2^-33 of the row's
+// largest), p_j in three bf16 thirds (2^-24 relative, down to 2^-100 of the largest: fp16 halves
+// lose the rows 2^-24 below a sink), V widened to bf16 for them: 132 us on the dense batch below
+// with fp32 q, 126 with halves.
 //
 // What bounds it: HBM, and for short calls the chain of dependent loads at a CTA's start.  A
 // row is 2 D bytes for 4 D G flops (<= 8 flops per byte; the 8 columns of an mma cost the
@@ -189,21 +193,42 @@ struct QuantWarp {
       y[e] = ex2_approx(y[e] - ref[e & 1]);
       l[e & 1] = fmaf(y[e], inv[e >> 1], l[e & 1]);
     }
-    const uint32_t p0 = f16x2_rn(y[0], y[1]), p1 = f16x2_rn(y[2], y[3]);
-    const uint32_t b0 = movmatrix_trans(p0), b1 = movmatrix_trans(p1);
-    uint32_t c0 = 0, c1 = 0;
-    if constexpr (XQ) {
-      c0 = movmatrix_trans(f16x2_rest(y[0], y[1], p0));
-      c1 = movmatrix_trans(f16x2_rest(y[2], y[3], p1));
-    }
     uint32_t w[4][Tile::kVW];
-    Tile::load_v(tile + Tile::kBytes, lane, w);
+    if constexpr (XQ) {
+      // thirds of 8 bits; what bf16 took off a float is a float, so the thirds add up
+      uint32_t b[3][2];
 #pragma unroll
-    for (int mt = 0; mt < NK; ++mt) {
-      uint32_t a[4];
-      Tile::frag_v(w, mt, a);
-      mma_f16(acc[mt], a[0], a[1], a[2], a[3], b0, b1);
-      if constexpr (XQ) mma_f16(acc[mt], a[0], a[1], a[2], a[3], c0, c1);
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t part = bf16x2_rn(y[2 * r], y[2 * r + 1]);
+          y[2 * r] -= bf16_lo(part);
+          y[2 * r + 1] -= bf16_hi(part);
+          b[k][r] = movmatrix_trans(part);
+        }
+      Tile::load_v(tile + Tile::kBytes, lane, w);
+#pragma unroll
+      for (int mt = 0; mt < NK; ++mt) {
+        uint32_t a[4];
+        Tile::frag_v(w, mt, a);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // 4 bits: exact in bf16 too
+          const float2 v = f16x2_f32x2(a[k]);
+          a[k] = bf16x2_rn(v.x, v.y);
+        }
+#pragma unroll
+        for (int k = 2; k >= 0; --k) mma_bf16(acc[mt], a, b[k][0], b[k][1]);
+      }
+    } else {
+      const uint32_t b0 = movmatrix_trans(f16x2_rn(y[0], y[1]));
+      const uint32_t b1 = movmatrix_trans(f16x2_rn(y[2], y[3]));
+      Tile::load_v(tile + Tile::kBytes, lane, w);
+#pragma unroll
+      for (int mt = 0; mt < NK; ++mt) {
+        uint32_t a[4];
+        Tile::frag_v(w, mt, a);
+        mma_f16(acc[mt], a[0], a[1], a[2], a[3], b0, b1);
+      }
     }
   }
 

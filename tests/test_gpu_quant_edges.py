@@ -9,10 +9,11 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from kv_cache_serving_gb300 import dsa
 from kv_cache_serving_gb300 import workloads as wl
 from kv_cache_serving_gb300.session import DecodeBatch, QuantBatch
-from test_gpu_quant import case
+from test_gpu_quant import TABLE, case, dequantised
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +60,101 @@ def test_from_batch_of_shared_pages():
         for x, y in ((qb.k, alone.k), (qb.v, alone.v), (qb.k_scale, alone.k_scale),
                      (qb.v_scale, alone.v_scale)):
             assert torch.equal(x.view(torch.uint8)[at], y.view(torch.uint8)[at])
+
+
+# ---------------------------------------------------------------------------
+# weights far below the largest
+# ---------------------------------------------------------------------------
+
+def attend64(w, qb, mode):
+    """Decode in 64 bits on the dequantised rows, head by head: out, and the sums that bound what
+    roundings do to it -- S = sum w |v| / sum w, the largest w t and sum |code| / sum w of a head
+    (t: the V scale of a row's page), B = scale * max_j sum_i |q_i k_ji|, X = the largest |score|."""
+    kp, vp = (x.double().numpy() for x in dequantised(qb))
+    ts = qb.v_scale.double().cpu().numpy()
+    q = qb.batch.q.double().cpu().numpy()
+    g, table = w["hq"] // w["hkv"], np.asarray(w["page_table"])
+    res = {x: np.zeros(q.shape) for x in ("out", "S", "floor")}
+    res.update({x: np.zeros(q.shape[:2]) for x in ("B", "X")})
+    for b in range(w["batch"]):
+        L = int(w["seq_len"][b])
+        for hk in range(w["hkv"]):
+            j = np.arange(L) if mode == "dense" else oracle.kept_set(
+                L, int(w["prompt_len"][b]), int(w["window"][b]), w["keep_mask"][b, hk])
+            pg = table[b, j // 16]
+            k, v, t = kp[pg, j % 16, hk], vp[pg, j % 16, hk], ts[pg, hk]
+            for h in range(hk * g, hk * g + g):
+                x = k @ q[b, h] * qb.batch.scale
+                p = np.exp(x - x.max())
+                res["out"][b, h] = p @ v / p.sum()
+                res["S"][b, h] = p @ np.abs(v) / p.sum()
+                res["floor"][b, h] = (p * t).max() * np.abs(v / t[:, None]).sum(0) / p.sum()
+                res["B"][b, h] = (np.abs(k) @ np.abs(q[b, h])).max() * qb.batch.scale
+                res["X"][b, h] = np.abs(x).max()
+    return res
+
+
+def check_against(w, qb, mode):
+    """out against attend64, element by element and relative to what the element is made of.
+    A score is off by 2 * 2^-22 B (the halves of q: 11 bits each) and by what fp32 sums of 2 d
+    terms lose, 2 d * 2^-23 B, and its exponent by 2^-23 X for each of three roundings; a weight is
+    off by as much twice over (numerator and sum), by 2^-22 for 2^x and 2^-24 for its own halves
+    or thirds.  The n weighted rows are added in fp32, n * 2^-23 S at most.  bf16 q: the weights
+    round once more, 2^-11 S, or below fp16's normal range by half of its last step, 2^-25 where
+    the largest weight (times its page's scale) stands at 2^4 or more; out rounds by 2^-8."""
+    out = torch.full_like(qb.out, float("nan"))
+    {"dense": qb.decode_dense, "list": qb.decode_sparse, "masked": qb.decode_sparse_masked}[mode](out=out)
+    torch.cuda.synchronize()
+    assert qb.batch.device_error() == 0
+    r = attend64(w, qb, mode)
+    d, n = w["head_dim"], int(max(w["seq_len"]))
+    score = (2 * 2.0 ** -22 + 2 * d * 2.0 ** -23) * r["B"] + 3 * 2.0 ** -23 * r["X"]
+    tol = (2 * np.expm1(score)[..., None] + 2.0 ** -21 + n * 2.0 ** -23) * r["S"]
+    if w["dtype"] == "bf16":
+        tol = tol + 2.0 ** -11 * r["S"] + 2.0 ** -29 * r["floor"]
+        tol = tol + 2.0 ** -8 * (np.abs(r["out"]) + tol)
+    else:
+        tol = tol + 2.0 ** -24 * np.abs(r["out"])
+    err = np.abs(out.double().cpu().numpy() - r["out"])
+    bad = ~(err <= tol)
+    assert not bad.any(), (mode, (err / tol)[bad].max(), bad.mean())
+
+
+@pytest.mark.parametrize("lead", [12, 16, 20, 24, 30, 90])
+@pytest.mark.parametrize("d,g,dtype", [(64, 1, "f32"), (128, 2, "f32"), (128, 4, "bf16")])
+def test_rows_below_a_sink(d, g, dtype, lead):
+    """A prompt row whose score leads by 2^lead and whose V is zero: the output is made of
+    weights 2^-lead of the largest, which keep their bits."""
+    w = wl.generate(case(d, g, dtype, batch=3, lo=150, hi=400, prompt=(100, 140), W=64, seed=lead))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    bt = qb.batch
+    bt.q[..., 0] = lead * np.log(2) / bt.scale
+    w["q"] = bt.q.cpu()
+    qb.k_scale.fill_(2.0 ** -5)
+    codes = TABLE[qb.k.view(torch.uint8).cpu().numpy()]
+    qb.k.copy_(torch.as_tensor(codes / 8).float().cuda().to(torch.float8_e4m3fn))  # scores of about one
+    qb.k.view(torch.uint8)[..., 0] = 0
+    for b in range(w["batch"]):
+        page = int(w["page_table"][b, 0])
+        qb.k[page, :, 3] = torch.zeros(d, device="cuda").to(torch.float8_e4m3fn)
+        qb.k.view(torch.uint8)[page, :, 3, 0] = int(np.flatnonzero(TABLE == 32.0)[0])
+        qb.v.view(torch.uint8)[page, :, 3] = 0
+    bt.build_index()
+    for mode in ("dense", "list", "masked"):
+        check_against(w, qb, mode)
+
+
+@pytest.mark.parametrize("spread", [12, 30])
+@pytest.mark.parametrize("d,g,dtype", [(64, 2, "f32"), (128, 4, "f32"), (128, 4, "bf16"), (64, 1, "bf16")])
+def test_scales_far_apart_head_by_head(d, g, dtype, spread):
+    """V scales that differ from page to page and head to head by up to 2^60, each head judged by
+    its own rows; every fourth page's V is zero whatever its scale."""
+    w = wl.generate(case(d, g, dtype, batch=4, lo=200, hi=500, prompt=(150, 180), W=64, seed=spread))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    rng = np.random.default_rng(spread)
+    shift = torch.as_tensor(2.0 ** rng.integers(-spread, spread + 1, tuple(qb.v_scale.shape))).float()
+    qb.v_scale.copy_(shift)
+    qb.v.view(torch.uint8)[::4] = 0
+    qb.batch.build_index()
+    for mode in ("dense", "list", "masked"):
+        check_against(w, qb, mode)
