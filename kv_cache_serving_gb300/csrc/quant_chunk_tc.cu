@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   uint64_t* o_done = s_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_done + 2);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* redo = failed + 1;
+  uint32_t* redo = tmem_slot + 2;  // columns to be done again
   uint32_t* msk = reinterpret_cast<uint32_t*>(smem + Sh::kMask);
 
   // q: a thread holds 128 kTCols / 256 elements of one column
@@ -635,8 +635,25 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
       }
     }
     // A NaN may come from a row of V that other queries of the CTA keep (weight 0 times
-    // NaN): such a tile is done again query by query, from the rows each one keeps.
-    if (nan_probe != nan_probe) *redo = 1;
+    // NaN): such a column is done again, from the rows it keeps.  Not a place without a query
+    // (0 / 0 where it keeps no row), nor a column whose own scores are NaN.
+    if (__any_sync(0xffffffffu, nan_probe != nan_probe)) {
+      uint32_t hit = 0u;
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q) {
+        uint32_t o[16];
+        tmem_load<16>(t_lane + Sh::kO + 16 * q, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float u = __uint_as_float(o[c]) * fac[cg * W + 16 * q + c];
+          if (u != u) hit |= 1u << (cg * W + 16 * q + c);
+        }
+      }
+      hit = __reduce_or_sync(0xffffffffu, hit) &
+            __ballot_sync(0xffffffffu, t0 + (lane >> LG) < t1 && quant_redo_needed(fac[lane], ref[lane]));
+      if (lane == 0 && hit != 0u) atomicOr(redo, hit);
+    }
     tc_fence_before();
   } else {
     // give products in flight a bounded time to finish before the memory goes back
@@ -649,9 +666,9 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     tc_fence_after();
     tmem_dealloc<Sh::kTmem>(tmem);
   }
-  if (ok && *redo != 0)
+  if (ok && *redo != 0u)
     for (int col = warp; col < kTCols; col += kTThreads / 32)
-      if (t0 + (col >> LG) < t1 && quant_redo_needed(fac[col], ref[col]))
+      if ((*redo >> col) & 1u)
         quant_redo_query<kTD>(a, b, hk, L - n + t0 + (col >> LG), P, Wn, qh_of(col), lane);
 }
 

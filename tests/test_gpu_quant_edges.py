@@ -13,7 +13,7 @@ import oracle
 from kv_cache_serving_gb300 import dsa
 from kv_cache_serving_gb300 import workloads as wl
 from kv_cache_serving_gb300.session import DecodeBatch, QuantBatch
-from test_gpu_quant import TABLE, case, dequantised
+from test_gpu_quant import TABLE, case, dequantised, split  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +158,61 @@ def test_scales_far_apart_head_by_head(d, g, dtype, spread):
     qb.batch.build_index()
     for mode in ("dense", "list", "masked"):
         check_against(w, qb, mode)
+
+
+# ---------------------------------------------------------------------------
+# chunks: queries that keep nothing, hold NaN, or keep a NaN
+# ---------------------------------------------------------------------------
+
+def chunk(qb, q, n):
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:3], 7.0, device="cuda")
+    ql = torch.full((q.shape[0],), n, dtype=torch.int32, device="cuda")
+    qb.prefill_sparse(q, ql, out, lse)
+    torch.cuda.synchronize()
+    assert qb.batch.device_error() == 0
+    return out, lse
+
+
+def same_bits(a, b):
+    return all(torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+               for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
+@pytest.mark.parametrize("d,g,n", [(128, 1, 5), (128, 4, 5), (128, 1, 40), (64, 2, 5), (64, 4, 20)])
+def test_chunk_places_without_a_query_change_nothing(d, g, n, split):
+    """A tile that is not full, of whose empty places some keep no row at all under the mask
+    (offsets 1 and 2 kept) or every one keeps some (offsets past the chunk kept too, which no
+    query of the request reaches): the same bits."""
+    w = wl.generate(case(d, g, batch=3, lo=n, hi=n, prompt=(0, 0), W=300, seed=d + n))
+    gen = torch.Generator().manual_seed(n)
+    q = torch.randn(3, n, w["hq"], d, generator=gen).to(torch.bfloat16).cuda()
+    w["window"][:] = 300
+    got = []
+    for far in (False, True):
+        bits = np.zeros(w["mask_words"] * 32, np.uint8)
+        bits[[0, 1]] = 1
+        if far:
+            bits[n - 1:300] = 1
+        w["keep_mask"][:] = np.packbits(bits, bitorder="little").view(np.uint32)
+        got.append(chunk(QuantBatch.from_batch(DecodeBatch.from_workload(w)), q, n))
+    assert torch.isfinite(got[0][0]).all() and torch.isfinite(got[0][1]).all()
+    assert same_bits(*got)
+
+
+@pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
+@pytest.mark.parametrize("d,g,n", [(128, 1, 20), (128, 4, 7), (128, 4, 40), (64, 2, 16), (64, 4, 40)])
+def test_chunk_nan_query_leaves_the_others_bits(d, g, n, split):
+    w = wl.generate(case(d, g, batch=2, lo=200, hi=260, prompt=(40, 60), W=64, seed=d + n))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    gen = torch.Generator().manual_seed(n)
+    q = torch.randn(2, n, w["hq"], d, generator=gen).to(torch.bfloat16).cuda()
+    want = chunk(qb, q, n)
+    x = q.clone()
+    x[:, 2, 0, 3] = float("nan")
+    got = chunk(qb, x, n)
+    assert torch.isnan(got[0][:, 2, 0]).all() and torch.isnan(got[1][:, 2, 0]).all()
+    for a, b in zip(want, got):
+        b[:, 2, 0] = a[:, 2, 0]
+    assert same_bits(want, got)
