@@ -489,7 +489,9 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
     }
   // A NaN may come from a row of V that other queries of the tile keep (weight 0 times
   // NaN): the warp's columns are done again from the rows each one keeps.
-  if (__any_sync(0xffffffffu, nan_probe != nan_probe))
+  const bool redo = __any_sync(0xffffffffu, nan_probe != nan_probe);
+  __syncwarp();  // after the columns' first output: other lanes store to the same places
+  if (redo)
     for (int col = 0; col < kCols; ++col) {
       const int t = gt0 + (col >> lg);
       if (t >= gt1) break;
