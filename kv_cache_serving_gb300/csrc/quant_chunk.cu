@@ -131,6 +131,17 @@ struct ChunkState {
   }
 };
 
+template <int KG>
+struct ChunkTile {  // the last tokens, which see the most rows, first
+  static constexpr int kColumns = kCols * (kCW / KG);
+  __device__ __forceinline__ static void at(const QuantChunkLaunch& a, int& bpos, int& hk, int& t0) {
+    const int unit = blockIdx.x / a.parts;
+    bpos = unit / (a.q_tiles * a.hkv);
+    hk = unit / a.q_tiles % a.hkv;
+    t0 = (a.q_tiles - 1 - unit % a.q_tiles) * (kColumns >> a.group_log2);
+  }
+};
+
 template <int D, int KG>
 __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
     quant_chunk_kernel(const QuantChunkLaunch a) {
@@ -257,6 +268,7 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
     }
     cp_async_commit();
   };
+  if (threadIdx.x < 4) quant_redo_clear();
   __syncthreads();  // the mask
   {
     int pg[kCStages - 1];
@@ -459,47 +471,44 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
       for (int p = 0; p < nparts; ++p) st.template join<true>(of(p), lane);
     }
   }
-  if (kg != 0 || !active) return;
-  float nan_probe = 0.f;
+  if (kg == 0 && active) {
 #pragma unroll
-  for (int nt = 0; nt < kNT; ++nt)
+    for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float l = st.l[nt][h];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      const int col = 8 * nt + 2 * c + h, t = gt0 + (col >> lg);
-      if (t >= gt1) continue;
-      const size_t qh =
-          (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << lg) + (col & ((1 << lg) - 1));
-      const float r = 1.f / l;
-      uint32_t o[NK];
+      for (int h = 0; h < 2; ++h) {
+        float l = st.l[nt][h];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int col = 8 * nt + 2 * c + h, t = gt0 + (col >> lg);
+        if (t >= gt1) continue;
+        const size_t qh =
+            (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << lg) + (col & ((1 << lg) - 1));
+        const float r = 1.f / l;
+        float probe = 0.f;
+        uint32_t o[NK];
 #pragma unroll
-      for (int mt = 0; mt < NK; ++mt) {
-        o[mt] = bf16x2_rn(st.acc[nt][mt][h] * r, st.acc[nt][mt][2 + h] * r);
-        if (quant_redo_needed(l, st.ref[nt][h])) nan_probe += st.acc[nt][mt][h] + st.acc[nt][mt][2 + h];
+        for (int mt = 0; mt < NK; ++mt) {
+          o[mt] = bf16x2_rn(st.acc[nt][mt][h] * r, st.acc[nt][mt][2 + h] * r);
+          probe += st.acc[nt][mt][h] + st.acc[nt][mt][2 + h];
+        }
+        // A NaN may come from a row of V that other queries of the tile keep (weight 0 times NaN):
+        // such a column is done again, from the rows it keeps.
+        if (probe != probe && quant_redo_needed(l, st.ref[nt][h])) {
+          quant_redo().hit = 1;
+          atomicOr(&quant_redo().out[cg], 1u << col);
+          if (quant_sum_unsure(l, st.ref[nt][h])) atomicOr(&quant_redo().sum[cg], 1u << col);
+        }
+        uint4* to = reinterpret_cast<uint4*>(a.out + qh * D + g * (D / 8));
+#pragma unroll
+        for (int i = 0; i < NK / 4; ++i)
+          to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        if (a.lse != nullptr && g == 0)
+          a.lse[qh] = (st.ref[nt][h] + log2f(l)) * kLn2;
       }
-      uint4* to = reinterpret_cast<uint4*>(a.out + qh * D + g * (D / 8));
-#pragma unroll
-      for (int i = 0; i < NK / 4; ++i)
-        to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      if (a.lse != nullptr && g == 0)
-        a.lse[qh] = (st.ref[nt][h] + log2f(l)) * kLn2;
-    }
-  // A NaN may come from a row of V that other queries of the tile keep (weight 0 times
-  // NaN): the warp's columns are done again from the rows each one keeps.
-  const bool redo = __any_sync(0xffffffffu, nan_probe != nan_probe);
-  __syncwarp();  // after the columns' first output: other lanes store to the same places
-  if (redo)
-    for (int col = 0; col < kCols; ++col) {
-      const int t = gt0 + (col >> lg);
-      if (t >= gt1) break;
-      quant_redo_query<D>(a, b, hk, L - n + t, P, W,
-                          (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << lg) +
-                              (col & ((1 << lg) - 1)),
-                          lane);
-    }
+  }
+  __syncthreads();  // after the columns' first output
+  if (quant_redo().hit != 0) quant_redo_tile<D, ChunkTile<KG>>(a);
 }
 
 template <int D, int KG>

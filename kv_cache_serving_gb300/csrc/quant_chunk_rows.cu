@@ -82,6 +82,16 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t* w) {
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
+template <int LG>
+struct RowsTile {  // the last query tokens, which see the most rows, first
+  static constexpr int kColumns = kRRows;
+  __device__ __forceinline__ static void at(const QuantChunkLaunch&, int& bpos, int& hk, int& t0) {
+    bpos = blockIdx.z;
+    hk = blockIdx.y;
+    t0 = (gridDim.x - 1 - blockIdx.x) * (kRRows >> LG);
+  }
+};
+
 template <int D, int LG>
 __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const QuantChunkLaunch a) {
   using Sh = RowsShape<D>;
@@ -240,6 +250,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     fence_mbar_init();
     *failed = 0;
   }
+  if (tid < 4) quant_redo_clear();
   const bool converts = warp >= 4 && warp < 8;
   const int id0 = converts ? load_id(0) : 0;
   __syncthreads();  // barriers, tensor-memory address
@@ -581,13 +592,15 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       tc_fence_before();
       // A NaN may come from a row of V that other queries of the CTA keep (weight 0 times
       // NaN): such a query is done again, from the rows it keeps.
-      unsigned nan =
+      const unsigned nan =
           __ballot_sync(0xffffffffu, mine && probe != probe && quant_redo_needed(l, ref));
-      __syncwarp();  // after the rows' first output
-      while (nan != 0u) {
-        const int rr = 32 * warp + __ffs(nan) - 1;
-        nan &= nan - 1u;
-        quant_redo_query<D>(a, b, hk, i_first + (rr >> LG), P, Wn, qh_of(rr), lane);
+      if (nan != 0u) {
+        const unsigned sums = __ballot_sync(0xffffffffu, quant_sum_unsure(l, ref));
+        if (lane == 0) {
+          quant_redo().out[warp] = nan;
+          quant_redo().sum[warp] = sums;
+          quant_redo().hit = 1;
+        }
       }
     }
   }
@@ -605,6 +618,7 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
     tc_fence_after();
     tmem_dealloc<Sh::kTmem>(tmem);
   }
+  if (quant_redo().hit != 0) quant_redo_tile<D, RowsTile<LG>>(a);
 }
 
 template <int D, int LG>

@@ -94,6 +94,16 @@ __device__ __forceinline__ float scatter_max(float (&v)[16], int lane) {
 }
 
 template <int LG>
+struct TcTile {
+  static constexpr int kColumns = kTCols;
+  __device__ __forceinline__ static void at(const QuantChunkLaunch&, int& bpos, int& hk, int& t0) {
+    bpos = blockIdx.z;
+    hk = blockIdx.y;
+    t0 = blockIdx.x * (kTCols >> LG);
+  }
+};
+
+template <int LG>
 __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const QuantChunkLaunch a) {
   using Sh = TcShape;
   constexpr int W = kTCols / 2;              // columns per warp ...
@@ -163,7 +173,6 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
   uint64_t* o_done = s_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_done + 2);
   volatile int* failed = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* redo = tmem_slot + 2;  // columns to be done again
   uint32_t* msk = reinterpret_cast<uint32_t*>(smem + Sh::kMask);
 
   // q: a thread holds 128 kTCols / 256 elements of one column
@@ -195,8 +204,8 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     mbar_init(o_done, 1);
     fence_mbar_init();
     *failed = 0;
-    *redo = 0;
   }
+  if (tid < 4) quant_redo_clear();
   if (tid < kTCols) {
     ref[tid] = -INFINITY;
     nref[tid] = INFINITY;
@@ -608,6 +617,15 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     if (tid < kTCols) {
       const float t = cmax[tid] + cmax[kTCols + tid] + cmax[2 * kTCols + tid] + cmax[3 * kTCols + tid];
       fac[tid] = 1.f / t;
+      // columns to be done again should their output hold a NaN: not a place without a query
+      // (0 / 0 where it keeps no row), nor one whose own scores are NaN
+      const uint32_t out =
+          __ballot_sync(0xffffffffu, t0 + (tid >> LG) < t1 && quant_redo_needed(t, ref[tid]));
+      const uint32_t sum = __ballot_sync(0xffffffffu, quant_sum_unsure(t, ref[tid]));
+      if (tid == 0) {
+        quant_redo().out[0] = out;
+        quant_redo().sum[0] = sum;
+      }
       if (a.lse != nullptr && t0 + (tid >> LG) < t1)
         a.lse[qh_of(tid)] = (ref[tid] - kTHead + log2f(t)) * kLn2;
     }
@@ -626,34 +644,22 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
       for (int c = 0; c < 16; c += 2) {
         const float2 r = *reinterpret_cast<const float2*>(fac + cg * W + 16 * q + c);
         const float u = __uint_as_float(o[c]) * r.x, v = __uint_as_float(o[c + 1]) * r.y;
-        nan_probe += u + v;
         const float got = __shfl_xor_sync(0xffffffffu, odd ? u : v, 1);
-        const uint32_t w = odd ? bf16x2_rn(got, v) : bf16x2_rn(u, got);
-        const int col = cg * W + 16 * q + c + odd;
-        if (t0 + (col >> LG) < t1)
-          *reinterpret_cast<uint32_t*>(a.out + qh_of(col) * kTD + (row & ~1)) = w;
+        const float lo = odd ? got : u, hi = odd ? v : got;
+        // (column and place worked out again: held in registers until here they spill, 130
+        // us instead of 123 on 32 tokens of 64 requests)
+        const int col = static_cast<int>(threadIdx.x >> 7) * W + 16 * q + c + odd, t = t0 + (col >> LG);
+        if (t < t1) {
+          const size_t qh =
+              (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << LG) + (col & ((1 << LG) - 1));
+          *reinterpret_cast<uint32_t*>(a.out + qh * kTD + (row & ~1)) = bf16x2_rn(lo, hi);
+          nan_probe += lo + hi;
+        }
       }
     }
     // A NaN may come from a row of V that other queries of the CTA keep (weight 0 times
-    // NaN): such a column is done again, from the rows it keeps.  Not a place without a query
-    // (0 / 0 where it keeps no row), nor a column whose own scores are NaN.
-    if (__any_sync(0xffffffffu, nan_probe != nan_probe)) {
-      uint32_t hit = 0u;
-#pragma unroll
-      for (int q = 0; q < kChunks; ++q) {
-        uint32_t o[16];
-        tmem_load<16>(t_lane + Sh::kO + 16 * q, o);
-        tc_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float u = __uint_as_float(o[c]) * fac[cg * W + 16 * q + c];
-          if (u != u) hit |= 1u << (cg * W + 16 * q + c);
-        }
-      }
-      hit = __reduce_or_sync(0xffffffffu, hit) &
-            __ballot_sync(0xffffffffu, t0 + (lane >> LG) < t1 && quant_redo_needed(fac[lane], ref[lane]));
-      if (lane == 0 && hit != 0u) atomicOr(redo, hit);
-    }
+    // NaN): such a column is done again, from the rows it keeps.
+    if (nan_probe != nan_probe) quant_redo().hit = 1;
     tc_fence_before();
   } else {
     // give products in flight a bounded time to finish before the memory goes back
@@ -662,14 +668,11 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 0) {
+  if (threadIdx.x < 32) {
     tc_fence_after();
     tmem_dealloc<Sh::kTmem>(tmem);
   }
-  if (ok && *redo != 0u)
-    for (int col = warp; col < kTCols; col += kTThreads / 32)
-      if ((*redo >> col) & 1u)
-        quant_redo_query<kTD>(a, b, hk, L - n + t0 + (col >> LG), P, Wn, qh_of(col), lane);
+  if (*reinterpret_cast<volatile int*>(&quant_redo().hit) != 0) quant_redo_tile<kTD, TcTile<LG>>(a);
 }
 
 template <int LG>

@@ -216,3 +216,69 @@ def test_chunk_nan_query_leaves_the_others_bits(d, g, n, split):
     for a, b in zip(want, got):
         b[:, 2, 0] = a[:, 2, 0]
     assert same_bits(want, got)
+
+
+@pytest.mark.parametrize("split", [0, 1, 2], indirect=True)
+@pytest.mark.parametrize("d,g,n", [(128, 1, 20), (128, 4, 7), (128, 4, 40), (64, 2, 16), (64, 4, 40)])
+def test_chunk_nan_values_reach_their_element_alone(d, g, n, split):
+    """NaN codes of both signs in V rows of the prompt, the window and the chunk: NaN in those
+    elements of the queries that keep the row, no sum touched, and elements without a NaN
+    within two roundings (fp16 weights, bf16 out) of what they were."""
+    w = wl.generate(case(d, g, batch=3, hkv=2, lo=200, hi=260, prompt=(40, 60), W=64, seed=d + n))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    gen = torch.Generator().manual_seed(n)
+    q = torch.randn(3, n, w["hq"], d, generator=gen).to(torch.bfloat16).cuda()
+    base, lse = chunk(qb, q, n)
+    codes = qb.v.view(torch.uint8)
+    rng = np.random.default_rng(n)
+    want = torch.zeros(base.shape, dtype=torch.bool)
+    for b in range(3):
+        L, P, W = (int(w[x][b]) for x in ("seq_len", "prompt_len", "window"))
+        # request 0: a prompt row; 1: a window row and one of the chunk; 2: many, the last one too
+        js = ([5], [L - n - 9, L - n // 2], list(rng.choice(L, 40, replace=False)) + [L - 1])[b]
+        for hk in range(2):
+            kept = [set(oracle.kept_set(L - n + t + 1, P, W, w["keep_mask"][b, hk])) for t in range(n)]
+            for j in js:
+                dims = rng.choice(d, 3, replace=False)
+                row = codes[int(w["page_table"][b, j // 16]), hk, j % 16]
+                row[torch.as_tensor(dims).cuda()] = torch.as_tensor([127, 255, 127], dtype=torch.uint8).cuda()
+                for t in range(n):
+                    if j in kept[t]:
+                        want[b, t, hk * g:hk * g + g, dims] = True
+    out, l = chunk(qb, q, n)
+    assert torch.equal(torch.isnan(out).cpu(), want)
+    assert same_bits([l], [lse])
+    # rows that hold a NaN lose nothing but that element: each other element is the same sum
+    ok = ~want.cuda()
+    assert torch.allclose(out[ok].float(), base[ok].float(), rtol=2 ** -7, atol=4e-3)
+
+
+@pytest.mark.parametrize("split", [0, 1], indirect=True)
+@pytest.mark.parametrize("d,n,L", [(128, 8, 2000), (128, 2000, 2000), (64, 8, 2000), (64, 2000, 2000)])
+def test_chunk_nan_value_costs_no_more_than_a_few_calls(d, n, L, split):
+    """One NaN element in the first V row, which every query keeps, and one in a row that some
+    queries keep: no order of magnitude slower than the same call without."""
+    w = wl.generate(case(d, 4, batch=4, hkv=4, lo=L, hi=L, prompt=(50, 60), W=300, seed=5))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    q = torch.randn(4, n, w["hq"], d, device="cuda").to(torch.bfloat16)
+    out, ql = torch.empty_like(q), torch.full((4,), n, dtype=torch.int32, device="cuda")
+
+    def best():
+        times = []
+        for _ in range(7):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(3):
+                qb.prefill_sparse(q, ql, out, None)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) / 3)
+        return min(times)
+
+    clean = best()
+    codes = qb.v.view(torch.uint8)
+    for j in (0, L - 20):
+        codes[qb.batch.page_table[:, j // 16].long(), :, j % 16, 3] = 127
+    slow = best()
+    assert torch.isnan(out.float()).any()
+    assert slow <= 6 * clean + 0.02, (slow, clean)  # milliseconds
