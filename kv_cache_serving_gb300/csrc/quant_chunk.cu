@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kCW * 32, D == 128 ? 2 : 3)
               z[nt][v] = fmaf(z[nt][v], c1, lv);
               if (decltype(masked)::value && !((keep >> (4 * nt + v)) & 1u)) z[nt][v] = -INFINITY;
             }
-            over |= fmaxf(z[nt][h], z[nt][2 + h]) > st.ref[nt][h] + (kCHead + kCSlack);
+            over |= fmaxf(z[nt][h], z[nt][2 + h]) - st.ref[nt][h] > kCHead + kCSlack;
           }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll

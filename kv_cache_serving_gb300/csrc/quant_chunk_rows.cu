@@ -505,8 +505,11 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
           top = fmaxf(top, fmaf(fmaxf(max3(m[0], m[1], m[2]), m[3]), f * pgi.x, pgi.y));
         }
       }
-      if (__any_sync(0xffffffffu, top > ref + (kRHead + kRSlack))) {
-        const float to = top > ref + (kRHead + kRSlack) ? top - kRHead : ref;
+      // (the difference is exact where it counts; ref + 14 rounds to as much as ref + 16 from
+      // 2^25 on, and 2^16 is no fp16)
+      const bool over = top - ref > kRHead + kRSlack;
+      if (__any_sync(0xffffffffu, over)) {
+        const float to = over ? top - kRHead : ref;
         const float down = ex2_approx(ref - to);
         ref = to;
         l *= down;
@@ -591,9 +594,10 @@ __global__ void __launch_bounds__(kRThreads, 2) quant_chunk_rows_kernel(const Qu
       }
       tc_fence_before();
       // A NaN may come from a row of V that other queries of the CTA keep (weight 0 times
-      // NaN): such a query is done again, from the rows it keeps.
+      // NaN), an infinity from a weight past fp16 (scores of 2^20 and more): such a query is done
+      // again, from the rows it keeps.
       const unsigned nan =
-          __ballot_sync(0xffffffffu, mine && probe != probe && quant_redo_needed(l, ref));
+          __ballot_sync(0xffffffffu, mine && !(fabsf(probe) < INFINITY) && quant_redo_needed(l, ref));
       if (nan != 0u) {
         const unsigned sums = __ballot_sync(0xffffffffu, quant_sum_unsure(l, ref));
         if (lane == 0) {

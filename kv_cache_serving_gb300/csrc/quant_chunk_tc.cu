@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
     // lane pairs exchange columns: an even lane stores column c, dims row and row + 1,
     // its neighbour column c + 1
     const int odd = lane & 1;
-    float nan_probe = 0.f;
+    float probe = 0.f;
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
       uint32_t o[16];
@@ -653,13 +653,14 @@ __global__ void __launch_bounds__(kTThreads, 2) quant_chunk_tc_kernel(const Quan
           const size_t qh =
               (static_cast<size_t>(b) * a.max_q + t) * a.hq + (hk << LG) + (col & ((1 << LG) - 1));
           *reinterpret_cast<uint32_t*>(a.out + qh * kTD + (row & ~1)) = bf16x2_rn(lo, hi);
-          nan_probe += lo + hi;
+          probe += lo + hi;
         }
       }
     }
     // A NaN may come from a row of V that other queries of the CTA keep (weight 0 times
-    // NaN): such a column is done again, from the rows it keeps.
-    if (nan_probe != nan_probe) quant_redo().hit = 1;
+    // NaN), an infinity from a weight past fp16 (scores of 2^20 and more): such a column is done
+    // again, from the rows it keeps.
+    if (!(fabsf(probe) < INFINITY)) quant_redo().hit = 1;
     tc_fence_before();
   } else {
     // give products in flight a bounded time to finish before the memory goes back

@@ -168,8 +168,10 @@ struct QuantWarp {
           inv[r] = 0.f;
         }
     }
-    const bool over = fmaxf(y[0], y[2]) > ref[0] + (kHead + kSlack) ||
-                      fmaxf(y[1], y[3]) > ref[1] + (kHead + kSlack);
+    // (the difference is exact where it counts; ref + 14 rounds to as much as ref + 16 from 2^25
+    // on, and 2^16 is no fp16)
+    const bool over = fmaxf(y[0], y[2]) - ref[0] > kHead + kSlack ||
+                      fmaxf(y[1], y[3]) - ref[1] > kHead + kSlack;
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {

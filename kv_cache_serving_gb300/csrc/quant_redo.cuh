@@ -44,8 +44,8 @@ __device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) {
 __device__ __forceinline__ uint32_t e4m3_nan_bits(uint32_t is) { return (is >> 7) * 0x10204080u >> 28; }
 
 // The columns of a CTA's tile that may have to be done again (`out`), and those whose sum may be
-// wrong as well: a bit each, up to 128 columns; `hit`: some output holds a NaN.  At an address
-// that takes no register.
+// wrong as well: a bit each, up to 128 columns; `hit`: some output holds a
+// NaN or an infinity.  At an address that takes no register.
 struct QuantRedo {
   uint32_t out[4], sum[4];
   int hit;

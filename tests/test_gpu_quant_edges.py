@@ -282,3 +282,78 @@ def test_chunk_nan_value_costs_no_more_than_a_few_calls(d, n, L, split):
     slow = best()
     assert torch.isnan(out.float()).any()
     assert slow <= 6 * clean + 0.02, (slow, clean)  # milliseconds
+
+
+# ---------------------------------------------------------------------------
+# scores of any size
+# ---------------------------------------------------------------------------
+
+def huge_case(d, g, dtype, E, L, prompt):
+    """Scores of exactly 2^E + 2^s u (log2 units, scale * log2(e) being 1 in fp32), u = 0 in the
+    first half of the rows, 1 in the second, 2 in the last quarter of that; all of it exact in fp32."""
+    s = max(4, E - 23)
+    w = wl.generate(case(d, g, dtype, batch=2, hkv=2, lo=L, hi=L, prompt=(prompt, prompt), W=64, seed=E))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    log2e = np.float32(1.4426950408889634)
+    near = [np.nextafter(np.float32(np.log(2)), np.float32(x)) for x in (0, 0.5, 1)] + [np.float32(np.log(2))]
+    qb.batch.scale = float(next(x for x in near if x * log2e == np.float32(1)))
+    codes = np.zeros(tuple(qb.k.shape), np.float32)
+    u = np.zeros(L)
+    u[L // 2:], u[L - L // 8:] = 1, 2
+    for b in range(2):
+        page = np.asarray(w["page_table"])[b, np.arange(L) // 16]
+        codes[page, :, np.arange(L) % 16, 0] = 16
+        codes[page, :, np.arange(L) % 16, 1] = u[:, None]
+    qb.k.copy_(torch.as_tensor(codes).cuda().to(torch.float8_e4m3fn))
+    qb.k_scale.fill_(1.0)
+    qb.v_scale.fill_(1.0)
+    qb.v.view(torch.uint8).clamp_(1, 119)  # above zero: an infinite weight would make no NaN
+    q = torch.zeros(d, device="cuda")
+    q[0], q[1] = 2.0 ** (E - 4), 2.0 ** s
+    return w, qb, q, u * 2.0 ** s
+
+
+def check_huge(w, qb, out, lse, rows, x, E, hk, g, b):
+    """out and lse [heads of hk] of one query over `rows`; the roundings are those of any call:
+    fp16 weights 2^-11, sums 2^-13, of max |V|, and out's own (bf16 2^-8, fp32 2^-24)."""
+    v = dequantised(qb)[1].double().numpy()[np.asarray(w["page_table"])[b, rows // 16], rows % 16, hk]
+    p = np.exp2(x[rows] - x[rows].max())
+    ref, vmax = p @ v / p.sum(), np.abs(v).max()
+    u = 2.0 ** -24 if out.dtype == torch.float32 else 2.0 ** -8
+    weights = 0.0 if out.dtype == torch.float32 else 2.0 ** -11
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert (err <= u * np.abs(ref) + (weights + 2.0 ** -13) * vmax).all()
+    want = (2.0 ** E + x[rows].max() + np.log2(p.sum())) * np.log(2)
+    assert (np.abs(lse.double().cpu().numpy() - want) <= 2.0 ** -20 * want).all()
+
+
+@pytest.mark.parametrize("E", [20, 23, 24, 25, 26, 27, 28, 29])
+@pytest.mark.parametrize("d,g,dtype", [(128, 4, "bf16"), (64, 1, "bf16"), (128, 2, "f32")])
+def test_decode_scores_of_any_size(d, g, dtype, E):
+    w, qb, q, x = huge_case(d, g, dtype, E, 640, 500)
+    bt = qb.batch
+    bt.q.copy_(q.expand_as(bt.q))
+    bt.build_index()
+    for mode, call in (("dense", qb.decode_dense), ("list", qb.decode_sparse), ("masked", qb.decode_sparse_masked)):
+        out, lse = call()
+        torch.cuda.synchronize()
+        assert bt.device_error() == 0
+        for b in range(2):
+            for hk in range(2):
+                rows = np.arange(640) if mode == "dense" else oracle.kept_set(
+                    640, 500, int(w["window"][b]), w["keep_mask"][b, hk])
+                check_huge(w, qb, out[b, hk * g:hk * g + g], lse[b, hk * g:hk * g + g], rows, x, E, hk, g, b)
+
+
+@pytest.mark.parametrize("split", [1, 2], indirect=True)
+@pytest.mark.parametrize("E", [20, 24, 25, 26, 27, 28, 29])
+@pytest.mark.parametrize("d,g,n", [(128, 4, 5), (128, 1, 40), (64, 2, 12), (64, 4, 40)])
+def test_chunk_scores_of_any_size(d, g, n, E, split):
+    w, qb, q, x = huge_case(d, g, "bf16", E, 640, 560)
+    qs = q.to(torch.bfloat16).expand(2, n, w["hq"], d).contiguous()
+    out, lse = chunk(qb, qs, n)
+    for b in range(2):
+        for hk in range(2):
+            for t in (0, n // 2, n - 1):
+                rows = oracle.kept_set(640 - n + t + 1, 560, int(w["window"][b]), w["keep_mask"][b, hk])
+                check_huge(w, qb, out[b, t, hk * g:hk * g + g], lse[b, t, hk * g:hk * g + g], rows, x, E, hk, g, b)
