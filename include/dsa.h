@@ -528,8 +528,8 @@ typedef struct {
 /*
  * dsa_rope_axes -- rotate the query and key heads of `tokens` tokens:
  *   (x, y) -> (x cos a - y sin a, y cos a + x sin a)   for every pair of a head,
- * with a = angle_i above, kept as a 64-bit fixed-point fraction of a turn (far
- * positions lose nothing), the rotation in fp32, rounded once to the output.
+ * with a = angle_i above, kept as a fixed-point fraction of a turn and good to 2^-27
+ * turns at any position, the rotation in fp32, rounded once to the output.
  * The model side of the method's decode step: the pages it serves are image
  * models whose tokens sit on a grid, so a token's rows, columns and frame are
  * positions of their own.

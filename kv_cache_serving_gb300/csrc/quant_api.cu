@@ -109,6 +109,21 @@ dsa_status rows_common(const dsa_dims* d, const dsa_quant_cache* c, int32_t max_
   return DSA_OK;
 }
 
+// f radians (0 <= f <= 2 pi) in turns, as a 64-bit fraction (a whole turn is none), to half a unit:
+// the double's whole mantissa times 1 / (2 pi) to 128 bits, so that a position of 31 bits times
+// the result is still good to 2^-34 turns.
+uint64_t turns_of(double f) {
+  if (f == 0.0) return 0;
+  using u128 = unsigned __int128;
+  int e;
+  const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(f, &e), 53));  // f = m 2^(e - 53)
+  // 2^130 / (2 pi), rounded down
+  constexpr uint64_t hi = 0xa2f9836e4e441529ull, lo = 0xfc2757d1f534ddc0ull;
+  const u128 p = static_cast<u128>(m) * hi + ((static_cast<u128>(m) * lo) >> 64);  // m / (2 pi) 2^66
+  const int shift = 55 - e;  // to f / (2 pi) 2^64; at least 52, as f < 2^3
+  return shift >= 127 ? 0 : static_cast<uint64_t>((p + (static_cast<u128>(1) << (shift - 1))) >> shift);
+}
+
 bool row_stride_ok(int64_t stride, int64_t least, int elt) {
   return stride >= least && (stride * elt) % 16 == 0;
 }
@@ -138,10 +153,7 @@ dsa_status dsa_rope_axes(const dsa_dims* dims, const dsa_rope* rope, int32_t tok
     const double f = rope->inv_freq[i];
     if (!std::isfinite(f) || std::fabs(f) > 6.283185307179587 || rope->pair_axis[i] >= rope->axes)
       return DSA_ERR_INVALID_ARG;
-    // turns per position as a 64-bit fraction (2^64 / 2 pi units per radian): at most one
-    // turn, and a whole turn is none
-    const double scaled = std::fabs(f) * 2935890503282001226.5;
-    const uint64_t t = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
+    const uint64_t t = turns_of(std::fabs(f));
     a.turn[i] = f < 0 ? 0 - t : t;
     a.pair_axis[i] = rope->pair_axis[i];
   }

@@ -3,9 +3,10 @@
 //
 // Pair i of every head of a token turns by positions[axis(i)] * inv_freq[i].  The angle
 // is a fixed-point fraction of a turn: the host gives pair i's turns per position as a
-// 64-bit fraction, the kernel multiplies by the position modulo 2^64 -- which is the
-// reduction to one turn, exact for any position -- and takes the sine and cosine of the
-// top 32 bits (error 2^-32 turns) with sincospi.
+// 64-bit fraction (2^-65), the kernel multiplies by the position modulo 2^64 -- which is the
+// reduction to one turn, good to 2^-34 turns at the farthest position -- and takes the rest to
+// the nearest quarter turn as an fp32, at most an eighth of a turn and so good to 2^-28, for
+// sincospi; the quarters swap and negate the two.
 //
 // Bound by HBM: each element is read and written once.  A CTA computes the table of
 // its tokens' cosines and sines in shared memory once for all heads, then streams the
@@ -95,11 +96,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeLaunch a) 
     const int t = x / kPairs, i = x % kPairs;
     const int64_t pos = a.positions[static_cast<size_t>(t0 + t) * a.axes + a.pair_axis[i]];
     const uint64_t turn = static_cast<uint64_t>(pos) * a.turn[i];
-    // signed half turns in [-1, 1)
-    const float half = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-    float s, c;
-    sincospif(half, &s, &c);
-    reinterpret_cast<float2*>(&cs[t][table_unit(i >> 1)])[i & 1] = make_float2(c, s);
+    const uint32_t quarter = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);  // the nearest, 0 .. 3
+    const int64_t rest = static_cast<int64_t>(turn - (static_cast<uint64_t>(quarter) << 62));
+    float s, c;  // of half turns in [-1/4, 1/4)
+    sincospif(static_cast<float>(static_cast<int32_t>(rest >> 30)) * 0x1p-33f, &s, &c);
+    const float cq = quarter & 1 ? s : c, sq = quarter & 1 ? c : s;
+    reinterpret_cast<float2*>(&cs[t][table_unit(i >> 1)])[i & 1] =
+        make_float2(quarter == 1 || quarter == 2 ? -cq : cq, quarter >= 2 ? -sq : sq);
   }
   __syncthreads();
   const int nq = a.q != nullptr ? a.hq : 0, nk = a.k != nullptr ? a.hkv : 0;

@@ -357,3 +357,72 @@ def test_chunk_scores_of_any_size(d, g, n, E, split):
             for t in (0, n // 2, n - 1):
                 rows = oracle.kept_set(640 - n + t + 1, 560, int(w["window"][b]), w["keep_mask"][b, hk])
                 check_huge(w, qb, out[b, t, hk * g:hk * g + g], lse[b, t, hk * g:hk * g + g], rows, x, E, hk, g, b)
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+
+def _inv_two_pi():
+    """1 / (2 pi) over 2^256, rounded down."""
+    one = 1 << 320
+
+    def arctan_inv(x):  # arctan(1 / x) over 2^320 (Machin's formula)
+        total, term, k, sign = 0, one // x, 1, 1
+        while term:
+            total += sign * (term // k)
+            term //= x * x
+            k, sign = k + 2, -sign
+        return total
+
+    pi = 4 * (4 * arctan_inv(5) - arctan_inv(239))
+    return (one << 256) // (2 * pi)
+
+
+def rope64(x, positions, inv_freq, axis, pairing):
+    """The rotation with its angle reduced to one turn in whole numbers and its sine and cosine
+    in 64 bits (of an angle within a quarter turn)."""
+    inv, d = _inv_two_pi(), x.shape[-1]
+    c, s = (np.empty((x.shape[0], d // 2)) for _ in range(2))
+    for i in range(d // 2):
+        num, den = float(inv_freq[i]).as_integer_ratio()
+        for t in range(x.shape[0]):
+            turn = (num * int(positions[t, axis[i]]) * inv // den) % (1 << 256)
+            k = (turn + (1 << 253)) >> 254                      # nearest quarter turn
+            a = 2 * np.pi * ((turn - (k << 254)) / (1 << 256))
+            c[t, i], s[t, i] = ((np.cos(a), np.sin(a)), (-np.sin(a), np.cos(a)), (-np.cos(a), -np.sin(a)),
+                                (np.sin(a), -np.cos(a)))[k % 4]
+    c, s = c[:, None], s[:, None]
+    lo, hi = ((slice(0, d // 2), slice(d // 2, d)) if pairing == "halves" else
+              (slice(0, d, 2), slice(1, d, 2)))
+    y, size = np.empty(x.shape), np.empty(x.shape)
+    y[..., lo] = x[..., lo] * c - x[..., hi] * s
+    y[..., hi] = x[..., hi] * c + x[..., lo] * s
+    size[..., lo] = size[..., hi] = np.abs(x[..., lo]) + np.abs(x[..., hi])
+    return y, size
+
+
+@pytest.mark.parametrize("pairing", ["halves", "neighbours"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rope_angles_to_the_last_bits(d, pairing):
+    """Positions from 0 to the ends of their type, frequencies from one turn per position down.
+    fp32: the angle is off by 2^-32 turns and by half a step of an fp32 below 1/8, 2^-28 turns,
+    together below 2^-25 radians; sine and cosine by 2^-24 (one unit in the last place below 1);
+    the two products and their sum by 2^-24 each of what they hold.  Relative to |x| + |y| that
+    is 2^-25 + 2^-24 + 2 * 2^-24, below 2^-22."""
+    rng = np.random.default_rng(d)
+    pos = np.concatenate([np.array([0, 1, -1, 2**31 - 1, -2**31, 2**24 + 1, 2**30 + 12345]),
+                          rng.integers(-2**31, 2**31, 30), rng.integers(0, 70000, 30)])[:, None]
+    inv = np.concatenate([[2 * np.pi * (1 - 2**-53), 1.0, -1.0, 3.0, 0.7, 1e-3, 6.28, 1e-9, 2.0**-60, np.pi / 2],
+                          10000.0 ** (-2 * np.arange(d // 2 - 10) / d)])
+    dims = dsa.make_dims(1, 2, 1, d, 1, 1, 0, 1, 1, "f32", "bf16")
+    rope = dsa.make_rope(inv, [0] * (d // 2), pairing=pairing)
+    q = torch.randn(len(pos), 2, d, device="cuda")
+    k = torch.randn(len(pos), 1, d, device="cuda").to(torch.bfloat16)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    dsa.dsa_rope_axes(dims, rope, torch.as_tensor(pos.astype(np.int32)).cuda(), q, k, qo, ko)
+    for got, x, u in ((qo, q, 0.0), (ko, k, 2.0 ** -8)):
+        ref, size = rope64(x.double().cpu().numpy(), pos, inv, [0] * (d // 2), pairing)
+        tol = size * 2.0 ** -22
+        err = np.abs(got.double().cpu().numpy() - ref)
+        assert (err <= tol + u * (np.abs(ref) + tol)).all(), (err / size).max()
