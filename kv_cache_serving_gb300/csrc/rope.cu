@@ -24,6 +24,9 @@ namespace dsa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+// Cosine of a pair that does not turn at any position: its elements stay what they are, where
+// x 1 - y 0 would carry an infinity or a NaN from one to the other.
+constexpr float kStill = 2.f;
 
 template <bool BF16>
 __device__ __forceinline__ void load8(const void* p, size_t at, float (&x)[8]) {
@@ -77,8 +80,8 @@ __device__ __forceinline__ void rotate8(const void* in, size_t at_in, void* out,
       float& x = !NEAR ? u[2 * i + k] : i < 2 ? u[4 * i + 2 * k] : v[4 * i - 8 + 2 * k];
       float& y = !NEAR ? v[2 * i + k] : i < 2 ? u[4 * i + 2 * k + 1] : v[4 * i - 7 + 2 * k];
       const float rx = x * c - y * n, ry = y * c + x * n;
-      x = rx;
-      y = ry;
+      x = c == kStill ? x : rx;
+      y = c == kStill ? y : ry;
     }
   }
   store8<BF16>(out, at_out + lo, u);
@@ -101,8 +104,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeLaunch a) 
     float s, c;  // of half turns in [-1/4, 1/4)
     sincospif(static_cast<float>(static_cast<int32_t>(rest >> 30)) * 0x1p-33f, &s, &c);
     const float cq = quarter & 1 ? s : c, sq = quarter & 1 ? c : s;
+    const float co = a.turn[i] == 0 ? kStill : quarter == 1 || quarter == 2 ? -cq : cq;
     reinterpret_cast<float2*>(&cs[t][table_unit(i >> 1)])[i & 1] =
-        make_float2(quarter == 1 || quarter == 2 ? -cq : cq, quarter >= 2 ? -sq : sq);
+        make_float2(co, quarter >= 2 ? -sq : sq);
   }
   __syncthreads();
   const int nq = a.q != nullptr ? a.hq : 0, nk = a.k != nullptr ? a.hkv : 0;

@@ -426,3 +426,35 @@ def test_rope_angles_to_the_last_bits(d, pairing):
         tol = size * 2.0 ** -22
         err = np.abs(got.double().cpu().numpy() - ref)
         assert (err <= tol + u * (np.abs(ref) + tol)).all(), (err / size).max()
+
+
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+@pytest.mark.parametrize("pairing", ["halves", "neighbours"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rope_leaves_pairs_without_a_frequency(d, pairing, qt):
+    """A partial embedding: pairs of inv_freq 0 come out as they went in whatever they hold --
+    infinities, NaN, zeros of both signs, the largest and smallest numbers -- and turn nothing
+    else; the other pairs are the bits of a call with finite values there."""
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[qt]
+    dims = dsa.make_dims(1, 2, 1, d, 1, 1, 0, 1, 1, qt, qt)
+    inv = np.array([10000.0 ** (-2 * i / d) if i < d // 4 else 0.0 for i in range(d // 2)])
+    rope = dsa.make_rope(inv, [0] * (d // 2), pairing=pairing)
+    pos = torch.tensor([[0], [7], [-3], [2**31 - 1], [100000]], dtype=torch.int32, device="cuda")
+    still = np.zeros(d, bool)
+    i = np.flatnonzero(inv == 0)
+    still[np.concatenate([i, i + d // 2] if pairing == "halves" else [2 * i, 2 * i + 1])] = True
+    still = torch.as_tensor(still).cuda()
+    q = torch.randn(5, 2, d, device="cuda").to(dt)
+    want = torch.empty_like(q)
+    dsa.dsa_rope_axes(dims, rope, pos, q, None, want, None)
+    special = torch.tensor([float("inf"), -0.0, float("nan"), 1.0, float("-inf"), 0.0, 3e38, 1e-38, -1e-38],
+                           device="cuda").to(dt)
+    x = q.clone()
+    x[..., still] = special[torch.randint(0, 9, x[..., still].shape, device="cuda")]
+    got = torch.empty_like(x)
+    dsa.dsa_rope_axes(dims, rope, pos, x, None, got, None)
+    torch.cuda.synchronize()
+    assert same_bits([got[..., ~still]], [want[..., ~still]])
+    a, b = got[..., still], x[..., still]
+    assert torch.equal(torch.isnan(a), torch.isnan(b))
+    assert same_bits([a.nan_to_num(9.0, posinf=8.0, neginf=-8.0)], [b.nan_to_num(9.0, posinf=8.0, neginf=-8.0)])
