@@ -195,6 +195,7 @@ struct NewRows {
       const int r = i * kRpp + lr;
       if (r >= r0 && r < r1) *reinterpret_cast<uint2*>(codes + r * D + d0) = x[i].codes(down);
     }
+    __syncwarp();  // behind the other lanes' reads of the old scale
     if (lane == 0) *scale = pow2i(e);
   }
 };
@@ -233,8 +234,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) quant_write_kernel(const Quant
     return;
   }
   const size_t ph = static_cast<size_t>(pg) * a.hkv + hk;
-  // every lane has the old scales before lane 0 writes the new ones (the maxima's shuffles
-  // lie between)
+  // every lane has the old scales before lane 0 writes the new ones (store())
   const uint32_t ks = r0 > 0 ? __float_as_uint(a.k_scale[ph]) : 0u;
   const uint32_t vs = r0 > 0 ? __float_as_uint(a.v_scale[ph]) : 0u;
   k.store(a.k + ph * (16 * D), a.k_scale + ph, ks, r0, r1, a.err, lane);
