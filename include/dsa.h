@@ -631,7 +631,8 @@ dsa_status dsa_quant_read(const dsa_dims* dims, const dsa_quant_cache* cache, in
  * rounded to 11 bits for the product with V, below out's own rounding (weights
  * below 2^-18 of the largest to steps of 2^-28 of it, a weight counted with its
  * page's V scale); fp32 q: q enters as two 11-bit halves (2^-22), the weights as
- * three 8-bit thirds (2^-24 of a weight, down to 2^-100 of the largest).
+ * two or, far below the largest, as three 8-bit thirds (2^-22 of each weight, down
+ * to 2^-100 of the largest).
  * dsa_decode_sparse_quant takes the kept lists of dsa_build_index and schedules
  * requests by its order like dsa_decode_sparse.
  * The calls use the partials and the arrival counters of `ws` (the counters are

@@ -13,9 +13,10 @@
 // bf16 q: p_j <= 2^14 is rounded to fp16 (2^-11 relative, below the bf16 output's own 2^-8;
 // the largest is 2^4 or more, so below 2^-18 of it, where fp16's normal range ends, by steps of
 // 2^-28 of the largest).  fp32 q: q in two fp16 halves (2^-22 relative, 2^-33 of the row's
-// largest), p_j in three bf16 thirds (2^-24 relative, down to 2^-100 of the largest: fp16 halves
-// lose the rows 2^-24 below a sink), V widened to bf16 for them: 132 us on the dense batch below
-// with fp32 q, 126 with halves.
+// largest), p_j <= 2^15 likewise (2^-22), or, in a tile with weights below 2^-2, which halves
+// hold worse and lose 2^-24 below a sink, in three bf16 thirds (2^-24 relative, down to 2^-100
+// of the largest), V widened to bf16 for them.  The dense batch below with fp32 q: 126 us, 132
+// with thirds throughout.
 //
 // What bounds it: HBM, and for short calls the chain of dependent loads at a CTA's start.  A
 // row is 2 D bytes for 4 D G flops (<= 8 flops per byte; the 8 columns of an mma cost the
@@ -50,7 +51,7 @@ namespace {
 
 // Weights are 2^(y - ref).  ref follows the largest y so that it stands for 2^kHead, once
 // a y passes it by kSlack; before the first row it is far below every score, and finite.
-constexpr float kHead = 4.f, kSlack = 10.f, kNoRef = -3e38f;
+constexpr float kNoRef = -3e38f;
 
 template <int D, int NW>
 struct QuantRing {
@@ -66,6 +67,8 @@ template <int D, bool XQ>
 struct QuantWarp {
   using Tile = QuantTile<D>;
   static constexpr int NK = D / 16;
+  // fp32 q: high, so that most weights lie where fp16 halves hold them (2^15 is still one)
+  static constexpr float kHead = XQ ? 13.f : 4.f, kSlack = XQ ? 2.f : 10.f;
   uint32_t qh[NK][2], ql[XQ ? NK : 1][2];  // B operand: head lane / 4
   float f[2];                                // score factor of heads 2c, 2c + 1
   float ref[2], l[2], acc[NK][4];
@@ -179,7 +182,8 @@ struct QuantWarp {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float to = fmaxf(ref[j], mx - kHead);
+        // (mx - 13 rounds to mx - 16 from 2^26 on)
+        const float to = fmaxf(ref[j], fabsf(mx) < 0x1p20f ? mx - kHead : mx);
         const float down = ex2_approx(ref[j] - to);
         ref[j] = to;
         l[j] *= down;
@@ -196,8 +200,32 @@ struct QuantWarp {
       l[e & 1] = fmaf(y[e], inv[e >> 1], l[e & 1]);
     }
     uint32_t w[4][Tile::kVW];
+    // fp32 q: fp16 halves are good to 2^-22 from 2^-2 on (the second one's last step is 2^-24);
+    // a tile with smaller weights takes thirds
+    bool thirds = false;
     if constexpr (XQ) {
-      // thirds of 8 bits; what bf16 took off a float is a float, so the thirds add up
+#pragma unroll
+      for (int e = 0; e < 4; ++e) thirds |= y[e] < 0.25f && y[e] != 0.f;
+      thirds = __any_sync(0xffffffffu, thirds);
+    }
+    if (!thirds) {
+      const uint32_t p0 = f16x2_rn(y[0], y[1]), p1 = f16x2_rn(y[2], y[3]);
+      const uint32_t b0 = movmatrix_trans(p0), b1 = movmatrix_trans(p1);
+      uint32_t c0 = 0, c1 = 0;
+      if constexpr (XQ) {
+        c0 = movmatrix_trans(f16x2_rest(y[0], y[1], p0));
+        c1 = movmatrix_trans(f16x2_rest(y[2], y[3], p1));
+      }
+      Tile::load_v(tile + Tile::kBytes, lane, w);
+#pragma unroll
+      for (int mt = 0; mt < NK; ++mt) {
+        uint32_t a[4];
+        Tile::frag_v(w, mt, a);
+        mma_f16(acc[mt], a[0], a[1], a[2], a[3], b0, b1);
+        if constexpr (XQ) mma_f16(acc[mt], a[0], a[1], a[2], a[3], c0, c1);
+      }
+    } else {
+      // of 8 bits; what bf16 took off a float is a float, so the thirds add up
       uint32_t b[3][2];
 #pragma unroll
       for (int k = 0; k < 3; ++k)
@@ -220,16 +248,6 @@ struct QuantWarp {
         }
 #pragma unroll
         for (int k = 2; k >= 0; --k) mma_bf16(acc[mt], a, b[k][0], b[k][1]);
-      }
-    } else {
-      const uint32_t b0 = movmatrix_trans(f16x2_rn(y[0], y[1]));
-      const uint32_t b1 = movmatrix_trans(f16x2_rn(y[2], y[3]));
-      Tile::load_v(tile + Tile::kBytes, lane, w);
-#pragma unroll
-      for (int mt = 0; mt < NK; ++mt) {
-        uint32_t a[4];
-        Tile::frag_v(w, mt, a);
-        mma_f16(acc[mt], a[0], a[1], a[2], a[3], b0, b1);
       }
     }
   }

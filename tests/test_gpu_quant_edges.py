@@ -98,8 +98,8 @@ def check_against(w, qb, mode):
     """out against attend64, element by element and relative to what the element is made of.
     A score is off by 2 * 2^-22 B (the halves of q: 11 bits each) and by what fp32 sums of 2 d
     terms lose, 2 d * 2^-23 B, and its exponent by 2^-23 X for each of three roundings; a weight is
-    off by as much twice over (numerator and sum), by 2^-22 for 2^x and 2^-24 for its own halves
-    or thirds.  The n weighted rows are added in fp32, n * 2^-23 S at most.  bf16 q: the weights
+    off by as much twice over (numerator and sum), by 2^-22 for 2^x and 2^-22 for its own halves
+    or thirds, together 2^-21.  The n weighted rows are added in fp32, n * 2^-23 S at most.  bf16 q: the weights
     round once more, 2^-11 S, or below fp16's normal range by half of its last step, 2^-25 where
     the largest weight (times its page's scale) stands at 2^4 or more; out rounds by 2^-8."""
     out = torch.full_like(qb.out, float("nan"))
