@@ -658,7 +658,8 @@ dsa_status dsa_decode_sparse_masked_quant(const dsa_dims* dims, const void* q,
  * dsa_prefill_sparse_quant -- dsa_prefill_sparse over the 8-bit cache: several
  * query tokens per request, each over its own causal kept set (their rows
  * already written with dsa_quant_write).  Arguments and errors as there; q and out
- * are bf16 (q_dtype), else DSA_ERR_UNSUPPORTED.  dsa_set_prefill_split applies: with 1
+ * are bf16 (q_dtype), else DSA_ERR_UNSUPPORTED, and must not overlap, else
+ * DSA_ERR_INVALID_ARG.  dsa_set_prefill_split applies: with 1
  * no unit is cut along its rows, with n >= 2 every unit is cut into n parts (fewer where
  * the workspace does not hold them), with 0 each call picks.
  */

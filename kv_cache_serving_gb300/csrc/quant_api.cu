@@ -295,6 +295,10 @@ dsa_status dsa_prefill_sparse_quant(const dsa_dims* dims, int32_t max_q, const v
   if (static_cast<int64_t>(dims->batch) * dims->hkv > INT32_MAX / kQuantMaxParts ||
       static_cast<int64_t>(dims->batch) * dims->hkv * ceil_div(max_q, 4) > INT32_MAX)
     return DSA_ERR_UNSUPPORTED;
+  // queries of a tile may be read again after its first output (NaN in V)
+  const uintptr_t bytes = static_cast<uintptr_t>(dims->batch) * max_q * dims->hq * dims->head_dim * 2;
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
+  if (qa < oa + bytes && oa < qa + bytes) return DSA_ERR_INVALID_ARG;
   QuantChunkLaunch a{};
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint8_t*>(cache->k_codes);

@@ -137,3 +137,11 @@ def test_binding_checks():
         dsa.quant_cache(t, t, torch.ones(4, 2), torch.ones(4, 2))  # CUDA tensors wanted
     with pytest.raises(TypeError):
         dsa._cache(dims(), object(), 0)
+
+
+def test_chunk_refuses_overlapping_q_and_out():
+    """[2][3][8][128] bf16: 12 KB each; the same memory, or a byte of it shared, is refused."""
+    n = 2 * 3 * 8 * 128 * 2
+    for at in (0, 16, n - 16):
+        for a, b in ((BASE, BASE + at), (BASE + at, BASE)):
+            assert attend("chunk", q=ctypes.c_void_p(a), out=ctypes.c_void_p(b)) == dsa.DSA_ERR_INVALID_ARG
