@@ -13,8 +13,9 @@
 // registers (64 conversions per page and warp) and the scores of every (row, column)
 // pass through an exponential, so a warp takes 32 columns: the conversions, the shared
 // memory reads and the row bookkeeping of a page are paid once for 32 queries and
-// heads, with q and the 32 columns of output in registers (255 of them: 8 warps per SM; 16
-// columns and 16 warps measured a third slower).  The accumulators hold the output
+// heads, with q and the 32 columns of output in registers (255 of them at D = 128, and 112 to
+// 232 bytes spilled: 8 warps per SM; 16 columns and 16 warps measured a third slower).  The
+// accumulators hold the output
 // transposed (dims x columns), which lets the weights go from the score accumulators to
 // the second product by movmatrix alone.
 // This kernel serves head_dim 64 up to 32 columns, calls of few tiles over long caches and

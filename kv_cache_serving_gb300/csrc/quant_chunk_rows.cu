@@ -23,12 +23,12 @@
 // from 485 to 447 us.
 //
 // What bounds it: latency and instruction issue of the weighing and the prologue, not the
-// products (11% of the tensor pipe) and not HBM.  Of a tile of prompts (3.5 blocks on
+// products (12% of the tensor pipe) and not HBM.  Of a tile of prompts (3.5 blocks on
 // average) 2.3 K cycles go by until its sizes and tensor memory are there, 7 K until q is
 // converted and the first scores exist, 3 K per block, 4 K for the output; two CTAs per SM
-// fill each other's gaps to 1.3 instructions per cycle.
-// Measured (head_dim 128): prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 430 us =
-// 273 TFLOP/s of kept pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 396 us
+// fill each other's gaps to 1.4 instructions per cycle.
+// Measured (head_dim 128): prompts of 32 .. 512 rows of 128 requests, 32/8 heads, 427 us =
+// 275 TFLOP/s of kept pairs (694 us with quant_chunk.cu); all 2048 rows of 8 requests 387 us
 // (1017).
 #include <math.h>
 

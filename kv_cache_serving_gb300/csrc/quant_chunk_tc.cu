@@ -25,8 +25,8 @@
 // conversions are 130 and the softmax 300.  Two CTAs per SM, so that one converts while the
 // other's products run; the next block's K and V are loaded an iteration ahead, past the
 // L1 (whose 20 KB keep page ids, masks and spills).  Measured: 32 tokens of 64 requests of 320 ..
-// 1280 rows under the mask, 32/32 heads: 85 us (88 with a flushed L2; 136 with quant_chunk.cu).  A persistent
-// form (tiles of several units in one CTA, the next tile's q and first block ahead)
+// 1280 rows under the mask, 32/32 heads: 91 us with a flushed L2 (136 with quant_chunk.cu).  A
+// persistent form (tiles of several units in one CTA, the next tile's q and first block ahead)
 // measured slower: 141 us, its second set of tile values spills.
 #include <math.h>
 

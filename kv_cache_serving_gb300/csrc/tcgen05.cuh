@@ -127,7 +127,7 @@ __device__ __forceinline__ void tmem_load<32>(uint32_t addr, uint32_t (&r)[32]) 
       : "r"(addr)
       : "memory");
 }
-// 16 consecutive columns of this warp's 32 lanes; complete after tc_wait_st.
+// 8 or 16 consecutive columns of this warp's 32 lanes; complete after tc_wait_st.
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),

@@ -270,9 +270,12 @@ class DecodeBatch:
 
 
 class QuantBatch:
-    """A DecodeBatch whose K/V cache is held in 8 bits: e4m3 codes [num_pages, hkv, 16, d]
-    and power-of-two scales [num_pages, hkv] (dsa_quant_cache).  Lengths, masks, page
-    table and workspace are the batch's own; out has q's type."""
+    """The K/V cache of a DecodeBatch in 8 bits: e4m3 codes [num_pages, hkv, 16, d] and
+    power-of-two scales [num_pages, hkv] (dsa_quant_cache).  Lengths, masks, page
+    table and workspace are the batch's own; out has q's type.  The batch keeps its
+    pages beside it (both forms of a cache for comparison); a program that wants the
+    memory of the 8-bit form alone makes the tensors itself (dsa.quant_cache) and
+    calls dsa.dsa_*_quant."""
 
     def __init__(self, batch: DecodeBatch):
         self.batch = batch
