@@ -253,6 +253,43 @@ def test_chunk_nan_values_reach_their_element_alone(d, g, n, split):
     assert torch.allclose(out[ok].float(), base[ok].float(), rtol=2 ** -7, atol=4e-3)
 
 
+@pytest.mark.parametrize("split", [1, 2], indirect=True)
+@pytest.mark.parametrize("d,g,n", [(128, 4, 7), (128, 2, 40), (64, 4, 40)])
+def test_chunk_nan_values_in_a_graph_and_an_order(d, g, n, split):
+    """NaN codes of V with ragged query counts (none for one request), requests handed out in
+    another order, without lse, replayed from a graph on another stream: the bits of the plain
+    call, and places behind a request's queries left as they were."""
+    w = wl.generate(case(d, g, batch=4, hkv=2, lo=150, hi=260, prompt=(40, 60), W=64, seed=d + n))
+    qb = QuantBatch.from_batch(DecodeBatch.from_workload(w))
+    bt = qb.batch
+    q = torch.randn(4, n, w["hq"], d, device="cuda").to(torch.bfloat16)
+    ql = torch.tensor([n, 0, n - 3, 1], dtype=torch.int32, device="cuda")
+    codes, rng = qb.v.view(torch.uint8), np.random.default_rng(n)
+    for b in range(4):
+        L = int(w["seq_len"][b])
+        for j in [3] + list(L - 1 - rng.integers(0, 80, 3)):
+            codes[int(w["page_table"][b, j // 16]), :, j % 16, int(rng.integers(d))] = 127
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:3], 7.0, device="cuda")
+    qb.prefill_sparse(q, ql, out, lse)
+    torch.cuda.synchronize()
+    assert torch.isnan(out).any() and torch.isfinite(lse).all()
+    for b, k in enumerate(ql.tolist()):
+        assert (out[b, k:] == 7.0).all() and (lse[b, k:] == 7.0).all()
+    got = torch.full_like(q, 7.0)
+    order = torch.tensor([2, 0, 3, 1], dtype=torch.int32, device="cuda")
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        qb.prefill_sparse(q, ql, got, None, stream=stream, request_order=order)
+    for _ in range(3):
+        got.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = got.view(torch.int16), out.view(torch.int16)
+        assert torch.equal(torch.isnan(got), torch.isnan(out))
+        assert torch.equal(a[~torch.isnan(got)], b[~torch.isnan(out)])
+    assert bt.device_error() == 0
+
+
 @pytest.mark.parametrize("split", [0, 1], indirect=True)
 @pytest.mark.parametrize("d,n,L", [(128, 8, 2000), (128, 2000, 2000), (64, 8, 2000), (64, 2000, 2000)])
 def test_chunk_nan_value_costs_no_more_than_a_few_calls(d, n, L, split):
