@@ -86,17 +86,27 @@ enum {
   DSA_DEV_BAD_WINDOW = 3,   /* window < 0 or > max_window                  */
   DSA_DEV_BAD_PAGE = 4,     /* page id outside 0..num_pages-1              */
   DSA_DEV_BAD_INDEX = 5,    /* kept index outside 0..seq_len-1             */
-  DSA_DEV_BAD_COUNT = 6,    /* kept count < 1 or > max_kept                */
+  DSA_DEV_BAD_COUNT = 6,    /* kept count < 1 or > max_kept; dsa_assign_pages:
+                               free_count outside 0..capacity, or more new
+                               rows than max_tokens                         */
   DSA_DEV_TIMEOUT = 7,      /* a bounded wait for an async copy gave up    */
   DSA_DEV_BAD_GRID_W = 8,   /* grid width < 1 (attention mass)             */
   DSA_DEV_BAD_ORDER = 9,    /* request_order entry outside 0..batch-1      */
   DSA_DEV_FREE_LIST_FULL = 10, /* dsa_evict_pages: more pages than capacity  */
   DSA_DEV_BAD_QLEN = 11,    /* dsa_prefill_sparse: q_len < 0 or above
                                min(seq_len, max_q); dsa_quant_write: new_len
-                               likewise; dsa_quant_read: rows outside the
+                               likewise; dsa_assign_pages: new_len < 0 or
+                               above seq_len; dsa_quant_read: rows outside the
                                request or more than max_rows                */
-  DSA_DEV_BAD_SCALE = 12    /* 8-bit cache: a scale that is not a power of two
+  DSA_DEV_BAD_SCALE = 12,   /* 8-bit cache: a scale that is not a power of two
                                in 2^-40 .. 2^40                             */
+  DSA_DEV_FREE_LIST_EMPTY = 13, /* dsa_assign_pages: fewer free pages than needed */
+  DSA_DEV_BAD_GROUP = 14,   /* shared prefix: group_start does not rise from 0 to
+                               batch                                        */
+  DSA_DEV_BAD_PREFIX = 15   /* shared prefix: prefix_len < 0 or above max_prefix
+                               or the request's (prompt) rows, or another one
+                               than its group's; more than max_suffix rows
+                               behind it                                    */
 };
 
 /* Problem sizes, shared by all calls on one KV cache. */
@@ -548,6 +558,149 @@ dsa_status dsa_rope_axes(const dsa_dims* dims, const dsa_rope* rope, int32_t tok
                          const int32_t* positions, const void* q, int64_t q_stride, const void* k,
                          int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
                          int64_t k_out_stride, void* stream);
+
+/*
+ * dsa_qk_norm -- the norm of query and key heads before their rotation, each head of a token
+ * for itself:
+ *   y = (x - mu) / sqrt(mean((x - mu)^2) + eps) * weight + bias
+ * with mu = 0 (DSA_NORM_RMS) or mu = mean(x) (DSA_NORM_LAYER).  Held by value on the host; the
+ * vectors are device pointers owned by the caller, 16-byte aligned.
+ *   per_head          0: weight and bias [head_dim], the same for every head; else
+ *                     [heads][head_dim] (hq or hkv heads)
+ *   weight_dtype      dsa_dtype of the vectors
+ *   eps               finite, >= 0
+ *   q_weight, k_weight   or NULL: ones
+ *   q_bias, k_bias       or NULL: zeros
+ */
+typedef enum { DSA_NORM_RMS = 0, DSA_NORM_LAYER = 1 } dsa_norm_kind;
+typedef struct {
+  int32_t kind;
+  int32_t per_head;
+  int32_t weight_dtype;
+  float eps;
+  const void* q_weight;
+  const void* k_weight;
+  const void* q_bias;
+  const void* k_bias;
+} dsa_qk_norm;
+
+/*
+ * dsa_qk_norm_rope -- dsa_rope_axes with the head norm in the same pass: the query and key
+ * heads of `tokens` tokens normed, then turned to their positions.  Statistics, norm and
+ * rotation in fp32, rounded once to the output.  Arguments and errors as for dsa_rope_axes
+ * (inv_freq 0 everywhere norms without turning); norm as above, else DSA_ERR_INVALID_ARG.
+ * Squares that leave fp32 are taken of the head scaled by a power of two, so any finite input
+ * has its result; a head of zeros with eps 0 gives NaN, as the formula does.
+ */
+dsa_status dsa_qk_norm_rope(const dsa_dims* dims, const dsa_qk_norm* norm, const dsa_rope* rope,
+                            int32_t tokens, const int32_t* positions, const void* q,
+                            int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
+                            int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                            void* stream);
+
+/*
+ * dsa_assign_pages -- pages and slots for the rows that requests append: the way back from the
+ * free list of dsa_evict_pages into the page tables.  The last new_len[b] rows of request b,
+ * positions L_b - new_len[b] .. L_b - 1, are new; a page whose first row is new gets a page of
+ * the free list, taken from its end: the k-th page needed (requests in order, a request's pages
+ * in order) is free_pages[*free_count - 1 - k].  A page that already holds older rows of the
+ * request stays (its entry must be mapped).
+ * The new rows of all requests are packed in request order, as a fused projection of ragged
+ * prompts has them: row i of request b is token token_start[b] + i.
+ *   seq_len      [batch] int32, L_b >= 1 counting the new rows
+ *   new_len      [batch] int32, 0 <= new_len[b] <= L_b, or NULL: one row each (a decode step)
+ *   free_pages   [capacity] int32, page ids
+ *   free_count   one int32: ids in free_pages, 0 .. capacity
+ *   free_count_out (out) one int32: ids left; may be free_count itself.  Apart from it, the
+ *                call can be repeated (a scheduler's trial) with the same result.
+ *   page_table   [batch][max_pages_per_req] int32 (in/out): entries of fresh pages are written,
+ *                whatever they held; others are left alone
+ *   max_tokens   places in row_slot and row_pos (>= 0)
+ *   token_start  (out) [batch + 1] int32, the sums of new_len, or NULL
+ *   row_slot     (out) [max_tokens] int32: page * 16 + slot of each new row (dsa_write_rows);
+ *                -1 behind the last one, so that a fixed max_tokens suits a recorded step
+ *   row_pos      (out) [max_tokens] int32: position of each new row in its request (0 behind the
+ *                last one), or NULL; positions of a rotary embedding with one axis
+ * A request that finds fewer free pages than it needs gets none: DSA_DEV_FREE_LIST_EMPTY, -1 for
+ * all its rows, its entries unchanged; so do later requests that need pages, while requests that
+ * need none are served.  Invalid lengths (DSA_DEV_BAD_SEQ_LEN, DSA_DEV_BAD_QLEN) count as no new
+ * rows; a page id outside the pool gives DSA_DEV_BAD_PAGE and -1 for its rows; free_count outside
+ * 0 .. capacity counts as 0, and with more new rows than max_tokens no request is served
+ * (DSA_DEV_BAD_COUNT).  num_pages * 16 < 2^31, else DSA_ERR_UNSUPPORTED.
+ */
+dsa_status dsa_assign_pages(const dsa_dims* dims, const int32_t* seq_len, const int32_t* new_len,
+                            const int32_t* free_pages, int32_t capacity,
+                            const int32_t* free_count, int32_t* free_count_out,
+                            int32_t* page_table, int32_t max_tokens, int32_t* token_start,
+                            int32_t* row_slot, int32_t* row_pos, void* ws, void* stream);
+
+/*
+ * dsa_write_rows -- K and V rows of `tokens` tokens stored at their slots, as they are (kv_dtype,
+ * fp32 or bf16): row t goes to slot row_slot[t] % 16 of page row_slot[t] / 16.
+ *   tokens       >= 0 (0 is a no-op)
+ *   row_slot     [tokens] int32 (device); negative: the row is skipped; a page outside the pool:
+ *                DSA_DEV_BAD_PAGE, skipped.  No slot may be named twice.
+ *   k, v         [tokens][hkv][head_dim], token t at element t * k_stride (v_stride): slices of a
+ *                fused projection are fine
+ *   k_pages, v_pages  [num_pages][16][hkv][head_dim] (written)
+ * k and k_pages, or v and v_pages, may both be NULL.  Pointers are 16-byte aligned and strides
+ * multiples of 16 bytes, at least hkv * head_dim elements; else DSA_ERR_INVALID_ARG.
+ */
+dsa_status dsa_write_rows(const dsa_dims* dims, int32_t tokens, const int32_t* row_slot,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          void* k_pages, void* v_pages, void* ws, void* stream);
+
+/*
+ * dsa_shared_prefix -- requests whose first rows are the same (many images of one prompt, many
+ * answers behind one instruction), for decode calls that attend over those rows once for all of
+ * them.  Held by value on the host.
+ *   groups       groups of requests (>= 0); group g is requests group_start[g] ..
+ *                group_start[g+1] - 1 of the batch
+ *   max_prefix   bound of prefix_len, at most max_pages_per_req * 16; 0: nothing is shared
+ *   max_suffix   bound of the rows that a request attends over besides the shared ones; the
+ *                call plans its work with it (a bound much above the batch's rows costs time)
+ *   group_start  [groups + 1] int32 (device), rising from 0 to batch (groups may be empty)
+ *   prefix_len   [batch] int32 (device): rows 0 .. prefix_len[b] - 1 of request b are those of
+ *                every request of its group; the same number for all of a group, at most
+ *                seq_len[b] (and, under a mask, prompt_len[b], so that all keep them).  Any
+ *                number of rows: the last one may lie inside a page.
+ * The shared rows are read through the page table of the group's first request; the others may
+ * map the same pages or copies of them.  A group of one request, or of prefix_len 0, is one that
+ * shares nothing.
+ */
+typedef struct {
+  int32_t groups;
+  int32_t max_prefix;
+  int32_t max_suffix;
+  const int32_t* group_start;
+  const int32_t* prefix_len;
+} dsa_shared_prefix;
+
+/*
+ * dsa_decode_dense_shared, dsa_decode_sparse_masked_shared -- dsa_decode_dense and
+ * dsa_decode_sparse_masked (without order and append) for such a batch: the same row sets and
+ * softmax, the shared rows read once per group and multiplied on the tensor cores with the queries
+ * of all its requests, the others row by row, the two joined by log-sum-exp.  q and K/V bf16,
+ * else DSA_ERR_UNSUPPORTED; out [batch][hq][head_dim] bf16 (q's type), not overlapping q; lse
+ * float32 or NULL.  Softmax weights of the shared rows are rounded to bf16 for the product with V
+ * (2^-8 of each), sums are taken of them unrounded in fp32.  batch <= 65535 and hkv <= 65535.
+ * A request with invalid lengths, a prefix_len outside 0 .. max_prefix or above its rows, or more
+ * than max_suffix other rows (DSA_DEV_BAD_PREFIX), or one that no group holds or that states
+ * another prefix_len than its group's first (DSA_DEV_BAD_GROUP or _BAD_PREFIX) gets NaN; a
+ * group_start that does not rise from 0 to batch sets DSA_DEV_BAD_GROUP.
+ * The calls use regions of `ws` that no other call reads; they are ready for the next call
+ * unless one set a device error (then zero-fill the workspace again).
+ */
+dsa_status dsa_decode_dense_shared(const dsa_dims* dims, const dsa_shared_prefix* shared,
+                                   const void* q, const void* k_pages, const void* v_pages,
+                                   const int32_t* page_table, const int32_t* seq_len, float scale,
+                                   void* out, float* lse, void* ws, void* stream);
+dsa_status dsa_decode_sparse_masked_shared(const dsa_dims* dims, const dsa_shared_prefix* shared,
+                                           const void* q, const void* k_pages, const void* v_pages,
+                                           const int32_t* page_table, const int32_t* seq_len,
+                                           const int32_t* prompt_len, const int32_t* window,
+                                           const uint32_t* keep_mask, float scale, void* out,
+                                           float* lse, void* ws, void* stream);
 
 /*
  * dsa_quant_cache -- a paged K/V cache held in 8 bits: half the bytes of the

@@ -24,10 +24,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Workspace: [0, 256) header, then per-call regions.  Header words: 0 the
 // device error word; 1 the tag of the request schedule dsa_build_index leaves
 // for dsa_decode_sparse (kSchedMagic ^ batch when valid); 2 the count of
-// index-compaction CTAs done (the last one writes the schedule, then resets it).
+// index-compaction CTAs done (the last one writes the schedule, then resets it); 3 the count
+// of dsa_assign_pages CTAs done (likewise).
 constexpr size_t kWsHeader = 256;
 constexpr int kWsSchedTag = 1;
 constexpr int kWsDoneCount = 2;
+constexpr int kWsAssignCount = 3;
 constexpr int32_t kSchedMagic = 0x5c4ed000;
 // Largest batch whose schedule the index compaction sorts (one CTA, rank sort).
 constexpr int kSchedMaxBatch = 1024;

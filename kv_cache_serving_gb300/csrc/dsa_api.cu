@@ -329,7 +329,7 @@ const char* dsa_status_string(dsa_status status) {
 size_t dsa_workspace_size(const dsa_dims* dims) {
   if (check_dims(dims) != DSA_OK) return 0;
   return kWsHeader + partials_region(dims) + unit_ints_region(dims) + sched_bytes(dims) +
-         kMultiCountBytes;
+         kMultiCountBytes + shared_bytes(dims);
 }
 
 dsa_status dsa_build_index(const dsa_dims* dims, const int32_t* seq_len,

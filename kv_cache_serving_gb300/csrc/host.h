@@ -163,4 +163,36 @@ inline int32_t* multi_count_region(const dsa_dims* d, void* ws) {
 
 constexpr size_t kMultiCountBytes = kMultiCounters * sizeof(int32_t);
 
+// The calls over a shared prefix, behind the counters: [batch][hkv] states of each unit's prefix,
+// [batch][hkv] chunks done, then kSharedExtra states of each (request, query head).
+inline int shared_in_part(const dsa_dims* d) {
+  const int64_t n_max = dense_rows(d) > d->max_kept ? dense_rows(d) : d->max_kept;
+  return chunk_bound(n_max) * (d->head_dim + 2) / (d->head_dim + 4);
+}
+inline int32_t* shared_pieces(const dsa_dims* d, void* ws) {
+  return multi_count_region(d, ws) + kMultiCounters;
+}
+inline int32_t* shared_arrive(const dsa_dims* d, void* ws) {
+  return shared_pieces(d, ws) + unit_ints_region(d) / sizeof(int32_t);
+}
+inline SharedStates shared_states(const dsa_dims* d, void* ws) {
+  return SharedStates{partials(ws),
+                      reinterpret_cast<float*>(shared_arrive(d, ws) + unit_ints_region(d) / sizeof(int32_t)),
+                      shared_in_part(d), d->head_dim + 4};
+}
+inline size_t shared_bytes(const dsa_dims* d) {
+  return 2 * unit_ints_region(d) + round_up(static_cast<size_t>(d->batch) * d->hq * kSharedExtra *
+                                                (d->head_dim + 4) * sizeof(float), 256);
+}
+
+// Whether a row stride is at least `least` elements and whole 16-byte pieces.
+inline bool row_stride_ok(int64_t stride, int64_t least, int elt) {
+  return stride >= least && (stride * elt) % 16 == 0;
+}
+
+dsa_status make_rope_launch(const dsa_dims* dims, const dsa_rope* rope, int32_t tokens,
+                       const int32_t* positions, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                       int64_t k_out_stride, RopeLaunch* launch);
+
 }  // namespace dsa

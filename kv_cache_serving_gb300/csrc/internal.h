@@ -15,6 +15,23 @@ constexpr int kMaxChunks = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kChunkQuantum = 64;  // chunk sizes are multiples of this
 
+// States (acc[head_dim], reference, sum, padding) that the calls over a shared prefix leave in the
+// workspace: `in_part` of a (request, query head) in the partials region, kSharedExtra more behind
+// it.  The first prefix_slots are the prefix's, the others those of chunks.
+constexpr int kSharedExtra = 3;
+constexpr int kSharedRows = 128, kSharedBlock = 128;  // query rows of a tile, cache rows of a block
+struct SharedStates {
+  float* part;
+  float* extra;
+  int32_t in_part, floats;  // floats of a state: head_dim + 4
+};
+#ifdef __CUDACC__
+__device__ __forceinline__ float* shared_state(const SharedStates& s, size_t qh, int slot) {
+  return slot < s.in_part ? s.part + (qh * s.in_part + slot) * s.floats
+                          : s.extra + (qh * kSharedExtra + (slot - s.in_part)) * s.floats;
+}
+#endif
+
 struct DecodeLaunch {
   const void* q;
   int q_bf16;
@@ -45,6 +62,31 @@ struct DecodeLaunch {
   float* lse;
   float* part;  // [batch][hq][num_chunks][head_dim + 2]
   int32_t* err;
+  // rows behind a shared prefix only (then out is bf16)
+  const int32_t* prefix_len;  // [batch]
+  int32_t max_prefix, max_suffix;
+  int32_t early;              // the prefix kernel runs before: wait for it late
+  int32_t prefix_slots;       // states 0 .. prefix_slots - 1 are the prefix's
+  SharedStates states;
+  int32_t* pieces;            // [batch][hkv] states of the prefix
+  int32_t* arrive;            // [batch][hkv] chunks done, 0 between launches
+};
+
+// The prefixes of groups of requests (shared_prefix.cu): bf16 q and pages.
+struct SharedLaunch {
+  const uint16_t* q;
+  const void* k;
+  const void* v;
+  const int32_t* page_table;
+  const int32_t* group_start;  // [groups + 1]
+  const int32_t* prefix_len;   // [batch]
+  int32_t groups, batch, hq, hkv, group_log2, head_dim, max_pages, num_pages, max_prefix;
+  int32_t prefix_slots;        // >= 2
+  float scale_log2;
+  SharedStates states;
+  int32_t* pieces;
+  int32_t* err;
+  int32_t sms;
 };
 
 struct MassLaunch {
@@ -137,6 +179,9 @@ constexpr int kMaskModeMaxWindow = 1024;
 cudaError_t launch_decode_bf16(const DecodeLaunch& a, int mode, cudaStream_t s);
 cudaError_t launch_decode_f32(const DecodeLaunch& a, int mode, cudaStream_t s);
 cudaError_t launch_merge(const DecodeLaunch& a, int mode, cudaStream_t s);
+// Behind a shared prefix: dense rows or those of the mask; resident CTAs and rows of a pass.
+cudaError_t launch_decode_shared(const DecodeLaunch& a, int mode, cudaStream_t s);
+cudaError_t launch_shared_prefix(const SharedLaunch& a, cudaStream_t s);
 cudaError_t launch_mass(const MassLaunch& a, bool kv_bf16, cudaStream_t s);
 // Rows one pass of all warps of an attention-mass CTA covers, and its resident
 // CTAs per SM (>= 1), for the host's chunk choice.
@@ -195,6 +240,7 @@ struct DecodeShape {
 // The requested build of (head_dim, group, mode) when there is one, else the
 // default build.
 DecodeShape decode_shape_bf16(int head_dim, int group, int mode, int build);
+DecodeShape decode_shape_shared(int head_dim, int group, int mode);
 DecodeShape decode_shape_f32(int head_dim, int group, int mode, int build);
 
 // ---- 8-bit K/V cache (quant_*.cu) and rotary positions (rope.cu) ----
@@ -304,6 +350,46 @@ struct RopeLaunch {
   uint64_t turn[64];         // pair i: 2^64 turns per position, modulo 2^64
   uint8_t pair_axis[64];
 };
+
+// ---- head norms (qk_norm.cu), pages and rows (pages.cu) ----
+
+struct NormLaunch {
+  RopeLaunch rope;
+  // per head kind (0: q, 1: k): weight and bias, or null; of every head's own when per_head
+  const void* weight[2];
+  const void* bias[2];
+  int32_t layer, per_head, weight_bf16;
+  float eps;
+};
+
+struct AssignLaunch {
+  const int32_t* seq_len;
+  const int32_t* new_len;    // or null: one row each
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* free_out;         // may be free_count
+  int32_t* page_table;
+  int32_t* token_start;      // [batch + 1], or null
+  int32_t* row_slot;         // [max_tokens]
+  int32_t* row_pos;          // [max_tokens], or null
+  int32_t batch, max_pages, num_pages, capacity, max_tokens;
+  int32_t* err;
+  int32_t* done;             // CTAs done, zero between calls
+};
+
+struct RowsLaunch {
+  const int32_t* row_slot;
+  const void* rows[2];       // K, V; null: not written
+  void* pages[2];
+  int64_t stride[2];         // bytes between two rows
+  int64_t slots;             // num_pages * 16
+  int32_t tokens, row_bytes;
+  int32_t* err;
+};
+
+cudaError_t launch_qk_norm_rope(const NormLaunch& a, int sms, cudaStream_t s);
+cudaError_t launch_assign_pages(const AssignLaunch& a, cudaStream_t s);
+cudaError_t launch_write_rows(const RowsLaunch& a, cudaStream_t s);
 
 cudaError_t launch_quant_decode(const QuantDecodeLaunch& a, int mode, cudaStream_t s);
 cudaError_t launch_quant_chunk(const QuantChunkLaunch& a, cudaStream_t s);

@@ -124,21 +124,13 @@ uint64_t turns_of(double f) {
   return shift >= 127 ? 0 : static_cast<uint64_t>((p + (static_cast<u128>(1) << (shift - 1))) >> shift);
 }
 
-bool row_stride_ok(int64_t stride, int64_t least, int elt) {
-  return stride >= least && (stride * elt) % 16 == 0;
-}
-
 }  // namespace
-}  // namespace dsa
 
-using namespace dsa;
-
-extern "C" {
-
-dsa_status dsa_rope_axes(const dsa_dims* dims, const dsa_rope* rope, int32_t tokens,
-                         const int32_t* positions, const void* q, int64_t q_stride, const void* k,
-                         int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
-                         int64_t k_out_stride, void* stream) {
+// The checks and the launch of dsa_rope_axes and dsa_qk_norm_rope; tokens 0: nothing to do.
+dsa_status make_rope_launch(const dsa_dims* dims, const dsa_rope* rope, int32_t tokens,
+                       const int32_t* positions, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                       int64_t k_out_stride, RopeLaunch* launch) {
   const dsa_status st = check_dims(dims);
   if (st != DSA_OK) return st;
   if (rope == nullptr || tokens < 0 || (q == nullptr) != (q_out == nullptr) ||
@@ -148,7 +140,8 @@ dsa_status dsa_rope_axes(const dsa_dims* dims, const dsa_rope* rope, int32_t tok
       (rope->pairing != DSA_ROPE_HALVES && rope->pairing != DSA_ROPE_NEIGHBOURS))
     return DSA_ERR_INVALID_ARG;
   const int pairs = dims->head_dim / 2;
-  RopeLaunch a{};
+  RopeLaunch& a = *launch;
+  a = RopeLaunch{};
   for (int i = 0; i < pairs; ++i) {
     const double f = rope->inv_freq[i];
     if (!std::isfinite(f) || std::fabs(f) > 6.283185307179587 || rope->pair_axis[i] >= rope->axes)
@@ -188,6 +181,23 @@ dsa_status dsa_rope_axes(const dsa_dims* dims, const dsa_rope* rope, int32_t tok
   a.neighbours = rope->pairing == DSA_ROPE_NEIGHBOURS;
   a.q_bf16 = dims->q_dtype == DSA_BF16;
   a.k_bf16 = dims->kv_dtype == DSA_BF16;
+  return DSA_OK;
+}
+
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+dsa_status dsa_rope_axes(const dsa_dims* dims, const dsa_rope* rope, int32_t tokens,
+                         const int32_t* positions, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                         int64_t k_out_stride, void* stream) {
+  RopeLaunch a{};
+  const dsa_status st = make_rope_launch(dims, rope, tokens, positions, q, q_stride, k, k_stride,
+                                         q_out, q_out_stride, k_out, k_out_stride, &a);
+  if (st != DSA_OK || a.tokens == 0) return st;
   return from_cuda(launch_rope(a, sm_count(), static_cast<cudaStream_t>(stream)));
 }
 

@@ -82,16 +82,19 @@ struct WarpQ {
     return u * (128 / kElt) + j * kVE + w;
   }
 
-  // q rows qhead0 .. qhead0+G-1 of [*][D] (bf16 when q_bf16, else fp32).
+  // q rows qhead0 .. qhead0+G-1 of [*][D] (bf16 when q_bf16, else fp32).  CG: past the SM's
+  // own cache (bf16 q and K).
+  template <bool CG = false>
   __device__ __forceinline__ void load(const void* q, bool q_bf16, size_t qhead0, int lane) {
+    static_assert(!CG || QMIX, "bf16 q and K");
     if constexpr (kMMA) {
       const int g4 = lane >> 2, tig = lane & 3;
       const uint32_t* q32 =
           reinterpret_cast<const uint32_t*>(q) + (qhead0 + (g4 < G ? g4 : 0)) * (D / 2);
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
-        qf[kk][0] = g4 < G ? __ldg(q32 + kk * 8 + tig) : 0u;
-        qf[kk][1] = g4 < G ? __ldg(q32 + kk * 8 + 4 + tig) : 0u;
+        qf[kk][0] = g4 < G ? (CG ? __ldcg(q32 + kk * 8 + tig) : __ldg(q32 + kk * 8 + tig)) : 0u;
+        qf[kk][1] = g4 < G ? (CG ? __ldcg(q32 + kk * 8 + 4 + tig) : __ldg(q32 + kk * 8 + 4 + tig)) : 0u;
       }
     } else {
       const int jl = lane & 7;
@@ -103,7 +106,7 @@ struct WarpQ {
               reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(q) + qrow);
 #pragma unroll
           for (int u = 0; u < kNV; ++u) {
-            const uint4 v = __ldg(q4 + u * 8 + jl);
+            const uint4 v = CG ? __ldcg(q4 + u * 8 + jl) : __ldg(q4 + u * 8 + jl);
             qv[h][4 * u] = v.x;
             qv[h][4 * u + 1] = v.y;
             qv[h][4 * u + 2] = v.z;

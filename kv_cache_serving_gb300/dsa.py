@@ -19,7 +19,8 @@ NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 DSA_F32, DSA_BF16 = 0, 1
 DEV_ERRORS = {0: "OK", 1: "BAD_SEQ_LEN", 2: "BAD_PROMPT", 3: "BAD_WINDOW", 4: "BAD_PAGE",
               5: "BAD_INDEX", 6: "BAD_COUNT", 7: "TIMEOUT", 8: "BAD_GRID_W", 9: "BAD_ORDER",
-              10: "FREE_LIST_FULL", 11: "BAD_QLEN", 12: "BAD_SCALE"}
+              10: "FREE_LIST_FULL", 11: "BAD_QLEN", 12: "BAD_SCALE", 13: "FREE_LIST_EMPTY",
+              14: "BAD_GROUP", 15: "BAD_PREFIX"}
 PAGE = 16
 
 
@@ -51,6 +52,22 @@ ROPE_HALVES, ROPE_NEIGHBOURS = 0, 1
 class dsa_rope(ctypes.Structure):
     _fields_ = [("axes", ctypes.c_int32), ("pairing", ctypes.c_int32),
                 ("inv_freq", ctypes.c_double * 64), ("pair_axis", ctypes.c_uint8 * 64)]
+
+
+NORM_RMS, NORM_LAYER = 0, 1
+
+
+class dsa_qk_norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("per_head", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("q_bias", ctypes.c_void_p), ("k_bias", ctypes.c_void_p)]
+
+
+class dsa_shared_prefix(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("max_prefix", ctypes.c_int32),
+                ("max_suffix", ctypes.c_int32), ("group_start", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p)]
 
 
 class dsa_quant_cache(ctypes.Structure):
@@ -109,6 +126,14 @@ def _load():
         "dsa_get_prefill_split": ([], I32),
         "dsa_rope_axes": ([D, ctypes.POINTER(dsa_rope), I32, P, P, I64, P, I64, P, I64, P, I64,
                            P], I32),
+        "dsa_qk_norm_rope": ([D, ctypes.POINTER(dsa_qk_norm), ctypes.POINTER(dsa_rope), I32, P, P,
+                              I64, P, I64, P, I64, P, I64, P], I32),
+        "dsa_assign_pages": ([D, P, P, P, I32, P, P, P, I32, P, P, P, P, P], I32),
+        "dsa_write_rows": ([D, I32, P, P, I64, P, I64, P, P, P, P], I32),
+        "dsa_decode_dense_shared": ([D, ctypes.POINTER(dsa_shared_prefix), P, P, P, P, P, F32, P, P,
+                                     P, P], I32),
+        "dsa_decode_sparse_masked_shared": ([D, ctypes.POINTER(dsa_shared_prefix), P, P, P, P, P, P,
+                                             P, P, F32, P, P, P, P], I32),
         "dsa_quant_write": ([D, C, I32, P, P, I64, P, P, P, P, P], I32),
         "dsa_quant_read": ([D, C, I32, P, P, P, P, P, P, P, P], I32),
         "dsa_decode_dense_quant": ([D, P, C, P, P, F32, P, P, P, P], I32),
@@ -528,6 +553,106 @@ def dsa_rope_axes(dims, rope, positions, q, k, q_out, k_out, stream=None):
                                  ks, qo, qos, ko, kos, st), "dsa_rope_axes")
 
 
+def make_qk_norm(kind, eps, q_weight=None, k_weight=None, q_bias=None, k_bias=None) -> dsa_qk_norm:
+    """A dsa_qk_norm: kind "rms" or "layer"; weights and biases CUDA tensors of one type (fp32 or
+    bf16), all [head_dim] or all [heads, head_dim], or None (ones, zeros); keeps them alive."""
+    if kind not in ("rms", "layer"):
+        raise ValueError(f"make_qk_norm: kind {kind!r}")
+    given = [t for t in (q_weight, k_weight, q_bias, k_bias) if t is not None]
+    n = dsa_qk_norm(kind=NORM_RMS if kind == "rms" else NORM_LAYER, eps=float(eps))
+    n.tensors, n.facts = (q_weight, k_weight, q_bias, k_bias), None
+    if given:
+        dt, dev, ndim = given[0].dtype, given[0].get_device(), given[0].dim()
+        if dev < 0 or dt not in _QKV or ndim not in (1, 2):
+            raise TypeError("make_qk_norm: weights must be fp32 or bf16 CUDA tensors, [head_dim] or "
+                            "[heads, head_dim]")
+        if any(t.dtype is not dt or t.dim() != ndim for t in given):
+            raise ValueError("make_qk_norm: weights and biases of one type and one kind of shape")
+        n.weight_dtype, n.per_head = DSA_F32 if dt is torch.float32 else DSA_BF16, ndim - 1
+        for name, t in zip(("q_weight", "k_weight", "q_bias", "k_bias"), n.tensors):
+            setattr(n, name, _arg(t, dt, dev, name))
+        n.facts = (dev, ndim)
+    return n
+
+
+def _norm(dims, norm, dev):
+    """The norm, its vectors checked against dims."""
+    if norm.__class__ is not dsa_qk_norm:
+        raise TypeError("norm must be a dsa_qk_norm (see make_qk_norm)")
+    facts = getattr(norm, "facts", None)  # of the tensors it was made over
+    if facts is not None:
+        if facts[0] != dev:
+            raise ValueError(f"norm is on cuda:{facts[0]}, current device cuda:{dev}")
+        hd = dims.head_dim
+        for t, heads in zip(norm.tensors, (dims.hq, dims.hkv, dims.hq, dims.hkv)):
+            _shape(t, (hd,) if facts[1] == 1 else (heads, hd), "a norm vector")
+    return norm
+
+
+def dsa_qk_norm_rope(dims, norm, rope, positions, q, k, q_out, k_out, stream=None):
+    """dsa_rope_axes with each head of q and k normed first (norm: see make_qk_norm)."""
+    if positions.dim() != 2 or positions.shape[1] != rope.axes:
+        raise ValueError(f"positions must be [tokens, {rope.axes}]")
+    hd = dims.head_dim
+    if getattr(rope, "pairs", hd // 2) != hd // 2:
+        raise ValueError(f"rope has {rope.pairs} pairs, head_dim {hd}")
+    dev, st = _launch_on(stream)
+    n = positions.shape[0]
+    qw, kw = (n, dims.hq, hd), (n, dims.hkv, hd)
+    qt, kt = _TYPE.get(dims.q_dtype), _TYPE.get(dims.kv_dtype)
+    qp, qs = _rows_arg(q, qw, qt, dev, "q")
+    kp, ks = _rows_arg(k, kw, kt, dev, "k")
+    qo, qos = _rows_arg(q_out, qw, qt, dev, "q_out")
+    ko, kos = _rows_arg(k_out, kw, kt, dev, "k_out")
+    _check(_load().dsa_qk_norm_rope(dims, _norm(dims, norm, dev), rope, n,
+                                    _arg(positions, _I32, dev, "positions"), qp, qs, kp, ks, qo, qos,
+                                    ko, kos, st), "dsa_qk_norm_rope")
+
+
+def dsa_assign_pages(dims, seq_len, new_len, free_pages, free_count, free_count_out, page_table,
+                     token_start, row_slot, row_pos, ws, stream=None):
+    """Pages of the free list (free_pages, free_count) for the last new_len[b] rows of each request
+    (None: one row each) into page_table, and the slot and position of every new row, packed in
+    request order: token_start [batch + 1] or None, row_slot [max_tokens], row_pos alike or None."""
+    dev, st = _launch_on(stream)
+    B = dims.batch
+    _shape(seq_len, (B,), "seq_len")
+    _shape(new_len, (B,), "new_len")
+    _shape(page_table, (B, dims.max_pages_per_req), "page_table")
+    _shape(token_start, (B + 1,), "token_start")
+    n = row_slot.shape[0]
+    _shape(row_slot, (n,), "row_slot")
+    _shape(row_pos, (n,), "row_pos")
+    for t, what in ((free_count, "free_count"), (free_count_out, "free_count_out")):
+        if t.numel() != 1:
+            raise ValueError(f"{what} must be one int32")
+    _check(_load().dsa_assign_pages(
+        dims, _arg(seq_len, _I32, dev, "seq_len"), _arg(new_len, _I32, dev, "new_len"),
+        _arg(free_pages, _I32, dev, "free_pages"), free_pages.numel(),
+        _arg(free_count, _I32, dev, "free_count"), _arg(free_count_out, _I32, dev, "free_count_out"),
+        _arg(page_table, _I32, dev, "page_table"), n, _arg(token_start, _I32, dev, "token_start"),
+        _arg(row_slot, _I32, dev, "row_slot"), _arg(row_pos, _I32, dev, "row_pos"),
+        _arg(ws, torch.uint8, dev, "ws"), st), "dsa_assign_pages")
+
+
+def dsa_write_rows(dims, row_slot, k, v, k_pages, v_pages, ws, stream=None):
+    """Store rows k and v [tokens, hkv, head_dim] (either may be None, with its pages; rows may be
+    strided) at slots row_slot [tokens] of k_pages and v_pages; negative slots are skipped."""
+    dev, st = _launch_on(stream)
+    n = row_slot.shape[0]
+    _shape(row_slot, (n,), "row_slot")
+    want = (n, dims.hkv, dims.head_dim)
+    kt = _TYPE.get(dims.kv_dtype)
+    kp, ks = _rows_arg(k, want, kt, dev, "k")
+    vp, vs = _rows_arg(v, want, kt, dev, "v")
+    pool = (dims.num_pages, PAGE, dims.hkv, dims.head_dim)
+    _shape(k_pages, pool, "k_pages")
+    _shape(v_pages, pool, "v_pages")
+    _check(_load().dsa_write_rows(dims, n, _arg(row_slot, _I32, dev, "row_slot"), kp, ks, vp, vs,
+                                  _arg(k_pages, kt, dev, "k_pages"), _arg(v_pages, kt, dev, "v_pages"),
+                                  _arg(ws, torch.uint8, dev, "ws"), st), "dsa_write_rows")
+
+
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
@@ -665,6 +790,76 @@ def dsa_prefill_sparse_quant(dims, q, cache, page_table, seq_len, q_len, prompt_
         _arg(prompt_len, _I32, dev, "prompt_len"), _arg(window, _I32, dev, "window"),
         _arg(keep_mask, _MASK, dev, "keep_mask"), _arg(request_order, _I32, dev, "request_order"),
         scale, op, lp, _arg(ws, torch.uint8, dev, "ws"), st), "dsa_prefill_sparse_quant")
+
+
+def shared_prefix(group_start, prefix_len, max_prefix, max_suffix) -> dsa_shared_prefix:
+    """dsa_shared_prefix over group_start [groups + 1] and prefix_len [batch] (int32 CUDA tensors)
+    with host bounds of the shared rows and of the rows behind them; keeps the tensors alive."""
+    dev = prefix_len.get_device()
+    if dev < 0:
+        raise TypeError("prefix_len must be a CUDA tensor")
+    if group_start.dim() != 1 or group_start.shape[0] < 1 or prefix_len.dim() != 1:
+        raise ValueError("group_start must be [groups + 1] and prefix_len [batch]")
+    p = dsa_shared_prefix(group_start.shape[0] - 1, int(max_prefix), int(max_suffix),
+                          _arg(group_start, _I32, dev, "group_start"),
+                          _arg(prefix_len, _I32, dev, "prefix_len"))
+    p.tensors = (group_start, prefix_len)
+    p.facts = (dev, prefix_len.shape[0])
+    return p
+
+
+def _shared(dims, shared, dev):
+    """The groups, checked against dims."""
+    if shared.__class__ is not dsa_shared_prefix:
+        raise TypeError("shared must be a dsa_shared_prefix (see shared_prefix)")
+    facts = getattr(shared, "facts", None)  # of the tensors it was made over
+    if facts is not None and facts != (dev, dims.batch):
+        raise ValueError(f"shared is for {facts[1]} requests on cuda:{facts[0]}; the call has "
+                         f"{dims.batch} on cuda:{dev}")
+    return shared
+
+
+def _pages(dims, k_pages, v_pages, dev):
+    """Addresses of the pages, their shapes checked."""
+    pool = (dims.num_pages, PAGE, dims.hkv, dims.head_dim)
+    _shape(k_pages, pool, "k_pages")
+    _shape(v_pages, pool, "v_pages")
+    kt = _TYPE.get(dims.kv_dtype)
+    return _arg(k_pages, kt, dev, "k_pages"), _arg(v_pages, kt, dev, "v_pages")
+
+
+def dsa_decode_dense_shared(dims, shared, q, k_pages, v_pages, page_table, seq_len, scale, out, lse,
+                            ws, stream=None):
+    """dsa_decode_dense for requests that share prefixes (shared: see shared_prefix), each prefix
+    attended once for its group; out has q's type (bf16)."""
+    dev, st = _launch_on(stream)
+    qp, op, lp = _q_out(dims, q, out, lse, dev, (dims.batch,))
+    kp, vp = _pages(dims, k_pages, v_pages, dev)
+    _shape(page_table, (dims.batch, dims.max_pages_per_req), "page_table")
+    _shape(seq_len, (dims.batch,), "seq_len")
+    _check(_load().dsa_decode_dense_shared(
+        dims, _shared(dims, shared, dev), qp, kp, vp, _arg(page_table, _I32, dev, "page_table"),
+        _arg(seq_len, _I32, dev, "seq_len"), scale, op, lp, _arg(ws, torch.uint8, dev, "ws"), st),
+        "dsa_decode_dense_shared")
+
+
+def dsa_decode_sparse_masked_shared(dims, shared, q, k_pages, v_pages, page_table, seq_len,
+                                    prompt_len, window, keep_mask, scale, out, lse, ws, stream=None):
+    """dsa_decode_sparse_masked for requests that share prefixes of their prompts; out has q's type
+    (bf16)."""
+    dev, st = _launch_on(stream)
+    qp, op, lp = _q_out(dims, q, out, lse, dev, (dims.batch,))
+    kp, vp = _pages(dims, k_pages, v_pages, dev)
+    B = dims.batch
+    _shape(page_table, (B, dims.max_pages_per_req), "page_table")
+    for t, what in ((seq_len, "seq_len"), (prompt_len, "prompt_len"), (window, "window")):
+        _shape(t, (B,), what)
+    _shape(keep_mask, (B, dims.hkv, dims.mask_words), "keep_mask")
+    _check(_load().dsa_decode_sparse_masked_shared(
+        dims, _shared(dims, shared, dev), qp, kp, vp, _arg(page_table, _I32, dev, "page_table"),
+        _arg(seq_len, _I32, dev, "seq_len"), _arg(prompt_len, _I32, dev, "prompt_len"),
+        _arg(window, _I32, dev, "window"), _arg(keep_mask, _MASK, dev, "keep_mask"), scale, op, lp,
+        _arg(ws, torch.uint8, dev, "ws"), st), "dsa_decode_sparse_masked_shared")
 
 
 PLAN_DENSE, PLAN_SPARSE, PLAN_MASKED = 0, 1, 2
