@@ -31,11 +31,6 @@
 // or -- when the CTAs of a (request, kv head) form a thread-block cluster --
 // its state into the first CTA's shared memory for an in-cluster merge.
 //
-// SHARED: the rows behind a prefix that other requests share (shared_prefix.cu leaves the
-// states of its rows).  The row source starts behind the prefix; the kernel is scheduled while
-// the prefix kernel runs and waits for it only before it joins the states; a unit cut into chunks
-// is joined by the chunk that arrives last.
-//
 // Builds (warps per CTA, stage bytes, stages) are template parameters: the
 // default one, and for the sparse calls with bf16 KV a big-batch build (more
 // warps per SM), a small-batch build (one wave of CTAs) and a wide build (one
@@ -179,16 +174,8 @@ constexpr int decode_min_ctas() {
              : 0;
 }
 
-// A load of what a kernel before the one still running wrote: past the SM's own cache, which may
-// hold lines from before, as nothing has been waited for in the kernel.
-template <bool SHARED, typename T>
-__device__ __forceinline__ T ld_now(const T* p) {
-  return SHARED ? __ldcg(p) : __ldg(p);
-}
-
 template <int D, typename KV, int G, int MODE, bool QMIX, int NWARPS = DSA_DECODE_WARPS,
-          int STAGE_BYTES = DSA_DECODE_STAGE_BYTES, int STAGES = DSA_DECODE_STAGES,
-          bool SHARED = false>
+          int STAGE_BYTES = DSA_DECODE_STAGE_BYTES, int STAGES = DSA_DECODE_STAGES>
 __global__ void __launch_bounds__(NWARPS * 32,
                                   (decode_min_ctas<D, KV, G, QMIX, NWARPS, STAGE_BYTES, STAGES>()))
     decode_kernel(const DecodeLaunch a) {
@@ -200,9 +187,7 @@ __global__ void __launch_bounds__(NWARPS * 32,
   // Launched as a programmatic dependent: the CTAs may be scheduled while the
   // previous kernel on the stream drains, but touch no memory before it has
   // completed; the next launch may then be scheduled the same way.
-  // (SHARED behind a prefix kernel: that one has waited for its own predecessor before this
-  // grid could start, and what it writes itself is waited for below.)
-  if (!SHARED || a.early == 0) griddep_wait();
+  griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x, hk = blockIdx.y;
@@ -216,8 +201,7 @@ __global__ void __launch_bounds__(NWARPS * 32,
     if (c == 0 && hk == 0 && threadIdx.x == 0) set_error(a.err, DSA_DEV_BAD_ORDER);
     return;
   }
-  const int L = SHARED ? __ldcg(a.seq_len + b) : a.seq_len[b];
-  const int S0 = SHARED ? __ldcg(a.prefix_len + b) : 0;  // first row of the row source
+  const int L = a.seq_len[b];
   // Page ids of this lane's rows in the warp's first S+1 tiles, loaded
   // speculatively with the request's sizes (they need only b and the CTA's
   // first row): a row that is its own kept index -- every dense row, and the
@@ -225,7 +209,7 @@ __global__ void __launch_bounds__(NWARPS * 32,
   // builds (the ids are used only where the loaded kept index equals the row;
   // on the split-staged build the kept-list step measured slower with them) --
   // then needs no dependent page-table load before its first copy.
-  constexpr bool kSpec = !SHARED && (MODE != kRowsList || !Tl::kSplit);
+  constexpr bool kSpec = MODE != kRowsList || !Tl::kSplit;
   const int spec_row0 = a.cluster > 1 ? (c == 0 ? 0 : -1) : c * a.chunk;
   int spec_pg[Tl::S + 1];
 #pragma unroll
@@ -243,9 +227,8 @@ __global__ void __launch_bounds__(NWARPS * 32,
   int wincl = 0;
   if constexpr (MODE == kRowsMask) {
     const uint32_t* mrow = a.keep_mask + (static_cast<size_t>(b) * a.hkv + hk) * a.mask_words;
-    const unsigned raw = lane < a.mask_words ? ld_now<SHARED>(mrow + lane) : 0u;  // issued with the sizes
-    const int P = SHARED ? __ldcg(a.prompt_len + b) : a.prompt_len[b];
-    const int W = SHARED ? __ldcg(a.window + b) : a.window[b];
+    const unsigned raw = lane < a.mask_words ? __ldg(mrow + lane) : 0u;  // issued with the sizes
+    const int P = a.prompt_len[b], W = a.window[b];
     int code = 0;
     if (L < 1 || L > a.max_pages * kPage) code = DSA_DEV_BAD_SEQ_LEN;
     else if (P < 0) code = DSA_DEV_BAD_PROMPT;
@@ -265,32 +248,20 @@ __global__ void __launch_bounds__(NWARPS * 32,
       }
       wcnt = __shfl_sync(0xffffffffu, wincl, 31);
       n = np + (omax >= 0 ? wcnt + 1 : 0);
-      if (!SHARED && n > a.max_kept) n = -DSA_DEV_BAD_COUNT;
+      if (n > a.max_kept) n = -DSA_DEV_BAD_COUNT;
     } else {
       n = -code;
     }
-    if (!SHARED && c == 0 && threadIdx.x == 0) a.unit_rows[static_cast<size_t>(b) * a.hkv + hk] = n;
+    if (c == 0 && threadIdx.x == 0) a.unit_rows[static_cast<size_t>(b) * a.hkv + hk] = n;
   } else {
     n = request_rows<MODE>(a, b, hk, L);
   }
-  if constexpr (SHARED) {
-    // all of the prefix is kept, and left to the prefix kernel
-    if (n >= 0) {
-      if (S0 < 0 || S0 > a.max_prefix || S0 > (MODE == kRowsMask ? np : L) || n - S0 > a.max_suffix)
-        n = -DSA_DEV_BAD_PREFIX;
-      else
-        n -= S0;
-      np -= S0;
-    }
-  }
   if (n < 0) {
     if (c == 0) {
-      if (SHARED) griddep_wait();
       if (threadIdx.x == 0) set_error(a.err, -n);
       for (int x = threadIdx.x; x < G * D; x += NW * 32) {
         const size_t qh = static_cast<size_t>(b) * a.hq + hk * G + x / D;
-        if (SHARED) reinterpret_cast<uint16_t*>(a.out)[qh * D + x % D] = 0x7fc0;
-        else a.out[qh * D + x % D] = __int_as_float(0x7fc00000);
+        a.out[qh * D + x % D] = __int_as_float(0x7fc00000);
         if (a.lse != nullptr && x % D == 0) a.lse[qh] = __int_as_float(0x7fc00000);
       }
     }
@@ -332,7 +303,7 @@ __global__ void __launch_bounds__(NWARPS * 32,
     nchunks = 1;
   } else {
     row0 = c * a.chunk;
-    if (row0 >= n && (!SHARED || c > 0)) return;  // (no rows but those of the prefix: one chunk)
+    if (row0 >= n) return;
     row1 = min(n, row0 + a.chunk);
     nchunks = (n + a.chunk - 1) / a.chunk;
   }
@@ -404,12 +375,12 @@ __global__ void __launch_bounds__(NWARPS * 32,
     if constexpr (MODE == kRowsMask) {
       if (tile_r0(t) + tile_rows(t) > np) {  // warp-uniform: the tile reaches window rows
         const int jw = window_row(r - np);
-        return my_r >= tile_rows(t) ? 0 : (r < np ? S0 + r : jw);
+        return my_r >= tile_rows(t) ? 0 : (r < np ? r : jw);
       }
     }
     if (my_r >= tile_rows(t)) return 0;
     if constexpr (MODE == kRowsList) return __ldg(idx + r);
-    return S0 + r;
+    return r;
   };
   auto load_pg = [&](int t, int& j) -> int {
     if (t >= my_tiles || my_r >= tile_rows(t)) return 0;
@@ -417,7 +388,7 @@ __global__ void __launch_bounds__(NWARPS * 32,
       set_error(a.err, DSA_DEV_BAD_INDEX);
       j = 0;
     }
-    return ld_now<SHARED>(pt + (j >> 4));
+    return __ldg(pt + (j >> 4));
   };
   // Enqueue the bulk copies of local tile t (rows of global tile warp + t*NW).
   auto issue = [&](int t, int stage, int j, int pg) {
@@ -489,7 +460,7 @@ __global__ void __launch_bounds__(NWARPS * 32,
   WarpAttn<D, KV, G, QMIX, T> wa;
   static_assert(WarpAttn<D, KV, G, QMIX, T>::kRowStride == Tl::kRowStride, "row stride");
   typename WarpAttn<D, KV, G, QMIX, T>::Q wq_;
-  wq_.template load<SHARED>(a.q, a.q_bf16 != 0, static_cast<size_t>(b) * a.hq + hk * G, lane);
+  wq_.load(a.q, a.q_bf16 != 0, static_cast<size_t>(b) * a.hq + hk * G, lane);
   wa.reset();
 
   // prologue: kept indices of tiles 0..S+1, page ids of tiles 0..S, copies of
@@ -651,77 +622,6 @@ __global__ void __launch_bounds__(NWARPS * 32,
     }
     return;
   }
-  if constexpr (SHARED) {
-    // The chunk that arrives last joins the unit's states: those of the prefix, then the
-    // chunks' in their order, whoever comes last.
-    const size_t unit = static_cast<size_t>(b) * a.hkv + hk;
-    if (nchunks > 1) {
-      __shared__ int arrived;
-#pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        const int x = threadIdx.x + k * NW * 32;
-        if (x < G * D) {
-          const int h = x / D, d = x % D;
-          float* to = shared_state(a.states, static_cast<size_t>(b) * a.hq + hk * G + h, a.prefix_slots + c);
-          __stcg(to + d, it_o[k]);
-          if (d == 0) __stcg(reinterpret_cast<float2*>(to + D), make_float2(it_m[k], it_l[k]));
-        }
-      }
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) arrived = atomicAdd(a.arrive + unit, 1);
-      __syncthreads();
-      if (arrived != nchunks - 1) return;
-      __threadfence();
-      if (threadIdx.x == 0) a.arrive[unit] = 0;
-    }
-    if (a.early != 0) griddep_wait();
-    int pieces = 0;
-    if (S0 > 0) {
-      pieces = __ldcg(a.pieces + unit);
-      if (pieces < 1 || pieces > a.prefix_slots) {
-        // no group holds this request (or another prefix was given for its group)
-        if (threadIdx.x == 0) set_error(a.err, DSA_DEV_BAD_GROUP);
-        pieces = -1;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-      const int x = threadIdx.x + k * NW * 32;
-      if (x < G * D) {
-        const int h = x / D, d = x % D;
-        const size_t qh = static_cast<size_t>(b) * a.hq + hk * G + h;
-        float m = nchunks > 1 ? -INFINITY : it_m[k];
-        for (int p = 0; p < pieces; ++p) m = fmaxf(m, __ldcg(shared_state(a.states, qh, p) + D));
-        if (nchunks > 1)
-          for (int p = 0; p < nchunks; ++p)
-            m = fmaxf(m, __ldcg(shared_state(a.states, qh, a.prefix_slots + p) + D));
-        float o = 0.f, l = 0.f;
-        auto add = [&](float od, float om, float ol) {
-          const float sc = om == -INFINITY ? 0.f : exp2f(om - m);
-          o = fmaf(sc, od, o);
-          l = fmaf(sc, ol, l);
-        };
-        auto add_at = [&](int slot) {
-          const float* s = shared_state(a.states, qh, slot);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + D));
-          add(__ldcg(s + d), ml.x, ml.y);
-        };
-#pragma unroll 4
-        for (int p = 0; p < pieces; ++p) add_at(p);
-        if (nchunks > 1)
-#pragma unroll 4
-          for (int p = 0; p < nchunks; ++p) add_at(a.prefix_slots + p);
-        else add(it_o[k], it_m[k], it_l[k]);
-        if (pieces < 0) o = l = m = __int_as_float(0x7fc00000);
-        reinterpret_cast<uint16_t*>(a.out)[qh * D + d] = f32_to_bf16_rn(o / l);
-        if (a.lse != nullptr && d == 0) a.lse[qh] = (m + log2f(l)) * kLn2;
-      }
-    }
-    __syncthreads();
-    if (S0 > 0 && threadIdx.x == 0) a.pieces[unit] = 0;  // the next call's prefix kernel states it anew
-    return;
-  }
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int x = threadIdx.x + k * NW * 32;
@@ -788,11 +688,10 @@ struct IsBf16<bf16_t> {
   static constexpr bool value = true;
 };
 
-template <int D, typename KV, int G, int MODE, bool QMIX, int NWARPS, int SB, int ST,
-          bool SHARED = false>
+template <int D, typename KV, int G, int MODE, bool QMIX, int NWARPS, int SB, int ST>
 cudaError_t launch_decode_one(const DecodeLaunch& a, cudaStream_t s) {
   using Tl = DecodeTiling<D, KV, G, QMIX && G >= 2, NWARPS, SB, ST>;
-  auto kern = decode_kernel<D, KV, G, MODE, QMIX, NWARPS, SB, ST, SHARED>;
+  auto kern = decode_kernel<D, KV, G, MODE, QMIX, NWARPS, SB, ST>;
   const int smem = Tl::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

@@ -21,7 +21,9 @@ constexpr int kMaxDevices = 64;
 // microsecond of a decode step's launch).  One object per kernel; any thread.
 class KernelSlots {
  public:
-  cudaError_t get(const void* kern, int threads, int smem, int* per_sm) {
+  // `all_shared`: an SM that runs the kernel is set up with all the shared memory there is, so
+  // that CTAs of another kernel fit beside it.
+  cudaError_t get(const void* kern, int threads, int smem, int* per_sm, bool all_shared = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -44,6 +46,11 @@ class KernelSlots {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              most - static_cast<int>(fa.sharedSizeBytes));
     if (e != cudaSuccess) return e;
+    if (all_shared) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+      if (e != cudaSuccess) return e;
+    }
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kern, threads, smem);
     if (e != cudaSuccess) return e;
     if (known) cache_[dev].store(want | static_cast<uint32_t>(*per_sm), std::memory_order_release);
@@ -163,26 +170,26 @@ inline int32_t* multi_count_region(const dsa_dims* d, void* ws) {
 
 constexpr size_t kMultiCountBytes = kMultiCounters * sizeof(int32_t);
 
-// The calls over a shared prefix, behind the counters: [batch][hkv] states of each unit's prefix,
-// [batch][hkv] chunks done, then kSharedExtra states of each (request, query head).
+// The calls over a shared prefix, behind the counters: [batch][hq] states of each prefix, then kSharedExtra states of each (request, query head).
 inline int shared_in_part(const dsa_dims* d) {
   const int64_t n_max = dense_rows(d) > d->max_kept ? dense_rows(d) : d->max_kept;
   return chunk_bound(n_max) * (d->head_dim + 2) / (d->head_dim + 4);
 }
+inline size_t shared_piece_bytes(const dsa_dims* d) {
+  return round_up(static_cast<size_t>(d->batch) * d->hq * sizeof(int32_t), 256);
+}
 inline int32_t* shared_pieces(const dsa_dims* d, void* ws) {
   return multi_count_region(d, ws) + kMultiCounters;
 }
-inline int32_t* shared_arrive(const dsa_dims* d, void* ws) {
-  return shared_pieces(d, ws) + unit_ints_region(d) / sizeof(int32_t);
-}
 inline SharedStates shared_states(const dsa_dims* d, void* ws) {
   return SharedStates{partials(ws),
-                      reinterpret_cast<float*>(shared_arrive(d, ws) + unit_ints_region(d) / sizeof(int32_t)),
-                      shared_in_part(d), d->head_dim + 4};
+                      reinterpret_cast<float*>(shared_pieces(d, ws) + shared_piece_bytes(d) / sizeof(int32_t)),
+                      shared_in_part(d), d->head_dim + 4,
+                      static_cast<int64_t>(d->batch) * d->hq};
 }
 inline size_t shared_bytes(const dsa_dims* d) {
-  return 2 * unit_ints_region(d) + round_up(static_cast<size_t>(d->batch) * d->hq * kSharedExtra *
-                                                (d->head_dim + 4) * sizeof(float), 256);
+  return shared_piece_bytes(d) + round_up(static_cast<size_t>(d->batch) * d->hq * kSharedExtra *
+                                              (d->head_dim + 4) * sizeof(float), 256);
 }
 
 // Whether a row stride is at least `least` elements and whole 16-byte pieces.

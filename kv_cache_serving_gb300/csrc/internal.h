@@ -16,19 +16,22 @@ constexpr int kMaxCluster = 8;
 constexpr int kChunkQuantum = 64;  // chunk sizes are multiples of this
 
 // States (acc[head_dim], reference, sum, padding) that the calls over a shared prefix leave in the
-// workspace: `in_part` of a (request, query head) in the partials region, kSharedExtra more behind
-// it.  The first prefix_slots are the prefix's, the others those of chunks.
+// workspace: slots 0 .. in_part - 1 in the partials region, kSharedExtra more behind it, the
+// states of one slot side by side (few slots are used, so those read lie together).  The first
+// prefix_slots are the prefix's, the others those of chunks.
 constexpr int kSharedExtra = 3;
+constexpr int kSharedStates = kMaxChunks + kSharedExtra;  // of a (request, query head), at most
 constexpr int kSharedRows = 128, kSharedBlock = 128;  // query rows of a tile, cache rows of a block
 struct SharedStates {
   float* part;
   float* extra;
   int32_t in_part, floats;  // floats of a state: head_dim + 4
+  int64_t heads;            // batch * hq
 };
 #ifdef __CUDACC__
 __device__ __forceinline__ float* shared_state(const SharedStates& s, size_t qh, int slot) {
-  return slot < s.in_part ? s.part + (qh * s.in_part + slot) * s.floats
-                          : s.extra + (qh * kSharedExtra + (slot - s.in_part)) * s.floats;
+  return slot < s.in_part ? s.part + (slot * s.heads + qh) * s.floats
+                          : s.extra + ((slot - s.in_part) * s.heads + qh) * s.floats;
 }
 #endif
 
@@ -62,14 +65,32 @@ struct DecodeLaunch {
   float* lse;
   float* part;  // [batch][hq][num_chunks][head_dim + 2]
   int32_t* err;
-  // rows behind a shared prefix only (then out is bf16)
+};
+
+// The rows behind shared prefixes, and the joining (shared_rest.cu): bf16 q, pages and out.
+struct RestLaunch {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const int32_t* page_table;
+  const int32_t* seq_len;
   const int32_t* prefix_len;  // [batch]
+  const int32_t* prompt_len;  // masks only
+  const int32_t* window;      // masks only
+  const uint32_t* keep_mask;  // masks only
+  int32_t batch, hq, hkv, head_dim, max_pages, num_pages, max_window, mask_words;
   int32_t max_prefix, max_suffix;
-  int32_t early;              // the prefix kernel runs before: wait for it late
+  int32_t chunk, num_chunks;  // rows of a chunk, chunks of a unit at most
+  int32_t early;              // behind a prefix kernel
+  int32_t deep;               // few warps: more of a warp's rows on their way at a time
   int32_t prefix_slots;       // states 0 .. prefix_slots - 1 are the prefix's
+  float scale_log2;
   SharedStates states;
-  int32_t* pieces;            // [batch][hkv] states of the prefix
-  int32_t* arrive;            // [batch][hkv] chunks done, 0 between launches
+  int32_t* unit_rows;         // [batch][hkv] rows behind the prefix, or -error
+  int32_t* pieces;            // [batch][hq] states of the prefix
+  uint16_t* out;
+  float* lse;
+  int32_t* err;
 };
 
 // The prefixes of groups of requests (shared_prefix.cu): bf16 q and pages.
@@ -179,8 +200,9 @@ constexpr int kMaskModeMaxWindow = 1024;
 cudaError_t launch_decode_bf16(const DecodeLaunch& a, int mode, cudaStream_t s);
 cudaError_t launch_decode_f32(const DecodeLaunch& a, int mode, cudaStream_t s);
 cudaError_t launch_merge(const DecodeLaunch& a, int mode, cudaStream_t s);
-// Behind a shared prefix: dense rows or those of the mask; resident CTAs and rows of a pass.
-cudaError_t launch_decode_shared(const DecodeLaunch& a, int mode, cudaStream_t s);
+// Rows behind shared prefixes, dense or the kept set of the mask; warps of an SM at a time.
+cudaError_t launch_shared_rest(const RestLaunch& a, bool mask, cudaStream_t s);
+cudaError_t shared_rest_warps(int head_dim, int group, bool mask, int* warps);
 cudaError_t launch_shared_prefix(const SharedLaunch& a, cudaStream_t s);
 cudaError_t launch_mass(const MassLaunch& a, bool kv_bf16, cudaStream_t s);
 // Rows one pass of all warps of an attention-mass CTA covers, and its resident
@@ -240,7 +262,6 @@ struct DecodeShape {
 // The requested build of (head_dim, group, mode) when there is one, else the
 // default build.
 DecodeShape decode_shape_bf16(int head_dim, int group, int mode, int build);
-DecodeShape decode_shape_shared(int head_dim, int group, int mode);
 DecodeShape decode_shape_f32(int head_dim, int group, int mode, int build);
 
 // ---- 8-bit K/V cache (quant_*.cu) and rotary positions (rope.cu) ----
@@ -360,6 +381,9 @@ struct NormLaunch {
   const void* bias[2];
   int32_t layer, per_head, weight_bf16;
   float eps;
+  // set by the launch: heads of q and of k, tokens per CTA, threads per token, tokens side by
+  // side, whether a pair does not turn
+  int32_t q_heads, k_heads, tile, lanes, subs, still;
 };
 
 struct AssignLaunch {
@@ -387,7 +411,7 @@ struct RowsLaunch {
   int32_t* err;
 };
 
-cudaError_t launch_qk_norm_rope(const NormLaunch& a, int sms, cudaStream_t s);
+cudaError_t launch_qk_norm_rope(NormLaunch a, int sms, cudaStream_t s);
 cudaError_t launch_assign_pages(const AssignLaunch& a, cudaStream_t s);
 cudaError_t launch_write_rows(const RowsLaunch& a, cudaStream_t s);
 

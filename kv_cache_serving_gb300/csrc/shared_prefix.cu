@@ -13,8 +13,8 @@
 // pieces, one per CTA, whatever the groups' sizes: a CTA takes parts of a tile or several tiles,
 // and a tile has as many states as pieces touch it.
 //
-// Six warps: one loads (a page's 16 rows of 64 dims per tensor copy, into the swizzled tiles that
-// the products read), one issues the products, four weigh, one query row per thread.  Scores and
+// Seven warps: two load (K, and V; a page's 16 rows of 64 dims per tensor copy, into
+// the swizzled tiles that the products read), one issues the products, four weigh, one query row per thread.  Scores and
 // weights exist twice, so that the scores of a block are made while the one before it is
 // weighed; weights go back to tensor memory over their scores as the left operand of P V.  The
 // reference follows the row's maximum when that passes it by 2^8, so that acc is rarely
@@ -40,7 +40,7 @@ namespace {
 constexpr int kPRows = kSharedRows;    // query rows per tile
 constexpr int kPBlock = kSharedBlock;  // cache rows per block ...
 constexpr int kPPages = kPBlock / 16;  // ... and pages
-constexpr int kPThreads = 192;         // 4 weighing warps, a loading one, an issuing one
+constexpr int kPThreads = 224;         // 4 weighing warps, two loading ones, an issuing one
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 bf16
 constexpr float kSlackLog2 = 8.f, kNoRef = -3e38f;
 
@@ -49,10 +49,11 @@ struct PrefixShape {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kHalfBytes;  // 128 rows
   static constexpr int kSlots = D == 128 ? 4 : 6;     // tiles of K and V in shared memory
-  static constexpr int kQ = 0, kRing = kTile;
-  static constexpr int kBar = kRing + kSlots * kTile;
+  static constexpr int kRing = 0, kStage = kSlots * kTile;  // the ring; 4 KB of each weighing warp
+  static constexpr int kBar = kStage + 4 * 4096;
   static constexpr int kSmem = 1024 + kBar + 256;     // the base is rounded up to 1024
-  static constexpr int kS = 0, kO = 256, kTmem = 512; // tensor memory: S and P twice, O
+  // tensor memory: S and P twice, O, Q
+  static constexpr int kS = 0, kO = 256, kQ = 256 + D, kTmem = 512;
 };
 
 constexpr uint32_t kBf16Operands = (1u << 7) | (1u << 10);
@@ -64,6 +65,14 @@ __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map
       "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
       : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
@@ -105,7 +114,8 @@ struct Cursor {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kPThreads, 1)
+// 160 registers: two warps of it leave a quarter of an SM room for two warps of the rest kernel
+__global__ void __maxnreg__(160)
     prefix_kernel(const SharedLaunch a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
   using Sh = PrefixShape<D>;
@@ -130,8 +140,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   uint64_t* s_done = empty + Sh::kSlots;                         // scores of an even, odd block
   uint64_t* p_full = s_done + 2;                                 // its weights
   uint64_t* o_done = s_done + 4;                                 // its second product
-  uint64_t* q_full = s_done + 6;
+  uint64_t* q_full = s_done + 6;                                 // a tile's queries are there
   if (warp == 5) tmem_alloc<Sh::kTmem>(&tmem_slot);
+  if (tid == 128 || tid == 192)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tid == 128 ? &kmap : &vmap) : "memory");
   if (tid == 128) {
     for (int s = 0; s < Sh::kSlots; ++s) {
       mbar_init(full + s, 1);
@@ -154,11 +166,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto units_of = [&](const Group& g) {
     return static_cast<int64_t>(g.tiles) * g.blocks * a.hkv;
   };
-  int64_t sum = 0;
+  int64_t sum = 0, mine0 = 0;  // mine0: of the first group this thread looks at
   int most = 0;
   for (int g = tid; g < a.groups; g += kPThreads) {
     const Group r = load_group(a, g, blockIdx.x == 0 ? a.err : nullptr);
     sum += units_of(r);
+    if (g == tid) mine0 = sum;
     most = max(most, r.blocks);
   }
 #pragma unroll
@@ -179,7 +192,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     most = max(most, most_of[w]);
   }
   // a tile of `most` blocks is touched by at most ceil(most / per) + 1 pieces
-  int64_t per = (sum + gridDim.x - 1) / gridDim.x;
+  int64_t per = max((sum + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(1));
   per = max(per, static_cast<int64_t>((most + a.prefix_slots - 2) / (a.prefix_slots - 1)));
   Cursor c0;
   c0.at = per * blockIdx.x;
@@ -189,7 +202,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __syncthreads();  // scan is used again
   for (int g0 = 0; g0 < a.groups && c0.at < c0.end; g0 += kPThreads) {
     const int g = g0 + tid;
-    const int64_t u = g < a.groups ? units_of(load_group(a, g, nullptr)) : 0;
+    const int64_t u = g0 == 0 ? mine0 : g < a.groups ? units_of(load_group(a, g, nullptr)) : 0;
     int64_t x = u;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -242,49 +255,60 @@ __global__ void __launch_bounds__(kPThreads, 1)
   bool ok = true;
   int count = 0;  // blocks done, over all tiles of the CTA
   if (!work) {
-  } else if (warp == 4) {
-    // ================= loading: K and V of every block into the ring =================
+  } else if (warp == 4 || warp == 6) {
+    // ================= loading: K, or V, of every block into the ring =================
+    // One elected lane issues, from values that the whole warp holds: sixteen lanes with a page
+    // half each took 95 cycles a copy, three times a block's products.
+    const bool k = warp == 4;
+    const CUtensorMap* map = k ? &kmap : &vmap;
     for (Cursor c = c0; ok && c.at < c.end; next_tile(c)) {
       const int nb = blocks_here(c);
       const int32_t* pt = a.page_table + static_cast<size_t>(c.grp.b0) * a.max_pages;
       const int all_pages = (c.grp.rows + 15) >> 4;
-      const int x = lane & 7, half = lane >> 3;
       auto load_id = [&](int blk) {
-        const int p = blk * kPPages + x;
+        const int p = blk * kPPages + (lane & 7);
         return p < all_pages ? __ldg(pt + p) : 0;
       };
       int id = load_id(c.blk);
-      for (int i = 0; ok && i < nb; ++i, ++count) {
+      for (int i = 0; i < nb; ++i, ++count) {
         const int pages = min(kPPages, all_pages - (c.blk + i) * kPPages);
-        if (x < pages && static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_pages)) {
+        if ((lane & 7) < pages && static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_pages)) {
           set_error(a.err, DSA_DEV_BAD_PAGE);
           id = 0;
         }
+        int ids[kPPages];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int item = 2 * count + kv, s = item % Sh::kSlots;
-          if (item >= Sh::kSlots)
-            ok = mbar_wait(empty + s, static_cast<uint32_t>(item / Sh::kSlots - 1) & 1u) && ok;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(full + s, static_cast<uint32_t>(pages * 16 * D * 2));
-          __syncwarp();
-          if (half < kHalves && x < pages)
-            tensor_copy(sm + Sh::kRing + s * Sh::kTile + half * kHalfBytes + x * 2048,
-                        kv == 0 ? &kmap : &vmap, 64 * half, 0, c.hk, id, full + s);
-        }
+        for (int x = 0; x < kPPages; ++x) ids[x] = __shfl_sync(0xffffffffu, id, x);
         if (i + 1 < nb) id = load_id(c.blk + i + 1);
+        const int item = 2 * count + (k ? 0 : 1), s = item % Sh::kSlots;
+        if (item >= Sh::kSlots)
+          ok = mbar_wait(empty + s, static_cast<uint32_t>(item / Sh::kSlots - 1) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full + s, static_cast<uint32_t>(pages * 16 * D * 2));
+          const uint32_t to = sm + Sh::kRing + s * Sh::kTile;
+#pragma unroll
+          for (int x = 0; x < kPPages; ++x)
+            if (x < pages) {
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                tensor_copy(to + h * kHalfBytes + x * 2048, map, 64 * h, 0, c.hk, ids[x], full + s);
+            }
+        }
+        __syncwarp();
       }
     }
     if (!ok) {
       *failed = 1;
       // copies in flight get a bounded time to land
-      for (int item = max(0, 2 * count - Sh::kSlots + 1); item < 2 * count; ++item)
+      for (int n = max(0, count - Sh::kSlots / 2); n < count; ++n) {
+        const int item = 2 * n + (k ? 0 : 1);
         mbar_wait(full + item % Sh::kSlots, static_cast<uint32_t>(item / Sh::kSlots) & 1u);
+      }
     }
   } else if (warp == 5) {
     // ================= issuing =================
-    const uint64_t q_desc = tc_desc(sm + Sh::kQ, 16, 1024, kSwizzle128);
     const uint64_t k_desc = tc_desc(sm + Sh::kRing, 16, 1024, kSwizzle128);
     const uint64_t v_desc = tc_desc(sm + Sh::kRing, kHalfBytes, 1024, kSwizzle128);
     int tiles = 0;
@@ -303,8 +327,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           const uint64_t kd = k_desc + (s * Sh::kTile >> 4);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
-            const int off = ((x >> 2) * kHalfBytes + (x & 3) * 32) >> 4;
-            tc_mma_f16(tmem + Sh::kS + e * 128, q_desc + off, kd + off, id_s, x > 0);
+            tc_mma_f16_ta(tmem + Sh::kS + e * 128, tmem + Sh::kQ + 8 * x,
+                          kd + (((x >> 2) * kHalfBytes + (x & 3) * 32) >> 4), id_s, x > 0);
           }
           tc_commit(s_done + e);
           tc_commit(empty + s);
@@ -347,44 +371,42 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     // at least 2^-100, so that a masked score (-inf) times it stays one
     const float c1 = fmaxf(fabsf(a.scale_log2), 0x1p-100f);
-    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // q changes its sign
     for (Cursor c = c0; ok && c.at < c.end; next_tile(c)) {
       const int nb = blocks_here(c);
       const int req0 = c.t * per_tile;  // first request of the tile, within the group
       const bool idle = req0 + ((32 * warp) >> lg) >= c.grp.n;
       const bool mine = req0 + (r >> lg) < c.grp.n;
       const int b = c.grp.b0 + req0 + (r >> lg);
-      // q rows of the tile, swizzled; rows without a request are zeros.  All products that read
-      // the last tile's rows are done: their scores were.
+      // The row's query into tensor memory (zeros where there is no request); the products that
+      // read the last tile's are done: its scores were.
       if (!idle) {
-        constexpr int kLanes = D / 8, kStep = 32 / kLanes;
-        const int piece = lane % kLanes, r0 = 32 * warp + lane / kLanes;
+        const size_t qh = static_cast<size_t>(b) * a.hq + (c.hk << lg) + (r & ((1 << lg) - 1));
+        const uint4* from = reinterpret_cast<const uint4*>(a.q + (mine ? qh : 0) * D);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 v[16 / kStep];
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t w[32];
 #pragma unroll
-          for (int y = 0; y < 16 / kStep; ++y) {
-            const int row = r0 + 16 * h + kStep * y, q = req0 + (row >> lg);
-            const size_t qh = static_cast<size_t>(c.grp.b0 + q) * a.hq + (c.hk << lg) + (row & ((1 << lg) - 1));
-            v[y] = q < c.grp.n ? __ldg(reinterpret_cast<const uint4*>(a.q + qh * D) + piece)
-                               : make_uint4(0u, 0u, 0u, 0u);
+          for (int y = 0; y < 8; ++y) {
+            const uint4 v = mine ? __ldg(from + 8 * h + y) : make_uint4(0u, 0u, 0u, 0u);
+            w[4 * y] = v.x ^ flip;
+            w[4 * y + 1] = v.y ^ flip;
+            w[4 * y + 2] = v.z ^ flip;
+            w[4 * y + 3] = v.w ^ flip;
           }
-#pragma unroll
-          for (int y = 0; y < 16 / kStep; ++y) {
-            const int row = r0 + 16 * h + kStep * y;
-            sts128(sm + Sh::kQ + (piece >> 3) * kHalfBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4),
-                   make_uint4(v[y].x ^ flip, v[y].y ^ flip, v[y].z ^ flip, v[y].w ^ flip));
-          }
+          tmem_store16(t_lane + Sh::kQ + 32 * h, w);
+          tmem_store16(t_lane + Sh::kQ + 32 * h + 16, w + 16);
         }
+        tc_wait_st();
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
       bool same = true;  // a member states the group's prefix
       if (mine && __ldg(a.prefix_len + b) != c.grp.rows) {
         set_error(a.err, DSA_DEV_BAD_PREFIX);
         same = false;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
       float ref = kNoRef, l = 0.f;
       for (int i = 0; i < nb; ++i) {
         const int now = count + i, e = now & 1;
@@ -411,23 +433,32 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         if (!idle) {
           const uint32_t t_s = t_lane + Sh::kS + e * 128;
-          uint32_t s[4][32];
+          // 64 columns at a time: the second half for its maximum, the first for its maximum and
+          // its weights (over its own scores), the second again
+          uint32_t s[2][32];
+          auto load_half = [&](int h) {
+            tmem_load<32>(t_s + 64 * h, s[0]);
+            tmem_load<32>(t_s + 64 * h + 32, s[1]);
+            tc_wait_ld();
+            if (valid < kPBlock) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) tmem_load<32>(t_s + 32 * x, s[x]);
-          tc_wait_ld();
-          if (valid < kPBlock) {
+              for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-              for (int q = 0; q < 32; ++q)
-                if (32 * x + q >= valid) s[x][q] = 0xff800000u;
-          }
+                for (int q = 0; q < 32; ++q)
+                  if (64 * h + 32 * x + q >= valid) s[x][q] = 0xff800000u;
+            }
+          };
           float m[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            m[x] = __uint_as_float(s[x][0]);
+          for (int h = 1; h >= 0; --h) {
+            load_half(h);
 #pragma unroll
-            for (int q = 1; q < 32; ++q) m[x] = fmaxf(m[x], __uint_as_float(s[x][q]));
+            for (int x = 0; x < 2; ++x) {
+              float& t = m[2 * h + x];
+              t = __uint_as_float(s[x][0]);
+#pragma unroll
+              for (int q = 1; q < 32; ++q) t = fmaxf(t, __uint_as_float(s[x][q]));
+            }
           }
           const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c1;
           const bool over = top - ref > kSlackLog2;
@@ -454,18 +485,22 @@ __global__ void __launch_bounds__(kPThreads, 1)
           const f32x2 a1 = pack2(c1, c1), a2 = pack2(-ref, -ref);
           f32x2 sums[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t w[16];
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) load_half(1);
 #pragma unroll
-            for (int q = 0; q < 32; q += 2) {
-              float z0, z1;
-              unpack2(fma2(pack2(__uint_as_float(s[x][q]), __uint_as_float(s[x][q + 1])), a1, a2), z0, z1);
-              z0 = ex2_approx(z0);
-              z1 = ex2_approx(z1);
-              sums[(q >> 1) & 1] = add2(sums[(q >> 1) & 1], pack2(z0, z1));
-              w[q / 2] = bf16x2_rn(z0, z1);
+            for (int x = 0; x < 2; ++x) {
+              uint32_t w[16];
+#pragma unroll
+              for (int q = 0; q < 32; q += 2) {
+                float z0, z1;
+                unpack2(fma2(pack2(__uint_as_float(s[x][q]), __uint_as_float(s[x][q + 1])), a1, a2), z0, z1);
+                z0 = ex2_approx(z0);
+                z1 = ex2_approx(z1);
+                sums[(q >> 1) & 1] = add2(sums[(q >> 1) & 1], pack2(z0, z1));
+                w[q / 2] = bf16x2_rn(z0, z1);
+              }
+              tmem_store16(t_s + 32 * h + 16 * x, w);
             }
-            tmem_store16(t_s + 16 * x, w);
           }
           float u, v;
           unpack2(add2(sums[0], sums[1]), u, v);
@@ -490,22 +525,34 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tc_fence_after();
         const size_t qh = static_cast<size_t>(b) * a.hq + (c.hk << lg) + (r & ((1 << lg) - 1));
         float* to = shared_state(a.states, mine ? qh : 0, slot);
+        // 32 dims of the warp's 32 rows at a time, by way of shared memory (swizzled), so that 8
+        // lanes store a row's line: a thread that stores its row alone touches 32 lines with every
+        // store
+        const uint32_t stage = sm + Sh::kStage + warp * 4096;
 #pragma unroll 1
         for (int h = 0; h < D / 32; ++h) {
           uint32_t o[32];
           tmem_load<32>(t_lane + Sh::kO + 32 * h, o);
           tc_wait_ld();
-          if (mine) {
+          __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              reinterpret_cast<uint4*>(to + 32 * h)[q] =
-                  make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          for (int q = 0; q < 8; ++q)
+            sts128(stage + lane * 128 + ((q ^ (lane & 7)) << 4),
+                   make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
+          __syncwarp();
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int row = 4 * y + (lane >> 3);  // of the warp
+            const uint64_t base = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(to), row);
+            const uint4 v = lds128(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+            if (req0 + ((32 * warp + row) >> lg) < c.grp.n)
+              reinterpret_cast<uint4*>(reinterpret_cast<float*>(base) + 32 * h)[lane & 7] = v;
           }
         }
         if (mine)
           *reinterpret_cast<float2*>(to + D) = make_float2(same ? ref : __int_as_float(0x7fc00000), l);
-        if (mine && slot == 0 && (r & ((1 << lg) - 1)) == 0)
-          a.pieces[static_cast<size_t>(b) * a.hkv + c.hk] =
+        if (mine && slot == 0)
+          a.pieces[qh] =
               static_cast<int32_t>((tile_at + c.grp.blocks - 1) / per - tile_at / per) + 1;
         tc_fence_before();
       }
@@ -569,12 +616,16 @@ cudaError_t launch_one(const SharedLaunch& a, const CUtensorMap& kmap, const CUt
   static KernelSlots cache;
   int per_sm = 0;
   const cudaError_t e =
-      cache.get(reinterpret_cast<const void*>(kern), kPThreads, PrefixShape<D>::kSmem, &per_sm);
+      cache.get(reinterpret_cast<const void*>(kern), kPThreads, PrefixShape<D>::kSmem, &per_sm, true);
   if (e != cudaSuccess) return e;
   // no more CTAs than blocks there can be
   const int64_t tiles = a.groups + ((static_cast<int64_t>(a.batch) << a.group_log2) / kPRows);
   const int64_t blocks = tiles * a.hkv * ceil_div(a.max_prefix, kPBlock);
-  const int64_t ctas = blocks < a.sms ? blocks : a.sms;
+  // A quarter of the blocks, but half of the SMs at least: a CTA keeps the rest kernel's CTAs from
+  // most of its SM, so few blocks are better on some SMs alone.
+  int64_t ctas = blocks / 4 > a.sms / 2 ? blocks / 4 : a.sms / 2;
+  ctas = ctas < a.sms ? ctas : a.sms;
+  ctas = ctas < blocks ? ctas : blocks;
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kPThreads),
                     static_cast<size_t>(PrefixShape<D>::kSmem), s, a, kmap, vmap);
 }

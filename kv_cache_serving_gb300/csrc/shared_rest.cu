@@ -1,0 +1,343 @@
+// shared_rest.cu -- decode attention over the rows that requests do not share, and the joining of
+// all states of a batch with shared prefixes (shared_prefix.cu leaves those of the prefixes).
+//
+// rest_kernel.  A work item is a chunk of the rows of one (request, kv head) behind the prefix:
+// dense rows, or the kept set of the mask without the prefix.  A warp takes an item by itself, with
+// its own ring of shared memory, and leaves a state (acc, m, l) per query head in the workspace:
+// no two warps wait for each other, and short units (a few tens of kept rows) occupy a warp each.
+// The warps of a CTA have neighbouring kv heads of the same rows, which lie side by side in
+// memory and end together.  The kernel runs beside the prefix kernel: it starts as soon as that
+// one's CTAs do, waits for nothing of it, and takes the places that its CTAs leave.
+//
+// join_kernel.  A warp per (request, query head): the log-sum-exp sum of the prefix's states and
+// the chunks', in their order, so results do not depend on who was first.
+#include <math.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "host.h"
+#include "internal.h"
+#include "mma.cuh"
+#include "rows.cuh"
+#include "warp_attn.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kRestWarps = 4;
+
+template <int D, int G, bool DEEP>
+struct RestShape {
+  static constexpr bool kMma = G >= 2;
+  static constexpr int kRowBytes = 2 * D;
+  static constexpr int kRows = (kMma || D == 64) ? 16 : 8;  // of a tile
+  static constexpr int kRowStride = kRowBytes + (kMma ? 16 : 0);
+  static constexpr int kTile = kRows * kRowStride;          // K or V of a tile
+  // K and V buffers of a warp: about 8 KB in all, so that some 20 warps fit an SM; twice as many
+  // where there are few warps and the latency of a tile counts
+  static constexpr int kBufs = (kTile > 4096 ? 1 : 2) * (DEEP ? 2 : 1);
+  static constexpr int kWarp = 2 * kBufs * kTile;
+  static constexpr int kBars = kRestWarps * kWarp;
+  static constexpr int kSmem = kBars + kRestWarps * 2 * kBufs * 8;
+  static constexpr bool kBulk = D == 128;  // a copy per row; rows of 128 bytes go in 16-byte pieces
+};
+
+template <int D, int G, bool MASK, bool DEEP>
+__global__ void __launch_bounds__(kRestWarps * 32, 20 / kRestWarps) rest_kernel(const RestLaunch a) {
+  using Sh = RestShape<D, G, DEEP>;
+  constexpr int T = Sh::kRows, NB = Sh::kBufs;
+  extern __shared__ __align__(128) unsigned char smem[];
+  // Behind a prefix kernel nothing is waited for here: that one has waited for its own
+  // predecessor before this grid could start.  What was written before is read past the SM's
+  // own cache, which may hold lines from earlier.
+  if (a.early == 0) griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const uint32_t item = blockIdx.x * kRestWarps + warp;
+  const int hk = static_cast<int>(item % a.hkv);
+  const int c = static_cast<int>(item / a.hkv % a.num_chunks);
+  const int b = static_cast<int>(item / a.hkv / a.num_chunks);
+  if (b < a.batch) {
+    const int L = __ldcg(a.seq_len + b), S0 = __ldcg(a.prefix_len + b);
+    int n = 0, np = 0;
+    MaskRows rows;
+    if constexpr (MASK) {
+      const uint32_t raw = lane < a.mask_words
+                               ? __ldcg(a.keep_mask + (static_cast<size_t>(b) * a.hkv + hk) * a.mask_words + lane)
+                               : 0u;
+      n = rows.init(raw, L, __ldcg(a.prompt_len + b), __ldcg(a.window + b), a.max_pages, a.max_window,
+                    INT32_MAX, lane);
+      np = rows.np;
+    } else {
+      n = L < 1 || L > a.max_pages * kPage ? -DSA_DEV_BAD_SEQ_LEN : L;
+      np = L;
+    }
+    // all of the prefix is kept, and left to the prefix kernel
+    if (n >= 0)
+      n = S0 < 0 || S0 > a.max_prefix || S0 > np || n - S0 > a.max_suffix ? -DSA_DEV_BAD_PREFIX : n - S0;
+    np -= S0;
+    if (c == 0 && lane == 0) {
+      a.unit_rows[static_cast<size_t>(b) * a.hkv + hk] = n;
+      if (n < 0) set_error(a.err, -n);
+    }
+    const int row0 = c * a.chunk, row1 = min(n, row0 + a.chunk);
+    const int tiles = row1 > row0 ? (row1 - row0 + T - 1) / T : 0;
+    unsigned char* kst = smem + warp * Sh::kWarp;
+    unsigned char* vst = kst + NB * Sh::kTile;
+    uint64_t* kbar = reinterpret_cast<uint64_t*>(smem + Sh::kBars) + warp * 2 * NB;
+    uint64_t* vbar = kbar + NB;
+    const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.max_pages;
+    const int my_r = lane & (T - 1);
+    auto rows_of = [&](int t) { return min(T, row1 - (row0 + t * T)); };
+    // Logical row of this lane in tile t (all lanes take part).
+    auto row_of = [&](int t) -> int {
+      const int r = row0 + t * T + my_r;
+      int j = S0 + r;
+      if constexpr (MASK)
+        if (t < tiles && row0 + t * T + rows_of(t) > np) {  // the tile reaches window rows
+          const int w = rows.window_row(r - np);
+          if (r >= np) j = w;
+        }
+      return j;
+    };
+    // Where the row lies: its page, asked for a tile ahead, and its slot.
+    struct Place {
+      int page, slot;
+    };
+    auto place_of = [&](int t, int j) -> Place {
+      if (t >= tiles || my_r >= rows_of(t)) return Place{0, 0};
+      return Place{__ldcg(pt + (j >> 4)), j & (kPage - 1)};
+    };
+    // K (half 0) or V of tile t on its way into its buffer.
+    auto issue = [&](int t, int half, const Place& p) {
+      const int nrows = rows_of(t), s = t % NB;
+      uint64_t* bar = (half == 0 ? kbar : vbar) + s;
+      unsigned char* to = (half == 0 ? kst : vst) + s * Sh::kTile;
+      const uint16_t* base = half == 0 ? a.k : a.v;
+      int64_t at = static_cast<int64_t>(p.page) * kPage + p.slot;
+      if (my_r < nrows && static_cast<uint32_t>(p.page) >= static_cast<uint32_t>(a.num_pages)) {
+        set_error(a.err, DSA_DEV_BAD_PAGE);
+        at = 0;
+      }
+      if constexpr (Sh::kBulk) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nrows * Sh::kRowBytes));
+        __syncwarp();
+        if (lane < nrows)
+          bulk_copy_g2s(to + lane * Sh::kRowStride, base + (static_cast<size_t>(at) * a.hkv + hk) * D,
+                        Sh::kRowBytes, bar);
+      } else {
+        constexpr int kLanes = Sh::kRowBytes / 16, kStep = 32 / kLanes;
+        const int piece = lane % kLanes;
+#pragma unroll
+        for (int y = 0; y < T / kStep; ++y) {
+          const int r = kStep * y + lane / kLanes;
+          const int64_t src = __shfl_sync(0xffffffffu, at, r);
+          if (r < nrows)
+            cp_async16(to + r * Sh::kRowStride + 16 * piece,
+                       reinterpret_cast<const unsigned char*>(
+                           base + (static_cast<size_t>(src) * a.hkv + hk) * D) + 16 * piece);
+        }
+        cp_async_arrive(bar);
+      }
+    };
+
+    if (tiles > 0) {
+      bool ok = true;
+      if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < 2 * NB; ++s) mbar_init(kbar + s, Sh::kBulk ? 1 : 32);
+        fence_mbar_init();
+      }
+      __syncwarp();
+      WarpAttn<D, bf16_t, G, true, T> wa;
+      static_assert(WarpAttn<D, bf16_t, G, true, T>::kRowStride == Sh::kRowStride, "row stride");
+      WarpQ<D, bf16_t, G, true> q;
+      const size_t qh0 = static_cast<size_t>(b) * a.hq + hk * G;
+      Place at[NB + 1];
+#pragma unroll
+      for (int t = 0; t <= NB; ++t) at[t] = place_of(t, row_of(t));
+      q.template load<true>(a.q, true, qh0, lane);
+      wa.reset();
+#pragma unroll
+      for (int t = 0; t < NB; ++t)
+        if (t < tiles) {
+          issue(t, 0, at[t]);
+          issue(t, 1, at[t]);
+        }
+      Place next = at[NB];  // of tile t + NB
+      int t = 0;
+      for (; t < tiles; ++t) {
+        const int s = t % NB, nrows = rows_of(t);
+        const uint32_t phase = static_cast<uint32_t>(t / NB) & 1u;
+        const Place now = next;
+        ok = mbar_wait(kbar + s, phase);
+        if constexpr (Sh::kMma) {
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          wa.qk_softmax(q, kst + s * Sh::kTile, nrows, a.scale_log2, lane);
+          __syncwarp();
+          fence_proxy_async_smem();
+          if (t + NB < tiles) issue(t + NB, 0, now);
+          next = place_of(t + NB + 1, row_of(t + NB + 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(vbar + s, phase));
+          if (!ok) break;
+          wa.pv(vst + s * Sh::kTile, nrows, lane);
+          __syncwarp();
+          fence_proxy_async_smem();
+          if (t + NB < tiles) issue(t + NB, 1, now);
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(vbar + s, phase) && ok);
+          if (!ok) break;
+          wa.tile(q, kst + s * Sh::kTile, vst + s * Sh::kTile, nrows, a.scale_log2, lane);
+          __syncwarp();
+          fence_proxy_async_smem();
+          if (t + NB < tiles) {
+            issue(t + NB, 0, now);
+            issue(t + NB, 1, now);
+          }
+          next = place_of(t + NB + 1, row_of(t + NB + 1));
+        }
+      }
+      if (!ok) {
+        // copies still in flight get a bounded time to land
+        if (lane == 0) set_error(a.err, DSA_DEV_TIMEOUT);
+        for (int s = 0; s < 2 * NB; ++s) {
+          mbar_wait(kbar + s, 0);
+          mbar_wait(kbar + s, 1);
+        }
+      }
+      float* to = shared_state(a.states, qh0, a.prefix_slots + c);
+      wa.flush(to, lane, shared_state(a.states, qh0 + 1, a.prefix_slots + c) - to);
+    }
+  }
+  // The grid ends behind the prefix kernel, so that whoever waits for it has waited for both.
+  if (a.early != 0 && blockIdx.x == 0) griddep_wait();
+}
+
+constexpr int kJoinWarps = 4;
+constexpr int kJoinBatch = 16;  // states whose dims are on their way at a time
+
+// A warp joins the states of one (request, query head): lane p weighs state p, all lanes add.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const RestLaunch a) {
+  constexpr int kDims = D / 32;  // of a lane
+  using Vec = typename std::conditional<kDims == 4, float4, float2>::type;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const uint32_t qh = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (qh >= static_cast<uint32_t>(a.batch) * a.hq) return;
+  const uint32_t b = qh / a.hq, hk = (qh - b * a.hq) / (static_cast<uint32_t>(a.hq) / a.hkv);
+  const int n = __ldcg(a.unit_rows + static_cast<size_t>(b) * a.hkv + hk), S0 = __ldcg(a.prefix_len + b);
+  int pieces = __ldcg(a.pieces + qh);
+  int chunks = n > 0 ? (n + a.chunk - 1) / a.chunk : 0;
+  bool bad = n < 0;
+  if (S0 <= 0) {
+    pieces = 0;
+  } else {
+    if (!bad && (pieces < 1 || pieces > a.prefix_slots)) {
+      // no group holds this request, or its group's first has another prefix
+      if (lane == 0) set_error(a.err, DSA_DEV_BAD_GROUP);
+      bad = true;
+    }
+    if (lane == 0) a.pieces[qh] = 0;  // the next call's prefix kernel states it anew
+  }
+  if (bad) pieces = chunks = 0;
+  // states in order, the prefix's, then the chunks'
+  const int count = pieces + chunks, skip = a.prefix_slots - pieces;
+  auto state = [&](int p) { return shared_state(a.states, qh, p < pieces ? p : p + skip); };
+  static_assert(kSharedStates <= 64, "two states per lane");
+  float2 ml[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    ml[y] = lane + 32 * y < count ? __ldcg(reinterpret_cast<const float2*>(state(lane + 32 * y) + D))
+                                  : make_float2(-INFINITY, 0.f);
+  Vec o{};
+  float sc[2], m = 0.f, l = 0.f;
+  for (int p0 = 0; p0 < count || p0 == 0; p0 += kJoinBatch) {
+    Vec v[kJoinBatch];
+#pragma unroll
+    for (int y = 0; y < kJoinBatch; ++y)
+      if (p0 + y < count) v[y] = __ldcg(reinterpret_cast<const Vec*>(state(p0 + y)) + lane);
+    if (p0 == 0) {
+      m = warp_max(fmaxf(ml[0].x, ml[1].x));
+      // (a NaN reference, which the maximum passes over, makes its weight NaN)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) sc[y] = ml[y].x == -INFINITY ? 0.f : exp2f(ml[y].x - m);
+      l = warp_sum(fmaf(sc[0], ml[0].y, sc[1] * ml[1].y));
+    }
+#pragma unroll
+    for (int y = 0; y < kJoinBatch; ++y)
+      if (p0 + y < count) {
+        const float w = __shfl_sync(0xffffffffu, p0 + y < 32 ? sc[0] : sc[1], (p0 + y) & 31);
+        o.x = fmaf(w, v[y].x, o.x);
+        o.y = fmaf(w, v[y].y, o.y);
+        if constexpr (kDims == 4) {
+          o.z = fmaf(w, v[y].z, o.z);
+          o.w = fmaf(w, v[y].w, o.w);
+        }
+      }
+  }
+  if (bad) l = m = __int_as_float(0x7fc00000);
+  const float inv = 1.f / l;
+  uint32_t* to = reinterpret_cast<uint32_t*>(a.out) + (static_cast<size_t>(qh) * D + kDims * lane) / 2;
+  to[0] = bf16x2_rn(o.x * inv, o.y * inv);
+  if constexpr (kDims == 4) to[1] = bf16x2_rn(o.z * inv, o.w * inv);
+  if (a.lse != nullptr && lane == 0) a.lse[qh] = (m + log2f(l)) * kLn2;
+}
+
+// One build: the launch when `a` is given, the warps of a wave when `warps` is.
+template <int D, int G, bool MASK, bool DEEP>
+cudaError_t one(const RestLaunch* a, cudaStream_t s, int* warps) {
+  using Sh = RestShape<D, G, DEEP>;
+  auto kern = rest_kernel<D, G, MASK, DEEP>;
+  static KernelSlots cache;
+  int per_sm = 0;
+  const cudaError_t e =
+      cache.get(reinterpret_cast<const void*>(kern), kRestWarps * 32, Sh::kSmem, &per_sm, true);
+  if (e != cudaSuccess) return e;
+  if (warps != nullptr) *warps = per_sm * kRestWarps;
+  if (a == nullptr) return cudaSuccess;
+  const int64_t items = static_cast<int64_t>(a->batch) * a->hkv * a->num_chunks;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ceil_div(items, kRestWarps))), dim3(kRestWarps * 32),
+                    static_cast<size_t>(Sh::kSmem), s, *a);
+}
+template <int D, int G>
+cudaError_t build(bool mask, const RestLaunch* a, cudaStream_t s, int* warps) {
+  if (a != nullptr && a->deep != 0)
+    return mask ? one<D, G, true, true>(a, s, warps) : one<D, G, false, true>(a, s, warps);
+  return mask ? one<D, G, true, false>(a, s, warps) : one<D, G, false, false>(a, s, warps);
+}
+
+cudaError_t any(int head_dim, int group, bool mask, const RestLaunch* a, cudaStream_t s, int* warps) {
+#define DSA_BODY(DD, GG) return build<DD, GG>(mask, a, s, warps);
+  if (head_dim == 64 && group == 1) { DSA_BODY(64, 1) }
+  if (head_dim == 64 && group == 2) { DSA_BODY(64, 2) }
+  if (head_dim == 64 && group == 4) { DSA_BODY(64, 4) }
+  if (head_dim == 64 && group == 8) { DSA_BODY(64, 8) }
+  if (head_dim == 128 && group == 1) { DSA_BODY(128, 1) }
+  if (head_dim == 128 && group == 2) { DSA_BODY(128, 2) }
+  if (head_dim == 128 && group == 4) { DSA_BODY(128, 4) }
+  if (head_dim == 128 && group == 8) { DSA_BODY(128, 8) }
+#undef DSA_BODY
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_shared_rest(const RestLaunch& a, bool mask, cudaStream_t s) {
+  const cudaError_t e = any(a.head_dim, a.hq / a.hkv, mask, &a, s, nullptr);
+  if (e != cudaSuccess) return e;
+  auto kern = a.head_dim == 128 ? join_kernel<128> : join_kernel<64>;
+  return launch_pdl(
+      kern, dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.batch) * a.hq, kJoinWarps))),
+      dim3(kJoinWarps * 32), 0, s, a);
+}
+
+cudaError_t shared_rest_warps(int head_dim, int group, bool mask, int* warps) {
+  return any(head_dim, group, mask, nullptr, nullptr, warps);
+}
+
+}  // namespace dsa

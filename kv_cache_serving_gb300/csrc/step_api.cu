@@ -15,16 +15,16 @@
 namespace dsa {
 namespace {
 
-// Waves of resident CTAs that the rows behind the prefixes are cut for: the host knows a bound
-// of a request's rows only.
-constexpr int kSharedDenseWaves = 4, kSharedMaskWaves = 1;
+// Half waves of resident warps that the rows behind the prefixes are cut for (the host knows a
+// bound of a request's rows only), and the rows that a chunk is a multiple of.
+constexpr int kSharedDenseWaves = 6, kSharedMaskWaves = 4, kSharedChunk = 32;
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
 
-dsa_status decode_shared(const dsa_dims* d, int mode, const dsa_shared_prefix* sh, const void* q,
+dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* sh, const void* q,
                          const void* k, const void* v, const int32_t* page_table,
                          const int32_t* seq_len, const int32_t* prompt_len, const int32_t* window,
                          const uint32_t* keep_mask, float scale, void* out, float* lse, void* ws,
@@ -37,65 +37,65 @@ dsa_status decode_shared(const dsa_dims* d, int mode, const dsa_shared_prefix* s
   if (!q || !k || !v || !page_table || !seq_len || !out || !ws || !sh->prefix_len ||
       (sh->max_prefix > 0 && (sh->groups < 1 || !sh->group_start)))
     return DSA_ERR_INVALID_ARG;
-  if (mode == kModeMask && (!prompt_len || !window || !keep_mask)) return DSA_ERR_INVALID_ARG;
+  if (mask && (!prompt_len || !window || !keep_mask)) return DSA_ERR_INVALID_ARG;
   const size_t bytes = static_cast<size_t>(d->batch) * d->hq * d->head_dim * 2;
   if (!std::isfinite(scale) || !aligned(ws, 256) || !aligned(q, 16) || !aligned(k, 16) ||
-      !aligned(v, 16) || !aligned(out, 2) || !aligned(lse, 4) || sh->max_prefix > dense_rows(d) ||
+      !aligned(v, 16) || !aligned(out, 8) || !aligned(lse, 4) || sh->max_prefix > dense_rows(d) ||
       overlap(q, bytes, out, bytes))
     return DSA_ERR_INVALID_ARG;
   if (d->q_dtype != DSA_BF16 || d->kv_dtype != DSA_BF16 || d->batch > 65535 || d->hkv > 65535 ||
-      (mode == kModeMask && d->max_window > kMaskModeMaxWindow))
+      (mask && d->max_window > kMaskModeMaxWindow))
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int group = d->hq / d->hkv;
-  DecodeLaunch a{};
-  a.q = q;
-  a.q_bf16 = 1;
-  a.k = k;
-  a.v = v;
+  RestLaunch a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
   a.page_table = page_table;
   a.seq_len = seq_len;
+  a.prefix_len = sh->prefix_len;
   a.prompt_len = prompt_len;
   a.window = window;
   a.keep_mask = keep_mask;
-  a.max_window = d->max_window;
-  a.mask_words = d->mask_words;
   a.batch = d->batch;
   a.hq = d->hq;
   a.hkv = d->hkv;
   a.head_dim = d->head_dim;
   a.max_pages = d->max_pages_per_req;
   a.num_pages = d->num_pages;
-  a.cluster = 1;
-  a.scale_log2 = scale * kLog2e;
-  a.out = static_cast<float*>(out);
-  a.lse = lse;
-  a.err = err_word(ws);
-  a.prefix_len = sh->prefix_len;
+  a.max_window = d->max_window;
+  a.mask_words = d->mask_words;
   a.max_prefix = sh->max_prefix;
   a.max_suffix = sh->max_suffix;
   a.early = sh->max_prefix > 0;
+  a.scale_log2 = scale * kLog2e;
   a.states = shared_states(d, ws);
+  a.unit_rows = unit_rows(d, ws);
   a.pieces = shared_pieces(d, ws);
-  a.arrive = shared_arrive(d, ws);
-  // chunks of the rows behind the prefix: enough for some waves of CTAs, as many as half of the
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.err = err_word(ws);
+  // chunks of the rows behind the prefix, a warp each: some waves of warps, at most half of the
   // states in the workspace
-  const DecodeShape shape = decode_shape_shared(d->head_dim, group, mode);
+  int warps = 0;
+  if (shared_rest_warps(d->head_dim, group, mask, &warps) != cudaSuccess) return DSA_ERR_CUDA;
   const int slots = a.states.in_part + kSharedExtra;
   const int64_t units = static_cast<int64_t>(d->batch) * d->hkv;
-  const int64_t target = static_cast<int64_t>(sm_count()) * shape.ctas_per_sm *
-                         (mode == kModeDense ? kSharedDenseWaves : kSharedMaskWaves);
-  int64_t parts = target / units;
+  int64_t parts = static_cast<int64_t>(sm_count()) * warps *
+                  (mask ? kSharedMaskWaves : kSharedDenseWaves) / (units * 2);
   if (parts > slots / 2) parts = slots / 2;
   if (parts < 1) parts = 1;
   const int64_t rows = sh->max_suffix > 1 ? sh->max_suffix : 1;
-  const int64_t quantum = shape.rows_per_pass;
-  a.chunk = static_cast<int32_t>(ceil_div(ceil_div(rows, parts), quantum) * quantum);
+  a.chunk = static_cast<int32_t>(ceil_div(ceil_div(rows, parts), kSharedChunk) * kSharedChunk);
   a.num_chunks = static_cast<int32_t>(ceil_div(rows, a.chunk));
   a.prefix_slots = slots - a.num_chunks;
+  a.deep = units * a.num_chunks <= static_cast<int64_t>(sm_count()) * 8;
+  if (units * a.num_chunks > INT32_MAX || static_cast<int64_t>(d->batch) * d->hq > INT32_MAX)
+    return DSA_ERR_UNSUPPORTED;
   if (a.early != 0) {
     SharedLaunch p{};
-    p.q = static_cast<const uint16_t*>(q);
+    p.q = a.q;
     p.k = k;
     p.v = v;
     p.page_table = page_table;
@@ -118,7 +118,7 @@ dsa_status decode_shared(const dsa_dims* d, int mode, const dsa_shared_prefix* s
     p.sms = sm_count();
     if (launch_shared_prefix(p, s) != cudaSuccess) return DSA_ERR_CUDA;
   }
-  return from_cuda(launch_decode_shared(a, mode, s));
+  return from_cuda(launch_shared_rest(a, mask, s));
 }
 
 }  // namespace
@@ -132,7 +132,7 @@ dsa_status dsa_decode_dense_shared(const dsa_dims* dims, const dsa_shared_prefix
                                    const void* q, const void* k_pages, const void* v_pages,
                                    const int32_t* page_table, const int32_t* seq_len, float scale,
                                    void* out, float* lse, void* ws, void* stream) {
-  return decode_shared(dims, kModeDense, shared, q, k_pages, v_pages, page_table, seq_len, nullptr,
+  return decode_shared(dims, false, shared, q, k_pages, v_pages, page_table, seq_len, nullptr,
                        nullptr, nullptr, scale, out, lse, ws, stream);
 }
 
@@ -142,7 +142,7 @@ dsa_status dsa_decode_sparse_masked_shared(const dsa_dims* dims, const dsa_share
                                            const int32_t* prompt_len, const int32_t* window,
                                            const uint32_t* keep_mask, float scale, void* out,
                                            float* lse, void* ws, void* stream) {
-  return decode_shared(dims, kModeMask, shared, q, k_pages, v_pages, page_table, seq_len, prompt_len,
+  return decode_shared(dims, true, shared, q, k_pages, v_pages, page_table, seq_len, prompt_len,
                        window, keep_mask, scale, out, lse, ws, stream);
 }
 

@@ -94,7 +94,8 @@ struct WarpQ {
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
         qf[kk][0] = g4 < G ? (CG ? __ldcg(q32 + kk * 8 + tig) : __ldg(q32 + kk * 8 + tig)) : 0u;
-        qf[kk][1] = g4 < G ? (CG ? __ldcg(q32 + kk * 8 + 4 + tig) : __ldg(q32 + kk * 8 + 4 + tig)) : 0u;
+        qf[kk][1] =
+            g4 < G ? (CG ? __ldcg(q32 + kk * 8 + 4 + tig) : __ldg(q32 + kk * 8 + 4 + tig)) : 0u;
       }
     } else {
       const int jl = lane & 7;
@@ -387,8 +388,8 @@ struct WarpAttn {
   }
 
   // The warp's state as G x [acc(D), m, l] floats at mw (shared or global
-  // memory): the lanes' partial sums are combined first.
-  __device__ __forceinline__ void flush(float* mw, int lane) {
+  // memory), head h at mw + h * apart: the lanes' partial sums are combined first.
+  __device__ __forceinline__ void flush(float* mw, int lane, int64_t apart = D + 2) {
     if constexpr (kMMA) {
       const int g4 = lane >> 2, tig = lane & 3;
 #pragma unroll
@@ -401,12 +402,12 @@ struct WarpAttn {
         if (h < G) {
 #pragma unroll
           for (int mt = 0; mt < NK; ++mt) {
-            mw[h * (D + 2) + mt * 16 + g4] = oacc[mt][j];
-            mw[h * (D + 2) + mt * 16 + g4 + 8] = oacc[mt][j + 2];
+            mw[h * apart + mt * 16 + g4] = oacc[mt][j];
+            mw[h * apart + mt * 16 + g4 + 8] = oacc[mt][j + 2];
           }
           if (g4 == 0) {
-            mw[h * (D + 2) + D] = m2[j];
-            mw[h * (D + 2) + D + 1] = l;
+            mw[h * apart + D] = m2[j];
+            mw[h * apart + D + 1] = l;
           }
         }
       }
@@ -426,11 +427,11 @@ struct WarpAttn {
 #pragma unroll
           for (int u = 0; u < kNV; ++u)
 #pragma unroll
-            for (int w = 0; w < kVE; ++w) mw[h * (D + 2) + elem(u, jl, w)] = acc[h][u * kVE + w];
+            for (int w = 0; w < kVE; ++w) mw[h * apart + elem(u, jl, w)] = acc[h][u * kVE + w];
         }
         if (lane == 0) {
-          mw[h * (D + 2) + D] = m_run[h];
-          mw[h * (D + 2) + D + 1] = l;
+          mw[h * apart + D] = m_run[h];
+          mw[h * apart + D + 1] = l;
         }
       }
     }
