@@ -6,10 +6,10 @@
 //   need_b = ceil(L_b / 16) - ceil((L_b - n_b) / 16),
 // and the k-th page needed, requests in order, is free_pages[count - 1 - k].  Everything is a
 // prefix sum over the requests, so the result does not depend on the order of CTAs.  Each CTA
-// takes 512 of the packed rows; it sums over all requests itself (a thousand take two passes of
-// its threads), which costs less than a second launch, and notes the requests that start in
-// its rows; a running maximum over the rows then gives each row its request.  Bound by the
-// chain of dependent loads: lengths, sums, page id, slot.
+// takes 512 of the packed rows; it sums over all requests itself, which costs less than a
+// second launch, and notes the requests that start in its rows; a running maximum over the rows
+// then gives each row its request.  Bound by the chain of dependent loads: lengths, sums, page
+// id, slot.
 //
 // write_kernel.  A copy bound by HBM; the rows do not wait for their slots, both are loaded
 // together.
@@ -57,60 +57,71 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignLaun
   owner[tid] = -1;
   if (tid == 0) taken = 0;
   __syncthreads();
-  int64_t rows_before = 0, pages_before = 0;  // of the requests of earlier passes
-  for (int b0 = 0; b0 < a.batch; b0 += kAssignThreads) {
-    const int b = b0 + tid;
-    int L = 0, n = 0;
-    if (b < a.batch) {
-      L = a.seq_len[b];
-      n = a.new_len != nullptr ? a.new_len[b] : 1;
-      int code = 0;
-      if (L < 1 || L > a.max_pages * kPage) code = DSA_DEV_BAD_SEQ_LEN;
-      else if (n < 0 || n > L) code = DSA_DEV_BAD_QLEN;
-      if (code != 0) {
-        if (first_cta) set_error(a.err, code);
-        n = 0;
-        L = 0;
-      }
+  // Every thread has some requests side by side: their sums, the sums before them, then each
+  // of them again (its lengths are in the SM's cache by then).
+  const int per = (a.batch + kAssignThreads - 1) / kAssignThreads;
+  const int first_b = tid * per, end_b = min(a.batch, first_b + per);
+  struct Request {
+    int L, n, first, need;  // rows, new ones; first fresh page, fresh pages
+  };
+  auto request = [&](int b, bool report) -> Request {
+    Request r{__ldg(a.seq_len + b), a.new_len != nullptr ? __ldg(a.new_len + b) : 1, 0, 0};
+    int code = 0;
+    if (r.L < 1 || r.L > a.max_pages * kPage) code = DSA_DEV_BAD_SEQ_LEN;
+    else if (r.n < 0 || r.n > r.L) code = DSA_DEV_BAD_QLEN;
+    if (code != 0) {
+      if (report) set_error(a.err, code);
+      r.L = r.n = 0;
     }
-    const int first = (L - n + kPage - 1) / kPage;
-    const int need = (L + kPage - 1) / kPage - first;
-    int64_t rows = warp_scan(n, lane), pages = warp_scan(need, lane);
-    if (lane == 31) {
-      rows_of[warp] = rows;
-      pages_of[warp] = pages;
-    }
-    __syncthreads();
-    int64_t all_rows = 0, all_pages = 0;
+    r.first = (r.L - r.n + kPage - 1) / kPage;
+    r.need = (r.L + kPage - 1) / kPage - r.first;
+    return r;
+  };
+  int64_t rows = 0, pages = 0;
+#pragma unroll 4
+  for (int b = first_b; b < end_b; ++b) {
+    const Request r = request(b, first_cta);
+    rows += r.n;
+    pages += r.need;
+  }
+  const int64_t own_rows = rows, own_pages = pages;
+  rows = warp_scan(rows, lane);
+  pages = warp_scan(pages, lane);
+  if (lane == 31) {
+    rows_of[warp] = rows;
+    pages_of[warp] = pages;
+  }
+  __syncthreads();
+  int64_t total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        rows += rows_of[w];
-        pages += pages_of[w];
-      }
-      all_rows += rows_of[w];
-      all_pages += pages_of[w];
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      rows += rows_of[w];
+      pages += pages_of[w];
     }
-    rows += rows_before - n;  // before this request
-    pages += pages_before - need;
-    if (b < a.batch && first_cta && a.token_start != nullptr)
+    total += rows_of[w];
+  }
+  rows -= own_rows;  // before this thread's requests
+  pages -= own_pages;
+  for (int b = first_b; b < end_b; ++b) {
+    const Request r = request(b, false);
+    if (first_cta && a.token_start != nullptr)
       a.token_start[b] = static_cast<int32_t>(rows < INT32_MAX ? rows : INT32_MAX);
-    const bool served = need == 0 || pages + need <= count;
-    if (need > 0 && served) atomicMax(&taken, static_cast<int32_t>(pages + need));
+    const bool served = r.need == 0 || pages + r.need <= count;
+    if (r.need > 0 && served) atomicMax(&taken, static_cast<int32_t>(pages + r.need));
     if (!served && first_cta) set_error(a.err, DSA_DEV_FREE_LIST_EMPTY);
     // the request's first row in this tile, if it has one
     const int64_t at = rows > t0 ? rows : t0;
-    if (n > 0 && at < t0 + kAssignThreads && at < rows + n) {
+    if (r.n > 0 && at < t0 + kAssignThreads && at < rows + r.n) {
       const int x = static_cast<int>(at - t0);
-      req[x] = TileRequest{b, static_cast<int32_t>(L - n + (at - rows)), first, served,
-                           served && need > 0 ? count - 1 - static_cast<int32_t>(pages) : 0};
+      req[x] = TileRequest{b, static_cast<int32_t>(r.L - r.n + (at - rows)), r.first, served,
+                           served && r.need > 0 ? count - 1 - static_cast<int32_t>(pages) : 0};
       owner[x] = x;
     }
-    rows_before += all_rows;
-    pages_before += all_pages;
-    __syncthreads();  // the warps' sums are used again
+    rows += r.n;
+    pages += r.need;
   }
-  const int64_t total = rows_before;
+  __syncthreads();
   const bool fits = total <= a.max_tokens;
   if (first_cta && tid == 0) {
     if (a.token_start != nullptr)

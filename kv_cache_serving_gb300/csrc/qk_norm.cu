@@ -12,10 +12,13 @@
 // squares are subnormal) is scaled by a power of two first.
 //
 // Bound by HBM: each element is read and written once, as without the norm (rope.cu).  What
-// stands in the way is issue: some 130 instructions per 16 elements with two fp32 per
-// instruction.  So a thread keeps its place in a head, and with it weight and bias in
-// registers, over the tokens of its CTA, and has the next token's elements on their way while
-// it computes.
+// stands in the way is issue and the latency of loads with few warps (96 registers): a thread
+// keeps its place in a head, and with it weight and bias in registers, over the tokens of its
+// CTA, computes on two fp32 at once, has the next two tokens' elements on their way and asks
+// the L2 for those of the fourth.  Measured: q and k of 65 K tokens, 32/8 heads of 128, bf16,
+// mean, weight and bias of every head's own, 225 us (0.87 of the copy rate): 370 us with a
+// thread's place changing from head to head, 252 without the L2's part; 8 elements per thread
+// instead of 16 took 298 us, 80 registers (more warps, spills) 293.
 #include <math.h>
 
 #include "common.cuh"
@@ -28,7 +31,8 @@ namespace dsa {
 namespace {
 
 constexpr int kNormThreads = 512;  // at most
-constexpr int kNormTurns = 8;      // tokens of a thread at most
+constexpr int kNormTurns = 16;     // tokens of a thread at most
+constexpr int kNormPrefetch = 4;   // tokens ahead that the L2 is asked for
 
 // Sum over the kGroups lanes of a head (the whole warp takes part).
 template <int kGroups>
@@ -214,6 +218,12 @@ __global__ void __maxnreg__(96) qk_norm_kernel(const __grid_constant__ NormLaunc
     for (int y = 1; y < kAhead; ++y) next[y - 1] = next[y];
     if (live && t + kAhead * a.subs < nt)
       next[kAhead - 1].load(in + kAhead * in_step, D / 2 * kElt);
+    // the lines of the head a few tokens on into the L2
+    if (l == 0 && live && t0 + t + kNormPrefetch * a.subs < a.rope.tokens) {
+#pragma unroll
+      for (int y = 0; y < D * kElt; y += 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(in + kNormPrefetch * in_step + y));
+    }
     float eps = a.eps;
     float ms = centre<kGroups>(x, layer);
     // squares that overflow, or are too small to be exact: once more, scaled by a power of two
@@ -272,7 +282,7 @@ cudaError_t launch_one(NormLaunch a, int sms, cudaStream_t s) {
   const int tokens = a.rope.tokens;
   a.subs = 256 / a.lanes > 1 ? 256 / a.lanes : 1;
   // Tokens of a CTA: weights are loaded and the table's latency is waited for once, so as many as
-  // leave some CTAs for every SM, at most 8 in turn.
+  // leave some CTAs for every SM, at most 16 in turn.
   int turns = static_cast<int>(tokens / (static_cast<int64_t>(a.subs) * sms * 8));
   turns = turns < 1 ? 1 : turns > kNormTurns ? kNormTurns : turns;
   a.tile = a.subs * turns;

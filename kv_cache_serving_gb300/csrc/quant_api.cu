@@ -2,6 +2,7 @@
 // positions (declared in dsa.h): host-side checks and dispatch.
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include <cuda_runtime.h>
 
@@ -113,10 +114,12 @@ dsa_status rows_common(const dsa_dims* d, const dsa_quant_cache* c, int32_t max_
 // the double's whole mantissa times 1 / (2 pi) to 128 bits, so that a position of 31 bits times
 // the result is still good to 2^-34 turns.
 uint64_t turns_of(double f) {
-  if (f == 0.0) return 0;
   using u128 = unsigned __int128;
-  int e;
-  const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(f, &e), 53));  // f = m 2^(e - 53)
+  uint64_t bits;
+  std::memcpy(&bits, &f, sizeof bits);
+  if ((bits >> 52) == 0) return 0;  // 0, or a subnormal: no turn at any position
+  const int e = static_cast<int>(bits >> 52) - 1022;
+  const uint64_t m = (bits & ((1ull << 52) - 1)) | (1ull << 52);  // f = m 2^(e - 53)
   // 2^130 / (2 pi), rounded down
   constexpr uint64_t hi = 0xa2f9836e4e441529ull, lo = 0xfc2757d1f534ddc0ull;
   const u128 p = static_cast<u128>(m) * hi + ((static_cast<u128>(m) * lo) >> 64);  // m / (2 pi) 2^66

@@ -102,13 +102,13 @@ __device__ __forceinline__ Group load_group(const SharedLaunch& a, int g, int32_
   r.n = hi - lo;
   r.rows = rows;
   r.blocks = (rows + kPBlock - 1) / kPBlock;
-  r.tiles = static_cast<int>(((static_cast<int64_t>(r.n) << a.group_log2) + kPRows - 1) / kPRows);
+  r.tiles = ((r.n << a.group_log2) + kPRows - 1) / kPRows;
   return r;
 }
 
 // A CTA's place on the line of blocks.
 struct Cursor {
-  int64_t at, end;  // blocks done and to do, counted over all tiles
+  int at, end;  // blocks done and to do, counted over all tiles
   int g, hk, t, blk;
   Group grp;
 };
@@ -121,10 +121,9 @@ __global__ void __maxnreg__(160)
   using Sh = PrefixShape<D>;
   constexpr int kHalves = Sh::kHalves;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ int64_t scan[kPThreads / 32];
+  __shared__ int32_t scan[kPThreads / 32];
   __shared__ int32_t most_of[kPThreads / 32];
-  __shared__ int64_t found_before;
-  __shared__ int32_t found;
+  __shared__ int32_t found_before, found;
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t failed_word;
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -163,10 +162,8 @@ __global__ void __maxnreg__(160)
 
   // ---- this CTA's piece of the line ----
   // blocks of all tiles of a group, summed over the groups
-  auto units_of = [&](const Group& g) {
-    return static_cast<int64_t>(g.tiles) * g.blocks * a.hkv;
-  };
-  int64_t sum = 0, mine0 = 0;  // mine0: of the first group this thread looks at
+  auto units_of = [&](const Group& g) { return g.tiles * g.blocks * a.hkv; };
+  int sum = 0, mine0 = 0;  // mine0: of the first group this thread looks at
   int most = 0;
   for (int g = tid; g < a.groups; g += kPThreads) {
     const Group r = load_group(a, g, blockIdx.x == 0 ? a.err : nullptr);
@@ -192,26 +189,26 @@ __global__ void __maxnreg__(160)
     most = max(most, most_of[w]);
   }
   // a tile of `most` blocks is touched by at most ceil(most / per) + 1 pieces
-  int64_t per = max((sum + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(1));
-  per = max(per, static_cast<int64_t>((most + a.prefix_slots - 2) / (a.prefix_slots - 1)));
+  const int grid = static_cast<int>(gridDim.x);
+  const int per = max(max((sum + grid - 1) / grid, 1), (most + a.prefix_slots - 2) / (a.prefix_slots - 1));
   Cursor c0;
-  c0.at = per * blockIdx.x;
+  c0.at = min(sum, per * static_cast<int>(blockIdx.x));
   c0.end = min(sum, c0.at + per);
   // the group that holds the first block
-  int64_t before = 0;
+  int before = 0;
   __syncthreads();  // scan is used again
   for (int g0 = 0; g0 < a.groups && c0.at < c0.end; g0 += kPThreads) {
     const int g = g0 + tid;
-    const int64_t u = g0 == 0 ? mine0 : g < a.groups ? units_of(load_group(a, g, nullptr)) : 0;
-    int64_t x = u;
+    const int u = g0 == 0 ? mine0 : g < a.groups ? units_of(load_group(a, g, nullptr)) : 0;
+    int x = u;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, x, s);
+      const int v = __shfl_up_sync(0xffffffffu, x, s);
       if (lane >= s) x += v;
     }
     if (lane == 31) scan[warp] = x;
     __syncthreads();
-    int64_t all = 0;
+    int all = 0;
     x += before;
 #pragma unroll
     for (int w = 0; w < kPThreads / 32; ++w) {
@@ -229,17 +226,15 @@ __global__ void __maxnreg__(160)
   if (work) {
     c0.g = found;
     c0.grp = load_group(a, c0.g, nullptr);
-    int64_t in = c0.at - found_before;
-    const int64_t per_head = static_cast<int64_t>(c0.grp.tiles) * c0.grp.blocks;
-    c0.hk = static_cast<int>(in / per_head);
+    int in = c0.at - found_before;
+    const int per_head = c0.grp.tiles * c0.grp.blocks;
+    c0.hk = in / per_head;
     in -= c0.hk * per_head;
-    c0.t = static_cast<int>(in / c0.grp.blocks);
-    c0.blk = static_cast<int>(in - static_cast<int64_t>(c0.t) * c0.grp.blocks);
+    c0.t = in / c0.grp.blocks;
+    c0.blk = in - c0.t * c0.grp.blocks;
   }
   // Blocks of the cursor's tile that are this CTA's; then on to the next tile.
-  auto blocks_here = [&](const Cursor& c) {
-    return static_cast<int>(min(static_cast<int64_t>(c.grp.blocks - c.blk), c.end - c.at));
-  };
+  auto blocks_here = [&](const Cursor& c) { return min(c.grp.blocks - c.blk, c.end - c.at); };
   auto next_tile = [&](Cursor& c) {
     c.at += blocks_here(c);
     c.blk = 0;
@@ -519,8 +514,8 @@ __global__ void __maxnreg__(160)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // the state of the row, at the number of this piece among those of its tile
-      const int64_t tile_at = c.at - c.blk;
-      const int slot = static_cast<int>(blockIdx.x - tile_at / per);
+      const int tile_at = c.at - c.blk;
+      const int slot = static_cast<int>(blockIdx.x) - tile_at / per;
       if (!idle) {
         tc_fence_after();
         const size_t qh = static_cast<size_t>(b) * a.hq + (c.hk << lg) + (r & ((1 << lg) - 1));
@@ -552,8 +547,7 @@ __global__ void __maxnreg__(160)
         if (mine)
           *reinterpret_cast<float2*>(to + D) = make_float2(same ? ref : __int_as_float(0x7fc00000), l);
         if (mine && slot == 0)
-          a.pieces[qh] =
-              static_cast<int32_t>((tile_at + c.grp.blocks - 1) / per - tile_at / per) + 1;
+          a.pieces[qh] = (tile_at + c.grp.blocks - 1) / per - tile_at / per + 1;
         tc_fence_before();
       }
     }

@@ -57,9 +57,9 @@ __global__ void __launch_bounds__(kRestWarps * 32, 20 / kRestWarps) rest_kernel(
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const uint32_t item = blockIdx.x * kRestWarps + warp;
   const int hk = static_cast<int>(item % a.hkv);
-  const int c = static_cast<int>(item / a.hkv % a.num_chunks);
-  const int b = static_cast<int>(item / a.hkv / a.num_chunks);
-  if (b < a.batch) {
+  const int b = static_cast<int>(item / a.hkv % a.batch);
+  const int c = static_cast<int>(item / a.hkv / a.batch);
+  if (c < a.num_chunks) {
     const int L = __ldcg(a.seq_len + b), S0 = __ldcg(a.prefix_len + b);
     int n = 0, np = 0;
     MaskRows rows;

@@ -94,6 +94,10 @@ dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* 
   if (units * a.num_chunks > INT32_MAX || static_cast<int64_t>(d->batch) * d->hq > INT32_MAX)
     return DSA_ERR_UNSUPPORTED;
   if (a.early != 0) {
+    // the blocks of all tiles are counted in 32 bits
+    const int64_t tiles = sh->groups + (static_cast<int64_t>(d->batch) * group) / kSharedRows;
+    if (tiles * d->hkv * ceil_div(sh->max_prefix, kSharedBlock) > INT32_MAX / 2 || sh->groups == INT32_MAX)
+      return DSA_ERR_UNSUPPORTED;
     SharedLaunch p{};
     p.q = a.q;
     p.k = k;

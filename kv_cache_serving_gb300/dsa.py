@@ -580,12 +580,13 @@ def _norm(dims, norm, dev):
     if norm.__class__ is not dsa_qk_norm:
         raise TypeError("norm must be a dsa_qk_norm (see make_qk_norm)")
     facts = getattr(norm, "facts", None)  # of the tensors it was made over
-    if facts is not None:
+    if facts is not None and getattr(norm, "fits", None) != (dev, dims.hq, dims.hkv, dims.head_dim):
         if facts[0] != dev:
             raise ValueError(f"norm is on cuda:{facts[0]}, current device cuda:{dev}")
         hd = dims.head_dim
         for t, heads in zip(norm.tensors, (dims.hq, dims.hkv, dims.hq, dims.hkv)):
             _shape(t, (hd,) if facts[1] == 1 else (heads, hd), "a norm vector")
+        norm.fits = (dev, dims.hq, dims.hkv, hd)
     return norm
 
 
