@@ -48,6 +48,13 @@ dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* 
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int group = d->hq / d->hkv;
+  // blocks of all tiles of the prefixes, and chunks of the rows behind them, are counted in 32 bits
+  const int64_t units = static_cast<int64_t>(d->batch) * d->hkv;
+  const int64_t tiles = sh->groups + (static_cast<int64_t>(d->batch) * group) / kSharedRows;
+  if (sh->groups == INT32_MAX || units * kSharedStates > INT32_MAX || units * group > INT32_MAX ||
+      (sh->max_prefix > 0 &&
+       ceil_div(sh->max_prefix, kSharedBlock) > INT32_MAX / 2 / (tiles * d->hkv)))
+    return DSA_ERR_UNSUPPORTED;
   RestLaunch a{};
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
@@ -81,7 +88,6 @@ dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* 
   int warps = 0;
   if (shared_rest_warps(d->head_dim, group, mask, &warps) != cudaSuccess) return DSA_ERR_CUDA;
   const int slots = a.states.in_part + kSharedExtra;
-  const int64_t units = static_cast<int64_t>(d->batch) * d->hkv;
   int64_t parts = static_cast<int64_t>(sm_count()) * warps *
                   (mask ? kSharedMaskWaves : kSharedDenseWaves) / (units * 2);
   if (parts > slots / 2) parts = slots / 2;
@@ -91,13 +97,7 @@ dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* 
   a.num_chunks = static_cast<int32_t>(ceil_div(rows, a.chunk));
   a.prefix_slots = slots - a.num_chunks;
   a.deep = units * a.num_chunks <= static_cast<int64_t>(sm_count()) * 8;
-  if (units * a.num_chunks > INT32_MAX || static_cast<int64_t>(d->batch) * d->hq > INT32_MAX)
-    return DSA_ERR_UNSUPPORTED;
   if (a.early != 0) {
-    // the blocks of all tiles are counted in 32 bits
-    const int64_t tiles = sh->groups + (static_cast<int64_t>(d->batch) * group) / kSharedRows;
-    if (tiles * d->hkv * ceil_div(sh->max_prefix, kSharedBlock) > INT32_MAX / 2 || sh->groups == INT32_MAX)
-      return DSA_ERR_UNSUPPORTED;
     SharedLaunch p{};
     p.q = a.q;
     p.k = k;

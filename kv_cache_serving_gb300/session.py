@@ -58,6 +58,34 @@ def page_rows(page_table, seq_len, num_pages) -> np.ndarray:
     return rows
 
 
+def shared_groups(page_table, seq_len):
+    """(group_start, prefix_len) for DecodeBatch.share_prefix from host arrays: runs of neighbouring
+    requests whose tables begin with the same whole pages.  A request joins the group before it
+    when it has at least half of that group's common rows in common with it (so one that shares a
+    few rows does not cost a group its long prefix)."""
+    table, L = np.asarray(page_table), np.asarray(seq_len, dtype=np.int64)
+    B = len(L)
+    start, common = [0] if B else [], []
+    for b in range(B):
+        whole = int(L[b]) // dsa.PAGE
+        if b == 0:
+            common.append(whole)
+            continue
+        first, most = start[-1], min(common[-1], whole)
+        same = (table[b, :most] == table[first, :most]) & (table[b, :most] >= 0)
+        n = most if same.all() else int(np.argmin(same))
+        if n > 0 and (b - first == 1 or 2 * n >= common[-1]):
+            common[-1] = n
+        else:
+            start.append(b)
+            common.append(whole)
+    start = np.array(start + [B], dtype=np.int32)
+    size = np.diff(start)
+    # a request alone shares nothing
+    rows = np.where(size > 1, dsa.PAGE * np.array(common, dtype=np.int64), 0) if B else np.zeros(0, np.int64)
+    return start, np.repeat(rows, size).astype(np.int32)
+
+
 class PackedIO:
     """One pinned host buffer and one device buffer per direction, so that a
     step's inputs go up in one copy and its results come back in one.  The
@@ -149,6 +177,7 @@ class DecodeBatch:
         for name in ("q", "page_table", "seq_len", "prompt_len", "window", "grid_w", "keep_mask",
                      "kept_idx", "kept_cnt", "out", "lse", "ws"):
             setattr(other, name, getattr(self, name).clone())
+        other.out_q = None
         other._host_lengths = tuple(x.copy() for x in self._host_lengths)
         return other
 
@@ -251,6 +280,47 @@ class DecodeBatch:
                              self.seq_len, self.scale, out, lse, self.ws, stream)
         return out, lse
 
+    def share_prefix(self, group_start, prefix_len, max_suffix=None, max_prefix=None):
+        """dsa_shared_prefix for the *_shared calls from host arrays (see shared_groups): the requests
+        group_start[g] .. group_start[g+1] - 1 have their first prefix_len rows in common.  The bounds
+        default to those of the batch's lengths as they were given; a batch that goes on growing
+        passes its own."""
+        group_start, prefix_len = (np.asarray(x, dtype=np.int32) for x in (group_start, prefix_len))
+        if max_suffix is None:
+            max_suffix = int((self._host_lengths[0] - prefix_len).max(initial=0))
+        if max_prefix is None:
+            max_prefix = int(prefix_len.max(initial=0))
+        return dsa.shared_prefix(_i32(group_start, self.device), _i32(prefix_len, self.device), max_prefix,
+                                 max_suffix)
+
+    def _out_of_q(self, out):
+        """Where a call whose out has q's type writes it."""
+        if out is not None:
+            return out
+        if getattr(self, "out_q", None) is None or self.out_q.dtype is not self.q.dtype:
+            self.out_q = torch.empty_like(self.q)
+        return self.out_q
+
+    def decode_dense_shared(self, shared, out=None, lse=None, stream=None):
+        """decode_dense, a shared prefix once for its group; out has q's type (bf16)."""
+        out, lse = self._out_of_q(out), self.lse if lse is None else lse
+        dsa.dsa_decode_dense_shared(self.dims, shared, self.q, self.k_pages, self.v_pages, self.page_table,
+                                    self.seq_len, self.scale, out, lse, self.ws, stream)
+        return out, lse
+
+    def decode_sparse_masked_shared(self, shared, out=None, lse=None, stream=None):
+        """decode_sparse_masked, a shared prefix of the prompts once for its group; out has q's
+        type (bf16)."""
+        out, lse = self._out_of_q(out), self.lse if lse is None else lse
+        dsa.dsa_decode_sparse_masked_shared(self.dims, shared, self.q, self.k_pages, self.v_pages,
+                                            self.page_table, self.seq_len, self.prompt_len, self.window,
+                                            self.keep_mask, self.scale, out, lse, self.ws, stream)
+        return out, lse
+
+    def write_rows(self, row_slot, k, v, stream=None):
+        """Store rows k and v [tokens, hkv, d] at their slots (PagePool.assign)."""
+        dsa.dsa_write_rows(self.dims, row_slot, k, v, self.k_pages, self.v_pages, self.ws, stream)
+
     def attention_mass(self, r_local=2, r_diag=2, with_offsets=True, stream=None):
         mass = torch.empty((self.batch, self.hq, 4), dtype=torch.float32, device=self.device)
         om = None
@@ -267,6 +337,36 @@ class DecodeBatch:
 
     def check(self, what="libdsa"):
         dsa.check_device_error(self.ws, what)
+
+
+class PagePool:
+    """The free pages of a cache, on the GPU: eviction appends to the list, new rows take their
+    pages from its end."""
+
+    def __init__(self, num_pages, used=(), device="cuda"):
+        free = np.setdiff1d(np.arange(num_pages), np.asarray(used, dtype=np.int64))[::-1]
+        self.free = torch.full((max(num_pages, 1),), -1, dtype=torch.int32, device=device)
+        self.free[:len(free)] = _i32(free, self.free.device)
+        self.count = torch.full((1,), len(free), dtype=torch.int32, device=device)
+
+    def assign(self, batch: DecodeBatch, new_len=None, max_tokens=None, stream=None):
+        """Pages for the last new_len[b] rows of the batch's requests (its seq_len counts them; None:
+        one row each) into its page table.  Returns (token_start, row_slot, row_pos): the packed new
+        rows' slots and positions; max_tokens places (default: the sum of new_len, which reads it
+        back)."""
+        dev = batch.device
+        if max_tokens is None:
+            max_tokens = batch.batch if new_len is None else int(new_len.sum())
+        start = torch.empty(batch.batch + 1, dtype=torch.int32, device=dev)
+        slot, pos = (torch.empty(max_tokens, dtype=torch.int32, device=dev) for _ in range(2))
+        dsa.dsa_assign_pages(batch.dims, batch.seq_len, new_len, self.free, self.count, self.count,
+                             batch.page_table, start, slot, pos, batch.ws, stream)
+        return start, slot, pos
+
+    def evict(self, batch: DecodeBatch, stream=None):
+        """Take back the pages that no later step of the batch reads."""
+        dsa.dsa_evict_pages(batch.dims, batch.seq_len, batch.prompt_len, batch.window, batch.page_table,
+                            self.free, self.count, batch.ws, stream)
 
 
 class QuantBatch:

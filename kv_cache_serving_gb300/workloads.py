@@ -235,6 +235,45 @@ def generate(cfg: Config, seed: int | None = None, device: str = "cpu",
     return out
 
 
+def share_prompts(w: dict, sizes) -> dict:
+    """A batch in which groups of sizes[g] neighbouring requests share their prompt: the prompt of
+    the group's first request, followed by each request's own rows (as many as it had behind its
+    own prompt).  The prompt's whole pages are the same pages of the pool; a page that ends inside
+    it is each request's own, with a copy of the prompt's rows.  Adds group_start [groups + 1] and
+    prefix_len [B]; the pool, and with it k_pages and v_pages, keep their size."""
+    B, table = w["batch"], w["page_table"]
+    if sum(sizes) != B or min(sizes) < 1:
+        raise ValueError(f"share_prompts: sizes {list(sizes)} for {B} requests")
+    start = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    P = np.repeat(w["prompt_len"][start[:-1]], sizes).astype(np.int32)
+    L = (P + w["seq_len"] - w["prompt_len"]).astype(np.int32)
+    ids = np.random.default_rng(w["seed"] + 1).permutation(w["num_pages"])
+    k, v = w["k_pages"].clone(), w["v_pages"].clone()
+    at, rows = 0, []
+    for g, n in enumerate(sizes):
+        whole, part = divmod(int(P[start[g]]), PAGE)
+        shared = ids[at:at + whole]
+        at += whole
+        for b in range(start[g], start[g] + n):
+            own = -(-int(L[b]) // PAGE) - whole
+            if at + own > len(ids):
+                raise ValueError("share_prompts: the pool is too small (generate with spare_pages)")
+            rows.append(np.concatenate([shared, ids[at:at + own]]))
+            if part and b > start[g]:
+                first = int(rows[start[g]][whole])
+                for t in (k, v):
+                    t[int(ids[at]), :part] = t[first, :part]
+            at += own
+    out = dict(w, prompt_len=P, seq_len=L, k_pages=k, v_pages=v, group_start=start, prefix_len=P.copy())
+    width = max(table.shape[1], max(len(r) for r in rows))
+    out["page_table"] = np.full((B, width), -1, dtype=np.int32)
+    for b, r in enumerate(rows):
+        out["page_table"][b, :len(r)] = r
+    out["max_pages"] = width
+    out["max_kept"] = int(np.minimum(L, P + w["window"] + 1).max())
+    return out
+
+
 def poison_unread(inp: dict, kept_rows_of, value: float = float("nan")) -> dict:
     """A copy of inp whose K/V rows outside `kept_rows_of(b, hk)` (and every
     slot no request uses) are set to `value`.  kept_rows_of returns the logical

@@ -208,6 +208,15 @@ def test_one_request_one_row():
     bt.check(*bt.run())
 
 
+def test_nothing_shared():
+    """max_prefix 0: no groups have to be given."""
+    bt = Batch([1] * 5, [0] * 5, [40, 1, 130, 7, 16], 2, 4, 64, seed=3)
+    none = dsa.shared_prefix(i32([0]), bt.pre, 0, 130)
+    assert none.groups == 0
+    bt.check(*bt.run(none))
+    assert dsa.dsa_get_device_error(bt.ws) == 0
+
+
 def test_many_groups():
     """More groups than a CTA has threads, most of a request or two."""
     rng = np.random.default_rng(3)
