@@ -181,11 +181,8 @@ inline size_t shared_piece_bytes(const dsa_dims* d) {
 inline int32_t* shared_pieces(const dsa_dims* d, void* ws) {
   return multi_count_region(d, ws) + kMultiCounters;
 }
-inline SharedStates shared_states(const dsa_dims* d, void* ws) {
-  return SharedStates{partials(ws),
-                      reinterpret_cast<float*>(shared_pieces(d, ws) + shared_piece_bytes(d) / sizeof(int32_t)),
-                      shared_in_part(d), d->head_dim + 4,
-                      static_cast<int64_t>(d->batch) * d->hq};
+inline float* shared_extra(const dsa_dims* d, void* ws) {
+  return reinterpret_cast<float*>(shared_pieces(d, ws) + shared_piece_bytes(d) / sizeof(int32_t));
 }
 inline size_t shared_bytes(const dsa_dims* d) {
   return shared_piece_bytes(d) + round_up(static_cast<size_t>(d->batch) * d->hq * kSharedExtra *

@@ -16,24 +16,17 @@ constexpr int kMaxCluster = 8;
 constexpr int kChunkQuantum = 64;  // chunk sizes are multiples of this
 
 // States (acc[head_dim], reference, sum, padding) that the calls over a shared prefix leave in the
-// workspace: slots 0 .. in_part - 1 in the partials region, kSharedExtra more behind it, the
-// states of one slot side by side (few slots are used, so those read lie together).  The first
-// prefix_slots are the prefix's, the others those of chunks.
+// workspace: those of the prefix's pieces and those of chunks, of one (request, query head)
+// `apart` floats from each other (few of them are used, so those read lie together).  They lie in
+// the partials region, or, where that holds fewer than four of them, in kSharedExtra of their own.
 constexpr int kSharedExtra = 3;
-constexpr int kSharedStates = kMaxChunks + kSharedExtra;  // of a (request, query head), at most
 constexpr int kSharedRows = 128, kSharedBlock = 128;  // query rows of a tile, cache rows of a block
 struct SharedStates {
-  float* part;
-  float* extra;
-  int32_t in_part, floats;  // floats of a state: head_dim + 4
-  int64_t heads;            // batch * hq
+  float* pieces;
+  float* chunks;
+  int64_t apart;
+  int32_t floats;  // of a state: head_dim + 4
 };
-#ifdef __CUDACC__
-__device__ __forceinline__ float* shared_state(const SharedStates& s, size_t qh, int slot) {
-  return slot < s.in_part ? s.part + (slot * s.heads + qh) * s.floats
-                          : s.extra + ((slot - s.in_part) * s.heads + qh) * s.floats;
-}
-#endif
 
 struct DecodeLaunch {
   const void* q;
@@ -83,7 +76,7 @@ struct RestLaunch {
   int32_t chunk, num_chunks;  // rows of a chunk, chunks of a unit at most
   int32_t early;              // behind a prefix kernel
   int32_t deep;               // few warps: more of a warp's rows on their way at a time
-  int32_t prefix_slots;       // states 0 .. prefix_slots - 1 are the prefix's
+  int32_t prefix_slots;       // states that the pieces of a prefix have room for
   float scale_log2;
   SharedStates states;
   int32_t* unit_rows;         // [batch][hkv] rows behind the prefix, or -error

@@ -5,7 +5,7 @@
 // Q of n * (hq / hkv) rows, and the prefix part of their attention is
 //   S = Q K^T,   P = 2^(scale log2(e) S - ref),   acc = P V,   l = sum P,
 // one pass over the prefix with a running reference per query row.  The state (acc, ref, l) of
-// each row goes to the workspace; decode.cuh's kernel adds the request's other rows and joins the
+// each row goes to the workspace; shared_rest.cu takes the request's other rows and joins the
 // states.
 //
 // A tile is 128 query rows of one (group, kv head); a block is 128 cache rows.  All blocks of all
@@ -13,16 +13,27 @@
 // pieces, one per CTA, whatever the groups' sizes: a CTA takes parts of a tile or several tiles,
 // and a tile has as many states as pieces touch it.
 //
-// Seven warps: two load (K, and V; a page's 16 rows of 64 dims per tensor copy, into
-// the swizzled tiles that the products read), one issues the products, four weigh, one query row per thread.  Scores and
-// weights exist twice, so that the scores of a block are made while the one before it is
-// weighed; weights go back to tensor memory over their scores as the left operand of P V.  The
-// reference follows the row's maximum when that passes it by 2^8, so that acc is rarely
-// rescaled.  P is rounded to bf16 (2^-8 of each weight, as V's type asks; the output is rounded to
-// bf16 as well), its sum is taken before.
+// Seven warps: two load (K, and V; a page's 16 rows of 64 dims per tensor copy, into the swizzled
+// tiles that the products read), one issues the products, four weigh, one query row per thread.
+// The queries lie in tensor memory.  Scores and weights exist twice, so that the scores of a
+// block are made while the one before it is weighed; weights go back to tensor memory over their
+// scores as the left operand of P V.  The reference follows the row's maximum when that passes it
+// by 2^8, so that acc is rarely rescaled.  P is rounded to bf16 (2^-8 of each weight, as V's type
+// asks; the output is rounded to bf16 as well), its sum is taken before.
 //
 // All members keep every row of the prefix, so there is no mask; rows of the last page behind the
 // prefix (another request's, or nothing yet) get weight 0 and V rows of zeros.
+//
+// What bounds it: a block takes 1700 cycles to weigh (1024 of them the exponentials) where its
+// products take 1024.  Alone on the GPU its loads keep up; beside the rest kernel, whose warps
+// fill the queues to memory, they are late by about as much again.  Before the first scores there
+// are the groups' two dependent loads, page ids and rows (3 us alone, 8 beside), behind the last
+// block the states of 128 rows (2 us).  Measured, whole calls: 64 requests of 32/8 heads behind
+// 16391 rows 44 us, where this kernel by itself takes 28 (34 while each of sixteen lanes issued
+// its own tensor copies, at 95 cycles a copy).  A CTA leaves room for two CTAs of the rest kernel
+// (160 registers a thread, 145 KB): without, that one starts behind it (128 requests of nine
+// prompts 77 us, 71 with it).  In its place, warps of 8 query rows with mma.sync for groups of few
+// rows: 28 us for 64 images of four prompts where this takes 24.
 #include <cuda.h>
 #include <math.h>
 
@@ -82,14 +93,16 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
 
 struct Group {
   int b0, n, rows, tiles, blocks;  // first request, requests, prefix rows; of one kv head
+  bool sound;                      // its ends lie in order within the batch
 };
 
-// Group g as the arrays say, or one without work.  `err`: where to flag what is wrong, or null.
+// Group g as the arrays say; one that is wrong has no work.  `err`: where to flag it, or null.
 __device__ __forceinline__ Group load_group(const SharedLaunch& a, int g, int32_t* err) {
-  Group r{0, 0, 0, 0, 0};
+  Group r{0, 0, 0, 0, 0, true};
   const int lo = __ldg(a.group_start + g), hi = __ldg(a.group_start + g + 1);
   if (lo < 0 || hi < lo || hi > a.batch || (g == 0 && lo != 0) || (g == a.groups - 1 && hi != a.batch)) {
     if (err != nullptr) set_error(err, DSA_DEV_BAD_GROUP);
+    r.sound = false;
     return r;
   }
   if (hi == lo) return r;
@@ -164,9 +177,10 @@ __global__ void __maxnreg__(160)
   // blocks of all tiles of a group, summed over the groups
   auto units_of = [&](const Group& g) { return g.tiles * g.blocks * a.hkv; };
   int sum = 0, mine0 = 0;  // mine0: of the first group this thread looks at
-  int most = 0;
+  int most = 0, wrong = 0;
   for (int g = tid; g < a.groups; g += kPThreads) {
     const Group r = load_group(a, g, blockIdx.x == 0 ? a.err : nullptr);
+    wrong |= !r.sound;
     sum += units_of(r);
     if (g == tid) mine0 = sum;
     most = max(most, r.blocks);
@@ -180,7 +194,10 @@ __global__ void __maxnreg__(160)
     scan[warp] = sum;
     most_of[warp] = most;
   }
-  __syncthreads();  // barriers and tensor-memory address too
+  // Groups that do not rise from 0 to the batch may overlap and be more than the host has counted
+  // with: then no prefix is computed at all.  (The barrier is that of the mbarriers and of the
+  // tensor-memory address too.)
+  wrong = __syncthreads_or(wrong);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   sum = 0;
 #pragma unroll
@@ -188,6 +205,7 @@ __global__ void __maxnreg__(160)
     sum += scan[w];
     most = max(most, most_of[w]);
   }
+  if (wrong != 0) sum = 0;
   // a tile of `most` blocks is touched by at most ceil(most / per) + 1 pieces
   const int grid = static_cast<int>(gridDim.x);
   const int per = max(max((sum + grid - 1) / grid, 1), (most + a.prefix_slots - 2) / (a.prefix_slots - 1));
@@ -519,7 +537,7 @@ __global__ void __maxnreg__(160)
       if (!idle) {
         tc_fence_after();
         const size_t qh = static_cast<size_t>(b) * a.hq + (c.hk << lg) + (r & ((1 << lg) - 1));
-        float* to = shared_state(a.states, mine ? qh : 0, slot);
+        float* to = a.states.pieces + slot * a.states.apart + (mine ? qh : 0) * a.states.floats;
         // 32 dims of the warp's 32 rows at a time, by way of shared memory (swizzled), so that 8
         // lanes store a row's line: a thread that stores its row alone touches 32 lines with every
         // store

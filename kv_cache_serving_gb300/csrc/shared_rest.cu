@@ -8,9 +8,17 @@
 // The warps of a CTA have neighbouring kv heads of the same rows, which lie side by side in
 // memory and end together.  The kernel runs beside the prefix kernel: it starts as soon as that
 // one's CTAs do, waits for nothing of it, and takes the places that its CTAs leave.
+// What bounds it: HBM while most warps are there (in the middle of 128 requests of nine prompts
+// 6.9 TB/s, 4.4 beside the prefix kernel's 2.3), at both ends the latency of a tile, 1.3 us alone
+// and 2.1 in company, times the tiles of a chunk; an item takes 0.9 us to its lengths and page
+// ids and 2.2 us to its first rows.  Measured: those 128 requests 65 us as a whole (floor 43).
+// CTAs that took a unit, waited for the prefix kernel and joined the states themselves: 77 us;
+// items fetched by warps from a counter: 70; rows in 16-byte copies instead of one each: 73
+// for 73.
 //
 // join_kernel.  A warp per (request, query head): the log-sum-exp sum of the prefix's states and
-// the chunks', in their order, so results do not depend on who was first.
+// the chunks', in their order, so results do not depend on who was first.  Three dependent loads
+// (counts; weights and dims), 3 us for few states and 8 for 18 MB of them.
 #include <math.h>
 
 #include <type_traits>
@@ -208,8 +216,7 @@ __global__ void __launch_bounds__(kRestWarps * 32, 20 / kRestWarps) rest_kernel(
           mbar_wait(kbar + s, 1);
         }
       }
-      float* to = shared_state(a.states, qh0, a.prefix_slots + c);
-      wa.flush(to, lane, shared_state(a.states, qh0 + 1, a.prefix_slots + c) - to);
+      wa.flush(a.states.chunks + c * a.states.apart + qh0 * a.states.floats, lane, a.states.floats);
     }
   }
   // The grid ends behind the prefix kernel, so that whoever waits for it has waited for both.
@@ -217,12 +224,13 @@ __global__ void __launch_bounds__(kRestWarps * 32, 20 / kRestWarps) rest_kernel(
 }
 
 constexpr int kJoinWarps = 4;
-constexpr int kJoinBatch = 16;  // states whose dims are on their way at a time
 
-// A warp joins the states of one (request, query head): lane p weighs state p, all lanes add.
+// A warp joins the states of one (request, query head): lane p weighs piece p and chunk p, all
+// lanes add.  The first states are asked for together with their weights.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const RestLaunch a) {
   constexpr int kDims = D / 32;  // of a lane
+  constexpr int kPieces = 8, kChunks = 6;
   using Vec = typename std::conditional<kDims == 4, float4, float2>::type;
   griddep_wait();
   griddep_launch_dependents();
@@ -245,46 +253,66 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const RestLaunch 
     if (lane == 0) a.pieces[qh] = 0;  // the next call's prefix kernel states it anew
   }
   if (bad) pieces = chunks = 0;
-  // states in order, the prefix's, then the chunks'
-  const int count = pieces + chunks, skip = a.prefix_slots - pieces;
-  auto state = [&](int p) { return shared_state(a.states, qh, p < pieces ? p : p + skip); };
-  static_assert(kSharedStates <= 64, "two states per lane");
-  float2 ml[2];
+  static_assert(kMaxChunks <= 32, "a piece and a chunk per lane");
+  const int64_t apart = a.states.apart;
+  const float* piece = a.states.pieces + static_cast<int64_t>(qh) * a.states.floats;
+  const float* chunk = a.states.chunks + static_cast<int64_t>(qh) * a.states.floats;
+  auto weight_of = [&](const float* s, int count) {
+    return lane < count ? __ldcg(reinterpret_cast<const float2*>(s + lane * apart + D))
+                        : make_float2(-INFINITY, 0.f);
+  };
+  auto dims_of = [&](const float* s, int p) { return __ldcg(reinterpret_cast<const Vec*>(s + p * apart) + lane); };
+  const float2 mp = weight_of(piece, pieces), mc = weight_of(chunk, chunks);
+  Vec vp[kPieces], vc[kChunks];
 #pragma unroll
-  for (int y = 0; y < 2; ++y)
-    ml[y] = lane + 32 * y < count ? __ldcg(reinterpret_cast<const float2*>(state(lane + 32 * y) + D))
-                                  : make_float2(-INFINITY, 0.f);
+  for (int y = 0; y < kPieces; ++y)
+    if (y < pieces) vp[y] = dims_of(piece, y);
+#pragma unroll
+  for (int y = 0; y < kChunks; ++y)
+    if (y < chunks) vc[y] = dims_of(chunk, y);
+  float m = warp_max(fmaxf(mp.x, mc.x));
+  // (a NaN reference, which the maximum passes over, makes its weight NaN)
+  const float sp = mp.x == -INFINITY ? 0.f : exp2f(mp.x - m), sc = mc.x == -INFINITY ? 0.f : exp2f(mc.x - m);
+  float l = warp_sum(fmaf(sp, mp.y, sc * mc.y));
   Vec o{};
-  float sc[2], m = 0.f, l = 0.f;
-  for (int p0 = 0; p0 < count || p0 == 0; p0 += kJoinBatch) {
-    Vec v[kJoinBatch];
-#pragma unroll
-    for (int y = 0; y < kJoinBatch; ++y)
-      if (p0 + y < count) v[y] = __ldcg(reinterpret_cast<const Vec*>(state(p0 + y)) + lane);
-    if (p0 == 0) {
-      m = warp_max(fmaxf(ml[0].x, ml[1].x));
-      // (a NaN reference, which the maximum passes over, makes its weight NaN)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) sc[y] = ml[y].x == -INFINITY ? 0.f : exp2f(ml[y].x - m);
-      l = warp_sum(fmaf(sc[0], ml[0].y, sc[1] * ml[1].y));
+  auto add = [&](const Vec& v, float w) {
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    if constexpr (kDims == 4) {
+      o.z = fmaf(w, v.z, o.z);
+      o.w = fmaf(w, v.w, o.w);
     }
+  };
 #pragma unroll
-    for (int y = 0; y < kJoinBatch; ++y)
-      if (p0 + y < count) {
-        const float w = __shfl_sync(0xffffffffu, p0 + y < 32 ? sc[0] : sc[1], (p0 + y) & 31);
-        o.x = fmaf(w, v[y].x, o.x);
-        o.y = fmaf(w, v[y].y, o.y);
-        if constexpr (kDims == 4) {
-          o.z = fmaf(w, v[y].z, o.z);
-          o.w = fmaf(w, v[y].w, o.w);
-        }
-      }
+  for (int y = 0; y < kPieces; ++y)
+    if (y < pieces) add(vp[y], __shfl_sync(0xffffffffu, sp, y));
+  for (int p = kPieces; p < pieces; p += kPieces) {
+#pragma unroll
+    for (int y = 0; y < kPieces; ++y)
+      if (p + y < pieces) vp[y] = dims_of(piece, p + y);
+#pragma unroll
+    for (int y = 0; y < kPieces; ++y)
+      if (p + y < pieces) add(vp[y], __shfl_sync(0xffffffffu, sp, p + y));
+  }
+#pragma unroll
+  for (int y = 0; y < kChunks; ++y)
+    if (y < chunks) add(vc[y], __shfl_sync(0xffffffffu, sc, y));
+  for (int p = kChunks; p < chunks; p += kChunks) {
+#pragma unroll
+    for (int y = 0; y < kChunks; ++y)
+      if (p + y < chunks) vc[y] = dims_of(chunk, p + y);
+#pragma unroll
+    for (int y = 0; y < kChunks; ++y)
+      if (p + y < chunks) add(vc[y], __shfl_sync(0xffffffffu, sc, p + y));
   }
   if (bad) l = m = __int_as_float(0x7fc00000);
   const float inv = 1.f / l;
   uint32_t* to = reinterpret_cast<uint32_t*>(a.out) + (static_cast<size_t>(qh) * D + kDims * lane) / 2;
-  to[0] = bf16x2_rn(o.x * inv, o.y * inv);
-  if constexpr (kDims == 4) to[1] = bf16x2_rn(o.z * inv, o.w * inv);
+  if constexpr (kDims == 4)
+    *reinterpret_cast<uint2*>(to) =
+        make_uint2(bf16x2_rn(o.x * inv, o.y * inv), bf16x2_rn(o.z * inv, o.w * inv));
+  else
+    to[0] = bf16x2_rn(o.x * inv, o.y * inv);
   if (a.lse != nullptr && lane == 0) a.lse[qh] = (m + log2f(l)) * kLn2;
 }
 

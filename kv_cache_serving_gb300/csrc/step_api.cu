@@ -16,7 +16,11 @@ namespace dsa {
 namespace {
 
 // Half waves of resident warps that the rows behind the prefixes are cut for (the host knows a
-// bound of a request's rows only), and the rows that a chunk is a multiple of.
+// bound of a request's rows only), and the rows that a chunk is a multiple of.  128 requests of
+// nine prompts, 1 .. 1024 own rows: 66 us cut for four half waves, 65 for six, 67 for eight, 69
+// for twelve; half as long chunks in the second half of the bound 64, but 45 instead of 44 for
+// 64 requests of 1 .. 600 own rows.  64 images, 40 kept rows on the average: 26 us for two half
+// waves, 25 for four or six.
 constexpr int kSharedDenseWaves = 6, kSharedMaskWaves = 4, kSharedChunk = 32;
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -51,7 +55,7 @@ dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* 
   // blocks of all tiles of the prefixes, and chunks of the rows behind them, are counted in 32 bits
   const int64_t units = static_cast<int64_t>(d->batch) * d->hkv;
   const int64_t tiles = sh->groups + (static_cast<int64_t>(d->batch) * group) / kSharedRows;
-  if (sh->groups == INT32_MAX || units * kSharedStates > INT32_MAX || units * group > INT32_MAX ||
+  if (sh->groups == INT32_MAX || units * kMaxChunks > INT32_MAX || units * group > INT32_MAX ||
       (sh->max_prefix > 0 &&
        ceil_div(sh->max_prefix, kSharedBlock) > INT32_MAX / 2 / (tiles * d->hkv)))
     return DSA_ERR_UNSUPPORTED;
@@ -77,7 +81,6 @@ dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* 
   a.max_suffix = sh->max_suffix;
   a.early = sh->max_prefix > 0;
   a.scale_log2 = scale * kLog2e;
-  a.states = shared_states(d, ws);
   a.unit_rows = unit_rows(d, ws);
   a.pieces = shared_pieces(d, ws);
   a.out = static_cast<uint16_t*>(out);
@@ -87,15 +90,23 @@ dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* 
   // states in the workspace
   int warps = 0;
   if (shared_rest_warps(d->head_dim, group, mask, &warps) != cudaSuccess) return DSA_ERR_CUDA;
-  const int slots = a.states.in_part + kSharedExtra;
+  // states of a (request, query head): in the partials region where that holds four or more
+  const int in_part = shared_in_part(d);
+  const bool few = in_part < 4;
+  const int slots = few ? kSharedExtra : in_part;
   int64_t parts = static_cast<int64_t>(sm_count()) * warps *
                   (mask ? kSharedMaskWaves : kSharedDenseWaves) / (units * 2);
   if (parts > slots / 2) parts = slots / 2;
   if (parts < 1) parts = 1;
-  const int64_t rows = sh->max_suffix > 1 ? sh->max_suffix : 1;
+  int64_t rows = sh->max_suffix < dense_rows(d) ? sh->max_suffix : dense_rows(d);
+  if (rows < 1) rows = 1;
   a.chunk = static_cast<int32_t>(ceil_div(ceil_div(rows, parts), kSharedChunk) * kSharedChunk);
   a.num_chunks = static_cast<int32_t>(ceil_div(rows, a.chunk));
   a.prefix_slots = slots - a.num_chunks;
+  a.states.floats = d->head_dim + 4;
+  a.states.apart = static_cast<int64_t>(d->batch) * d->hq * a.states.floats;
+  a.states.chunks = few ? shared_extra(d, ws) : partials(ws);
+  a.states.pieces = a.states.chunks + a.num_chunks * a.states.apart;
   a.deep = units * a.num_chunks <= static_cast<int64_t>(sm_count()) * 8;
   if (a.early != 0) {
     SharedLaunch p{};

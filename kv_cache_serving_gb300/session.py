@@ -280,14 +280,15 @@ class DecodeBatch:
                              self.seq_len, self.scale, out, lse, self.ws, stream)
         return out, lse
 
-    def share_prefix(self, group_start, prefix_len, max_suffix=None, max_prefix=None):
+    def share_prefix(self, group_start, prefix_len, max_suffix=None, max_prefix=None, masked=False):
         """dsa_shared_prefix for the *_shared calls from host arrays (see shared_groups): the requests
         group_start[g] .. group_start[g+1] - 1 have their first prefix_len rows in common.  The bounds
-        default to those of the batch's lengths as they were given; a batch that goes on growing
-        passes its own."""
+        default to those of the batch's lengths as they were given (with masked, of the rows that the
+        masked call can keep); a batch that goes on growing passes its own."""
         group_start, prefix_len = (np.asarray(x, dtype=np.int32) for x in (group_start, prefix_len))
         if max_suffix is None:
-            max_suffix = int((self._host_lengths[0] - prefix_len).max(initial=0))
+            rows = estimated_kept_rows(self._host_lengths) if masked else self._host_lengths[0]
+            max_suffix = int((rows - prefix_len).max(initial=0))
         if max_prefix is None:
             max_prefix = int(prefix_len.max(initial=0))
         return dsa.shared_prefix(_i32(group_start, self.device), _i32(prefix_len, self.device), max_prefix,

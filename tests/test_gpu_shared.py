@@ -370,6 +370,27 @@ def test_invalid_groups(starts):
     bt.check(*bt.run())
 
 
+def test_groups_that_overlap():
+    """Many groups that each claim the whole batch, more than any partition could have: no prefix is
+    computed, every request that states one gets NaN."""
+    bt = Batch([1, 60], [0, 640], [30] * 61, 2, 8, 64, seed=9)
+    out, lse = bt.run()
+    claim = dsa.shared_prefix(i32([0, 61] * 700 + [61]), bt.pre, 640, 40)
+    o2, l2 = bt.run(claim)
+    assert dsa.dsa_get_device_error(bt.ws) == 14
+    assert torch.isnan(o2[1:].float()).all() and torch.isnan(l2[1:]).all() and torch.equal(o2[0], out[0])
+    bt.ws.zero_()
+    o2, l2 = bt.run()
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+def test_bounds_far_above():
+    """max_suffix of any size plans for what the tables hold."""
+    bt = Batch([3], [50], [9, 70, 0], 2, 4, 128, seed=10)
+    bt.shared.max_suffix = 2**31 - 1
+    bt.check(*bt.run())
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, steps
 # ---------------------------------------------------------------------------
