@@ -42,7 +42,8 @@
  * kernels are launched as programmatic dependents: a kernel's CTAs may be
  * scheduled while the previous kernel on the stream is still running, but read
  * and write no memory before that kernel has completed, so stream order holds
- * exactly as for plain launches.
+ * exactly as for plain launches.  (Two kernels of one call may run side by side
+ * where neither needs what the other writes.)
  *
  * Errors: calls return a dsa_status and never throw or abort.  Shapes, dtypes,
  * sizes and null pointers are checked on the host before anything is launched
@@ -688,8 +689,7 @@ typedef struct {
  * than max_suffix other rows (DSA_DEV_BAD_PREFIX), or one that no group holds or that states
  * another prefix_len than its group's first (DSA_DEV_BAD_GROUP or _BAD_PREFIX) gets NaN; a
  * group_start that does not rise from 0 to batch sets DSA_DEV_BAD_GROUP.
- * The calls use regions of `ws` that no other call reads; they are ready for the next call
- * unless one set a device error (then zero-fill the workspace again).
+ * Behind every call, one that set a device error as well, `ws` is ready for the next.
  */
 dsa_status dsa_decode_dense_shared(const dsa_dims* dims, const dsa_shared_prefix* shared,
                                    const void* q, const void* k_pages, const void* v_pages,

@@ -170,7 +170,9 @@ inline int32_t* multi_count_region(const dsa_dims* d, void* ws) {
 
 constexpr size_t kMultiCountBytes = kMultiCounters * sizeof(int32_t);
 
-// The calls over a shared prefix, behind the counters: [batch][hq] states of each prefix, then kSharedExtra states of each (request, query head).
+// The calls over a shared prefix.  Their states lie in the partials region; behind the counters
+// are [batch][hq] numbers of prefix states, zero between calls, and kSharedExtra states of each
+// (request, query head) for dims whose partials region does not hold four of them.
 inline int shared_in_part(const dsa_dims* d) {
   const int64_t n_max = dense_rows(d) > d->max_kept ? dense_rows(d) : d->max_kept;
   return chunk_bound(n_max) * (d->head_dim + 2) / (d->head_dim + 4);

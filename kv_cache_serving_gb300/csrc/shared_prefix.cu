@@ -210,7 +210,7 @@ __global__ void __maxnreg__(160)
   const int grid = static_cast<int>(gridDim.x);
   const int per = max(max((sum + grid - 1) / grid, 1), (most + a.prefix_slots - 2) / (a.prefix_slots - 1));
   Cursor c0;
-  c0.at = min(sum, per * static_cast<int>(blockIdx.x));
+  c0.at = static_cast<int>(min(static_cast<int64_t>(sum), static_cast<int64_t>(per) * blockIdx.x));
   c0.end = min(sum, c0.at + per);
   // the group that holds the first block
   int before = 0;

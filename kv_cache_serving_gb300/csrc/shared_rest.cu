@@ -240,17 +240,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const RestLaunch 
   const uint32_t b = qh / a.hq, hk = (qh - b * a.hq) / (static_cast<uint32_t>(a.hq) / a.hkv);
   const int n = __ldcg(a.unit_rows + static_cast<size_t>(b) * a.hkv + hk), S0 = __ldcg(a.prefix_len + b);
   int pieces = __ldcg(a.pieces + qh);
+  if (pieces != 0 && lane == 0) a.pieces[qh] = 0;  // the next call's prefix kernel states it anew
   int chunks = n > 0 ? (n + a.chunk - 1) / a.chunk : 0;
   bool bad = n < 0;
   if (S0 <= 0) {
     pieces = 0;
-  } else {
-    if (!bad && (pieces < 1 || pieces > a.prefix_slots)) {
-      // no group holds this request, or its group's first has another prefix
-      if (lane == 0) set_error(a.err, DSA_DEV_BAD_GROUP);
-      bad = true;
-    }
-    if (lane == 0) a.pieces[qh] = 0;  // the next call's prefix kernel states it anew
+  } else if (!bad && (pieces < 1 || pieces > a.prefix_slots)) {
+    // no group holds this request, or its group's first has another prefix
+    if (lane == 0) set_error(a.err, DSA_DEV_BAD_GROUP);
+    bad = true;
   }
   if (bad) pieces = chunks = 0;
   static_assert(kMaxChunks <= 32, "a piece and a chunk per lane");

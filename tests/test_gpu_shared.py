@@ -370,6 +370,26 @@ def test_invalid_groups(starts):
     bt.check(*bt.run())
 
 
+def test_after_an_invalid_call():
+    """A call that set an error leaves nothing behind: a prefix whose states it computed for a request
+    that did not take it up is not found by the next call, which computes none."""
+    bt = Batch([4, 3], [64, 40], [30] * 7, 2, 4, 128, seed=33)
+    pre, gs = bt.pre.clone(), bt.gs.clone()
+    out, lse = bt.run()
+    bt.pre[5] = 0
+    bt.run(dsa.shared_prefix(bt.gs, bt.pre, 64, 100))
+    assert dsa.dsa_get_device_error(bt.ws) == 15
+    dsa.dsa_clear_device_error(bt.ws)
+    bt.pre.copy_(pre)
+    bt.gs.copy_(i32([0, 8, 7]))
+    o2, _ = bt.run()
+    assert dsa.dsa_get_device_error(bt.ws) == 14 and torch.isnan(o2.float()).all()
+    dsa.dsa_clear_device_error(bt.ws)
+    bt.gs.copy_(gs)
+    o2, l2 = bt.run()
+    assert dsa.dsa_get_device_error(bt.ws) == 0 and torch.equal(o2, out) and torch.equal(l2, lse)
+
+
 def test_groups_that_overlap():
     """Many groups that each claim the whole batch, more than any partition could have: no prefix is
     computed, every request that states one gets NaN."""
