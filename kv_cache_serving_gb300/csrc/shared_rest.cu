@@ -35,6 +35,23 @@ namespace {
 
 constexpr int kRestWarps = 4;
 
+// A row that nobody reads again: first to leave the L2, so that the states and the prefixes stay
+// there until the join and the next step.  128 requests of nine prompts 63 us, without 65; 64
+// images of four prompts 21, without 23.
+__device__ __forceinline__ uint64_t leaves_first() {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void row_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                         uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+
 template <int D, int G, bool DEEP>
 struct RestShape {
   static constexpr bool kMma = G >= 2;
@@ -119,6 +136,7 @@ __global__ void __launch_bounds__(kRestWarps * 32, 20 / kRestWarps) rest_kernel(
       return Place{__ldcg(pt + (j >> 4)), j & (kPage - 1)};
     };
     // K (half 0) or V of tile t on its way into its buffer.
+    const uint64_t policy = leaves_first();
     auto issue = [&](int t, int half, const Place& p) {
       const int nrows = rows_of(t), s = t % NB;
       uint64_t* bar = (half == 0 ? kbar : vbar) + s;
@@ -133,8 +151,8 @@ __global__ void __launch_bounds__(kRestWarps * 32, 20 / kRestWarps) rest_kernel(
         if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nrows * Sh::kRowBytes));
         __syncwarp();
         if (lane < nrows)
-          bulk_copy_g2s(to + lane * Sh::kRowStride, base + (static_cast<size_t>(at) * a.hkv + hk) * D,
-                        Sh::kRowBytes, bar);
+          row_copy(to + lane * Sh::kRowStride, base + (static_cast<size_t>(at) * a.hkv + hk) * D,
+                   Sh::kRowBytes, bar, policy);
       } else {
         constexpr int kLanes = Sh::kRowBytes / 16, kStep = 32 / kLanes;
         const int piece = lane % kLanes;
