@@ -244,11 +244,13 @@ __global__ void __launch_bounds__(kRestWarps * 32, 20 / kRestWarps) rest_kernel(
 constexpr int kJoinWarps = 4;
 
 // A warp joins the states of one (request, query head): lane p weighs piece p and chunk p, all
-// lanes add.  The first states are asked for together with their weights.
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const RestLaunch a) {
+// lanes add.  The first states are asked for together with their weights; fewer of them (MANY)
+// where the warps are more than an SM holds at once otherwise, 16: 128 requests of 32 heads 61.7 us
+// for 63.4, but 64 of them with up to 14 pieces 43.3 for 42.2.
+template <int D, bool MANY>
+__global__ void __launch_bounds__(kJoinWarps * 32, MANY ? 7 : 4) join_kernel(const RestLaunch a) {
   constexpr int kDims = D / 32;  // of a lane
-  constexpr int kPieces = 8, kChunks = 6;
+  constexpr int kPieces = MANY ? 6 : 8, kChunks = MANY ? 4 : 6;
   using Vec = typename std::conditional<kDims == 4, float4, float2>::type;
   griddep_wait();
   griddep_launch_dependents();
@@ -374,7 +376,9 @@ cudaError_t any(int head_dim, int group, bool mask, const RestLaunch* a, cudaStr
 cudaError_t launch_shared_rest(const RestLaunch& a, bool mask, cudaStream_t s) {
   const cudaError_t e = any(a.head_dim, a.hq / a.hkv, mask, &a, s, nullptr);
   if (e != cudaSuccess) return e;
-  auto kern = a.head_dim == 128 ? join_kernel<128> : join_kernel<64>;
+  const bool many = static_cast<int64_t>(a.batch) * a.hq > static_cast<int64_t>(sm_count()) * 16;
+  auto kern = a.head_dim == 128 ? (many ? join_kernel<128, true> : join_kernel<128, false>)
+                                : (many ? join_kernel<64, true> : join_kernel<64, false>);
   return launch_pdl(
       kern, dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.batch) * a.hq, kJoinWarps))),
       dim3(kJoinWarps * 32), 0, s, a);
