@@ -99,6 +99,7 @@ struct SharedLaunch {
   float scale_log2;
   SharedStates states;
   int32_t* pieces;
+  int32_t leave;       // rows of the prefixes leave the L2 first
   int32_t* err;
   int32_t sms;
 };

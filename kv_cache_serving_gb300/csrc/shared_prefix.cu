@@ -11,13 +11,14 @@
 // A tile is 128 query rows of one (group, kv head); a block is 128 cache rows.  All blocks of all
 // tiles, tiles of one (group, kv head) side by side, form one line that is cut into equal
 // pieces, one per CTA, whatever the groups' sizes: a CTA takes parts of a tile or several tiles,
-// and a tile has as many states as pieces touch it.
+// and a tile has as many states as pieces touch it.  (Beginning a tile counts as blocks too.)
 //
 // Seven warps: two load (K, and V; a page's 16 rows of 64 dims per tensor copy, into the swizzled
 // tiles that the products read), one issues the products, four weigh, one query row per thread.
-// The queries lie in tensor memory.  Scores and weights exist twice, so that the scores of a
-// block are made while the one before it is weighed; weights go back to tensor memory over their
-// scores as the left operand of P V.  The reference follows the row's maximum when that passes it
+// The queries lie in tensor memory.  Scores exist twice, so that the scores of a block are made
+// while the one before it is weighed; weights go back to tensor memory, to a place of their own, as
+// the left operand of P V (over their scores they hold up the scores after the next: a block 1150
+// ns, 1060 so).  The reference follows the row's maximum when that passes it
 // by 2^8, so that acc is rarely rescaled.  P is rounded to bf16 (2^-8 of each weight, as V's type
 // asks; the output is rounded to bf16 as well), its sum is taken before.
 //
@@ -63,18 +64,31 @@ struct PrefixShape {
   static constexpr int kRing = 0, kStage = kSlots * kTile;  // the ring; 4 KB of each weighing warp
   static constexpr int kBar = kStage + 4 * 4096;
   static constexpr int kSmem = 1024 + kBar + 256;     // the base is rounded up to 1024
-  // tensor memory: S and P twice, O, Q
-  static constexpr int kS = 0, kO = 256, kQ = 256 + D, kTmem = 512;
+  // tensor memory: S twice, P, O, Q
+  static constexpr int kS = 0, kP = 256, kO = 320, kQ = 320 + D, kTmem = 512;
 };
 
 constexpr uint32_t kBf16Operands = (1u << 7) | (1u << 10);
 
+// How long rows stay in the L2: prefixes that fit there as usual, for the next step; those that do
+// not (kStayBytes of K and V, by the host's bounds) leave first, which keeps the states there until
+// the join.  64 requests behind 16391 rows (67 MB) 36.1 us, as usual 38.0; 128 of nine prompts (73
+// MB) 60.1 and 61.8; but 64 images of four prompts (17 MB) 21.9 and 21.5, eight requests (6 MB)
+// 13.0 and 12.4.
+constexpr int64_t kStayBytes = 48 << 20;
+__device__ __forceinline__ uint64_t l2_policy(bool leave) {
+  uint64_t first, usual;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(usual));
+  return leave ? first : usual;
+}
+
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int x, int slot,
-                                            int head, int page, uint64_t* bar) {
+                                            int head, int page, uint64_t* bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -119,9 +133,14 @@ __device__ __forceinline__ Group load_group(const SharedLaunch& a, int g, int32_
   return r;
 }
 
+// Blocks that beginning another tile is worth (queries, the first rows, the state: 5 us), none for a
+// tile of few blocks, which is better not cut; the line has so many places before the tile's own.
+// 64 requests behind 16391 rows 38.1 us, 42.4 with tiles begun for nothing, 39.0 with 8 blocks.
+__device__ __forceinline__ int tile_cost(const Group& g) { return min(6, g.blocks >> 3); }
+
 // A CTA's place on the line of blocks.
 struct Cursor {
-  int at, end;  // blocks done and to do, counted over all tiles
+  int at, end;  // places done and to do, counted over all tiles
   int g, hk, t, blk;
   Group grp;
 };
@@ -175,7 +194,7 @@ __global__ void __maxnreg__(160)
 
   // ---- this CTA's piece of the line ----
   // blocks of all tiles of a group, summed over the groups
-  auto units_of = [&](const Group& g) { return g.tiles * g.blocks * a.hkv; };
+  auto units_of = [&](const Group& g) { return g.tiles * (g.blocks + tile_cost(g)) * a.hkv; };
   int sum = 0, mine0 = 0;  // mine0: of the first group this thread looks at
   int most = 0, wrong = 0;
   for (int g = tid; g < a.groups; g += kPThreads) {
@@ -183,7 +202,7 @@ __global__ void __maxnreg__(160)
     wrong |= !r.sound;
     sum += units_of(r);
     if (g == tid) mine0 = sum;
-    most = max(most, r.blocks);
+    most = max(most, r.blocks + tile_cost(r));
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
@@ -240,29 +259,35 @@ __global__ void __maxnreg__(160)
     before += all;
     __syncthreads();
   }
-  const bool work = c0.at < c0.end && found >= 0;
+  bool work = c0.at < c0.end && found >= 0;
   if (work) {
     c0.g = found;
     c0.grp = load_group(a, c0.g, nullptr);
     int in = c0.at - found_before;
-    const int per_head = c0.grp.tiles * c0.grp.blocks;
-    c0.hk = in / per_head;
-    in -= c0.hk * per_head;
-    c0.t = in / c0.grp.blocks;
-    c0.blk = in - c0.t * c0.grp.blocks;
+    const int cost = tile_cost(c0.grp), per_tile = c0.grp.blocks + cost;
+    c0.t = in / per_tile;
+    in -= c0.t * per_tile;
+    c0.hk = c0.t / c0.grp.tiles;
+    c0.t -= c0.hk * c0.grp.tiles;
+    c0.blk = max(in - cost, 0);
+    c0.at += max(cost - in, 0);
+    work = c0.at < c0.end;
   }
   // Blocks of the cursor's tile that are this CTA's; then on to the next tile.
   auto blocks_here = [&](const Cursor& c) { return min(c.grp.blocks - c.blk, c.end - c.at); };
   auto next_tile = [&](Cursor& c) {
     c.at += blocks_here(c);
     c.blk = 0;
-    if (++c.t < c.grp.tiles) return;
-    c.t = 0;
-    if (++c.hk < a.hkv) return;
-    c.hk = 0;
-    if (c.at >= c.end) return;
-    do c.grp = load_group(a, ++c.g, nullptr);
-    while (c.grp.blocks == 0 && c.g + 1 < a.groups);
+    if (++c.t == c.grp.tiles) {
+      c.t = 0;
+      if (++c.hk == a.hkv) {
+        c.hk = 0;
+        if (c.at >= c.end) return;
+        do c.grp = load_group(a, ++c.g, nullptr);
+        while (c.grp.blocks == 0 && c.g + 1 < a.groups);
+      }
+    }
+    c.at += tile_cost(c.grp);
   };
 
   bool ok = true;
@@ -274,6 +299,7 @@ __global__ void __maxnreg__(160)
     // half each took 95 cycles a copy, three times a block's products.
     const bool k = warp == 4;
     const CUtensorMap* map = k ? &kmap : &vmap;
+    const uint64_t policy = l2_policy(a.leave != 0);
     for (Cursor c = c0; ok && c.at < c.end; next_tile(c)) {
       const int nb = blocks_here(c);
       const int32_t* pt = a.page_table + static_cast<size_t>(c.grp.b0) * a.max_pages;
@@ -306,7 +332,8 @@ __global__ void __maxnreg__(160)
             if (x < pages) {
 #pragma unroll
               for (int h = 0; h < kHalves; ++h)
-                tensor_copy(to + h * kHalfBytes + x * 2048, map, 64 * h, 0, c.hk, ids[x], full + s);
+                tensor_copy(to + h * kHalfBytes + x * 2048, map, 64 * h, 0, c.hk, ids[x], full + s,
+                            policy);
             }
         }
         __syncwarp();
@@ -352,11 +379,7 @@ __global__ void __maxnreg__(160)
       issue_s(0);
       for (int i = 0; ok && i < nb; ++i) {
         const int now = count + i, e = now & 1;
-        if (i + 1 < nb) {
-          // the other place is free when the second product of the block before is done
-          if (now > 0) ok = mbar_wait(o_done + (e ^ 1), static_cast<uint32_t>((now - 1) >> 1) & 1u) && ok;
-          issue_s(i + 1);
-        }
+        if (i + 1 < nb) issue_s(i + 1);  // into the place whose scores became the last weights
         const int item = 2 * now + 1, s = item % Sh::kSlots;
         ok = mbar_wait(full + s, static_cast<uint32_t>(item / Sh::kSlots) & 1u) &&
              mbar_wait(p_full + e, static_cast<uint32_t>(now >> 1) & 1u) && ok;
@@ -366,7 +389,7 @@ __global__ void __maxnreg__(160)
         if (elect_one()) {  // O += P V, a step for each page
           constexpr uint32_t id_o = tc_idesc_b_rows(128, D) | kBf16Operands;
           const uint64_t vd = v_desc + (s * Sh::kTile >> 4);
-          const uint32_t from = tmem + Sh::kS + e * 128;
+          const uint32_t from = tmem + Sh::kP;
           const int pages = pages_of(i);
           for (int x = 0; x < pages; ++x)
             tc_mma_f16_ta(tmem + Sh::kO, from + 8 * x, vd + (x * 2048 >> 4), id_o, i > 0 || x > 0);
@@ -447,7 +470,7 @@ __global__ void __maxnreg__(160)
         if (!idle) {
           const uint32_t t_s = t_lane + Sh::kS + e * 128;
           // 64 columns at a time: the second half for its maximum, the first for its maximum and
-          // its weights (over its own scores), the second again
+          // its weights, the second again
           uint32_t s[2][32];
           auto load_half = [&](int h) {
             tmem_load<32>(t_s + 64 * h, s[0]);
@@ -475,34 +498,17 @@ __global__ void __maxnreg__(160)
           }
           const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c1;
           const bool over = top - ref > kSlackLog2;
-          if (__any_sync(0xffffffffu, over)) {
-            const float to = over ? top : ref;
-            const float down = ex2_approx(ref - to);
-            ref = to;
-            l *= down;
-            if (i > 0) {
-              ok = mbar_wait(o_done + (e ^ 1), static_cast<uint32_t>((now - 1) >> 1) & 1u) && ok;
-              __syncwarp();
-              tc_fence_after();
-#pragma unroll 1
-              for (int h = 0; h < D / 16; ++h) {
-                uint32_t o[16];
-                tmem_load<16>(t_lane + Sh::kO + 16 * h, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * down);
-                tmem_store16(t_lane + Sh::kO + 16 * h, o);
-              }
-            }
-          }
+          const float to = over ? top : ref, down = ex2_approx(ref - to);
+          ref = to;
+          l *= down;
           const f32x2 a1 = pack2(c1, c1), a2 = pack2(-ref, -ref);
           f32x2 sums[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == 1) load_half(1);
+            uint32_t w[2][16];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              uint32_t w[16];
 #pragma unroll
               for (int q = 0; q < 32; q += 2) {
                 float z0, z1;
@@ -510,10 +516,28 @@ __global__ void __maxnreg__(160)
                 z0 = ex2_approx(z0);
                 z1 = ex2_approx(z1);
                 sums[(q >> 1) & 1] = add2(sums[(q >> 1) & 1], pack2(z0, z1));
-                w[q / 2] = bf16x2_rn(z0, z1);
+                w[x][q / 2] = bf16x2_rn(z0, z1);
               }
-              tmem_store16(t_s + 32 * h + 16 * x, w);
             }
+            if (h == 0 && now > 0) {
+              // the last weights and O are free when the second product of the block before is done
+              ok = mbar_wait(o_done + (e ^ 1), static_cast<uint32_t>((now - 1) >> 1) & 1u) && ok;
+              __syncwarp();
+              tc_fence_after();
+              if (i > 0 && __any_sync(0xffffffffu, over)) {
+#pragma unroll 1
+                for (int y = 0; y < D / 16; ++y) {
+                  uint32_t o[16];
+                  tmem_load<16>(t_lane + Sh::kO + 16 * y, o);
+                  tc_wait_ld();
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * down);
+                  tmem_store16(t_lane + Sh::kO + 16 * y, o);
+                }
+              }
+            }
+            tmem_store16(t_lane + Sh::kP + 32 * h, w[0]);
+            tmem_store16(t_lane + Sh::kP + 32 * h + 16, w[1]);
           }
           float u, v;
           unpack2(add2(sums[0], sums[1]), u, v);
@@ -622,7 +646,7 @@ bool encode_pages(CUtensorMap* map, const void* pages, const SharedLaunch& a) {
 }
 
 template <int D>
-cudaError_t launch_one(const SharedLaunch& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+cudaError_t launch_one(SharedLaunch a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                        cudaStream_t s) {
   auto kern = prefix_kernel<D>;
   static KernelSlots cache;
@@ -638,6 +662,7 @@ cudaError_t launch_one(const SharedLaunch& a, const CUtensorMap& kmap, const CUt
   int64_t ctas = blocks / 4 > a.sms / 2 ? blocks / 4 : a.sms / 2;
   ctas = ctas < a.sms ? ctas : a.sms;
   ctas = ctas < blocks ? ctas : blocks;
+  a.leave = static_cast<int64_t>(a.groups) * a.max_prefix * a.hkv * D * 4 > kStayBytes;
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kPThreads),
                     static_cast<size_t>(PrefixShape<D>::kSmem), s, a, kmap, vmap);
 }
