@@ -18,23 +18,22 @@
 // The queries lie in tensor memory.  Scores exist twice, so that the scores of a block are made
 // while the one before it is weighed; weights go back to tensor memory, to a place of their own, as
 // the left operand of P V (over their scores they hold up the scores after the next: a block 1150
-// ns, 1060 so).  The reference follows the row's maximum when that passes it
-// by 2^8, so that acc is rarely rescaled.  P is rounded to bf16 (2^-8 of each weight, as V's type
-// asks; the output is rounded to bf16 as well), its sum is taken before.
+// ns, 1060 so).  The reference follows the row's maximum when that passes it by 2^8, so that acc is
+// rarely rescaled.  P is rounded to bf16 (2^-8 of each weight, as V's type asks; the output is
+// rounded to bf16 as well), its sum is taken before.
 //
 // All members keep every row of the prefix, so there is no mask; rows of the last page behind the
 // prefix (another request's, or nothing yet) get weight 0 and V rows of zeros.
 //
-// What bounds it: a block takes 1700 cycles to weigh (1024 of them the exponentials) where its
-// products take 1024.  Alone on the GPU its loads keep up; beside the rest kernel, whose warps
-// fill the queues to memory, they are late by about as much again.  Before the first scores there
-// are the groups' two dependent loads, page ids and rows (3 us alone, 8 beside), behind the last
-// block the states of 128 rows (2 us).  Measured, whole calls: 64 requests of 32/8 heads behind
-// 16391 rows 44 us, where this kernel by itself takes 28 (34 while each of sixteen lanes issued
-// its own tensor copies, at 95 cycles a copy).  A CTA leaves room for two CTAs of the rest kernel
-// (160 registers a thread, 145 KB): without, that one starts behind it (128 requests of nine
+// What bounds it: weighing, 0.9 us of a block's 1.06, of which the exponentials are half.  Alone on
+// the GPU its loads keep up; beside the rest kernel, whose warps fill the queues to memory, they
+// are late by 0.4 us a block.  Before the first scores there are the groups' two dependent loads,
+// page ids and rows (5 us, 7 beside), behind the last block the states of 128 rows (1.7 us).
+// Measured, whole calls: 64 requests of 32/8 heads behind 16391 rows 36 us, of which this kernel 28
+// (30 and 22 where the requests have one own row each).  A CTA leaves room for two CTAs of the rest
+// kernel (160 registers a thread, 145 KB): without, that one starts behind it (128 requests of nine
 // prompts 77 us, 71 with it).  In its place, warps of 8 query rows with mma.sync for groups of few
-// rows: 28 us for 64 images of four prompts where this takes 24.
+// rows: 28 us for 64 images of four prompts where this took 24.
 #include <cuda.h>
 #include <math.h>
 

@@ -11,14 +11,15 @@
 // What bounds it: HBM while most warps are there (in the middle of 128 requests of nine prompts
 // 6.9 TB/s, 4.4 beside the prefix kernel's 2.3), at both ends the latency of a tile, 1.3 us alone
 // and 2.1 in company, times the tiles of a chunk; an item takes 0.9 us to its lengths and page
-// ids and 2.2 us to its first rows.  Measured: those 128 requests 65 us as a whole (floor 43).
-// CTAs that took a unit, waited for the prefix kernel and joined the states themselves: 77 us;
-// items fetched by warps from a counter: 70; rows in 16-byte copies instead of one each: 73
-// for 73.
+// ids and 2.2 us to its first rows.  Measured: those 128 requests 60 us as a whole (floor 43), this
+// kernel's last rows at 56.  Twice the buffers and half of the warps: 65; items fetched by warps
+// from a counter: 70 where this took 65; CTAs that took a unit, waited for the prefix kernel and
+// joined the states themselves: 77 for 73; rows in 16-byte copies instead of one each: 73 for 73.
 //
 // join_kernel.  A warp per (request, query head): the log-sum-exp sum of the prefix's states and
 // the chunks', in their order, so results do not depend on who was first.  Three dependent loads
-// (counts; weights and dims), 3 us for few states and 8 for 18 MB of them.
+// (counts; weights and dims), 3 us for few states, 4 for 18 MB of them, 5 for 15 MB of up to 14 a
+// head.
 #include <math.h>
 
 #include <type_traits>

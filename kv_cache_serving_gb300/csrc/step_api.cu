@@ -17,10 +17,9 @@ namespace {
 
 // Half waves of resident warps that the rows behind the prefixes are cut for (the host knows a
 // bound of a request's rows only), and the rows that a chunk is a multiple of.  128 requests of
-// nine prompts, 1 .. 1024 own rows: 66 us cut for four half waves, 65 for six, 67 for eight, 69
-// for twelve; half as long chunks in the second half of the bound 64, but 45 instead of 44 for
-// 64 requests of 1 .. 600 own rows.  64 images, 40 kept rows on the average: 26 us for two half
-// waves, 25 for four or six.
+// nine prompts, 1 .. 1024 own rows: 60 us cut for six half waves, 63 for eight, ten or twelve.  64
+// images, 40 kept rows on the average: 24 us for two half waves, 21.5 for three or four, 22.5 for
+// five or six.
 constexpr int kSharedDenseWaves = 6, kSharedMaskWaves = 4, kSharedChunk = 32;
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
