@@ -64,12 +64,12 @@ FALLBACK_HBM_GBS = 6800.0
 # decode-kernel sources whose digest is `digest` and are reported as null
 # otherwise.
 NCU_TRAFFIC = {
-    "digest": "afac391cd849058f",
+    "digest": "3eec322670c4de8c",
     "bytes": {
-        "mixed-serving-gqa4": 168038912,
-        "janus-pro-7b-like-32x32": 316020736,
-        "llamagen-xl-like-24x24": 21442816,
-        "emu3-8b-like-90x90-gqa4": 3281664,
+        "mixed-serving-gqa4": 168322816,
+        "janus-pro-7b-like-32x32": 316365056,
+        "llamagen-xl-like-24x24": 21439488,
+        "emu3-8b-like-90x90-gqa4": 3278592,
     },
 }
 
