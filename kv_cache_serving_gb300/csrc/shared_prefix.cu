@@ -613,7 +613,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The driver's encoder, asked for once (the library links the runtime alone).
+// CUDA's encoder, asked for once (the library links the runtime alone).
 EncodeTiled encoder() {
   static std::atomic<void*> known{nullptr};
   void* p = known.load(std::memory_order_acquire);

@@ -228,6 +228,24 @@ def test_many_groups():
     assert dsa.dsa_get_device_error(bt.ws) == 0
 
 
+@pytest.mark.parametrize("hkv,g,d", [(3, 4, 128), (5, 2, 64), (1, 8, 128), (2, 1, 128)])
+def test_long_and_short_prefixes(hkv, g, d):
+    """Groups of several tiles and of few, prefixes of many blocks beside short ones; then with bounds
+    far above them, as of prefixes that the L2 does not hold."""
+    sizes, prefix = [3, 40, 1, 70, 9, 2], [5003, 1500, 2049, 1024, 700, 8]
+    bt = Batch(sizes, prefix, [(7 * i) % 50 for i in range(sum(sizes))], hkv, g, d, seed=hkv + d)
+    some = [0, 2, 3, 17, 42, 43, 44, 80, 113, 114, 122, 123, 124]
+    out, lse = bt.run()
+    bt.check(out, lse, requests=some)
+    assert dsa.dsa_get_device_error(bt.ws) == 0 and torch.isfinite(out.float()).all()
+    bt.table = np.pad(bt.table, ((0, 0), (0, 4000)), constant_values=-1)
+    bt.dev()
+    bt.shared.max_prefix = 60000
+    out, lse = bt.run()
+    bt.check(out, lse, requests=some)
+    assert dsa.dsa_get_device_error(bt.ws) == 0 and torch.isfinite(out.float()).all()
+
+
 def test_sharing_is_decode_over_own_rows():
     """The same batch with nothing shared: both within their bars, and lse equal to rounding."""
     bt = Batch([6, 3], [400, 90], [30] * 9, 4, 4, 128, seed=8)
