@@ -210,6 +210,7 @@ __global__ void __maxnreg__(96) qk_norm_kernel(const __grid_constant__ NormLaunc
   }
   __syncthreads();
   const bool layer = a.layer != 0;
+  const int ahead = a.rope.tokens - t0 - kNormPrefetch * a.subs;
   for (int t = sub; t - sub < nt; t += a.subs, in += in_step, out += out_step) {
     const bool now = live && t < nt;
     f32x2 x[8];
@@ -219,7 +220,7 @@ __global__ void __maxnreg__(96) qk_norm_kernel(const __grid_constant__ NormLaunc
     if (live && t + kAhead * a.subs < nt)
       next[kAhead - 1].load(in + kAhead * in_step, D / 2 * kElt);
     // the lines of the head a few tokens on into the L2
-    if (l == 0 && live && t0 + t + kNormPrefetch * a.subs < a.rope.tokens) {
+    if (l == 0 && live && t < ahead) {
 #pragma unroll
       for (int y = 0; y < D * kElt; y += 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(in + kNormPrefetch * in_step + y));

@@ -467,12 +467,14 @@ def rope_sections(sections, interleaved=False) -> list:
     return out
 
 
-def _arg(t, dtype, dev, what):
+def _arg(t, dtype, dev, what, want=None):
     """Device address of a contiguous CUDA tensor of `dtype` (or one of several) on device
-    `dev`, or None.  The calls launch on the current device, so a tensor of another one
-    is refused."""
+    `dev`, of shape `want` if that is given, or None.  The calls launch on the current device,
+    so a tensor of another one is refused."""
     if t is None:
         return None
+    if want is not None and t.shape != want:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(want)}")
     if t.get_device() != dev:
         raise TypeError(f"{what} must be a CUDA tensor on the current device cuda:{dev}, not on "
                         f"{t.device}")
@@ -616,23 +618,18 @@ def dsa_assign_pages(dims, seq_len, new_len, free_pages, free_count, free_count_
     (None: one row each) into page_table, and the slot and position of every new row, packed in
     request order: token_start [batch + 1] or None, row_slot [max_tokens], row_pos alike or None."""
     dev, st = _launch_on(stream)
-    B = dims.batch
-    _shape(seq_len, (B,), "seq_len")
-    _shape(new_len, (B,), "new_len")
-    _shape(page_table, (B, dims.max_pages_per_req), "page_table")
-    _shape(token_start, (B + 1,), "token_start")
-    n = row_slot.shape[0]
-    _shape(row_slot, (n,), "row_slot")
-    _shape(row_pos, (n,), "row_pos")
-    for t, what in ((free_count, "free_count"), (free_count_out, "free_count_out")):
-        if t.numel() != 1:
-            raise ValueError(f"{what} must be one int32")
+    per_request, per_row = (dims.batch,), row_slot.shape
+    if len(per_row) != 1:
+        raise ValueError(f"row_slot has shape {tuple(per_row)}, expected [max_tokens]")
+    if free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise ValueError("free_count and free_count_out must be one int32 each")
     _check(_load().dsa_assign_pages(
-        dims, _arg(seq_len, _I32, dev, "seq_len"), _arg(new_len, _I32, dev, "new_len"),
+        dims, _arg(seq_len, _I32, dev, "seq_len", per_request), _arg(new_len, _I32, dev, "new_len", per_request),
         _arg(free_pages, _I32, dev, "free_pages"), free_pages.numel(),
         _arg(free_count, _I32, dev, "free_count"), _arg(free_count_out, _I32, dev, "free_count_out"),
-        _arg(page_table, _I32, dev, "page_table"), n, _arg(token_start, _I32, dev, "token_start"),
-        _arg(row_slot, _I32, dev, "row_slot"), _arg(row_pos, _I32, dev, "row_pos"),
+        _arg(page_table, _I32, dev, "page_table", per_request + (dims.max_pages_per_req,)), per_row[0],
+        _arg(token_start, _I32, dev, "token_start", (per_request[0] + 1,)),
+        _arg(row_slot, _I32, dev, "row_slot"), _arg(row_pos, _I32, dev, "row_pos", per_row),
         _arg(ws, torch.uint8, dev, "ws"), st), "dsa_assign_pages")
 
 
@@ -641,17 +638,15 @@ def dsa_write_rows(dims, row_slot, k, v, k_pages, v_pages, ws, stream=None):
     strided) at slots row_slot [tokens] of k_pages and v_pages; negative slots are skipped."""
     dev, st = _launch_on(stream)
     n = row_slot.shape[0]
-    _shape(row_slot, (n,), "row_slot")
-    want = (n, dims.hkv, dims.head_dim)
+    row = (dims.hkv, dims.head_dim)
+    want, pool = (n,) + row, (dims.num_pages, PAGE) + row
     kt = _TYPE.get(dims.kv_dtype)
     kp, ks = _rows_arg(k, want, kt, dev, "k")
     vp, vs = _rows_arg(v, want, kt, dev, "v")
-    pool = (dims.num_pages, PAGE, dims.hkv, dims.head_dim)
-    _shape(k_pages, pool, "k_pages")
-    _shape(v_pages, pool, "v_pages")
-    _check(_load().dsa_write_rows(dims, n, _arg(row_slot, _I32, dev, "row_slot"), kp, ks, vp, vs,
-                                  _arg(k_pages, kt, dev, "k_pages"), _arg(v_pages, kt, dev, "v_pages"),
-                                  _arg(ws, torch.uint8, dev, "ws"), st), "dsa_write_rows")
+    _check(_load().dsa_write_rows(dims, n, _arg(row_slot, _I32, dev, "row_slot", (n,)), kp, ks, vp, vs,
+                                  _arg(k_pages, kt, dev, "k_pages", pool),
+                                  _arg(v_pages, kt, dev, "v_pages", pool), _arg(ws, torch.uint8, dev, "ws"),
+                                  st), "dsa_write_rows")
 
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -822,11 +817,8 @@ def _shared(dims, shared, dev):
 
 def _pages(dims, k_pages, v_pages, dev):
     """Addresses of the pages, their shapes checked."""
-    pool = (dims.num_pages, PAGE, dims.hkv, dims.head_dim)
-    _shape(k_pages, pool, "k_pages")
-    _shape(v_pages, pool, "v_pages")
-    kt = _TYPE.get(dims.kv_dtype)
-    return _arg(k_pages, kt, dev, "k_pages"), _arg(v_pages, kt, dev, "v_pages")
+    pool, kt = (dims.num_pages, PAGE, dims.hkv, dims.head_dim), _TYPE.get(dims.kv_dtype)
+    return _arg(k_pages, kt, dev, "k_pages", pool), _arg(v_pages, kt, dev, "v_pages", pool)
 
 
 def dsa_decode_dense_shared(dims, shared, q, k_pages, v_pages, page_table, seq_len, scale, out, lse,
@@ -834,14 +826,14 @@ def dsa_decode_dense_shared(dims, shared, q, k_pages, v_pages, page_table, seq_l
     """dsa_decode_dense for requests that share prefixes (shared: see shared_prefix), each prefix
     attended once for its group; out has q's type (bf16)."""
     dev, st = _launch_on(stream)
-    qp, op, lp = _q_out(dims, q, out, lse, dev, (dims.batch,))
+    per_request = (dims.batch,)
+    qp, op, lp = _q_out(dims, q, out, lse, dev, per_request)
     kp, vp = _pages(dims, k_pages, v_pages, dev)
-    _shape(page_table, (dims.batch, dims.max_pages_per_req), "page_table")
-    _shape(seq_len, (dims.batch,), "seq_len")
     _check(_load().dsa_decode_dense_shared(
-        dims, _shared(dims, shared, dev), qp, kp, vp, _arg(page_table, _I32, dev, "page_table"),
-        _arg(seq_len, _I32, dev, "seq_len"), scale, op, lp, _arg(ws, torch.uint8, dev, "ws"), st),
-        "dsa_decode_dense_shared")
+        dims, _shared(dims, shared, dev), qp, kp, vp,
+        _arg(page_table, _I32, dev, "page_table", per_request + (dims.max_pages_per_req,)),
+        _arg(seq_len, _I32, dev, "seq_len", per_request), scale, op, lp,
+        _arg(ws, torch.uint8, dev, "ws"), st), "dsa_decode_dense_shared")
 
 
 def dsa_decode_sparse_masked_shared(dims, shared, q, k_pages, v_pages, page_table, seq_len,
@@ -849,17 +841,16 @@ def dsa_decode_sparse_masked_shared(dims, shared, q, k_pages, v_pages, page_tabl
     """dsa_decode_sparse_masked for requests that share prefixes of their prompts; out has q's type
     (bf16)."""
     dev, st = _launch_on(stream)
-    qp, op, lp = _q_out(dims, q, out, lse, dev, (dims.batch,))
+    per_request = (dims.batch,)
+    qp, op, lp = _q_out(dims, q, out, lse, dev, per_request)
     kp, vp = _pages(dims, k_pages, v_pages, dev)
-    B = dims.batch
-    _shape(page_table, (B, dims.max_pages_per_req), "page_table")
-    for t, what in ((seq_len, "seq_len"), (prompt_len, "prompt_len"), (window, "window")):
-        _shape(t, (B,), what)
-    _shape(keep_mask, (B, dims.hkv, dims.mask_words), "keep_mask")
     _check(_load().dsa_decode_sparse_masked_shared(
-        dims, _shared(dims, shared, dev), qp, kp, vp, _arg(page_table, _I32, dev, "page_table"),
-        _arg(seq_len, _I32, dev, "seq_len"), _arg(prompt_len, _I32, dev, "prompt_len"),
-        _arg(window, _I32, dev, "window"), _arg(keep_mask, _MASK, dev, "keep_mask"), scale, op, lp,
+        dims, _shared(dims, shared, dev), qp, kp, vp,
+        _arg(page_table, _I32, dev, "page_table", per_request + (dims.max_pages_per_req,)),
+        _arg(seq_len, _I32, dev, "seq_len", per_request),
+        _arg(prompt_len, _I32, dev, "prompt_len", per_request),
+        _arg(window, _I32, dev, "window", per_request),
+        _arg(keep_mask, _MASK, dev, "keep_mask", per_request + (dims.hkv, dims.mask_words)), scale, op, lp,
         _arg(ws, torch.uint8, dev, "ws"), st), "dsa_decode_sparse_masked_shared")
 
 
