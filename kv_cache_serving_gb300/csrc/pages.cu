@@ -9,7 +9,8 @@
 // takes 512 of the packed rows; it sums over all requests itself, which costs less than a
 // second launch, and notes the requests that start in its rows; a running maximum over the rows
 // then gives each row its request.  Bound by the chain of dependent loads: lengths, sums, page
-// id, slot.
+// id, slot.  Measured: 1024 requests of 32 .. 512 new rows 8.5 us, 12.5 with 512 requests summed
+// at a time.
 //
 // write_kernel.  A copy bound by HBM; the rows do not wait for their slots, both are loaded
 // together.
@@ -42,8 +43,7 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignLaun
   __shared__ TileRequest req[kAssignThreads];
   __shared__ int32_t owner[kAssignThreads];
   __shared__ int64_t rows_of[kWarps], pages_of[kWarps];
-  __shared__ int32_t owner_of[kWarps];
-  __shared__ int32_t taken;
+  __shared__ int32_t owner_of[kWarps], taken_of[kWarps];
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -55,8 +55,6 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignLaun
     count = 0;
   }
   owner[tid] = -1;
-  if (tid == 0) taken = 0;
-  __syncthreads();
   // Every thread has some requests side by side: their sums, the sums before them, then each
   // of them again (its lengths are in the SM's cache by then).
   const int per = (a.batch + kAssignThreads - 1) / kAssignThreads;
@@ -92,6 +90,12 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignLaun
     pages_of[warp] = pages;
   }
   __syncthreads();
+  // The last CTA to come by here stores the count at its end: all have read theirs.
+  bool last = gridDim.x == 1;
+  if (tid == 0 && !last) {
+    __threadfence();
+    last = atomicAdd(a.done, 1) == static_cast<int32_t>(gridDim.x) - 1;
+  }
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -103,12 +107,13 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignLaun
   }
   rows -= own_rows;  // before this thread's requests
   pages -= own_pages;
+  int32_t taken = 0;  // pages up to the last request that is served
   for (int b = first_b; b < end_b; ++b) {
     const Request r = request(b, false);
     if (first_cta && a.token_start != nullptr)
       a.token_start[b] = static_cast<int32_t>(rows < INT32_MAX ? rows : INT32_MAX);
     const bool served = r.need == 0 || pages + r.need <= count;
-    if (r.need > 0 && served) atomicMax(&taken, static_cast<int32_t>(pages + r.need));
+    if (r.need > 0 && served) taken = static_cast<int32_t>(pages + r.need);
     if (!served && first_cta) set_error(a.err, DSA_DEV_FREE_LIST_EMPTY);
     // the request's first row in this tile, if it has one
     const int64_t at = rows > t0 ? rows : t0;
@@ -121,6 +126,8 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignLaun
     rows += r.n;
     pages += r.need;
   }
+  taken = __reduce_max_sync(0xffffffffu, taken);
+  if (lane == 0) taken_of[warp] = taken;
   __syncthreads();
   const bool fits = total <= a.max_tokens;
   if (first_cta && tid == 0) {
@@ -170,15 +177,10 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignLaun
     a.row_slot[t] = slot;
     if (a.row_pos != nullptr) a.row_pos[t] = row;
   }
-  // the last CTA stores the count: all others have read theirs
-  if (tid == 0) {
-    bool last = true;
-    if (gridDim.x > 1) {
-      __threadfence();
-      last = atomicAdd(a.done, 1) == static_cast<int32_t>(gridDim.x) - 1;
-      if (last) *a.done = 0;
-    }
-    if (last) *a.free_out = count - (fits ? taken : 0);
+  if (tid == 0 && last) {
+    if (gridDim.x > 1) *a.done = 0;
+    for (int w = 1; w < kWarps; ++w) taken = max(taken, taken_of[w]);
+    *a.free_out = count - (fits ? taken : 0);
   }
 }
 
