@@ -683,8 +683,8 @@ typedef struct {
  * softmax, the shared rows read once per group and multiplied on the tensor cores with the queries
  * of all its requests, the others row by row, the two joined by log-sum-exp.  q and K/V bf16,
  * else DSA_ERR_UNSUPPORTED; out [batch][hq][head_dim] bf16 (q's type), not overlapping q; lse
- * float32 or NULL.  Softmax weights of the shared rows are rounded to bf16 for the product with V
- * (2^-8 of each), sums are taken of them unrounded in fp32.  batch <= 65535 and hkv <= 65535.
+ * float32 or NULL.  Softmax weights enter the product with V as two bf16 numbers each (2^-16 of
+ * it), sums are taken of them unrounded in fp32.  batch <= 65535 and hkv <= 65535.
  * A request with invalid lengths, a prefix_len outside 0 .. max_prefix or above its rows, or more
  * than max_suffix other rows (DSA_DEV_BAD_PREFIX), or one that no group holds or that states
  * another prefix_len than its group's first (DSA_DEV_BAD_GROUP or _BAD_PREFIX) gets NaN; a

@@ -16,11 +16,11 @@
 // Seven warps: two load (K, and V; a page's 16 rows of 64 dims per tensor copy, into the swizzled
 // tiles that the products read), one issues the products, four weigh, one query row per thread.
 // The queries lie in tensor memory.  Scores exist twice, so that the scores of a block are made
-// while the one before it is weighed; weights go back to tensor memory, to a place of their own, as
-// the left operand of P V (over their scores they hold up the scores after the next: a block 1150
-// ns, 1060 so).  The reference follows the row's maximum when that passes it by 2^8, so that acc is
-// rarely rescaled.  P is rounded to bf16 (2^-8 of each weight, as V's type asks; the output is
-// rounded to bf16 as well), its sum is taken before.
+// while the one before it is weighed; weights go back to tensor memory as the left operand of P V,
+// as two bf16 numbers (V's type asks for bf16; the second is what the first leaves out, so that a
+// weight is good to 2^-16, as in the library's other decode calls): the first to a place of their
+// own, the second over the scores that they were.  The reference follows the row's maximum when
+// that passes it by 2^8, so that acc is rarely rescaled.  The sum is taken of the fp32 weights.
 //
 // All members keep every row of the prefix, so there is no mask; rows of the last page behind the
 // prefix (another request's, or nothing yet) get weight 0 and V rows of zeros.
@@ -378,20 +378,25 @@ __global__ void __maxnreg__(160)
       issue_s(0);
       for (int i = 0; ok && i < nb; ++i) {
         const int now = count + i, e = now & 1;
-        if (i + 1 < nb) issue_s(i + 1);  // into the place whose scores became the last weights
+        if (i + 1 < nb) {  // into the place of the block before, when its weights' second parts are used
+          if (i > 0) ok = mbar_wait(o_done + (e ^ 1), static_cast<uint32_t>((now - 1) >> 1) & 1u) && ok;
+          issue_s(i + 1);
+        }
         const int item = 2 * now + 1, s = item % Sh::kSlots;
         ok = mbar_wait(full + s, static_cast<uint32_t>(item / Sh::kSlots) & 1u) &&
              mbar_wait(p_full + e, static_cast<uint32_t>(now >> 1) & 1u) && ok;
         tc_fence_after();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (elect_one()) {  // O += P V, a step for each page
+        if (elect_one()) {  // O += P V, two steps for each page
           constexpr uint32_t id_o = tc_idesc_b_rows(128, D) | kBf16Operands;
           const uint64_t vd = v_desc + (s * Sh::kTile >> 4);
-          const uint32_t from = tmem + Sh::kP;
+          const uint32_t high = tmem + Sh::kP, low = tmem + Sh::kS + e * 128;
           const int pages = pages_of(i);
-          for (int x = 0; x < pages; ++x)
-            tc_mma_f16_ta(tmem + Sh::kO, from + 8 * x, vd + (x * 2048 >> 4), id_o, i > 0 || x > 0);
+          for (int x = 0; x < pages; ++x) {
+            tc_mma_f16_ta(tmem + Sh::kO, high + 8 * x, vd + (x * 2048 >> 4), id_o, i > 0 || x > 0);
+            tc_mma_f16_ta(tmem + Sh::kO, low + 8 * x, vd + (x * 2048 >> 4), id_o, true);
+          }
           tc_commit(o_done + e);
           tc_commit(empty + s);
         }
@@ -500,12 +505,12 @@ __global__ void __maxnreg__(160)
           const float to = over ? top : ref, down = ex2_approx(ref - to);
           ref = to;
           l *= down;
-          const f32x2 a1 = pack2(c1, c1), a2 = pack2(-ref, -ref);
+          const f32x2 a1 = pack2(c1, c1), a2 = pack2(-ref, -ref), minus1 = pack2(-1.f, -1.f);
           f32x2 sums[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == 1) load_half(1);
-            uint32_t w[2][16];
+            uint32_t w[2][16], rest[2][16];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
 #pragma unroll
@@ -514,10 +519,17 @@ __global__ void __maxnreg__(160)
                 unpack2(fma2(pack2(__uint_as_float(s[x][q]), __uint_as_float(s[x][q + 1])), a1, a2), z0, z1);
                 z0 = ex2_approx(z0);
                 z1 = ex2_approx(z1);
-                sums[(q >> 1) & 1] = add2(sums[(q >> 1) & 1], pack2(z0, z1));
-                w[x][q / 2] = bf16x2_rn(z0, z1);
+                const f32x2 z = pack2(z0, z1);
+                sums[(q >> 1) & 1] = add2(sums[(q >> 1) & 1], z);
+                const uint32_t high = bf16x2_rn(z0, z1);
+                unpack2(fma2(pack2(bf16_lo(high), bf16_hi(high)), minus1, z), z0, z1);
+                w[x][q / 2] = high;
+                rest[x][q / 2] = bf16x2_rn(z0, z1);
               }
             }
+            // (the first half's scores are in registers or done with, and these lie over them)
+            tmem_store16(t_s + 32 * h, rest[0]);
+            tmem_store16(t_s + 32 * h + 16, rest[1]);
             if (h == 0 && now > 0) {
               // the last weights and O are free when the second product of the block before is done
               ok = mbar_wait(o_done + (e ^ 1), static_cast<uint32_t>((now - 1) >> 1) & 1u) && ok;

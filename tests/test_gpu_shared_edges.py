@@ -1,0 +1,57 @@
+"""Decode over shared prefixes: how exact the shared rows' weights are.
+
+Bars of `fine` (relative to sum a |v|, the weighted magnitudes, with a the softmax weights): a weight
+is kept as two bf16 numbers, the second of what the first leaves out, so it is off by 2^-8 of
+2^-8; a score is a sum of d products in fp32, off by at most d 2^-24 sum |q k| scale, which is the
+weight's relative error; 2^x, the subtraction of the reference, the sums of up to some hundreds
+of terms and the joining stay below 2^-15.  The output's own rounding is half a step of bf16, 2^-8
+of itself."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_serving_gb300 import dsa
+from test_gpu_shared import BF, U, Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "GPU tests need CUDA"
+    torch.cuda.init()
+
+
+def fine(bt, b):
+    """out [hq, d] and its tolerance, in 64 bits."""
+    L = int(bt.L[b])
+    pages = torch.as_tensor(bt.table[b, :-(-L // 16)], device="cuda")
+    k, v = (t[pages].flatten(0, 1)[:L].double() for t in (bt.k, bt.v))
+    on = torch.as_tensor(np.stack([bt.rows(b, h) for h in range(bt.hkv)]), device="cuda")
+    q = bt.q[b].double().view(bt.hkv, bt.g, bt.d)
+    x = torch.einsum("hgd,nhd->hgn", q, k) * bt.scale
+    x = x.masked_fill(~on[:, None], -math.inf)
+    a = torch.softmax(x, -1)
+    off = bt.d * 2.0 ** -24 * abs(bt.scale) * torch.einsum("hgd,nhd->hgn", q.abs(), k.abs())
+    out = torch.einsum("hgn,nhd->hgd", a, v)
+    # (the weight itself, and its part in the sum that all are divided by)
+    size = torch.einsum("hgn,nhd->hgd", a * (off + 2.0 ** -16 + 2.0 ** -15), v.abs())
+    size = size + torch.einsum("hgn,hgn->hg", a, off + 2.0 ** -15)[..., None] * out.abs()
+    return out.reshape(-1, bt.d), (size * 1.01 + U * (out.abs() + size)).reshape(-1, bt.d)
+
+
+@pytest.mark.parametrize("S,n", [(2, 3), (3, 40), (16, 8), (130, 9), (700, 5)])
+@pytest.mark.parametrize("hkv,g,d,masked", [(2, 4, 128, None), (5, 1, 64, (40, 0.4, 0)), (1, 8, 64, None),
+                                            (3, 2, 128, (40, 0.4, 0))])
+def test_weights_as_exact_as_those_of_own_rows(S, n, hkv, g, d, masked):
+    """Rows of V that cancel each other: what is left of them shows every weight."""
+    bt = Batch([n], [S], [i % 3 for i in range(n)], hkv, g, d, masked, seed=S + d)
+    sign = torch.where(bt.randn(16, hkv, d) < 0, -1.0, 1.0)  # by slot: copies of a prefix's page are alike
+    bt.v.copy_(sign.expand_as(bt.v))
+    out, _ = bt.run()
+    for b in range(bt.B):
+        want, tol = fine(bt, b)
+        assert ((out[b].double() - want).abs() <= tol).all(), (b, float(((out[b].double() - want).abs() / tol).max()))
+    assert dsa.dsa_get_device_error(bt.ws) == 0
