@@ -409,8 +409,9 @@ __global__ void __maxnreg__(160)
     // ================= weighing: one query row per thread =================
     const int r = tid, lg = a.group_log2, per_tile = kPRows >> lg;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-    // at least 2^-100, so that a masked score (-inf) times it stays one
-    const float c1 = fmaxf(fabsf(a.scale_log2), 0x1p-100f);
+    // at least the smallest fp32 number, so that a masked score (-inf) times it stays one; a finite
+    // score (below 2^128) times that is nothing, as with scale 0
+    const float c1 = fmaxf(fabsf(a.scale_log2), 0x1p-149f);
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // q changes its sign
     for (Cursor c = c0; ok && c.at < c.end; next_tile(c)) {
       const int nb = blocks_here(c);

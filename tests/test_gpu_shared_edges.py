@@ -1,4 +1,4 @@
-"""Decode over shared prefixes: how exact the shared rows' weights are.
+"""Decode over shared prefixes: how exact the shared rows' weights are, and scales far below one.
 
 Bars of `fine` (relative to sum a |v|, the weighted magnitudes, with a the softmax weights): a weight
 is kept as two bf16 numbers, the second of what the first leaves out, so it is off by 2^-8 of
@@ -54,4 +54,15 @@ def test_weights_as_exact_as_those_of_own_rows(S, n, hkv, g, d, masked):
     for b in range(bt.B):
         want, tol = fine(bt, b)
         assert ((out[b].double() - want).abs() <= tol).all(), (b, float(((out[b].double() - want).abs() / tol).max()))
+    assert dsa.dsa_get_device_error(bt.ws) == 0
+
+
+@pytest.mark.parametrize("scale,size", [(0.0, 2.0 ** 60), (2.0 ** -110, 2.0 ** 54), (-2.0 ** -110, 2.0 ** 54),
+                                        (2.0 ** -120, 2.0 ** 59)])
+def test_scales_far_below_one(scale, size):
+    """Scores of up to 2^125 times a scale that brings them down to a few units, or to nothing."""
+    bt = Batch([5, 2], [200, 37], [20, 0, 3, 1, 9, 5, 0], 2, 4, 64, seed=2, scale=scale)
+    for t in (bt.q, bt.k):
+        t.copy_((t.float() * size).to(BF))
+    bt.check(*bt.run())
     assert dsa.dsa_get_device_error(bt.ws) == 0
