@@ -611,7 +611,8 @@ dsa_status dsa_qk_norm_rope(const dsa_dims* dims, const dsa_qk_norm* norm, const
  *   seq_len      [batch] int32, L_b >= 1 counting the new rows
  *   new_len      [batch] int32, 0 <= new_len[b] <= L_b, or NULL: one row each (a decode step)
  *   free_pages   [capacity] int32, page ids
- *   free_count   one int32: ids in free_pages, 0 .. capacity
+ *   free_count   one int32: ids in free_pages, 0 .. capacity (above it, as dsa_evict_pages leaves
+ *                it behind a list that was too small: capacity of them)
  *   free_count_out (out) one int32: ids left; may be free_count itself.  Apart from it, the
  *                call can be repeated (a scheduler's trial) with the same result.
  *   page_table   [batch][max_pages_per_req] int32 (in/out): entries of fresh pages are written,
@@ -625,9 +626,9 @@ dsa_status dsa_qk_norm_rope(const dsa_dims* dims, const dsa_qk_norm* norm, const
  * A request that finds fewer free pages than it needs gets none: DSA_DEV_FREE_LIST_EMPTY, -1 for
  * all its rows, its entries unchanged; so do later requests that need pages, while requests that
  * need none are served.  Invalid lengths (DSA_DEV_BAD_SEQ_LEN, DSA_DEV_BAD_QLEN) count as no new
- * rows; a page id outside the pool gives DSA_DEV_BAD_PAGE and -1 for its rows; free_count outside
- * 0 .. capacity counts as 0, and with more new rows than max_tokens no request is served
- * (DSA_DEV_BAD_COUNT).  num_pages * 16 < 2^31, else DSA_ERR_UNSUPPORTED.
+ * rows; a page id outside the pool gives DSA_DEV_BAD_PAGE and -1 for its rows.  free_count below 0
+ * counts as 0 and above capacity as capacity, and with more new rows than max_tokens no request is
+ * served (all DSA_DEV_BAD_COUNT).  num_pages * 16 < 2^31, else DSA_ERR_UNSUPPORTED.
  */
 dsa_status dsa_assign_pages(const dsa_dims* dims, const int32_t* seq_len, const int32_t* new_len,
                             const int32_t* free_pages, int32_t capacity,

@@ -49,10 +49,11 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignLaun
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kAssignThreads;
   const bool first_cta = blockIdx.x == 0;
+  // Eviction counts past a list that was too small; the list is full then.
   int count = *a.free_count;
   if (count < 0 || count > a.capacity) {
     if (first_cta && tid == 0) set_error(a.err, DSA_DEV_BAD_COUNT);
-    count = 0;
+    count = count < 0 ? 0 : a.capacity;
   }
   owner[tid] = -1;
   // Every thread has some requests side by side: their sums, the sums before them, then each
