@@ -60,30 +60,36 @@ def page_rows(page_table, seq_len, num_pages) -> np.ndarray:
 
 def shared_groups(page_table, seq_len):
     """(group_start, prefix_len) for DecodeBatch.share_prefix from host arrays: runs of neighbouring
-    requests whose tables begin with the same whole pages.  A request joins the group before it
-    when it has at least half of that group's common rows in common with it (so one that shares a
-    few rows does not cost a group its long prefix)."""
+    requests whose tables begin with the same whole pages, cut so that the pages a step reads once
+    instead of per request are the most there can be (of two such cuts the one with the longer
+    group at the end)."""
     table, L = np.asarray(page_table), np.asarray(seq_len, dtype=np.int64)
-    B = len(L)
-    start, common = [0] if B else [], []
+    B, whole = len(L), np.maximum(L, 0) // dsa.PAGE
+    common = np.zeros(B, np.int64)  # whole pages that request b begins with like request b - 1
+    for b in range(1, B):
+        n = int(min(whole[b - 1], whole[b], table.shape[1]))
+        same = (table[b, :n] == table[b - 1, :n]) & (table[b, :n] >= 0)
+        common[b] = n if same.all() else int(np.argmin(same))
+    # Requests i .. j have the least of common[i + 1 .. j] pages in common.  best[j]: the pages that
+    # requests 0 .. j - 1 save; at[j]: where their last group starts.
+    best, at, pages = np.zeros(B + 1, np.int64), np.zeros(B + 1, np.int64), np.zeros(B, np.int64)
+    run = 0  # no group reaches across two neighbours with nothing in common
     for b in range(B):
-        whole = int(L[b]) // dsa.PAGE
-        if b == 0:
-            common.append(whole)
-            continue
-        first, most = start[-1], min(common[-1], whole)
-        same = (table[b, :most] == table[first, :most]) & (table[b, :most] >= 0)
-        n = most if same.all() else int(np.argmin(same))
-        if n > 0 and (b - first == 1 or 2 * n >= common[-1]):
-            common[-1] = n
-        else:
-            start.append(b)
-            common.append(whole)
-    start = np.array(start + [B], dtype=np.int32)
-    size = np.diff(start)
-    # a request alone shares nothing
-    rows = np.where(size > 1, dsa.PAGE * np.array(common, dtype=np.int64), 0) if B else np.zeros(0, np.int64)
-    return start, np.repeat(rows, size).astype(np.int32)
+        if common[b] == 0:
+            run = b
+        pages[run:b] = np.minimum(pages[run:b], common[b])
+        pages[b] = whole[b]
+        saved = best[run:b + 1] + (b - np.arange(run, b + 1)) * pages[run:b + 1]
+        at[b + 1] = run + int(np.argmax(saved))
+        best[b + 1] = saved[at[b + 1] - run]
+    start, rows = [B], np.zeros(B, np.int32)
+    while start[-1] > 0:
+        j = start[-1]
+        i = int(at[j])
+        if j - i > 1:  # a request alone shares nothing
+            rows[i:j] = dsa.PAGE * int(common[i + 1:j].min())
+        start.append(i)
+    return np.array(start[::-1] if B else [0], dtype=np.int32), rows
 
 
 class PackedIO:
