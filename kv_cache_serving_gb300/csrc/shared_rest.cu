@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, MANY ? 7 : 4) join_kernel(con
   int chunks = n > 0 ? (n + a.chunk - 1) / a.chunk : 0;
   bool bad = n < 0;
   if (S0 <= 0) {
-    pieces = 0;
+    bad = bad || pieces != 0;  // its group has a prefix (flagged where that was computed)
   } else if (!bad && (pieces < 1 || pieces > a.prefix_slots)) {
     // no group holds this request, or its group's first has another prefix
     if (lane == 0) set_error(a.err, DSA_DEV_BAD_GROUP);

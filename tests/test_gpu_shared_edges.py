@@ -1,4 +1,5 @@
-"""Decode over shared prefixes: how exact the shared rows' weights are, and scales far below one.
+"""Decode over shared prefixes: how exact the shared rows' weights are, scales far below one, and
+what a member that states another prefix gets.
 
 Bars of `fine` (relative to sum a |v|, the weighted magnitudes, with a the softmax weights): a weight
 is kept as two bf16 numbers, the second of what the first leaves out, so it is off by 2^-8 of
@@ -66,3 +67,37 @@ def test_scales_far_below_one(scale, size):
         t.copy_((t.float() * size).to(BF))
     bt.check(*bt.run())
     assert dsa.dsa_get_device_error(bt.ws) == 0
+
+
+@pytest.mark.parametrize("masked", [None, (40, 0.4, 9)], ids=["dense", "masked"])
+@pytest.mark.parametrize("stated", [0, 1, 41])
+def test_a_member_states_another_prefix(stated, masked):
+    """NaN and BAD_PREFIX, also where what it states is none; its neighbours keep their results, and
+    the next call with sound data has all of them."""
+    bt = Batch([4, 3], [64, 40], [30] * 7, 2, 4, 128, masked, seed=31)
+    bt.shared = dsa.shared_prefix(bt.gs, bt.pre, 64, 100)
+    out, lse = bt.run()
+    pre = bt.pre.clone()
+    bt.pre[5] = stated
+    o2, l2 = bt.run()
+    assert dsa.dsa_get_device_error(bt.ws) == 15
+    assert torch.isnan(o2[5].float()).all() and torch.isnan(l2[5]).all()
+    good = [0, 1, 2, 3, 4, 6]
+    assert torch.equal(out[good], o2[good]) and torch.equal(lse[good], l2[good])
+    dsa.dsa_clear_device_error(bt.ws)
+    bt.pre.copy_(pre)
+    o2, l2 = bt.run()
+    assert dsa.dsa_get_device_error(bt.ws) == 0 and torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("first,members", [(0, 40), (65, 40), (-1, 40)])
+def test_the_first_of_a_group_states_another_prefix(first, members):
+    """The group's prefix is what its first request states: members that state another get NaN."""
+    bt = Batch([4, 3], [64, 40], [30] * 7, 2, 4, 128, seed=31)
+    bt.shared = dsa.shared_prefix(bt.gs, bt.pre, 64, 100)
+    out, lse = bt.run()
+    bt.pre[4] = first
+    o2, l2 = bt.run()
+    assert dsa.dsa_get_device_error(bt.ws) in (14, 15)
+    assert torch.equal(out[:4], o2[:4]) and torch.equal(lse[:4], l2[:4])
+    assert torch.isnan(o2[5:].float()).all() and torch.isnan(l2[5:]).all()
