@@ -6,6 +6,7 @@ binding.  PyTorch provides the device memory and the stream, nothing else.
 """
 from __future__ import annotations
 
+import contextlib
 import copy
 import math
 
@@ -17,6 +18,22 @@ from . import dsa
 
 def _i32(x, device):
     return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32)).to(device)
+
+
+@contextlib.contextmanager
+def _made_on(stream):
+    """Tensors made inside belong to `stream` (None: the current one), which the call that writes them
+    is launched on: their memory was free there and is free again, in its order, when the caller
+    lets go of them.  On a stream that records a graph nothing can be allocated; what a recorded
+    call writes comes from the current stream, and the caller keeps it as long as the graph."""
+    if stream is None:
+        yield
+        return
+    with torch.cuda.stream(stream):
+        if not torch.cuda.is_current_stream_capturing():
+            yield
+            return
+    yield
 
 
 def estimated_kept_rows(lengths) -> np.ndarray:
@@ -200,8 +217,9 @@ class DecodeBatch:
         """Unmap the pages no later step reads; returns (freed page ids tensor,
         count tensor) -- the ids are valid up to min(count, capacity)."""
         cap = self.page_table.numel() if capacity is None else capacity
-        freed = torch.full((max(cap, 1),), -1, dtype=torch.int32, device=self.device)
-        count = torch.zeros(1, dtype=torch.int32, device=self.device)
+        with _made_on(stream):
+            freed = torch.full((max(cap, 1),), -1, dtype=torch.int32, device=self.device)
+            count = torch.zeros(1, dtype=torch.int32, device=self.device)
         dsa.dsa_evict_pages(self.dims, self.seq_len, self.prompt_len, self.window, self.page_table,
                             freed[:cap] if cap > 0 else None, count, self.ws, stream)
         return freed, count
@@ -300,17 +318,18 @@ class DecodeBatch:
         return dsa.shared_prefix(_i32(group_start, self.device), _i32(prefix_len, self.device), max_prefix,
                                  max_suffix)
 
-    def _out_of_q(self, out):
-        """Where a call whose out has q's type writes it."""
+    def _out_of_q(self, out, stream):
+        """Where a call on `stream` whose out has q's type writes it."""
         if out is not None:
             return out
         if getattr(self, "out_q", None) is None or self.out_q.dtype is not self.q.dtype:
-            self.out_q = torch.empty_like(self.q)
+            with _made_on(stream):
+                self.out_q = torch.empty_like(self.q)
         return self.out_q
 
     def decode_dense_shared(self, shared, out=None, lse=None, stream=None):
         """decode_dense, a shared prefix once for its group; out has q's type (bf16)."""
-        out, lse = self._out_of_q(out), self.lse if lse is None else lse
+        out, lse = self._out_of_q(out, stream), self.lse if lse is None else lse
         dsa.dsa_decode_dense_shared(self.dims, shared, self.q, self.k_pages, self.v_pages, self.page_table,
                                     self.seq_len, self.scale, out, lse, self.ws, stream)
         return out, lse
@@ -318,7 +337,7 @@ class DecodeBatch:
     def decode_sparse_masked_shared(self, shared, out=None, lse=None, stream=None):
         """decode_sparse_masked, a shared prefix of the prompts once for its group; out has q's
         type (bf16)."""
-        out, lse = self._out_of_q(out), self.lse if lse is None else lse
+        out, lse = self._out_of_q(out, stream), self.lse if lse is None else lse
         dsa.dsa_decode_sparse_masked_shared(self.dims, shared, self.q, self.k_pages, self.v_pages,
                                             self.page_table, self.seq_len, self.prompt_len, self.window,
                                             self.keep_mask, self.scale, out, lse, self.ws, stream)
@@ -329,11 +348,12 @@ class DecodeBatch:
         dsa.dsa_write_rows(self.dims, row_slot, k, v, self.k_pages, self.v_pages, self.ws, stream)
 
     def attention_mass(self, r_local=2, r_diag=2, with_offsets=True, stream=None):
-        mass = torch.empty((self.batch, self.hq, 4), dtype=torch.float32, device=self.device)
         om = None
-        if with_offsets:
-            om = torch.empty((self.batch, self.hq, self.dims.max_window + 1), dtype=torch.float32,
-                             device=self.device)
+        with _made_on(stream):
+            mass = torch.empty((self.batch, self.hq, 4), dtype=torch.float32, device=self.device)
+            if with_offsets:
+                om = torch.empty((self.batch, self.hq, self.dims.max_window + 1),
+                                 dtype=torch.float32, device=self.device)
         dsa.dsa_attention_mass(self.dims, self.q, self.k_pages, self.page_table, self.seq_len,
                                self.prompt_len, self.window, self.grid_w, r_local, r_diag,
                                self.scale, mass, om, self.ws, stream)
@@ -364,8 +384,9 @@ class PagePool:
         dev = batch.device
         if max_tokens is None:
             max_tokens = batch.batch if new_len is None else int(new_len.sum())
-        start = torch.empty(batch.batch + 1, dtype=torch.int32, device=dev)
-        slot, pos = (torch.empty(max_tokens, dtype=torch.int32, device=dev) for _ in range(2))
+        with _made_on(stream):
+            start = torch.empty(batch.batch + 1, dtype=torch.int32, device=dev)
+            slot, pos = (torch.empty(max_tokens, dtype=torch.int32, device=dev) for _ in range(2))
         dsa.dsa_assign_pages(batch.dims, batch.seq_len, new_len, self.free, self.count, self.count,
                              batch.page_table, start, slot, pos, batch.ws, stream)
         return start, slot, pos

@@ -1,9 +1,12 @@
-"""Page assignment from free lists whose count is not one of the list, against the definition (equal)."""
+"""Page assignment from free lists whose count is not one of the list, against the definition (equal),
+and on another stream than the current one."""
 import numpy as np
 import pytest
 import torch
 
 from kv_cache_serving_gb300 import dsa
+from kv_cache_serving_gb300 import workloads as wl
+from kv_cache_serving_gb300.session import DecodeBatch, PagePool
 from test_gpu_step import assign_case, assign_ref, i32, run_assign
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +93,45 @@ def test_eviction_into_a_list_that_is_too_small_and_back():
     wt, want, _, _ = assign_ref(L + n, n, lst, 10 - taken, now, pool, int(n.sum()))
     dsa.check_device_error(ws)
     assert np.array_equal(pt.cpu().numpy(), wt) and np.array_equal(slot.cpu().numpy(), want)
+
+
+def step(spare=40):
+    w = wl.generate(wl.scaled(wl.WORKLOADS["llamagen-xl"], batch=4), spare_pages=spare)
+    bt = DecodeBatch.from_workload(w)
+    table = np.pad(w["page_table"], ((0, 0), (0, 2)), constant_values=-1)
+    bt.page_table = i32(table)
+    bt.dims.max_pages_per_req = table.shape[1]
+    bt.ws = dsa.alloc_workspace(bt.dims)
+    bt.seq_len.add_(1)
+    return w, bt, PagePool(w["num_pages"], table[table >= 0])
+
+
+def test_outputs_on_another_stream_are_let_go_of_in_its_order():
+    """Their memory is not the current stream's to hand out."""
+    w, bt, pool = step()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = pool.assign(bt, stream=s)
+    s.synchronize()
+    bt.check()
+    assert np.array_equal(got[2].cpu().numpy(), w["seq_len"]) and (got[1] >= 0).all()
+    at = {t.data_ptr() for t in got}
+    del got
+    assert not at & {torch.empty(k, dtype=torch.int32, device="cuda").data_ptr() for k in (4, 5, 4, 5)}
+
+
+def test_assignment_recorded_on_another_stream():
+    w, bt, pool = step()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    dsa.dsa_graph_begin(s)
+    start, slot, pos = pool.assign(bt, stream=s)
+    g = dsa.dsa_graph_end(s)
+    for i in range(3):
+        g.launch(s)
+        s.synchronize()
+        bt.check()
+        assert np.array_equal(pos.cpu().numpy(), w["seq_len"] + i) and (slot >= 0).all()
+        bt.seq_len.add_(1)
+        torch.cuda.synchronize()
+    g.close()
