@@ -171,8 +171,8 @@ inline int32_t* multi_count_region(const dsa_dims* d, void* ws) {
 constexpr size_t kMultiCountBytes = kMultiCounters * sizeof(int32_t);
 
 // The calls over a shared prefix.  Their states lie in the partials region; behind the counters
-// are [batch][hq] numbers of prefix states, zero between calls, and kSharedExtra states of each
-// (request, query head) for dims whose partials region does not hold four of them.
+// are [batch][hq] numbers of prefix states, zero between calls, and, for dims whose partials region
+// does not hold four states of each (request, query head), kSharedExtra of them.
 inline int shared_in_part(const dsa_dims* d) {
   const int64_t n_max = dense_rows(d) > d->max_kept ? dense_rows(d) : d->max_kept;
   return chunk_bound(n_max) * (d->head_dim + 2) / (d->head_dim + 4);
@@ -186,9 +186,12 @@ inline int32_t* shared_pieces(const dsa_dims* d, void* ws) {
 inline float* shared_extra(const dsa_dims* d, void* ws) {
   return reinterpret_cast<float*>(shared_pieces(d, ws) + shared_piece_bytes(d) / sizeof(int32_t));
 }
+inline bool shared_few(const dsa_dims* d) { return shared_in_part(d) < 4; }
 inline size_t shared_bytes(const dsa_dims* d) {
-  return shared_piece_bytes(d) + round_up(static_cast<size_t>(d->batch) * d->hq * kSharedExtra *
-                                              (d->head_dim + 4) * sizeof(float), 256);
+  const size_t extra = shared_few(d) ? static_cast<size_t>(d->batch) * d->hq * kSharedExtra *
+                                           (d->head_dim + 4) * sizeof(float)
+                                     : 0;
+  return shared_piece_bytes(d) + round_up(extra, 256);
 }
 
 // Whether a row stride is at least `least` elements and whole 16-byte pieces.

@@ -91,9 +91,8 @@ dsa_status decode_shared(const dsa_dims* d, bool mask, const dsa_shared_prefix* 
   int warps = 0;
   if (shared_rest_warps(d->head_dim, group, mask, &warps) != cudaSuccess) return DSA_ERR_CUDA;
   // states of a (request, query head): in the partials region where that holds four or more
-  const int in_part = shared_in_part(d);
-  const bool few = in_part < 4;
-  const int slots = few ? kSharedExtra : in_part;
+  const bool few = shared_few(d);
+  const int slots = few ? kSharedExtra : shared_in_part(d);
   int64_t parts = static_cast<int64_t>(sm_count()) * warps *
                   (mask ? kSharedMaskWaves : kSharedDenseWaves) / (units * 2);
   if (parts > slots / 2) parts = slots / 2;

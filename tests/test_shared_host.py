@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from kv_cache_serving_gb300 import session
+from kv_cache_serving_gb300 import dsa, session
 
 
 def tables(common, own, lens):
@@ -70,3 +70,20 @@ def test_large_batches():
     t = np.repeat(np.arange(40)[None], 3000, 0)
     start, rows = session.shared_groups(t, np.full(3000, 640))
     assert start.tolist() == [0, 3000] and (rows == 640).all()
+
+
+@pytest.mark.parametrize("batch,hq,hkv,d,pages", [(128, 32, 32, 128, 288), (128, 32, 8, 64, 100), (256, 32, 8, 128, 20),
+                                                  (64, 32, 8, 128, 16), (64, 32, 8, 64, 2)])
+def test_states_have_a_place_of_their_own_only_where_they_need_one(batch, hq, hkv, d, pages):
+    """Split decode keeps a state of d + 2 floats for every 64 rows of a head, 32 at most; four states of
+    d + 4 floats fit there, or three more are in the workspace."""
+    chunks = min(32, max(1, -(-16 * pages // 64)))
+    partials, few = batch * hq * chunks * (d + 2) * 4, chunks * (d + 2) // (d + 4) < 4
+    extra = batch * hq * 3 * (d + 4) * 4
+    dims = dsa.make_dims(batch, hq, hkv, d, 5000, pages, 96, 3, 16, "bf16", "bf16")
+    counts = 4 * batch * (hq + hkv + 1)
+    size = dsa.dsa_workspace_size(dims)
+    if few:
+        assert size >= partials + extra + counts
+    else:
+        assert partials + counts <= size < partials + counts + min(extra, 1 << 17)
