@@ -1,5 +1,5 @@
 """Decode over shared prefixes: how exact the shared rows' weights are, scales far below one, and
-what a member that states another prefix gets.
+what invalid data does to each request.
 
 Bars of `fine` (relative to sum a |v|, the weighted magnitudes, with a the softmax weights): a weight
 is kept as two bf16 numbers, the second of what the first leaves out, so it is off by 2^-8 of
@@ -14,7 +14,7 @@ import pytest
 import torch
 
 from kv_cache_serving_gb300 import dsa
-from test_gpu_shared import BF, U, Batch
+from test_gpu_shared import BF, U, Batch, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +101,36 @@ def test_the_first_of_a_group_states_another_prefix(first, members):
     assert dsa.dsa_get_device_error(bt.ws) in (14, 15)
     assert torch.equal(out[:4], o2[:4]) and torch.equal(lse[:4], l2[:4])
     assert torch.isnan(o2[5:].float()).all() and torch.isnan(l2[5:]).all()
+
+
+def test_more_kept_rows_than_the_bound():
+    """Under a mask the bound holds per kv head: heads above it get NaN, the others their results."""
+    bt = Batch([4, 3], [64, 40], [30] * 7, 4, 2, 128, (40, 0.5, 9), seed=5)
+    out, lse = bt.run()
+    rest = np.array([[int(bt.rows(b, h).sum()) - int(bt.S[b]) for h in range(bt.hkv)] for b in range(bt.B)])
+    bound = int(np.median(rest))
+    over = torch.as_tensor(rest > bound, device="cuda").repeat_interleave(bt.g, 1)
+    assert over.any() and not over.all()
+    o2, l2 = bt.run(dsa.shared_prefix(bt.gs, bt.pre, 64, bound))
+    assert dsa.dsa_get_device_error(bt.ws) == 15
+    assert torch.isnan(o2[over].float()).all() and torch.isnan(l2[over]).all()
+    assert torch.equal(o2[~over], out[~over]) and torch.equal(l2[~over], lse[~over])
+
+
+@pytest.mark.parametrize("starts", [[1, 1, 5, 8], [0, 1, 5, 7], [0, 9, 8, 8], [0, -1, 5, 8], [0, 1, 5, 10], [3, 2, 1, 0],
+                                    [0, 5, 1, 8]])
+def test_groups_that_are_no_partition(starts):
+    """No prefix is computed then: every request that states one gets NaN, one that states none its
+    result."""
+    bt = Batch([1, 4, 3], [0, 64, 40], [30] * 8, 2, 4, 128, seed=31)
+    out, lse = bt.run()
+    gs = bt.gs.clone()
+    bt.gs.copy_(i32(starts))
+    o2, l2 = bt.run()
+    assert dsa.dsa_get_device_error(bt.ws) == 14
+    assert torch.isnan(o2[1:].float()).all() and torch.isnan(l2[1:]).all()
+    assert torch.equal(o2[0], out[0]) and torch.equal(l2[0], lse[0])
+    dsa.dsa_clear_device_error(bt.ws)
+    bt.gs.copy_(gs)
+    o2, l2 = bt.run()
+    assert dsa.dsa_get_device_error(bt.ws) == 0 and torch.equal(o2, out) and torch.equal(l2, lse)
