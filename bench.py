@@ -64,12 +64,12 @@ FALLBACK_HBM_GBS = 6800.0
 # decode-kernel sources whose digest is `digest` and are reported as null
 # otherwise.
 NCU_TRAFFIC = {
-    "digest": "3eec322670c4de8c",
+    "digest": "5ef111899944e702",
     "bytes": {
-        "mixed-serving-gqa4": 168322816,
-        "janus-pro-7b-like-32x32": 316365056,
+        "mixed-serving-gqa4": 168335872,
+        "janus-pro-7b-like-32x32": 316503296,
         "llamagen-xl-like-24x24": 21439488,
-        "emu3-8b-like-90x90-gqa4": 3278592,
+        "emu3-8b-like-90x90-gqa4": 3278848,
     },
 }
 

@@ -406,7 +406,9 @@ dsa_status dsa_prefill_sparse(const dsa_dims* dims, int32_t max_q, const void* q
  * (freed_count may then exceed capacity: only the first `capacity` entries are
  * written).  Invalid sizes set DSA_DEV_BAD_SEQ_LEN / _PROMPT / _WINDOW and leave
  * that request's pages alone.  The decode calls never read evicted rows, so a
- * batch decodes the same after eviction.
+ * batch decodes the same after eviction.  A page that several requests map outside their prompts is
+ * handed back by each that evicts it, so a free list would hold it more than once: only pages of
+ * prompts, which are never evicted, may be shared by requests whose pages are.
  */
 dsa_status dsa_evict_pages(const dsa_dims* dims, const int32_t* seq_len,
                            const int32_t* prompt_len, const int32_t* window, int32_t* page_table,
@@ -669,6 +671,11 @@ dsa_status dsa_write_rows(const dsa_dims* dims, int32_t tokens, const int32_t* r
  * The shared rows are read through the page table of the group's first request; the others may
  * map the same pages or copies of them.  A group of one request, or of prefix_len 0, is one that
  * shares nothing.
+ * When it pays: the plain calls read rows that requests have in common out of the L2 and need one
+ * kernel where these need three.  On a GB300, 8 to 32 kv heads: from about 1000 shared rows in a
+ * group of 4 requests, 400 of 16, 100 of 64, that is where (requests - 1) * prefix summed over
+ * the groups passes 3000 to 6000 rows; head_dim 64 under a mask in many small groups takes 25000.
+ * Below, dsa_decode_dense and dsa_decode_sparse_masked are faster (by up to a factor of 3).
  */
 typedef struct {
   int32_t groups;
@@ -687,9 +694,10 @@ typedef struct {
  * float32 or NULL.  Softmax weights enter the product with V as two bf16 numbers each (2^-16 of
  * it), sums are taken of them unrounded in fp32.  batch <= 65535 and hkv <= 65535.
  * A request with invalid lengths, a prefix_len outside 0 .. max_prefix or above its rows, or more
- * than max_suffix other rows (DSA_DEV_BAD_PREFIX), or one that no group holds or that states
- * another prefix_len than its group's first (DSA_DEV_BAD_GROUP or _BAD_PREFIX) gets NaN; a
- * group_start that does not rise from 0 to batch sets DSA_DEV_BAD_GROUP.
+ * than max_suffix other rows (DSA_DEV_BAD_PREFIX; under a mask for the kv heads that keep more), or
+ * one that states another prefix_len than its group's first (DSA_DEV_BAD_GROUP or _BAD_PREFIX) gets
+ * NaN.  With a group_start that does not rise from 0 to batch (DSA_DEV_BAD_GROUP) no prefix is
+ * computed: every request that states one gets NaN.
  * Behind every call, one that set a device error as well, `ws` is ready for the next.
  */
 dsa_status dsa_decode_dense_shared(const dsa_dims* dims, const dsa_shared_prefix* shared,

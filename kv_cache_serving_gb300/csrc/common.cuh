@@ -56,7 +56,9 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 // kern<<<grid, block, smem, s>>>(args...) as a programmatic dependent launch:
 // the grid may be scheduled while the previous kernel on the stream drains.
 // Every libdsa kernel starts with griddep_wait(), so none touches memory before
-// its predecessor has completed.
+// its predecessor has completed, but for rest_kernel (shared_rest.cu) behind a
+// prefix kernel, whose CTAs let it go only after their own wait: it relies on that one
+// having waited, and its first CTA waits for the prefix kernel before the grid ends.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t s, Args&&... args) {

@@ -25,15 +25,16 @@
 // All members keep every row of the prefix, so there is no mask; rows of the last page behind the
 // prefix (another request's, or nothing yet) get weight 0 and V rows of zeros.
 //
-// What bounds it: weighing, 0.9 us of a block's 1.06, of which the exponentials are half.  Alone on
-// the GPU its loads keep up; beside the rest kernel, whose warps fill the queues to memory, they
-// are late by 0.4 us a block.  Before the first scores there are the groups' two dependent loads,
-// page ids and rows (5 us, 7 beside), behind the last block the states of 128 rows (1.7 us).
-// Measured, whole calls: 64 requests of 32/8 heads behind 16391 rows 36 us, of which this kernel 28
-// (30 and 22 where the requests have one own row each).  A CTA leaves room for two CTAs of the rest
-// kernel (160 registers a thread, 145 KB): without, that one starts behind it (128 requests of nine
-// prompts 77 us, 71 with it).  In its place, warps of 8 query rows with mma.sync for groups of few
-// rows: 28 us for 64 images of four prompts where this took 24.
+// What bounds it: weighing, one warp per scheduler: 1.04 us of a block's 1.11, and 1.41 of 1.52
+// beside the rest kernel, whose warps share the schedulers.  (With weights of one bf16 number a block
+// took 1.06 us by itself, and 64 requests behind 16391 rows 36.5 as a whole.)
+// Before the first scores there are the groups' two dependent loads, page ids and rows (5 us, 7
+// beside), behind the last block the states of 128 rows (1.7 us).  Measured, whole calls: 64
+// requests of 32/8 heads behind 16391 rows 40.7 us (31.4 where the requests have one own row each).
+// A CTA leaves room for two CTAs of the rest kernel (160 registers a thread, 145 KB): without, that
+// one started behind it (128 requests of nine prompts 77 us, 71 with it).  In its place, warps of 8
+// query rows with mma.sync for groups of few rows: 28 us for 64 images of four prompts where this
+// took 24.
 #include <cuda.h>
 #include <math.h>
 
@@ -71,9 +72,8 @@ constexpr uint32_t kBf16Operands = (1u << 7) | (1u << 10);
 
 // How long rows stay in the L2: prefixes that fit there as usual, for the next step; those that do
 // not (kStayBytes of K and V, by the host's bounds) leave first, which keeps the states there until
-// the join.  64 requests behind 16391 rows (67 MB) 36.1 us, as usual 38.0; 128 of nine prompts (73
-// MB) 60.1 and 61.8; but 64 images of four prompts (17 MB) 21.9 and 21.5, eight requests (6 MB)
-// 13.0 and 12.4.
+// the join.  64 requests behind 16391 rows (67 MB) 40.4 us, as usual 42.2; 128 of nine prompts (73
+// MB) 60.3 and 61.7; but eight requests (6 MB) 13.2 and 12.6.
 constexpr int64_t kStayBytes = 48 << 20;
 __device__ __forceinline__ uint64_t l2_policy(bool leave) {
   uint64_t first, usual;
@@ -134,7 +134,8 @@ __device__ __forceinline__ Group load_group(const SharedLaunch& a, int g, int32_
 
 // Blocks that beginning another tile is worth (queries, the first rows, the state: 5 us), none for a
 // tile of few blocks, which is better not cut; the line has so many places before the tile's own.
-// 64 requests behind 16391 rows 38.1 us, 42.4 with tiles begun for nothing, 39.0 with 8 blocks.
+// 64 requests behind 16391 rows 40.6 us, 47.5 with tiles begun for nothing, 45.8 with 4 blocks,
+// 43.5 with 8.
 __device__ __forceinline__ int tile_cost(const Group& g) { return min(6, g.blocks >> 3); }
 
 // A CTA's place on the line of blocks.

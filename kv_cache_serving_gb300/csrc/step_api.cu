@@ -19,8 +19,8 @@ namespace {
 // bound of a request's rows only), and the rows that a chunk is a multiple of.  128 requests of
 // nine prompts, 1 .. 1024 own rows: 60 us cut for six half waves, 63 for eight, ten or twelve.  64
 // images, 40 kept rows on the average: 24 us for two half waves, 21.5 for three or four, 22.5 for
-// five or six.  Eight requests of 1 .. 300 own rows: 12.1 us in chunks of 64, 12.6 of 32 (more to
-// join), 17.7 of 128.
+// five or six.  Eight requests of 1 .. 300 own rows: 12.8 us in chunks of 64, 13.3 of 32 (more to
+// join), 17.8 of 128.
 constexpr int kSharedDenseWaves = 6, kSharedMaskWaves = 4, kSharedChunk = 64;
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {

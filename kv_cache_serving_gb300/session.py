@@ -79,7 +79,8 @@ def shared_groups(page_table, seq_len):
     """(group_start, prefix_len) for DecodeBatch.share_prefix from host arrays: runs of neighbouring
     requests whose tables begin with the same whole pages, cut so that the pages a step reads once
     instead of per request are the most there can be (of two such cuts the one with the longer
-    group at the end)."""
+    group at the end).  Whether the shared calls are then faster than the plain ones is the
+    caller's to say: dsa_shared_prefix in include/dsa.h says from how many rows on."""
     table, L = np.asarray(page_table), np.asarray(seq_len, dtype=np.int64)
     B, whole = len(L), np.maximum(L, 0) // dsa.PAGE
     common = np.zeros(B, np.int64)  # whole pages that request b begins with like request b - 1
